@@ -318,6 +318,44 @@ size_t zc_moe_quantized_weight_bytes(const zc_moe_desc* desc);
 zc_status zc_moe_quantize_weights(const zc_moe_desc* desc, int which,
                                   const void* src, void* dst, void* stream);
 
+/* Root-mean-square norm with the residual's addition: the step in front of
+ * the layer.  Row by row (T rows of d values, dtype a zc_dtype):
+ *   r     = x + res, rounded to dtype (res NULL: r = x);
+ *   rstd  = 1 / sqrt(mean(r^2) + eps), fp32, from the rounded r;
+ *   y     = r * rstd * gamma in fp32, rounded once to dtype.
+ * r, rstd (fp32 [T]) and codes may be NULL: then they are not written.
+ * codes and scales (both or neither; bf16, d a multiple of 128) receive y
+ * as MXFP8, the operand that zc_moe_experts takes in place of quantizing x
+ * itself: codes [T][d] E4M3; scales [T][d/32] E8M0, block b of a row at
+ * 4*(b/4) + {0,2,1,3}[b%4].  The rule is that of zc_moe_quantize_weights,
+ * on the rounded y; a NaN becomes the E4M3 NaN, an infinity saturates.
+ * r may be x or res, and y may be x or res, in place (r and y are two
+ * buffers); any other overlap of an output with an input, or of two outputs,
+ * is ZC_ERR_INVALID.  Needs eps > 0, d at most 32768 and a multiple of
+ * 8 (bf16) or 4 (fp32). */
+typedef struct {
+  int64_t T;     /* rows (0 allowed: nothing is done) */
+  int64_t d;
+  int32_t dtype; /* zc_dtype of x, res, gamma, r, y and of every gradient */
+  float eps;
+} zc_norm_desc;
+zc_status zc_rmsnorm_forward(const zc_norm_desc* desc, const void* x, const void* res,
+                             const void* gamma, void* r, void* y, float* rstd, uint8_t* codes,
+                             uint8_t* scales, void* stream);
+
+/* Backward of zc_rmsnorm_forward from its r (x itself without res) and
+ * rstd: with a = dy * gamma and n = r * rstd,
+ *   dr     = rstd * (a - n * mean(a n)) + dres, rounded once;
+ *   dgamma = sum over rows of dy * n, [d] (zeros when T == 0).
+ * dr is the gradient of x and of res alike.  dres (nullable) is the gradient
+ * that reaches r by the residual stream.  dr may be dy, dres or r, in place; any
+ * other overlap is ZC_ERR_INVALID.  Both gradients are overwritten.
+ * ws: zc_rmsnorm_workspace_size bytes (0 for an invalid description). */
+size_t zc_rmsnorm_workspace_size(const zc_norm_desc* desc);
+zc_status zc_rmsnorm_backward(const zc_norm_desc* desc, const void* dy, const void* r,
+                              const void* gamma, const float* rstd, const void* dres, void* dr,
+                              void* dgamma, void* ws, size_t ws_bytes, void* stream);
+
 /* Kernel timing for benchmarks.  While profiling is on, every entry point
  * brackets each of its kernel launches with a pair of HIP events recorded on
  * the call's own stream, tagged with one of the phases below.  The events
@@ -331,7 +369,7 @@ enum {
   ZC_PH_BWD_COMBINE, ZC_PH_BWD_DOWN_DH, ZC_PH_BWD_DOWN_DW, ZC_PH_BWD_GATE_UP_DX,
   ZC_PH_BWD_GATE_UP_DW, ZC_PH_BWD_ROUTER_DW, ZC_PH_BWD_ROUTER_DX, ZC_PH_BWD_DX_GATHER,
   ZC_PH_BIAS_UPDATE, ZC_PH_TILE_OFFSETS, ZC_PH_LB_LOSS, ZC_PH_LB_COEF, ZC_PH_ROUTE_STATS,
-  ZC_PH_ACCUMULATE, ZC_PH_QUANTIZE, ZC_PH_BWD_GATHER, ZC_NUM_PHASES
+  ZC_PH_ACCUMULATE, ZC_PH_QUANTIZE, ZC_PH_BWD_GATHER, ZC_PH_NORM, ZC_PH_NORM_BWD, ZC_NUM_PHASES
 };
 zc_status zc_moe_profile(int on);
 zc_status zc_moe_profile_read(double* total_ms, int32_t* count);

@@ -721,6 +721,56 @@ zc_status scratch_ptr(void** out) {
   return ZC_OK;
 }
 
+// Two ranges share bytes.
+bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
+  const char *p = static_cast<const char*>(a), *q = static_cast<const char*>(b);
+  return p && q && na > 0 && nb > 0 && p < q + nb && q < p + na;
+}
+
+// A buffer a call reads or writes; outputs may be the very buffer of an
+// input where the call allows it (in place), and overlap nothing else.
+struct Range {
+  const void* p;
+  int64_t bytes;
+  const char* name;
+  bool inplace;  // input: an output may take its place
+};
+zc_status check_overlap(const Range* out, int nout, const Range* in, int nin) {
+  for (int i = 0; i < nout; ++i) {
+    for (int j = 0; j < nin; ++j)
+      if (overlap(out[i].p, out[i].bytes, in[j].p, in[j].bytes) &&
+          !(out[i].inplace && in[j].inplace && out[i].p == in[j].p && out[i].bytes == in[j].bytes))
+        return fail(ZC_ERR_INVALID, "%s overlaps %s", out[i].name, in[j].name);
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i].p, out[i].bytes, out[j].p, out[j].bytes))
+        return fail(ZC_ERR_INVALID, "%s overlaps %s", out[i].name, out[j].name);
+  }
+  return ZC_OK;
+}
+
+zc_status check_norm(const zc_norm_desc* d) {
+  if (!d) return fail(ZC_ERR_INVALID, "desc is NULL");
+  if (d->T < 0 || d->d < 1)
+    return fail(ZC_ERR_INVALID, "bad sizes T=%lld d=%lld", (long long)d->T, (long long)d->d);
+  if (d->dtype != ZC_F32 && d->dtype != ZC_BF16)
+    return fail(ZC_ERR_INVALID, "dtype %d is neither ZC_F32 nor ZC_BF16", d->dtype);
+  if (!std::isfinite(d->eps) || !(d->eps > 0.f))
+    return fail(ZC_ERR_INVALID, "eps is not a positive number");
+  const int mult = d->dtype == ZC_BF16 ? 8 : 4;
+  if (d->d % mult || d->d > zc::kNormMaxD)
+    return fail(ZC_ERR_UNSUPPORTED, "%s rows need d a multiple of %d and at most %d (d=%lld)",
+                d->dtype == ZC_BF16 ? "bf16" : "fp32", mult, zc::kNormMaxD, (long long)d->d);
+  if (d->T >= (int64_t(1) << 31)) return fail(ZC_ERR_UNSUPPORTED, "T too large for one grid");
+  return ZC_OK;
+}
+int64_t norm_esize(const zc_norm_desc* d) { return d->dtype == ZC_F32 ? 4 : 2; }
+int64_t norm_ws_bytes(const zc_norm_desc* d) {
+  const int n = static_cast<int>(d->d);
+  const int64_t np = d->dtype == ZC_BF16 ? zc::norm_bwd_parts<bf16_t>(d->T, n)
+                                         : zc::norm_bwd_parts<float>(d->T, n);
+  return a256(np * d->d * 4);
+}
+
 zc_status check_weights(const zc_moe_desc* d, const void* wg, const void* wu, const void* wd) {
   const bool opt = d->N == 0;
   ZC_CHECK(check_ptr(wg, "w_gate", opt));
@@ -974,6 +1024,93 @@ zc_status zc_moe_pid_update(int64_t N, int64_t Z, int64_t K, const int32_t* coun
   return ZC_OK;
 }
 
+zc_status zc_rmsnorm_forward(const zc_norm_desc* desc, const void* x, const void* res,
+                             const void* gamma, void* r, void* y, float* rstd, uint8_t* codes,
+                             uint8_t* scales, void* stream) {
+  ZC_CHECK(check_norm(desc));
+  const bool none = desc->T == 0;
+  ZC_CHECK(check_ptr(x, "x", none));
+  ZC_CHECK(check_ptr(res, "res", true));
+  ZC_CHECK(check_ptr(gamma, "gamma"));
+  ZC_CHECK(check_ptr(r, "r", true));
+  ZC_CHECK(check_ptr(y, "y", none));
+  ZC_CHECK(check_ptr(rstd, "rstd", true));
+  ZC_CHECK(check_ptr(codes, "codes", true));
+  ZC_CHECK(check_ptr(scales, "scales", true));
+  if ((codes == nullptr) != (scales == nullptr))
+    return fail(ZC_ERR_INVALID, "codes and scales must both be set or both be NULL");
+  if (codes && (desc->dtype != ZC_BF16 || desc->d % 128))
+    return fail(ZC_ERR_UNSUPPORTED, "MXFP8 output needs bf16 rows and d a multiple of 128 (d=%lld)",
+                (long long)desc->d);
+  const int64_t n = desc->T * desc->d, b = n * norm_esize(desc);
+  const Range in[] = {{x, b, "x", true}, {res, b, "res", true},
+                      {gamma, desc->d * norm_esize(desc), "gamma", false}};
+  const Range out[] = {{r, b, "r", true}, {y, b, "y", true}, {rstd, 4 * desc->T, "rstd", false},
+                       {codes, n, "codes", false}, {scales, n / 32, "scales", false}};
+  ZC_CHECK(check_overlap(out, 5, in, 3));
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const int d = static_cast<int>(desc->d);
+  if (desc->dtype == ZC_BF16)
+    ZC_LAUNCH(ZC_PH_NORM,
+              zc::launch_norm_fwd(static_cast<const bf16_t*>(x), static_cast<const bf16_t*>(res),
+                                  static_cast<const bf16_t*>(gamma), static_cast<bf16_t*>(r),
+                                  static_cast<bf16_t*>(y), rstd, codes, scales, desc->T, d,
+                                  desc->eps, s),
+              "norm launch");
+  else
+    ZC_LAUNCH(ZC_PH_NORM,
+              zc::launch_norm_fwd(static_cast<const float*>(x), static_cast<const float*>(res),
+                                  static_cast<const float*>(gamma), static_cast<float*>(r),
+                                  static_cast<float*>(y), rstd, codes, scales, desc->T, d,
+                                  desc->eps, s),
+              "norm launch");
+  return ZC_OK;
+}
+
+size_t zc_rmsnorm_workspace_size(const zc_norm_desc* desc) {
+  if (check_norm(desc) != ZC_OK) return 0;
+  return static_cast<size_t>(norm_ws_bytes(desc));
+}
+
+zc_status zc_rmsnorm_backward(const zc_norm_desc* desc, const void* dy, const void* r,
+                              const void* gamma, const float* rstd, const void* dres, void* dr,
+                              void* dgamma, void* ws, size_t ws_bytes, void* stream) {
+  ZC_CHECK(check_norm(desc));
+  const bool none = desc->T == 0;
+  ZC_CHECK(check_ptr(dy, "dy", none));
+  ZC_CHECK(check_ptr(r, "r", none));
+  ZC_CHECK(check_ptr(gamma, "gamma"));
+  ZC_CHECK(check_ptr(rstd, "rstd", none));
+  ZC_CHECK(check_ptr(dres, "dres", true));
+  ZC_CHECK(check_ptr(dr, "dr", none));
+  ZC_CHECK(check_ptr(dgamma, "dgamma"));
+  ZC_CHECK(check_ws(ws, ws_bytes, norm_ws_bytes(desc)));
+  const int64_t es = norm_esize(desc), b = desc->T * desc->d * es;
+  const Range in[] = {{dy, b, "dy", true}, {r, b, "r", true}, {dres, b, "dres", true},
+                      {gamma, desc->d * es, "gamma", false}, {rstd, 4 * desc->T, "rstd", false}};
+  const Range out[] = {{dr, b, "dr", true}, {dgamma, desc->d * es, "dgamma", false},
+                       {ws, norm_ws_bytes(desc), "ws", false}};
+  ZC_CHECK(check_overlap(out, 3, in, 5));
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const int d = static_cast<int>(desc->d);
+  float* part = static_cast<float*>(ws);
+  if (desc->dtype == ZC_BF16)
+    ZC_LAUNCH(ZC_PH_NORM_BWD,
+              zc::launch_norm_bwd(static_cast<const bf16_t*>(dy), static_cast<const bf16_t*>(r),
+                                  static_cast<const bf16_t*>(gamma), rstd,
+                                  static_cast<const bf16_t*>(dres), static_cast<bf16_t*>(dr),
+                                  static_cast<bf16_t*>(dgamma), part, desc->T, d, s),
+              "norm backward launch");
+  else
+    ZC_LAUNCH(ZC_PH_NORM_BWD,
+              zc::launch_norm_bwd(static_cast<const float*>(dy), static_cast<const float*>(r),
+                                  static_cast<const float*>(gamma), rstd,
+                                  static_cast<const float*>(dres), static_cast<float*>(dr),
+                                  static_cast<float*>(dgamma), part, desc->T, d, s),
+              "norm backward launch");
+  return ZC_OK;
+}
+
 zc_status zc_moe_profile(int on) {
   std::lock_guard<std::mutex> lk(g_prof_mu);
   if (!on) drop_records();
@@ -1009,7 +1146,8 @@ const char* zc_moe_phase_name(int phase) {
       "router_gemm", "topk", "dispatch", "gate_up_gemm", "down_gemm", "combine",
       "bwd_combine", "bwd_down_dh", "bwd_down_dw", "bwd_gate_up_dx", "bwd_gate_up_dw",
       "bwd_router_dw", "bwd_router_dx", "bwd_dx_gather", "bias_update", "tile_offsets",
-      "lb_loss", "lb_coef", "route_stats", "accumulate_counts", "quantize", "bwd_gather"};
+      "lb_loss", "lb_coef", "route_stats", "accumulate_counts", "quantize", "bwd_gather",
+      "norm", "norm_bwd"};
   return (phase >= 0 && phase < ZC_NUM_PHASES) ? names[phase] : "";
 }
 

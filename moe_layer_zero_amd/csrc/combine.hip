@@ -18,53 +18,6 @@ constexpr int kThreads = 256;
 constexpr int kCombineMaxThreads = 1024;
 constexpr int kMaxK = 32;
 
-// 16-byte vector of the layer dtype, widened to fp32.
-template <typename T> struct V16;
-template <> struct V16<bf16_t> {
-  static constexpr int n = 8;
-  typedef u32x4_t raw_t;  // the 16 bytes as loaded
-  static __device__ __forceinline__ raw_t ld_raw(const bf16_t* p) {
-    return *reinterpret_cast<const u32x4_t*>(p);
-  }
-  // for data read exactly once (the expert output rows)
-  static __device__ __forceinline__ raw_t ld_raw_once(const bf16_t* p) {
-    return __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(p));
-  }
-  static __device__ __forceinline__ void unpack(const raw_t& v, float* f) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      f[2 * e] = __uint_as_float(v[e] << 16);
-      f[2 * e + 1] = __uint_as_float(v[e] & 0xffff0000u);
-    }
-  }
-  static __device__ __forceinline__ void load(const bf16_t* p, float* f) { unpack(ld_raw(p), f); }
-  static __device__ __forceinline__ void store(bf16_t* p, const float* f) {
-    u32x4_t v;
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      v[e] = static_cast<uint32_t>(f2bf(f[2 * e])) | (static_cast<uint32_t>(f2bf(f[2 * e + 1])) << 16);
-    *reinterpret_cast<u32x4_t*>(p) = v;
-  }
-};
-template <> struct V16<float> {
-  static constexpr int n = 4;
-  typedef f32x4_t raw_t;
-  static __device__ __forceinline__ raw_t ld_raw(const float* p) {
-    return *reinterpret_cast<const f32x4_t*>(p);
-  }
-  static __device__ __forceinline__ raw_t ld_raw_once(const float* p) {
-    return __builtin_nontemporal_load(reinterpret_cast<const f32x4_t*>(p));
-  }
-  static __device__ __forceinline__ void unpack(const raw_t& v, float* f) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) f[e] = v[e];
-  }
-  static __device__ __forceinline__ void load(const float* p, float* f) { unpack(ld_raw(p), f); }
-  static __device__ __forceinline__ void store(float* p, const float* f) {
-    *reinterpret_cast<f32x4_t*>(p) = f32x4_t{f[0], f[1], f[2], f[3]};
-  }
-};
-
 // V consecutive fp32 values (V = 4 or 8, 16-byte aligned).
 template <int V>
 __device__ __forceinline__ void load_f32_n(const float* p, float* f) {

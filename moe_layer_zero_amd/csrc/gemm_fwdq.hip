@@ -97,19 +97,6 @@ __device__ __forceinline__ bf16_t cvt_bf16(float f) {
   return static_cast<bf16_t>(r);
 }
 
-// E8M0 scale of a block whose largest magnitude is amax (finite, >= 0).
-__device__ __forceinline__ int mx_scale(float amax) {
-  const int be = static_cast<int>((__float_as_uint(amax) >> 23) & 0xff);
-  return be > 8 ? be - 8 : 0;
-}
-
-// E4M3 code of v at scale S.
-__device__ __forceinline__ uint32_t mx_code(float v, int S) {
-  float q = __builtin_ldexpf(v, 127 - S);
-  q = fminf(fmaxf(q, -448.f), 448.f);
-  return static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(q, 0.f, 0, false)) & 0xffu;
-}
-
 __device__ __forceinline__ void lds_dma16(__amdgpu_buffer_rsrc_t r, lds_void* dst, uint32_t voff,
                                           int soff) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, dst, 16, voff, soff, 0, 0);

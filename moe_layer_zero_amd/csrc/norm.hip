@@ -1,0 +1,312 @@
+// Root-mean-square norm with the residual's addition, also quantized to
+// MXFP8, and its backward pass: what stands in front of every MoE layer.
+//
+// Forward, row by row (d values):
+//   r    = x + res, rounded to the layer dtype (the residual stream as the
+//          next block reads it); r = x without res
+//   rstd = 1 / sqrt(mean(r^2) + eps), from the rounded r, so that a backward
+//          pass that reads r differentiates what was computed
+//   y    = r * rstd * gamma in fp32, rounded once to the layer dtype
+//   codes, scales = MXFP8 of the rounded y: bit for bit what the FP8 expert
+//          kernels' own quantizer makes of y.
+// Backward, with a = dy * gamma and n = r * rstd:
+//   dr     = rstd * (a - n * mean(a n)) + dres, rounded once
+//   dgamma = sum over rows of dy * n (fp32 partials per workgroup, added in
+//          a fixed order, rounded once).
+//
+// Both passes are bound by HBM: a row is read once, kept in registers and
+// written once.  A row of up to 64 * NV vectors of 16 bytes belongs to one
+// wavefront (no LDS, no barrier), a longer one to a workgroup of 256 or
+// 1024 threads.
+#include "zc_common.h"
+
+namespace zc {
+namespace {
+
+// Sum over the TPR threads of a row; every thread gets it.  Wave butterflies,
+// then the wave sums in wave order.
+template <int TPR>
+__device__ __forceinline__ float row_sum(float v, float* s_red) {
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o);
+  if constexpr (TPR > 64) {
+    __syncthreads();  // the previous sum has been read
+    if ((threadIdx.x & 63) == 0) s_red[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = s_red[0];
+#pragma unroll
+    for (int w = 1; w < TPR / 64; ++w) v += s_red[w];
+  }
+  return v;
+}
+
+// MXFP8 of one thread's 8 values of a block of 32 held by 4 consecutive
+// lanes.  A NaN gets the NaN code; infinities saturate.
+__device__ __forceinline__ uint64_t mx_quad(const float* f, int& S) {
+  float amax = 0.f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(f[e]));
+  amax = fmaxf(amax, __shfl_xor(amax, 1));
+  amax = fmaxf(amax, __shfl_xor(amax, 2));
+  S = mx_scale(amax);
+  uint64_t q = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const uint32_t c = f[e] != f[e] ? 0x7fu : mx_code(f[e], S);
+    q |= static_cast<uint64_t>(c) << (8 * e);
+  }
+  return q;
+}
+
+template <typename T, int NV, int TPR, bool MX>
+__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_fwd_kernel(
+    const T* x, const T* res, const T* __restrict__ gamma, T* r, T* y, float* __restrict__ rstd,
+    uint8_t* __restrict__ codes, uint8_t* __restrict__ scales, int64_t Tn, int d, float eps) {
+  constexpr int V = V16<T>::n;
+  constexpr int RPB = (TPR < 256 ? 256 : TPR) / TPR;
+  __shared__ float s_red[TPR / 64];
+  const int tid = threadIdx.x % TPR;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * RPB + threadIdx.x / TPR;
+  if (row >= Tn) return;  // whole wavefronts only: with TPR > 64 a row is the workgroup's
+  const int64_t base = row * d;
+  // all loads of the row first; a vector past its end counts as zeros
+  typename V16<T>::raw_t wx[NV], wr[NV], wg[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int j = (tid + i * TPR) * V;
+    wx[i] = j < d ? V16<T>::ld_raw(x + base + j) : typename V16<T>::raw_t{};
+  }
+  if (res) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int j = (tid + i * TPR) * V;
+      wr[i] = j < d ? V16<T>::ld_raw(res + base + j) : typename V16<T>::raw_t{};
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int j = (tid + i * TPR) * V;
+    wg[i] = j < d ? V16<T>::ld_raw(gamma + j) : typename V16<T>::raw_t{};
+  }
+  float f[NV][V];
+  float ss = 0.f;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    V16<T>::unpack(wx[i], f[i]);
+    if (res) {
+      float g[V];
+      V16<T>::unpack(wr[i], g);
+#pragma unroll
+      for (int e = 0; e < V; ++e) f[i][e] = V16<T>::round(f[i][e] + g[e]);
+    }
+#pragma unroll
+    for (int e = 0; e < V; ++e) ss += f[i][e] * f[i][e];
+  }
+  ss = row_sum<TPR>(ss, s_red);
+  const float rs = 1.0f / sqrtf(ss / static_cast<float>(d) + eps);
+  if (rstd && tid == 0) rstd[row] = rs;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int j = (tid + i * TPR) * V;
+    if (j >= d) break;
+    float g[V];
+    V16<T>::unpack(wg[i], g);
+    if (r) V16<T>::store(r + base + j, f[i]);
+#pragma unroll
+    for (int e = 0; e < V; ++e) f[i][e] = V16<T>::round(f[i][e] * rs * g[e]);
+    V16<T>::store(y + base + j, f[i]);
+    if constexpr (MX) {
+      int S;
+      *reinterpret_cast<uint64_t*>(codes + base + j) = mx_quad(f[i], S);
+      // block b of the row; the four scales of 128 values in the order 0 2 1 3
+      const int b = j / 32, k = b & 3;
+      if ((tid & 3) == 0) scales[base / 32 + (b & ~3) + ((k & 1) << 1 | k >> 1)] = static_cast<uint8_t>(S);
+    }
+  }
+}
+
+// Rows are dealt to nblk workgroups (nblk fixed by T alone): workgroup b
+// takes rows b * RPB + sub, then every nblk * RPB further, and keeps the
+// dgamma sums of its columns in registers.
+template <typename T, int NV, int TPR>
+__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_bwd_kernel(
+    const T* dy, const T* r, const T* __restrict__ gamma,
+    const float* __restrict__ rstd, const T* dres, T* dr, float* __restrict__ part, int64_t Tn,
+    int d) {
+  constexpr int V = V16<T>::n;
+  constexpr int RPB = (TPR < 256 ? 256 : TPR) / TPR;
+  __shared__ float s_red[TPR / 64];
+  const int tid = threadIdx.x % TPR, sub = threadIdx.x / TPR;
+  float acc[NV][V], gm[NV][V];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int j = (tid + i * TPR) * V;
+#pragma unroll
+    for (int e = 0; e < V; ++e) acc[i][e] = 0.f;
+    V16<T>::unpack(j < d ? V16<T>::ld_raw(gamma + j) : typename V16<T>::raw_t{}, gm[i]);
+  }
+  for (int64_t row = static_cast<int64_t>(blockIdx.x) * RPB + sub; row < Tn;
+       row += static_cast<int64_t>(gridDim.x) * RPB) {
+    const int64_t base = row * d;
+    const float rs = rstd[row];
+    typename V16<T>::raw_t wa[NV], wn[NV], wg[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int j = (tid + i * TPR) * V;
+      wa[i] = j < d ? V16<T>::ld_raw(dy + base + j) : typename V16<T>::raw_t{};
+      wn[i] = j < d ? V16<T>::ld_raw(r + base + j) : typename V16<T>::raw_t{};
+      wg[i] = dres && j < d ? V16<T>::ld_raw(dres + base + j) : typename V16<T>::raw_t{};
+    }
+    float a[NV][V], n[NV][V], s = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      V16<T>::unpack(wa[i], a[i]);
+      V16<T>::unpack(wn[i], n[i]);
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        n[i][e] *= rs;
+        acc[i][e] += a[i][e] * n[i][e];
+        a[i][e] *= gm[i][e];
+        s += a[i][e] * n[i][e];
+      }
+    }
+    const float c = row_sum<TPR>(s, s_red) / static_cast<float>(d);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int j = (tid + i * TPR) * V;
+      if (j >= d) break;
+      float g[V];
+      V16<T>::unpack(wg[i], g);
+#pragma unroll
+      for (int e = 0; e < V; ++e) a[i][e] = rs * (a[i][e] - n[i][e] * c) + g[e];
+      V16<T>::store(dr + base + j, a[i]);
+    }
+  }
+  float* p = part + (static_cast<int64_t>(blockIdx.x) * RPB + sub) * d;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int j = (tid + i * TPR) * V;
+    if (j >= d) break;
+#pragma unroll
+    for (int q = 0; q < V / 4; ++q)
+      reinterpret_cast<f32x4_t*>(p + j)[q] =
+          f32x4_t{acc[i][4 * q], acc[i][4 * q + 1], acc[i][4 * q + 2], acc[i][4 * q + 3]};
+  }
+}
+
+// dgamma[j] = the np partial rows' column j: 16 groups of consecutive rows,
+// each summed ascending, added in group order.
+constexpr int kRedGroups = 16;
+template <typename T>
+__global__ __launch_bounds__(64 * kRedGroups) void norm_dgamma_kernel(const float* __restrict__ part,
+                                                                      int np, int d,
+                                                                      T* __restrict__ dgamma) {
+  __shared__ float s_p[kRedGroups][64];
+  const int lane = threadIdx.x & 63, g = threadIdx.x >> 6;
+  const int j = blockIdx.x * 64 + lane;
+  const int per = (np + kRedGroups - 1) / kRedGroups;
+  const int hi = min(np, (g + 1) * per);
+  float v = 0.f;
+  if (j < d)
+    for (int b = g * per; b < hi; ++b) v += part[static_cast<int64_t>(b) * d + j];
+  s_p[g][lane] = v;
+  __syncthreads();
+  if (g == 0 && j < d) {
+#pragma unroll
+    for (int k = 1; k < kRedGroups; ++k) v += s_p[k][lane];
+    Elem<T>::st(dgamma + j, v);
+  }
+}
+
+// Partial rows of the dgamma sum, by T alone.
+constexpr int kNormBlocks = 512;
+
+// One row's threads and vectors per thread: f(NV, TPR) with NV * TPR
+// vectors covering the row (d <= kNormMaxD).
+template <typename T, typename F>
+hipError_t norm_shape(int d, F&& f) {
+  const int vecs = (d + V16<T>::n - 1) / V16<T>::n;
+  using std::integral_constant;
+  if (vecs <= 64) return f(integral_constant<int, 1>{}, integral_constant<int, 64>{});
+  if (vecs <= 128) return f(integral_constant<int, 2>{}, integral_constant<int, 64>{});
+  if (vecs <= 256) return f(integral_constant<int, 4>{}, integral_constant<int, 64>{});
+  if (vecs <= 512) return f(integral_constant<int, 2>{}, integral_constant<int, 256>{});
+  if (vecs <= 768) return f(integral_constant<int, 3>{}, integral_constant<int, 256>{});
+  if (vecs <= 1024) return f(integral_constant<int, 4>{}, integral_constant<int, 256>{});
+  if (vecs <= 2048) return f(integral_constant<int, 2>{}, integral_constant<int, 1024>{});
+  if (vecs <= 4096) return f(integral_constant<int, 4>{}, integral_constant<int, 1024>{});
+  return f(integral_constant<int, 8>{}, integral_constant<int, 1024>{});
+}
+
+int64_t norm_bwd_blocks(int64_t Tn, int rpb) {
+  const int64_t b = (Tn + rpb - 1) / rpb;
+  return b < kNormBlocks ? b : kNormBlocks;
+}
+
+template <typename T>
+int norm_rows_per_block(int d) {
+  return (d + V16<T>::n - 1) / V16<T>::n <= 256 ? 4 : 1;
+}
+
+}  // namespace
+
+template <typename T>
+hipError_t launch_norm_fwd(const T* x, const T* res, const T* gamma, T* r, T* y, float* rstd,
+                           uint8_t* codes, uint8_t* scales, int64_t Tn, int d, float eps,
+                           hipStream_t s) {
+  if (Tn == 0) return hipSuccess;
+  return norm_shape<T>(d, [&](auto nv, auto tpr) {
+    constexpr int NV = decltype(nv)::value, TPR = decltype(tpr)::value;
+    constexpr int NT = TPR < 256 ? 256 : TPR, RPB = NT / TPR;
+    const dim3 grid(static_cast<unsigned>((Tn + RPB - 1) / RPB)), block(NT);
+    if constexpr (std::is_same<T, bf16_t>::value) {
+      if (codes) {
+        hipLaunchKernelGGL((norm_fwd_kernel<T, NV, TPR, true>), grid, block, 0, s, x, res, gamma, r,
+                           y, rstd, codes, scales, Tn, d, eps);
+        return hipGetLastError();
+      }
+    }
+    hipLaunchKernelGGL((norm_fwd_kernel<T, NV, TPR, false>), grid, block, 0, s, x, res, gamma, r, y,
+                       rstd, codes, scales, Tn, d, eps);
+    return hipGetLastError();
+  });
+}
+
+template <typename T>
+int64_t norm_bwd_parts(int64_t Tn, int d) {
+  const int rpb = norm_rows_per_block<T>(d);
+  return norm_bwd_blocks(Tn, rpb) * rpb;
+}
+
+template <typename T>
+hipError_t launch_norm_bwd(const T* dy, const T* r, const T* gamma, const float* rstd,
+                           const T* dres, T* dr, T* dgamma, float* part, int64_t Tn, int d,
+                           hipStream_t s) {
+  const int np = static_cast<int>(norm_bwd_parts<T>(Tn, d));
+  if (Tn > 0) {
+    const hipError_t e = norm_shape<T>(d, [&](auto nv, auto tpr) {
+      constexpr int NV = decltype(nv)::value, TPR = decltype(tpr)::value;
+      constexpr int NT = TPR < 256 ? 256 : TPR, RPB = NT / TPR;
+      hipLaunchKernelGGL((norm_bwd_kernel<T, NV, TPR>),
+                         dim3(static_cast<unsigned>(norm_bwd_blocks(Tn, RPB))), dim3(NT), 0, s, dy,
+                         r, gamma, rstd, dres, dr, part, Tn, d);
+      return hipGetLastError();
+    });
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL(norm_dgamma_kernel<T>, dim3((d + 63) / 64), dim3(64 * kRedGroups), 0, s, part,
+                     np, d, dgamma);
+  return hipGetLastError();
+}
+
+#define ZC_INST(T)                                                                              \
+  template hipError_t launch_norm_fwd<T>(const T*, const T*, const T*, T*, T*, float*, uint8_t*, \
+                                         uint8_t*, int64_t, int, float, hipStream_t);           \
+  template int64_t norm_bwd_parts<T>(int64_t, int);                                             \
+  template hipError_t launch_norm_bwd<T>(const T*, const T*, const T*, const float*, const T*,  \
+                                         T*, T*, float*, int64_t, int, hipStream_t);
+ZC_INST(bf16_t)
+ZC_INST(float)
+#undef ZC_INST
+
+}  // namespace zc

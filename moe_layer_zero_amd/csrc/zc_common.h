@@ -6,6 +6,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 namespace zc {
 
 // ---------------------------------------------------------------- types
@@ -47,6 +49,68 @@ template <> struct Elem<bf16_t> {
   static __device__ __forceinline__ void st(bf16_t* p, float v) { *p = f2bf(v); }
   static constexpr int kVec = 8;
 };
+
+// 16-byte vector of the layer dtype, widened to fp32; round: to the dtype.
+template <typename T> struct V16;
+template <> struct V16<bf16_t> {
+  static constexpr int n = 8;
+  static __device__ __forceinline__ float round(float f) { return bf2f(f2bf(f)); }
+  typedef u32x4_t raw_t;  // the 16 bytes as loaded
+  static __device__ __forceinline__ raw_t ld_raw(const bf16_t* p) {
+    return *reinterpret_cast<const u32x4_t*>(p);
+  }
+  // for data read exactly once (the expert output rows)
+  static __device__ __forceinline__ raw_t ld_raw_once(const bf16_t* p) {
+    return __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(p));
+  }
+  static __device__ __forceinline__ void unpack(const raw_t& v, float* f) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      f[2 * e] = __uint_as_float(v[e] << 16);
+      f[2 * e + 1] = __uint_as_float(v[e] & 0xffff0000u);
+    }
+  }
+  static __device__ __forceinline__ void load(const bf16_t* p, float* f) { unpack(ld_raw(p), f); }
+  static __device__ __forceinline__ void store(bf16_t* p, const float* f) {
+    u32x4_t v;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      v[e] = static_cast<uint32_t>(f2bf(f[2 * e])) | (static_cast<uint32_t>(f2bf(f[2 * e + 1])) << 16);
+    *reinterpret_cast<u32x4_t*>(p) = v;
+  }
+};
+template <> struct V16<float> {
+  static constexpr int n = 4;
+  static __device__ __forceinline__ float round(float f) { return f; }
+  typedef f32x4_t raw_t;
+  static __device__ __forceinline__ raw_t ld_raw(const float* p) {
+    return *reinterpret_cast<const f32x4_t*>(p);
+  }
+  static __device__ __forceinline__ raw_t ld_raw_once(const float* p) {
+    return __builtin_nontemporal_load(reinterpret_cast<const f32x4_t*>(p));
+  }
+  static __device__ __forceinline__ void unpack(const raw_t& v, float* f) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) f[e] = v[e];
+  }
+  static __device__ __forceinline__ void load(const float* p, float* f) { unpack(ld_raw(p), f); }
+  static __device__ __forceinline__ void store(float* p, const float* f) {
+    *reinterpret_cast<f32x4_t*>(p) = f32x4_t{f[0], f[1], f[2], f[3]};
+  }
+};
+
+// E8M0 scale of a block whose largest magnitude is amax (finite, >= 0).
+__device__ __forceinline__ int mx_scale(float amax) {
+  const int be = static_cast<int>((__float_as_uint(amax) >> 23) & 0xff);
+  return be > 8 ? be - 8 : 0;
+}
+
+// E4M3 code of v at scale S.
+__device__ __forceinline__ uint32_t mx_code(float v, int S) {
+  float q = __builtin_ldexpf(v, 127 - S);
+  q = fminf(fmaxf(q, -448.f), 448.f);
+  return static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(q, 0.f, 0, false)) & 0xffu;
+}
 
 // Row-tile height of the grouped GEMMs; the dispatch step publishes the
 // per-expert prefix of ceil(rows / kGemmBM) tiles for them.
@@ -277,6 +341,22 @@ template <typename T>
 hipError_t launch_dx_gather(const T* dout, const float* dxp, const float* dxr, const int32_t* topk_idx,
                             const float* gate, const int32_t* inv, int Tn, int d, int N, int K,
                             float out_scale, T* dx, hipStream_t s);
+
+// RMS norm with the residual's addition (norm.hip).  res, r, rstd, codes may
+// be NULL; codes (bf16 only, d % 128 == 0) come with scales, in the order of
+// launch_mxq_rows.  Rows of up to kNormMaxD values.
+constexpr int kNormMaxD = 32768;
+template <typename T>
+hipError_t launch_norm_fwd(const T* x, const T* res, const T* gamma, T* r, T* y, float* rstd,
+                           uint8_t* codes, uint8_t* scales, int64_t Tn, int d, float eps,
+                           hipStream_t s);
+// Its backward; part: norm_bwd_parts(T, d) rows of d floats.
+template <typename T>
+int64_t norm_bwd_parts(int64_t Tn, int d);
+template <typename T>
+hipError_t launch_norm_bwd(const T* dy, const T* r, const T* gamma, const float* rstd,
+                           const T* dres, T* dr, T* dgamma, float* part, int64_t Tn, int d,
+                           hipStream_t s);
 
 // Bias update, Eq.(2) of section 2.1.1.
 hipError_t launch_pid(int N, int K, const int32_t* counts, int64_t T_all, double mu, double K_e,

@@ -28,10 +28,11 @@ EXPORTS = ("zc_moe_workspace_size", "zc_moe_saved_size", "zc_moe_route", "zc_moe
            "zc_moe_forward_noalloc", "zc_moe_backward", "zc_moe_lb_loss", "zc_moe_route_stats", "zc_moe_accumulate_counts",
            "zc_moe_pid_update", "zc_moe_pack_weights", "zc_moe_quantized_weight_bytes",
            "zc_moe_quantize_weights",
+           "zc_rmsnorm_forward", "zc_rmsnorm_workspace_size", "zc_rmsnorm_backward",
            "zc_moe_profile",
            "zc_moe_profile_read",
            "zc_moe_phase_name", "zc_status_string", "zc_last_error")
-ZC_NUM_PHASES = 22
+ZC_NUM_PHASES = 24
 
 
 class ZcError(RuntimeError):
@@ -55,6 +56,10 @@ class zc_route_buf(C.Structure):
     _fields_ = [("logits", C.c_void_p), ("topk_idx", C.c_void_p), ("topk_gate", C.c_void_p),
                 ("counts", C.c_void_p), ("offsets", C.c_void_p), ("perm", C.c_void_p),
                 ("inv", C.c_void_p)]
+
+
+class zc_norm_desc(C.Structure):
+    _fields_ = [("T", C.c_int64), ("d", C.c_int64), ("dtype", C.c_int32), ("eps", C.c_float)]
 
 
 _LIB = None
@@ -87,7 +92,13 @@ def lib() -> C.CDLL:
         L.zc_moe_quantized_weight_bytes.argtypes = [P]
         L.zc_moe_quantized_weight_bytes.restype = sz
         L.zc_moe_quantize_weights.argtypes = [P, C.c_int, v, v, v]
-        for f in ("zc_moe_route", "zc_moe_forward", "zc_moe_forward_noalloc",
+        NP = C.POINTER(zc_norm_desc)
+        L.zc_rmsnorm_forward.argtypes = [NP, v, v, v, v, v, v, v, v, v]
+        L.zc_rmsnorm_workspace_size.argtypes = [NP]
+        L.zc_rmsnorm_workspace_size.restype = sz
+        L.zc_rmsnorm_backward.argtypes = [NP, v, v, v, v, v, v, v, v, sz, v]
+        for f in ("zc_rmsnorm_forward", "zc_rmsnorm_backward",
+                  "zc_moe_route", "zc_moe_forward", "zc_moe_forward_noalloc",
                   "zc_moe_backward", "zc_moe_lb_loss",
                   "zc_moe_route_stats", "zc_moe_accumulate_counts", "zc_moe_pid_update",
                   "zc_moe_pack_weights", "zc_moe_quantize_weights"):
@@ -127,6 +138,27 @@ def _stream(stream):
     if stream is None:
         stream = torch.cuda.current_stream()
     return C.c_void_p(stream.cuda_stream)
+
+
+def _run(where, tensors, stream, call, scratch=None):
+    """Runs call(stream handle) with the tensors' device current: they must all
+    live on one GPU, and a given stream must belong to it.  The default stream
+    is that device's current one.  scratch: a workspace the binding allocated
+    itself, kept from reuse until a given stream is done with it."""
+    devs = {t.device for t in tensors if t is not None}
+    if len(devs) != 1:
+        raise ValueError(f"{where}: tensors on different devices: {sorted(map(str, devs))}")
+    dev = devs.pop()
+    if dev.type != "cuda":
+        raise ValueError("tensors passed to the HIP library must live on the GPU")
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    elif stream.device != dev:
+        raise ValueError(f"{where}: stream of {stream.device}, tensors on {dev}")
+    with torch.cuda.device(dev):
+        _check(call(C.c_void_p(stream.cuda_stream)), where)
+    if scratch is not None:
+        scratch.record_stream(stream)
 
 
 @dataclass
@@ -416,3 +448,69 @@ def quantize_expert_weights(desc: LayerDesc, w_gate, w_up, w_down, stream=None):
     return (zc_moe_quantize_weights(desc, ZC_PACK_GATE_UP, w_gate, stream=stream),
             zc_moe_quantize_weights(desc, ZC_PACK_GATE_UP, w_up, stream=stream),
             zc_moe_quantize_weights(desc, ZC_PACK_DOWN, w_down, stream=stream))
+
+
+@dataclass
+class NormDesc:
+    """Rows of an RMS norm: T rows of d values, eps under the root."""
+    T: int
+    d: int
+    dtype: torch.dtype = torch.bfloat16
+    eps: float = 1e-6
+
+    def c(self) -> zc_norm_desc:
+        if self.dtype not in (torch.float32, torch.bfloat16):
+            raise ValueError("norm dtype must be float32 or bfloat16")
+        return zc_norm_desc(self.T, self.d, ZC_F32 if self.dtype == torch.float32 else ZC_BF16,
+                            self.eps)
+
+
+def mx_buffers(T: int, d: int, device="cuda"):
+    """(codes [T][d], scales [T][d/32]) uint8: the MXFP8 rows zc_rmsnorm_forward
+    writes and zc_moe_experts reads."""
+    return (torch.empty((T, d), dtype=torch.uint8, device=device),
+            torch.empty((T, d // 32), dtype=torch.uint8, device=device))
+
+
+def norm_workspace(desc: NormDesc, device="cuda") -> torch.Tensor:
+    d = desc.c()
+    n = int(lib().zc_rmsnorm_workspace_size(C.byref(d)))
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=device)
+
+
+def zc_rmsnorm_forward(desc: NormDesc, x, gamma, y, res=None, r=None, rstd=None, codes=None,
+                       scales=None, stream=None):
+    """r = x + res; y = r / sqrt(mean(r^2) + eps) * gamma, and y as MXFP8 in
+    codes and scales (mx_buffers) where given.  r and y may be x or res in
+    place."""
+    T, d, dt = desc.T, desc.d, desc.dtype
+    for t, n in ((x, "x"), (res, "res"), (r, "r"), (y, "y")):
+        _check_layer_tensor(t, (T, d), dt, n)
+    _check_layer_tensor(gamma, (d,), dt, "gamma")
+    _check_layer_tensor(rstd, (T,), torch.float32, "rstd")
+    _check_layer_tensor(codes, (T, d), torch.uint8, "codes")
+    _check_layer_tensor(scales, (T, d // 32), torch.uint8, "scales")
+    c = desc.c()
+    _run("zc_rmsnorm_forward", (x, res, gamma, r, y, rstd, codes, scales), stream,
+         lambda s: lib().zc_rmsnorm_forward(C.byref(c), _ptr(x), _ptr(res), _ptr(gamma), _ptr(r),
+                                            _ptr(y), _ptr(rstd), _ptr(codes), _ptr(scales), s))
+
+
+def zc_rmsnorm_backward(desc: NormDesc, dy, r, gamma, rstd, dr, dgamma, dres=None, ws=None,
+                        stream=None):
+    """Gradients of zc_rmsnorm_forward: dr (of x and res alike, with dres, the
+    residual stream's own gradient, added) and dgamma."""
+    T, d, dt = desc.T, desc.d, desc.dtype
+    for t, n in ((dy, "dy"), (r, "r"), (dres, "dres"), (dr, "dr")):
+        _check_layer_tensor(t, (T, d), dt, n)
+    for t, n in ((gamma, "gamma"), (dgamma, "dgamma")):
+        _check_layer_tensor(t, (d,), dt, n)
+    _check_layer_tensor(rstd, (T,), torch.float32, "rstd")
+    scratch = None
+    if ws is None:
+        ws = scratch = norm_workspace(desc, gamma.device)
+    c = desc.c()
+    _run("zc_rmsnorm_backward", (dy, r, gamma, rstd, dres, dr, dgamma, ws), stream,
+         lambda s: lib().zc_rmsnorm_backward(C.byref(c), _ptr(dy), _ptr(r), _ptr(gamma), _ptr(rstd),
+                                             _ptr(dres), _ptr(dr), _ptr(dgamma), _ptr(ws),
+                                             ws.numel(), s), scratch)
