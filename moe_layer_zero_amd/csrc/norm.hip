@@ -25,8 +25,8 @@ namespace {
 
 // Sum over the TPR threads of a row; every thread gets it.  Wave butterflies,
 // then the wave sums in wave order.
-template <int TPR>
-__device__ __forceinline__ float row_sum(float v, float* s_red) {
+template <int TPR, typename S>
+__device__ __forceinline__ S row_sum(S v, S* s_red) {
 #pragma unroll
   for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o);
   if constexpr (TPR > 64) {
@@ -38,6 +38,17 @@ __device__ __forceinline__ float row_sum(float v, float* s_red) {
     for (int w = 1; w < TPR / 64; ++w) v += s_red[w];
   }
   return v;
+}
+
+// m^-1/2 rounded to fp32 (m > 0): the hardware's fp32 estimate and one Newton
+// step in binary64.  Every value of the row is scaled by it, so its last bit
+// counts; the threads' fp32 sums are joined in binary64 for the same reason.
+// m beyond fp32 gives 0, NaN stays NaN.
+__device__ __forceinline__ float rsqrt_f64(double m) {
+  const float e = __frsqrt_rn(static_cast<float>(m));
+  if (!(e > 0.f) || isinf(e)) return e;
+  const double y = e;
+  return static_cast<float>(y * (1.5 - 0.5 * m * y * y));
 }
 
 // MXFP8 of one thread's 8 values of a block of 32 held by 4 consecutive
@@ -61,10 +72,11 @@ __device__ __forceinline__ uint64_t mx_quad(const float* f, int& S) {
 template <typename T, int NV, int TPR, bool MX>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_fwd_kernel(
     const T* x, const T* res, const T* __restrict__ gamma, T* r, T* y, float* __restrict__ rstd,
-    uint8_t* __restrict__ codes, uint8_t* __restrict__ scales, int64_t Tn, int d, float eps) {
+    uint8_t* __restrict__ codes, uint8_t* __restrict__ scales, int64_t Tn, int d, double inv_d,
+    double eps) {
   constexpr int V = V16<T>::n;
   constexpr int RPB = (TPR < 256 ? 256 : TPR) / TPR;
-  __shared__ float s_red[TPR / 64];
+  __shared__ double s_red[TPR / 64];
   const int tid = threadIdx.x % TPR;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * RPB + threadIdx.x / TPR;
   if (row >= Tn) return;  // whole wavefronts only: with TPR > 64 a row is the workgroup's
@@ -102,8 +114,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_fwd_kernel(
 #pragma unroll
     for (int e = 0; e < V; ++e) ss += f[i][e] * f[i][e];
   }
-  ss = row_sum<TPR>(ss, s_red);
-  const float rs = 1.0f / sqrtf(ss / static_cast<float>(d) + eps);
+  const float rs = rsqrt_f64(row_sum<TPR>(static_cast<double>(ss), s_red) * inv_d + eps);
   if (rstd && tid == 0) rstd[row] = rs;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
@@ -182,7 +193,24 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_bwd_kernel(
       V16<T>::store(dr + base + j, a[i]);
     }
   }
-  float* p = part + (static_cast<int64_t>(blockIdx.x) * RPB + sub) * d;
+  if constexpr (RPB > 1) {
+    // the workgroup's wavefronts, added in order
+    __shared__ float s_acc[RPB - 1][NV * TPR * V];
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int e = 0; e < V; ++e)
+        if (sub > 0) s_acc[sub - 1][(i * V + e) * TPR + tid] = acc[i][e];
+    __syncthreads();
+    if (sub > 0) return;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int e = 0; e < V; ++e)
+#pragma unroll
+        for (int w = 0; w < RPB - 1; ++w) acc[i][e] += s_acc[w][(i * V + e) * TPR + tid];
+  }
+  float* p = part + static_cast<int64_t>(blockIdx.x) * d;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int j = (tid + i * TPR) * V;
@@ -194,26 +222,31 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_bwd_kernel(
   }
 }
 
-// dgamma[j] = the np partial rows' column j: 16 groups of consecutive rows,
-// each summed ascending, added in group order.
-constexpr int kRedGroups = 16;
+// dgamma[j] = the np partial rows' column j: 32 groups of consecutive rows,
+// each summed ascending, added in group order.  32 columns a workgroup: the
+// sum is bound by the latency of its loads, so 16 go out at once a thread.
+constexpr int kRedCols = 32, kRedGroups = 32;
 template <typename T>
-__global__ __launch_bounds__(64 * kRedGroups) void norm_dgamma_kernel(const float* __restrict__ part,
-                                                                      int np, int d,
-                                                                      T* __restrict__ dgamma) {
-  __shared__ float s_p[kRedGroups][64];
-  const int lane = threadIdx.x & 63, g = threadIdx.x >> 6;
-  const int j = blockIdx.x * 64 + lane;
+__global__ __launch_bounds__(kRedCols * kRedGroups) void norm_dgamma_kernel(
+    const float* __restrict__ part, int np, int d, T* __restrict__ dgamma) {
+  __shared__ float s_p[kRedGroups][kRedCols];
+  const int c = threadIdx.x % kRedCols, g = threadIdx.x / kRedCols;
+  const int j = blockIdx.x * kRedCols + c;
   const int per = (np + kRedGroups - 1) / kRedGroups;
-  const int hi = min(np, (g + 1) * per);
+  const int hi = j < d ? min(np, (g + 1) * per) : 0;
   float v = 0.f;
-  if (j < d)
-    for (int b = g * per; b < hi; ++b) v += part[static_cast<int64_t>(b) * d + j];
-  s_p[g][lane] = v;
+  for (int b0 = g * per; b0 < hi; b0 += 16) {
+    float w[16];
+#pragma unroll
+    for (int u = 0; u < 16; ++u) w[u] = b0 + u < hi ? part[static_cast<int64_t>(b0 + u) * d + j] : 0.f;
+#pragma unroll
+    for (int u = 0; u < 16; ++u) v += w[u];
+  }
+  s_p[g][c] = v;
   __syncthreads();
   if (g == 0 && j < d) {
 #pragma unroll
-    for (int k = 1; k < kRedGroups; ++k) v += s_p[k][lane];
+    for (int k = 1; k < kRedGroups; ++k) v += s_p[k][c];
     Elem<T>::st(dgamma + j, v);
   }
 }
@@ -262,20 +295,19 @@ hipError_t launch_norm_fwd(const T* x, const T* res, const T* gamma, T* r, T* y,
     if constexpr (std::is_same<T, bf16_t>::value) {
       if (codes) {
         hipLaunchKernelGGL((norm_fwd_kernel<T, NV, TPR, true>), grid, block, 0, s, x, res, gamma, r,
-                           y, rstd, codes, scales, Tn, d, eps);
+                           y, rstd, codes, scales, Tn, d, 1.0 / d, static_cast<double>(eps));
         return hipGetLastError();
       }
     }
     hipLaunchKernelGGL((norm_fwd_kernel<T, NV, TPR, false>), grid, block, 0, s, x, res, gamma, r, y,
-                       rstd, codes, scales, Tn, d, eps);
+                       rstd, codes, scales, Tn, d, 1.0 / d, static_cast<double>(eps));
     return hipGetLastError();
   });
 }
 
 template <typename T>
 int64_t norm_bwd_parts(int64_t Tn, int d) {
-  const int rpb = norm_rows_per_block<T>(d);
-  return norm_bwd_blocks(Tn, rpb) * rpb;
+  return norm_bwd_blocks(Tn, norm_rows_per_block<T>(d));
 }
 
 template <typename T>
@@ -294,8 +326,8 @@ hipError_t launch_norm_bwd(const T* dy, const T* r, const T* gamma, const float*
     });
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL(norm_dgamma_kernel<T>, dim3((d + 63) / 64), dim3(64 * kRedGroups), 0, s, part,
-                     np, d, dgamma);
+  hipLaunchKernelGGL(norm_dgamma_kernel<T>, dim3((d + kRedCols - 1) / kRedCols),
+                     dim3(kRedCols * kRedGroups), 0, s, part, np, d, dgamma);
   return hipGetLastError();
 }
 

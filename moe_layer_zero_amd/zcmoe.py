@@ -140,25 +140,50 @@ def _stream(stream):
     return C.c_void_p(stream.cuda_stream)
 
 
-def _run(where, tensors, stream, call, scratch=None):
-    """Runs call(stream handle) with the tensors' device current: they must all
-    live on one GPU, and a given stream must belong to it.  The default stream
-    is that device's current one.  scratch: a workspace the binding allocated
-    itself, kept from reuse until a given stream is done with it."""
-    devs = {t.device for t in tensors if t is not None}
-    if len(devs) != 1:
-        raise ValueError(f"{where}: tensors on different devices: {sorted(map(str, devs))}")
-    dev = devs.pop()
-    if dev.type != "cuda":
-        raise ValueError("tensors passed to the HIP library must live on the GPU")
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    elif stream.device != dev:
-        raise ValueError(f"{where}: stream of {stream.device}, tensors on {dev}")
-    with torch.cuda.device(dev):
-        _check(call(C.c_void_p(stream.cuda_stream)), where)
-    if scratch is not None:
-        scratch.record_stream(stream)
+class _Args:
+    """Device addresses of one call's tensors, checked: shape, dtype, contiguity,
+    and that all of them live on one GPU.  (Calls of a few microseconds go
+    through here, so it touches each tensor as little as it can.)"""
+    __slots__ = ("where", "dev")
+
+    def __init__(self, where):
+        self.where, self.dev = where, None
+
+    def __call__(self, t, shape, dtype, name):
+        if t is None:
+            return None
+        if t.shape != shape or t.dtype != dtype:
+            _check_layer_tensor(t, shape, dtype, name)
+        dev = t.get_device()
+        if dev != self.dev:
+            if dev < 0:
+                raise ValueError("tensors passed to the HIP library must live on the GPU")
+            if self.dev is not None:
+                raise ValueError(f"{self.where}: {name} is on GPU {dev}, other tensors on GPU {self.dev}")
+            self.dev = dev
+        if not t.is_contiguous():
+            raise ValueError("tensors passed to the HIP library must be contiguous")
+        return t.data_ptr()
+
+    def run(self, fn, *args, stream=None, scratch=None):
+        """fn(*args, stream) with the tensors' device current.  The default
+        stream is that device's current one; scratch is a workspace the
+        binding allocated itself, kept until a given stream is done with it."""
+        if stream is None:
+            handle = torch.cuda.current_stream(self.dev).cuda_stream
+        elif stream.device_index != self.dev:
+            raise ValueError(f"{self.where}: stream of GPU {stream.device_index}, tensors on GPU {self.dev}")
+        else:
+            handle = stream.cuda_stream
+        if torch.cuda.current_device() == self.dev:
+            st = fn(*args, handle)
+        else:
+            with torch.cuda.device(self.dev):
+                st = fn(*args, handle)
+        if st != ZC_OK:
+            _check(st, self.where)
+        if scratch is not None and stream is not None:
+            scratch.record_stream(stream)
 
 
 @dataclass
@@ -484,16 +509,11 @@ def zc_rmsnorm_forward(desc: NormDesc, x, gamma, y, res=None, r=None, rstd=None,
     codes and scales (mx_buffers) where given.  r and y may be x or res in
     place."""
     T, d, dt = desc.T, desc.d, desc.dtype
-    for t, n in ((x, "x"), (res, "res"), (r, "r"), (y, "y")):
-        _check_layer_tensor(t, (T, d), dt, n)
-    _check_layer_tensor(gamma, (d,), dt, "gamma")
-    _check_layer_tensor(rstd, (T,), torch.float32, "rstd")
-    _check_layer_tensor(codes, (T, d), torch.uint8, "codes")
-    _check_layer_tensor(scales, (T, d // 32), torch.uint8, "scales")
-    c = desc.c()
-    _run("zc_rmsnorm_forward", (x, res, gamma, r, y, rstd, codes, scales), stream,
-         lambda s: lib().zc_rmsnorm_forward(C.byref(c), _ptr(x), _ptr(res), _ptr(gamma), _ptr(r),
-                                            _ptr(y), _ptr(rstd), _ptr(codes), _ptr(scales), s))
+    a, sh, u8 = _Args("zc_rmsnorm_forward"), (desc.T, desc.d), torch.uint8
+    p = (a(x, sh, dt, "x"), a(res, sh, dt, "res"), a(gamma, (d,), dt, "gamma"), a(r, sh, dt, "r"),
+         a(y, sh, dt, "y"), a(rstd, (T,), torch.float32, "rstd"), a(codes, sh, u8, "codes"),
+         a(scales, (T, d // 32), u8, "scales"))
+    a.run(lib().zc_rmsnorm_forward, C.byref(desc.c()), *p, stream=stream)
 
 
 def zc_rmsnorm_backward(desc: NormDesc, dy, r, gamma, rstd, dr, dgamma, dres=None, ws=None,
@@ -501,16 +521,13 @@ def zc_rmsnorm_backward(desc: NormDesc, dy, r, gamma, rstd, dr, dgamma, dres=Non
     """Gradients of zc_rmsnorm_forward: dr (of x and res alike, with dres, the
     residual stream's own gradient, added) and dgamma."""
     T, d, dt = desc.T, desc.d, desc.dtype
-    for t, n in ((dy, "dy"), (r, "r"), (dres, "dres"), (dr, "dr")):
-        _check_layer_tensor(t, (T, d), dt, n)
-    for t, n in ((gamma, "gamma"), (dgamma, "dgamma")):
-        _check_layer_tensor(t, (d,), dt, n)
-    _check_layer_tensor(rstd, (T,), torch.float32, "rstd")
+    a, sh = _Args("zc_rmsnorm_backward"), (desc.T, desc.d)
+    p = (a(dy, sh, dt, "dy"), a(r, sh, dt, "r"), a(gamma, (d,), dt, "gamma"),
+         a(rstd, (T,), torch.float32, "rstd"), a(dres, sh, dt, "dres"), a(dr, sh, dt, "dr"),
+         a(dgamma, (d,), dt, "dgamma"))
     scratch = None
     if ws is None:
         ws = scratch = norm_workspace(desc, gamma.device)
-    c = desc.c()
-    _run("zc_rmsnorm_backward", (dy, r, gamma, rstd, dres, dr, dgamma, ws), stream,
-         lambda s: lib().zc_rmsnorm_backward(C.byref(c), _ptr(dy), _ptr(r), _ptr(gamma), _ptr(rstd),
-                                             _ptr(dres), _ptr(dr), _ptr(dgamma), _ptr(ws),
-                                             ws.numel(), s), scratch)
+    n = ws.numel() * ws.element_size()
+    a.run(lib().zc_rmsnorm_backward, C.byref(desc.c()), *p, a(ws, ws.shape, ws.dtype, "ws"), n,
+          stream=stream, scratch=scratch)

@@ -63,7 +63,7 @@ def test_norm_pointer_checks():
     assert fwd(L, zcmoe.NormDesc(4, 192, BF), codes=A[6], scales=A[7]) == zcmoe.ZC_ERR_UNSUPPORTED
     d = desc.c()
     need = L.zc_rmsnorm_workspace_size(C.byref(d))
-    assert need >= 4 * 256 * 4
+    assert need >= 256 * 4  # one row of partial sums at least
     assert bwd(L, desc, ws_bytes=need - 1) == zcmoe.ZC_ERR_WORKSPACE
     assert bwd(L, desc, ws=None) == zcmoe.ZC_ERR_WORKSPACE
 
