@@ -224,6 +224,16 @@ zc_status zc_moe_backward(const zc_moe_desc* desc, const void* x,
                           const zc_lb_cfg* lb, void* ws, size_t ws_bytes,
                           void* stream);
 
+/* zc_moe_backward with a further gradient of the router scores: dlogits
+ * (fp32 [T][E], nullable) is added to dl above, so that dw_router and dx
+ * carry the loss it belongs to (zc_moe_seq_balance writes one). */
+zc_status zc_moe_backward_scores(const zc_moe_desc* desc, const void* x, const void* w_router,
+                                 const void* w_gate, const void* w_up, const void* w_down,
+                                 const zc_route_buf* r, const void* saved, const void* dout,
+                                 void* dx, void* dw_router, void* dw_gate, void* dw_up,
+                                 void* dw_down, const zc_lb_cfg* lb, const float* dlogits,
+                                 void* ws, size_t ws_bytes, void* stream);
+
 /* Device-level load-balance loss, section 2.1.2 of the report:
  *   L = alpha * sum_{j=1}^{D+1} f_j P_j,
  *   P_j = (1/T) sum over i in group j and all tokens t of R_{t,i}  (Eq.(4)),
@@ -242,6 +252,33 @@ zc_status zc_moe_backward(const zc_moe_desc* desc, const void* x,
 zc_status zc_moe_lb_loss(const zc_moe_desc* desc, const zc_lb_cfg* lb,
                          const zc_route_buf* r, double* out, void* ws,
                          size_t ws_bytes, void* stream);
+
+/* The balance loss of section 2.1.2 taken sequence by sequence, for batches
+ * of packed or padded sequences, with its per-expert counts and the gradient
+ * of the router scores.  Sequence s holds the tokens cu_seqlens[s] ..
+ * cu_seqlens[s+1]-1 (device, int32 [S+1], starting at 0 and not descending;
+ * NULL: S = 1, all tokens) whose mask byte is not 0 (device, uint8 [T];
+ * NULL: all).  Tokens behind the last sequence belong to none.  With T_s the
+ * valid tokens of s, f and P as in zc_moe_lb_loss over them alone, and S'
+ * the number of sequences with T_s > 0:
+ *   L_s = alpha * sum_g f_{s,g} P_{s,g} (0 when T_s = 0);  L = sum_s L_s / S'
+ *   counts[s][j] = picks of expert j by the valid tokens of s;
+ *   dlogits[t][j] = dL/dl_{t,j} = p_j (k_j - sum_i p_i k_i),
+ *                   k_j = alpha f_{s,g(j)} / (S' T_s), f held fixed,
+ * and 0 for a masked token or one of no sequence, whatever its scores hold.
+ * lb->D = N balances expert by expert.  The softmax, k and dlogits are fp32;
+ * sums over tokens binary64.  loss: fp32 [1+S], L then L_s.  counts: int32
+ * [S][E].  dlogits: fp32 [T][E], or NULL (loss and counts only); every entry
+ * is overwritten.  Only logits and topk_idx of r are read; a pick outside
+ * 0..E-1 counts nowhere.  Offsets outside 0..T are clamped; with descending
+ * ones the results mean nothing, but no access leaves its buffer.  1 <= S <=
+ * 2^20.  No output may overlap an input or another output.
+ * ws: zc_moe_seq_balance_workspace_size(desc, S) bytes. */
+size_t zc_moe_seq_balance_workspace_size(const zc_moe_desc* desc, int64_t S);
+zc_status zc_moe_seq_balance(const zc_moe_desc* desc, const zc_lb_cfg* lb, const zc_route_buf* r,
+                             int64_t S, const int32_t* cu_seqlens, const uint8_t* mask,
+                             float* loss, int32_t* counts, float* dlogits, void* ws,
+                             size_t ws_bytes, void* stream);
 
 /* Eq.(2) bias update, in place on bias [N+Z] (fp32), for FFN experts i < N:
  *   b_i += mu * ( K_e/(K*N) - T_i/(K*T_all) ),  T_i = counts[i],
@@ -369,7 +406,8 @@ enum {
   ZC_PH_BWD_COMBINE, ZC_PH_BWD_DOWN_DH, ZC_PH_BWD_DOWN_DW, ZC_PH_BWD_GATE_UP_DX,
   ZC_PH_BWD_GATE_UP_DW, ZC_PH_BWD_ROUTER_DW, ZC_PH_BWD_ROUTER_DX, ZC_PH_BWD_DX_GATHER,
   ZC_PH_BIAS_UPDATE, ZC_PH_TILE_OFFSETS, ZC_PH_LB_LOSS, ZC_PH_LB_COEF, ZC_PH_ROUTE_STATS,
-  ZC_PH_ACCUMULATE, ZC_PH_QUANTIZE, ZC_PH_BWD_GATHER, ZC_PH_NORM, ZC_PH_NORM_BWD, ZC_NUM_PHASES
+  ZC_PH_ACCUMULATE, ZC_PH_QUANTIZE, ZC_PH_BWD_GATHER, ZC_PH_NORM, ZC_PH_NORM_BWD,
+  ZC_PH_SEQ_BALANCE, ZC_NUM_PHASES
 };
 zc_status zc_moe_profile(int on);
 zc_status zc_moe_profile_read(double* total_ms, int32_t* count);

@@ -581,8 +581,8 @@ zc_status do_forward(const zc_moe_desc* d, const T* x, const T* wr, const float*
 template <typename T>
 zc_status do_backward(const zc_moe_desc* d, const T* x, const T* wr, const T* wg, const T* wu,
                       const T* wd, const zc_route_buf* r, const void* saved, const T* dout, T* dx,
-                      T* dwr, T* dwg, T* dwu, T* dwd, const zc_lb_cfg* lb, char* ws,
-                      hipStream_t s) {
+                      T* dwr, T* dwg, T* dwu, T* dwd, const zc_lb_cfg* lb, const float* dlogits,
+                      char* ws, hipStream_t s) {
   const int Tn = static_cast<int>(d->T), N = static_cast<int>(d->N), K = static_cast<int>(d->K);
   const int E = static_cast<int>(d->N + d->Z), dd = static_cast<int>(d->d);
   const int I = static_cast<int>(d->I), ldl = static_cast<int>(ldl_of(E));
@@ -612,7 +612,7 @@ zc_status do_backward(const zc_moe_desc* d, const T* x, const T* wr, const T* wg
   ZC_LAUNCH(ZC_PH_BWD_COMBINE,
             zc::launch_combine_bwd<T>(x, y, dout, r->logits, r->topk_idx, r->topk_gate, r->inv, Tn,
                                       dd, N, E, K, d->gate_norm, d->out_scale,
-                                      lb ? w.lbc : nullptr, w.gs, w.dg, w.dl, ldl, s),
+                                      lb ? w.lbc : nullptr, dlogits, w.gs, w.dg, w.dl, ldl, s),
             "combine backward launch");
   if (N > 0) {
     if (Tn > 0 && bwdp) {
@@ -748,6 +748,13 @@ zc_status check_overlap(const Range* out, int nout, const Range* in, int nin) {
   return ZC_OK;
 }
 
+// Sequences of a packed batch.
+zc_status check_seqs(const zc_moe_desc* d, int64_t S) {
+  if (S < 1 || S > (int64_t(1) << 20))
+    return fail(ZC_ERR_INVALID, "S=%lld sequences outside 1..2^20", (long long)S);
+  return ZC_OK;
+}
+
 zc_status check_norm(const zc_norm_desc* d) {
   if (!d) return fail(ZC_ERR_INVALID, "desc is NULL");
   if (d->T < 0 || d->d < 1)
@@ -874,6 +881,17 @@ zc_status zc_moe_backward(const zc_moe_desc* desc, const void* x, const void* w_
                           const zc_route_buf* r, const void* saved, const void* dout, void* dx,
                           void* dw_router, void* dw_gate, void* dw_up, void* dw_down,
                           const zc_lb_cfg* lb, void* ws, size_t ws_bytes, void* stream) {
+  return zc_moe_backward_scores(desc, x, w_router, w_gate, w_up, w_down, r, saved, dout, dx,
+                                dw_router, dw_gate, dw_up, dw_down, lb, nullptr, ws, ws_bytes,
+                                stream);
+}
+
+zc_status zc_moe_backward_scores(const zc_moe_desc* desc, const void* x, const void* w_router,
+                                 const void* w_gate, const void* w_up, const void* w_down,
+                                 const zc_route_buf* r, const void* saved, const void* dout,
+                                 void* dx, void* dw_router, void* dw_gate, void* dw_up,
+                                 void* dw_down, const zc_lb_cfg* lb, const float* dlogits,
+                                 void* ws, size_t ws_bytes, void* stream) {
   ZC_CHECK(check_desc(desc));
   if (desc->weight_layout != ZC_WEIGHTS_ROWMAJOR)
     return fail(ZC_ERR_UNSUPPORTED, "the backward needs row-major weights");
@@ -888,6 +906,7 @@ zc_status zc_moe_backward(const zc_moe_desc* desc, const void* x, const void* w_
   ZC_CHECK(check_ptr(dw_router, "dw_router"));
   ZC_CHECK(check_weights(desc, dw_gate, dw_up, dw_down));
   if (lb) ZC_CHECK(check_lb(desc, lb));
+  ZC_CHECK(check_ptr(dlogits, "dlogits", true));
   ZC_CHECK(check_ws(ws, ws_bytes, bwd_ws_bytes(desc)));
   hipStream_t s = static_cast<hipStream_t>(stream);
   char* w = static_cast<char*>(ws);
@@ -897,13 +916,13 @@ zc_status zc_moe_backward(const zc_moe_desc* desc, const void* x, const void* w_
         static_cast<const bf16_t*>(w_gate), static_cast<const bf16_t*>(w_up),
         static_cast<const bf16_t*>(w_down), r, saved, static_cast<const bf16_t*>(dout),
         static_cast<bf16_t*>(dx), static_cast<bf16_t*>(dw_router), static_cast<bf16_t*>(dw_gate),
-        static_cast<bf16_t*>(dw_up), static_cast<bf16_t*>(dw_down), lb, w, s);
+        static_cast<bf16_t*>(dw_up), static_cast<bf16_t*>(dw_down), lb, dlogits, w, s);
   return do_backward<float>(desc, static_cast<const float*>(x), static_cast<const float*>(w_router),
                             static_cast<const float*>(w_gate), static_cast<const float*>(w_up),
                             static_cast<const float*>(w_down), r, saved,
                             static_cast<const float*>(dout), static_cast<float*>(dx),
                             static_cast<float*>(dw_router), static_cast<float*>(dw_gate),
-                            static_cast<float*>(dw_up), static_cast<float*>(dw_down), lb, w, s);
+                            static_cast<float*>(dw_up), static_cast<float*>(dw_down), lb, dlogits, w, s);
 }
 
 zc_status zc_moe_lb_loss(const zc_moe_desc* desc, const zc_lb_cfg* lb, const zc_route_buf* r,
@@ -922,6 +941,49 @@ zc_status zc_moe_lb_loss(const zc_moe_desc* desc, const zc_lb_cfg* lb, const zc_
                                static_cast<int>(desc->N), E, static_cast<int>(desc->K),
                                static_cast<int>(lb->D), lb->K_e, lb->alpha, out, ws, s),
             "load-balance loss launch");
+  return ZC_OK;
+}
+
+size_t zc_moe_seq_balance_workspace_size(const zc_moe_desc* desc, int64_t S) {
+  if (check_desc(desc) != ZC_OK || check_seqs(desc, S) != ZC_OK) return 0;
+  return zc::seq_balance_scratch_bytes(desc->T, desc->N + desc->Z, S);
+}
+
+zc_status zc_moe_seq_balance(const zc_moe_desc* desc, const zc_lb_cfg* lb, const zc_route_buf* r,
+                             int64_t S, const int32_t* cu_seqlens, const uint8_t* mask,
+                             float* loss, int32_t* counts, float* dlogits, void* ws,
+                             size_t ws_bytes, void* stream) {
+  ZC_CHECK(check_desc(desc));
+  ZC_CHECK(check_lb(desc, lb));
+  ZC_CHECK(check_seqs(desc, S));
+  const bool none = desc->T == 0;
+  if (!r) return fail(ZC_ERR_INVALID, "route buffer is NULL");
+  ZC_CHECK(check_ptr(r->logits, "r->logits", none));
+  ZC_CHECK(check_ptr(r->topk_idx, "r->topk_idx", none));
+  if (!cu_seqlens && S != 1)
+    return fail(ZC_ERR_INVALID, "S=%lld sequences need cu_seqlens", (long long)S);
+  ZC_CHECK(check_ptr(cu_seqlens, "cu_seqlens", true));
+  ZC_CHECK(check_ptr(mask, "mask", true));
+  ZC_CHECK(check_ptr(loss, "loss"));
+  ZC_CHECK(check_ptr(counts, "counts"));
+  ZC_CHECK(check_ptr(dlogits, "dlogits", true));
+  const int64_t E = desc->N + desc->Z, T = desc->T;
+  const int64_t need = static_cast<int64_t>(zc::seq_balance_scratch_bytes(T, E, S));
+  ZC_CHECK(check_ws(ws, ws_bytes, need));
+  const Range in[] = {{r->logits, 4 * T * E, "r->logits", false},
+                      {r->topk_idx, 4 * T * desc->K, "r->topk_idx", false},
+                      {cu_seqlens, 4 * (S + 1), "cu_seqlens", false}, {mask, T, "mask", false}};
+  const Range out[] = {{loss, 4 * (S + 1), "loss", false}, {counts, 4 * S * E, "counts", false},
+                       {dlogits, 4 * T * E, "dlogits", false}, {ws, need, "ws", false}};
+  ZC_CHECK(check_overlap(out, 4, in, 4));
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  ZC_LAUNCH(ZC_PH_SEQ_BALANCE,
+            zc::launch_seq_balance(r->logits, r->topk_idx, static_cast<int>(T),
+                                   static_cast<int>(desc->N), static_cast<int>(E),
+                                   static_cast<int>(desc->K), static_cast<int>(lb->D), lb->K_e,
+                                   lb->alpha, static_cast<int>(S), cu_seqlens, mask, loss, counts,
+                                   dlogits, ws, s),
+            "balance loss launch");
   return ZC_OK;
 }
 
@@ -1147,7 +1209,7 @@ const char* zc_moe_phase_name(int phase) {
       "bwd_combine", "bwd_down_dh", "bwd_down_dw", "bwd_gate_up_dx", "bwd_gate_up_dw",
       "bwd_router_dw", "bwd_router_dx", "bwd_dx_gather", "bias_update", "tile_offsets",
       "lb_loss", "lb_coef", "route_stats", "accumulate_counts", "quantize", "bwd_gather",
-      "norm", "norm_bwd"};
+      "norm", "norm_bwd", "seq_balance"};
   return (phase >= 0 && phase < ZC_NUM_PHASES) ? names[phase] : "";
 }
 

@@ -116,13 +116,15 @@ __device__ __forceinline__ float block_sum(float v, float* s_red) {
 //        Jacobian restricted to the picks (renormalised gates) or over all
 //        experts (Eq.(1) gates), written as one fp32 row of width ldl;
 //        with lbc, plus the device-level load-balance loss's gradient
-//        p_j (lbc_j - sum_k p_k lbc_k) (section 2.1.2, f held fixed).
+//        p_j (lbc_j - sum_k p_k lbc_k) (section 2.1.2, f held fixed);
+//        with dle, plus the caller's own gradient of the scores (row of E).
 template <typename T>
 __global__ __launch_bounds__(kThreads) void combine_bwd_kernel(
     const T* __restrict__ x, const T* __restrict__ y, const T* __restrict__ dout,
     const float* __restrict__ logits, const int32_t* __restrict__ topk_idx,
     const float* __restrict__ gate, const int32_t* __restrict__ inv, int d, int N, int E, int K,
-    int gate_norm, float out_scale, const float* __restrict__ lbc, float* __restrict__ gs,
+    int gate_norm, float out_scale, const float* __restrict__ lbc,
+    const float* __restrict__ dle, float* __restrict__ gs,
     float* __restrict__ dg_out, float* __restrict__ dl, int ldl) {
   __shared__ float s_g[kMaxK];
   __shared__ int32_t s_inv[kMaxK];
@@ -172,9 +174,13 @@ __global__ __launch_bounds__(kThreads) void combine_bwd_kernel(
   for (int r = 0; r < K; ++r) sgd += s_g[r] * s_dg[r];
   float* dlr = dl + t * ldl;
   if (gate_norm && !lbc) {
-    for (int j = threadIdx.x; j < ldl; j += kThreads) dlr[j] = 0.f;
+    for (int j = threadIdx.x; j < ldl; j += kThreads) dlr[j] = dle && j < E ? dle[t * E + j] : 0.f;
     __syncthreads();
-    if (threadIdx.x < K) dlr[s_e[threadIdx.x]] = s_g[threadIdx.x] * (s_dg[threadIdx.x] - sgd);
+    if (threadIdx.x < K) {
+      const float v = s_g[threadIdx.x] * (s_dg[threadIdx.x] - sgd);
+      const int j = s_e[threadIdx.x];
+      dlr[j] = dle ? dle[t * E + j] + v : v;
+    }
     return;
   }
   // the full softmax p of the token's scores
@@ -208,6 +214,7 @@ __global__ __launch_bounds__(kThreads) void combine_bwd_kernel(
       else
         v = pj * ((r >= 0 ? s_dg[r] : 0.f) - sgd);
       if (lbc) v += pj * (lbc[j] - sc);
+      if (dle) v += dle[t * E + j];
     }
     dlr[j] = v;
   }
@@ -283,12 +290,12 @@ template <typename T>
 hipError_t launch_combine_bwd(const T* x, const T* y, const T* dout, const float* logits,
                               const int32_t* topk_idx, const float* gate, const int32_t* inv,
                               int Tn, int d, int N, int E, int K, int gate_norm, float out_scale,
-                              const float* lb_coef, float* gs, float* dg, float* dl, int ldl,
-                              hipStream_t s) {
+                              const float* lb_coef, const float* dlogits, float* gs, float* dg,
+                              float* dl, int ldl, hipStream_t s) {
   if (Tn == 0) return hipSuccess;
   hipLaunchKernelGGL(combine_bwd_kernel<T>, dim3(Tn), dim3(kThreads), 0, s, x, y, dout, logits,
-                     topk_idx, gate, inv, d, N, E, K, gate_norm, out_scale, lb_coef, gs, dg, dl,
-                     ldl);
+                     topk_idx, gate, inv, d, N, E, K, gate_norm, out_scale, lb_coef, dlogits, gs,
+                     dg, dl, ldl);
   return hipGetLastError();
 }
 
@@ -309,7 +316,8 @@ hipError_t launch_dx_gather(const T* dout, const float* dxp, const float* dxr, c
   template hipError_t launch_combine_bwd<T>(const T*, const T*, const T*, const float*,         \
                                             const int32_t*, const float*, const int32_t*, int,  \
                                             int, int, int, int, int, float, const float*,       \
-                                            float*, float*, float*, int, hipStream_t);          \
+                                            const float*, float*, float*, float*, int,          \
+                                            hipStream_t);                                       \
   template hipError_t launch_dx_gather<T>(const T*, const float*, const float*, const int32_t*, \
                                           const float*, const int32_t*, int, int, int, int,     \
                                           float, T*, hipStream_t);

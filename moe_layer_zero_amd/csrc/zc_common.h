@@ -328,19 +328,29 @@ hipError_t launch_combine(const T* x, const T* y, const int32_t* topk_idx, const
 // Combine backward: dg per slot, out_scale * gate of every FFN pick in
 // dispatch order (gs), and the router-score gradient dl [T][ldl] (fp32);
 // with lb_coef (from launch_lb_coef, else NULL) dl also takes the
-// load-balance loss's score gradient.
+// load-balance loss's score gradient; with dlogits ([T][E], else NULL) dl
+// takes that gradient of the scores too.
 template <typename T>
 hipError_t launch_combine_bwd(const T* x, const T* y, const T* dout, const float* logits,
                               const int32_t* topk_idx, const float* gate, const int32_t* inv,
                               int Tn, int d, int N, int E, int K, int gate_norm, float out_scale,
-                              const float* lb_coef, float* gs, float* dg, float* dl, int ldl,
-                              hipStream_t s);
+                              const float* lb_coef, const float* dlogits, float* gs, float* dg,
+                              float* dl, int ldl, hipStream_t s);
 
 // dx gather: dx = out_scale * c_t * dout_t + sum_r dxp[inv] + dxr_t.
 template <typename T>
 hipError_t launch_dx_gather(const T* dout, const float* dxp, const float* dxr, const int32_t* topk_idx,
                             const float* gate, const int32_t* inv, int Tn, int d, int N, int K,
                             float out_scale, T* dx, hipStream_t s);
+
+// Balance loss of packed sequences (balance.hip): loss [1+S], counts [S][E]
+// and the score gradient dlogits [T][E] (may be NULL).  cu [S+1] and mask [T]
+// may be NULL.  Scratch: seq_balance_scratch_bytes(T, E, S).
+size_t seq_balance_scratch_bytes(int64_t Tn, int64_t E, int64_t S);
+hipError_t launch_seq_balance(const float* logits, const int32_t* topk_idx, int Tn, int N, int E,
+                              int K, int D, double K_e, double alpha, int S, const int32_t* cu,
+                              const uint8_t* mask, float* loss, int32_t* counts, float* dlogits,
+                              void* scratch, hipStream_t s);
 
 // RMS norm with the residual's addition (norm.hip).  res, r, rstd, codes may
 // be NULL; codes (bf16 only, d % 128 == 0) come with scales, in the order of

@@ -28,11 +28,12 @@ EXPORTS = ("zc_moe_workspace_size", "zc_moe_saved_size", "zc_moe_route", "zc_moe
            "zc_moe_forward_noalloc", "zc_moe_backward", "zc_moe_lb_loss", "zc_moe_route_stats", "zc_moe_accumulate_counts",
            "zc_moe_pid_update", "zc_moe_pack_weights", "zc_moe_quantized_weight_bytes",
            "zc_moe_quantize_weights",
+           "zc_moe_backward_scores", "zc_moe_seq_balance_workspace_size", "zc_moe_seq_balance",
            "zc_rmsnorm_forward", "zc_rmsnorm_workspace_size", "zc_rmsnorm_backward",
            "zc_moe_profile",
            "zc_moe_profile_read",
            "zc_moe_phase_name", "zc_status_string", "zc_last_error")
-ZC_NUM_PHASES = 24
+ZC_NUM_PHASES = 25
 
 
 class ZcError(RuntimeError):
@@ -92,12 +93,17 @@ def lib() -> C.CDLL:
         L.zc_moe_quantized_weight_bytes.argtypes = [P]
         L.zc_moe_quantized_weight_bytes.restype = sz
         L.zc_moe_quantize_weights.argtypes = [P, C.c_int, v, v, v]
+        L.zc_moe_backward_scores.argtypes = [P, v, v, v, v, v, D, v, v, v, v, v, v, v, LB, v, v, sz,
+                                             v]
+        L.zc_moe_seq_balance_workspace_size.argtypes = [P, i64]
+        L.zc_moe_seq_balance_workspace_size.restype = sz
+        L.zc_moe_seq_balance.argtypes = [P, LB, D, i64, v, v, v, v, v, v, sz, v]
         NP = C.POINTER(zc_norm_desc)
         L.zc_rmsnorm_forward.argtypes = [NP, v, v, v, v, v, v, v, v, v]
         L.zc_rmsnorm_workspace_size.argtypes = [NP]
         L.zc_rmsnorm_workspace_size.restype = sz
         L.zc_rmsnorm_backward.argtypes = [NP, v, v, v, v, v, v, v, v, sz, v]
-        for f in ("zc_rmsnorm_forward", "zc_rmsnorm_backward",
+        for f in ("zc_moe_backward_scores", "zc_moe_seq_balance", "zc_rmsnorm_forward", "zc_rmsnorm_backward",
                   "zc_moe_route", "zc_moe_forward", "zc_moe_forward_noalloc",
                   "zc_moe_backward", "zc_moe_lb_loss",
                   "zc_moe_route_stats", "zc_moe_accumulate_counts", "zc_moe_pid_update",
@@ -347,7 +353,10 @@ class LoadBalance:
 
 def zc_moe_backward(desc: LayerDesc, x, w_router, w_gate, w_up, w_down, route: RouteBuffers,
                     saved, dout, dx, dw_router, dw_gate, dw_up, dw_down, ws=None, stream=None,
-                    lb: "LoadBalance | None" = None):
+                    lb: "LoadBalance | None" = None, dlogits=None):
+    """All gradients of the layer.  lb adds the device-level load-balance
+    loss; dlogits (fp32 [T][E], from zc_moe_seq_balance or the caller's own
+    loss) is added to the gradient of the router scores."""
     for t, n in ((x, "x"), (dout, "dout"), (dx, "dx")):
         _check_layer_tensor(t, (desc.T, desc.d), desc.dtype, n)
     _check_weights(desc, w_router, w_gate, w_up, w_down)
@@ -356,10 +365,15 @@ def zc_moe_backward(desc: LayerDesc, x, w_router, w_gate, w_up, w_down, route: R
         ws = workspace(desc, ZC_OP_BACKWARD, x.device)
     d, r = desc.c(), route.c()
     lbc = None if lb is None else C.byref(lb.c())
-    _check(lib().zc_moe_backward(C.byref(d), _ptr(x), _ptr(w_router), _ptr(w_gate), _ptr(w_up),
-                                 _ptr(w_down), C.byref(r), _ptr(saved), _ptr(dout), _ptr(dx),
-                                 _ptr(dw_router), _ptr(dw_gate), _ptr(dw_up), _ptr(dw_down),
-                                 lbc, _ptr(ws), ws.numel(), _stream(stream)), "zc_moe_backward")
+    a = (C.byref(d), _ptr(x), _ptr(w_router), _ptr(w_gate), _ptr(w_up), _ptr(w_down), C.byref(r),
+         _ptr(saved), _ptr(dout), _ptr(dx), _ptr(dw_router), _ptr(dw_gate), _ptr(dw_up),
+         _ptr(dw_down), lbc)
+    if dlogits is None:
+        _check(lib().zc_moe_backward(*a, _ptr(ws), ws.numel(), _stream(stream)), "zc_moe_backward")
+    else:
+        _check_layer_tensor(dlogits, (desc.T, desc.E), torch.float32, "dlogits")
+        _check(lib().zc_moe_backward_scores(*a, _ptr(dlogits), _ptr(ws), ws.numel(),
+                                            _stream(stream)), "zc_moe_backward_scores")
 
 
 def zc_moe_lb_loss(desc: LayerDesc, lb: LoadBalance, route: RouteBuffers, out=None, ws=None,
@@ -375,6 +389,37 @@ def zc_moe_lb_loss(desc: LayerDesc, lb: LoadBalance, route: RouteBuffers, out=No
     _check(lib().zc_moe_lb_loss(C.byref(d), C.byref(c), C.byref(r), _ptr(out), _ptr(ws),
                                 ws.numel(), _stream(stream)), "zc_moe_lb_loss")
     return out
+
+
+def seq_balance_workspace(desc: LayerDesc, S: int, device="cuda") -> torch.Tensor:
+    d = desc.c()
+    n = int(lib().zc_moe_seq_balance_workspace_size(C.byref(d), S))
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=device)
+
+
+def zc_moe_seq_balance(desc: LayerDesc, lb: LoadBalance, route: RouteBuffers, loss, counts,
+                       dlogits=None, cu_seqlens=None, mask=None, ws=None, stream=None):
+    """Balance loss of the packed sequences of a routed batch: loss fp32 [1+S]
+    (L, then each sequence's), counts int32 [S][E] and, where given, the
+    gradient of the router scores dlogits fp32 [T][E].  cu_seqlens int32
+    [S+1]; mask uint8 or bool [T], nonzero for valid tokens."""
+    S = 1 if cu_seqlens is None else cu_seqlens.numel() - 1
+    T, E, i32, f32 = desc.T, desc.E, torch.int32, torch.float32
+    a = _Args("zc_moe_seq_balance")
+    lg = a(route.logits, (T, E), f32, "route.logits")
+    ti = a(route.topk_idx, (T, desc.K), i32, "route.topk_idx")
+    p = (a(cu_seqlens, (S + 1,), i32, "cu_seqlens"),
+         a(mask, (T,), torch.bool if mask is not None and mask.dtype == torch.bool else torch.uint8,
+           "mask"),
+         a(loss, (1 + S,), f32, "loss"), a(counts, (S, E), i32, "counts"),
+         a(dlogits, (T, E), f32, "dlogits"))
+    scratch = None
+    if ws is None:
+        ws = scratch = seq_balance_workspace(desc, S, loss.device)
+    n = ws.numel() * ws.element_size()
+    r = zc_route_buf(logits=lg, topk_idx=ti)
+    a.run(lib().zc_moe_seq_balance, C.byref(desc.c()), C.byref(lb.c()), C.byref(r), S, *p,
+          a(ws, ws.shape, ws.dtype, "ws"), n, stream=stream, scratch=scratch)
 
 
 def zc_moe_route_stats(desc: LayerDesc, route: RouteBuffers, hist=None, moments=None, ws=None,
