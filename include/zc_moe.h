@@ -95,8 +95,14 @@ typedef struct {
  *      blockwise-quantized expert weights (see there).  Accepted by
  *      zc_moe_forward for bf16 layers with d and I multiples of 512 and no
  *      saved buffer: the FP8 inference forward. */
+/*  ZC_WEIGHTS_INT4_G32, _G64, _G128: the output of zc_moe_int4_pack: 4-bit
+ *      expert weights with a scale for each group of 32, 64 or 128 (see
+ *      there).  Accepted by zc_moe_forward, zc_moe_forward_noalloc and
+ *      zc_moe_experts for bf16 layers with d and I multiples of 128 and no
+ *      saved buffer. */
 typedef enum {
-  ZC_WEIGHTS_ROWMAJOR = 0, ZC_WEIGHTS_PACKED = 1, ZC_WEIGHTS_MXFP8 = 2
+  ZC_WEIGHTS_ROWMAJOR = 0, ZC_WEIGHTS_PACKED = 1, ZC_WEIGHTS_MXFP8 = 2,
+  ZC_WEIGHTS_INT4_G32 = 4, ZC_WEIGHTS_INT4_G64 = 5, ZC_WEIGHTS_INT4_G128 = 6
 } zc_weight_layout;
 
 /* Routing state: written by zc_moe_route / zc_moe_forward, read by
@@ -115,7 +121,7 @@ typedef struct {
 
 enum {
   ZC_OP_ROUTE = 0, ZC_OP_FORWARD = 1, ZC_OP_BACKWARD = 2, ZC_OP_LB_LOSS = 3,
-  ZC_OP_ROUTE_STATS = 4
+  ZC_OP_ROUTE_STATS = 4, ZC_OP_EXPERTS = 5
 };
 
 /* Device-level load-balance loss settings ("LongCat-Flash Technical
@@ -176,6 +182,20 @@ zc_status zc_moe_forward(const zc_moe_desc* desc, const void* x,
                          const void* w_gate, const void* w_up,
                          const void* w_down, void* out, zc_route_buf* r,
                          void* saved, void* ws, size_t ws_bytes, void* stream);
+
+/* The experts and the combine of zc_moe_forward on routing that is there
+ * already: r as zc_moe_route wrote it for a layer of the same T, N, Z and K
+ * (topk_idx, topk_gate, offsets, perm and inv are read, and trusted to be
+ * consistent).  Inference: nothing is saved; any weight layout.  With MXFP8
+ * weights, x_codes and x_scales (both or neither; NULL otherwise) are x as
+ * zc_rmsnorm_forward quantized it, and the call's own quantization of x is
+ * left out; the zero-computation experts return x itself.  Neither out nor ws
+ * (ZC_OP_EXPERTS bytes) may overlap an input or the other.  out is bit for bit
+ * what zc_moe_forward gives on the same routing. */
+zc_status zc_moe_experts(const zc_moe_desc* desc, const void* x, const zc_route_buf* r,
+                         const void* w_gate, const void* w_up, const void* w_down,
+                         const uint8_t* x_codes, const uint8_t* x_scales, void* out, void* ws,
+                         size_t ws_bytes, void* stream);
 
 /* The inference forward of zc_moe_forward (saved = NULL) without a
  * workspace argument, for callers that cannot allocate device memory:
@@ -354,6 +374,30 @@ zc_status zc_moe_pack_weights(const zc_moe_desc* desc, int which, const void* sr
 size_t zc_moe_quantized_weight_bytes(const zc_moe_desc* desc);
 zc_status zc_moe_quantize_weights(const zc_moe_desc* desc, int which,
                                   const void* src, void* dst, void* stream);
+
+/* 4-bit expert weights with group scales, for inference bound by the weights'
+ * bytes (decode).  desc->weight_layout (ZC_WEIGHTS_INT4_G32, _G64 or _G128)
+ * gives the group size G; which and the matrix sizes [N][R][C] are those of
+ * zc_moe_pack_weights; dtype bf16, d and I multiples of 128.  A weight is
+ *   W[r][c] = s[r][c/G] * (q[r][c] - 8),  q in 0..15.
+ * Natural layout: codes [N][R][C/2], two a byte, the even c in the low half;
+ * scales [N][R][C/G] bf16, of any value and sign.  Codes made elsewhere in
+ * this form can be packed as they are.
+ *  zc_moe_int4_quantize: src (bf16) -> natural codes and scales:
+ *      s = max|w| / 7 over the group, rounded to bf16;
+ *      q = 8 + w / s, nearest with ties to even, w / s clamped to -8..7; a
+ *      group of zeros has s = 0 and q = 8, one that holds a NaN or an infinity
+ *      the scale NaN.
+ *  zc_moe_int4_pack: natural -> dst, zc_moe_int4_weight_bytes(desc) bytes, in
+ *      an order private to this library: what the forward takes.
+ * The products keep x and h in bf16 and every sum, and the experts' outputs
+ * y, in fp32; an infinity in a row of x gives NaN.  Their grids are not
+ * persistent: cu_limit does not size them.  No output may overlap an input. */
+size_t zc_moe_int4_weight_bytes(const zc_moe_desc* desc);
+zc_status zc_moe_int4_quantize(const zc_moe_desc* desc, int which, const void* src, uint8_t* codes,
+                               void* scales, void* stream);
+zc_status zc_moe_int4_pack(const zc_moe_desc* desc, int which, const uint8_t* codes,
+                           const void* scales, void* dst, void* stream);
 
 /* Root-mean-square norm with the residual's addition: the step in front of
  * the layer.  Row by row (T rows of d values, dtype a zc_dtype):

@@ -158,6 +158,24 @@ zc_status check_mxfp8(const zc_moe_desc* d) {
   return ZC_OK;
 }
 
+// Group size of a 4-bit weight layout, 0 for the other layouts.
+int int4_group(const zc_moe_desc* d) {
+  switch (d->weight_layout) {
+    case ZC_WEIGHTS_INT4_G32: return 32;
+    case ZC_WEIGHTS_INT4_G64: return 64;
+    case ZC_WEIGHTS_INT4_G128: return 128;
+    default: return 0;
+  }
+}
+
+zc_status check_int4(const zc_moe_desc* d) {
+  if (d->dtype != ZC_BF16) return fail(ZC_ERR_UNSUPPORTED, "4-bit weights need a bf16 layer");
+  if (d->d % 128 || d->I % 128)
+    return fail(ZC_ERR_UNSUPPORTED, "4-bit weights need d and I multiples of 128 (d=%lld I=%lld)",
+                (long long)d->d, (long long)d->I);
+  return ZC_OK;
+}
+
 zc_status check_desc(const zc_moe_desc* d) {
   if (!d) return fail(ZC_ERR_INVALID, "desc is NULL");
   const int64_t E = d->N + d->Z;
@@ -173,8 +191,8 @@ zc_status check_desc(const zc_moe_desc* d) {
     return fail(ZC_ERR_INVALID, "gate_norm %d is neither 0 nor 1", d->gate_norm);
   if (!std::isfinite(d->out_scale)) return fail(ZC_ERR_INVALID, "out_scale is not finite");
   if (d->weight_layout != ZC_WEIGHTS_ROWMAJOR && d->weight_layout != ZC_WEIGHTS_PACKED &&
-      d->weight_layout != ZC_WEIGHTS_MXFP8)
-    return fail(ZC_ERR_INVALID, "weight_layout %d is not ROWMAJOR, PACKED or MXFP8",
+      d->weight_layout != ZC_WEIGHTS_MXFP8 && !int4_group(d))
+    return fail(ZC_ERR_INVALID, "weight_layout %d is not ROWMAJOR, PACKED, MXFP8 or INT4",
                 d->weight_layout);
   if (d->cu_limit < 0 || d->cu_limit % 8)
     return fail(ZC_ERR_INVALID, "cu_limit %d is neither 0 nor a positive multiple of 8",
@@ -188,6 +206,7 @@ zc_status check_desc(const zc_moe_desc* d) {
                 (long long)d->I);
   if (d->weight_layout == ZC_WEIGHTS_PACKED) ZC_CHECK(check_packable(d));
   if (d->weight_layout == ZC_WEIGHTS_MXFP8) ZC_CHECK(check_mxfp8(d));
+  if (int4_group(d)) ZC_CHECK(check_int4(d));
   return ZC_OK;
 }
 
@@ -223,8 +242,10 @@ struct RouteWs {
   void* dispatch;
 };
 // Row tiles of the second prefix, at most: every FFN pick in a tile of its
-// own expert, tiles at least 32 rows high.
-int64_t max_tiles2(const zc_moe_desc* d) { return d->T * d->K / 32 + d->N + 1; }
+// own expert, tiles at least 32 rows high (16 with 4-bit weights).
+int64_t max_tiles2(const zc_moe_desc* d) {
+  return d->T * d->K / (int4_group(d) ? 16 : 32) + d->N + 1;
+}
 int64_t rpart_bytes(const zc_moe_desc* d) {
   const int64_t E = d->N + d->Z;
   const int s = zc::router_gemm_splits(d->T, E, d->d);
@@ -275,7 +296,9 @@ Saved carve_saved(char* p, const zc_moe_desc* d) {
 // fits in the h piece.
 int64_t fwd_ws_bytes(const zc_moe_desc* d) {
   const int64_t rows = d->T * d->K, es = esize(d);
-  int64_t b = route_ws_bytes(d) + a256(rows * d->I * es) + a256(rows * d->d * es);
+  // y is fp32 with 4-bit weights
+  const int64_t ys = int4_group(d) ? 4 : es;
+  int64_t b = route_ws_bytes(d) + a256(rows * d->I * es) + a256(rows * d->d * ys);
   if (d->weight_layout == ZC_WEIGHTS_MXFP8) b += a256(d->T * d->d) + a256(d->T * d->d / 32);
   return b;
 }
@@ -436,6 +459,7 @@ bool use_dense_router(const zc_moe_desc* d) {
 // bf16 forward kernels use 256.
 int fwd_rows_per_tile(const zc_moe_desc* d) {
   if (d->N == 0) return zc::kFwdBM;
+  if (int4_group(d)) return zc::int4_rows_per_tile(d->T * d->K / d->N);
   const int tm = zc::fwdp_rows_per_tile(d->T * d->K / d->N);
   if (d->weight_layout != ZC_WEIGHTS_ROWMAJOR) return tm;
   return rmw_layer(d) ? (tm < 64 ? 64 : tm) : zc::kFwdBM;
@@ -470,12 +494,12 @@ zc_status do_route(const zc_moe_desc* d, const T* x, const T* wr, const float* b
   return ZC_OK;
 }
 
+// The experts and the combine of a routed batch whose tile tables are in ws
+// (rw).  mxq, mxs: x as MXFP8 rows, NULL to quantize it here (MXFP8 layers).
 template <typename T>
-zc_status do_forward(const zc_moe_desc* d, const T* x, const T* wr, const float* bias,
-                     const T* wg, const T* wu, const T* wd, T* out, zc_route_buf* r, void* saved,
-                     char* ws, hipStream_t s) {
-  RouteWs rw = carve_route(ws, d);
-  ZC_CHECK(do_route<T>(d, x, wr, bias, r, rw, s));
+zc_status do_experts(const zc_moe_desc* d, const T* x, const T* wg, const T* wu, const T* wd,
+                     T* out, const zc_route_buf* r, void* saved, const uint8_t* mxq,
+                     const uint8_t* mxs, const RouteWs& rw, char* ws, hipStream_t s) {
   const int Tn = static_cast<int>(d->T), N = static_cast<int>(d->N), K = static_cast<int>(d->K);
   const int dd = static_cast<int>(d->d), I = static_cast<int>(d->I);
   const int64_t rows = d->T * d->K;
@@ -500,11 +524,12 @@ zc_status do_forward(const zc_moe_desc* d, const T* x, const T* wr, const float*
       uint8_t* xs = xq + a256(d->T * d->d);
       uint8_t* hq = reinterpret_cast<uint8_t*>(h);
       uint8_t* hs = hq + a256(rows * d->I);
-      ZC_LAUNCH(ZC_PH_QUANTIZE,
-                zc::launch_mxq_rows(reinterpret_cast<const bf16_t*>(x), d->T, dd, xq, xs, s),
-                "activation quantization launch");
+      if (!mxq)
+        ZC_LAUNCH(ZC_PH_QUANTIZE,
+                  zc::launch_mxq_rows(reinterpret_cast<const bf16_t*>(x), d->T, dd, xq, xs, s),
+                  "activation quantization launch");
       ZC_LAUNCH(ZC_PH_GATE_UP,
-                zc::launch_fwdq_gateup(xq, xs, d->T, reinterpret_cast<const uint8_t*>(wg),
+                zc::launch_fwdq_gateup(mxq ? mxq : xq, mxq ? mxs : xs, d->T, reinterpret_cast<const uint8_t*>(wg),
                                        reinterpret_cast<const uint8_t*>(wu), r->offsets, r->perm,
                                        rw.tile_off2, rw.tile_exp, rw.sched, fwd_rows_per_tile(d), N,
                                        I, dd, K, hq, hs, cu, s),
@@ -514,6 +539,22 @@ zc_status do_forward(const zc_moe_desc* d, const T* x, const T* wr, const float*
                                      rw.tile_off2, rw.tile_exp, rw.sched + 8,
                                      fwd_rows_per_tile(d), N, I, dd,
                                      reinterpret_cast<bf16_t*>(y), cu, s),
+                "down GEMM launch");
+    } else if (const int G = int4_group(d)) {
+      // 4-bit weights (validated: bf16, no saved buffer); y is fp32
+      float* yf = reinterpret_cast<float*>(y);
+      const int tm = fwd_rows_per_tile(d);
+      ZC_LAUNCH(ZC_PH_GATE_UP,
+                zc::launch_int4_gateup(reinterpret_cast<const bf16_t*>(x),
+                                       reinterpret_cast<const uint8_t*>(wg),
+                                       reinterpret_cast<const uint8_t*>(wu), G, r->offsets, r->perm,
+                                       rw.tile_off2, rw.tile_exp, tm, rows, N, I, dd, K,
+                                       reinterpret_cast<bf16_t*>(h), s),
+                "gate/up GEMM launch");
+      ZC_LAUNCH(ZC_PH_DOWN,
+                zc::launch_int4_down(reinterpret_cast<const bf16_t*>(h),
+                                     reinterpret_cast<const uint8_t*>(wd), G, r->offsets,
+                                     rw.tile_off2, rw.tile_exp, tm, rows, N, I, dd, yf, s),
                 "down GEMM launch");
     } else if (d->weight_layout == ZC_WEIGHTS_PACKED) {
       // bf16 inference on packed weights (validated: bf16, no saved buffer)
@@ -572,10 +613,45 @@ zc_status do_forward(const zc_moe_desc* d, const T* x, const T* wr, const float*
                 "down GEMM launch");
     }
   }
-  ZC_LAUNCH(ZC_PH_COMBINE, zc::launch_combine<T>(x, y, r->topk_idx, r->topk_gate, r->inv, Tn, dd, N, K, d->out_scale,
-                               out, s),
+  if constexpr (std::is_same<T, bf16_t>::value) {
+    if (int4_group(d)) {
+      ZC_LAUNCH(ZC_PH_COMBINE,
+                (zc::launch_combine<T, float>(x, reinterpret_cast<const float*>(y), r->topk_idx,
+                                              r->topk_gate, r->inv, Tn, dd, N, K, d->out_scale, out,
+                                              s)),
+                "combine launch");
+      return ZC_OK;
+    }
+  }
+  ZC_LAUNCH(ZC_PH_COMBINE, (zc::launch_combine<T, T>(x, y, r->topk_idx, r->topk_gate, r->inv, Tn, dd, N, K, d->out_scale,
+                               out, s)),
          "combine launch");
   return ZC_OK;
+}
+
+template <typename T>
+zc_status do_forward(const zc_moe_desc* d, const T* x, const T* wr, const float* bias,
+                     const T* wg, const T* wu, const T* wd, T* out, zc_route_buf* r, void* saved,
+                     char* ws, hipStream_t s) {
+  RouteWs rw = carve_route(ws, d);
+  ZC_CHECK(do_route<T>(d, x, wr, bias, r, rw, s));
+  return do_experts<T>(d, x, wg, wu, wd, out, r, saved, nullptr, nullptr, rw, ws, s);
+}
+
+// The same on routing that an earlier call left in r.
+template <typename T>
+zc_status do_routed_experts(const zc_moe_desc* d, const T* x, const T* wg, const T* wu, const T* wd,
+                            T* out, const zc_route_buf* r, const uint8_t* mxq, const uint8_t* mxs,
+                            char* ws, hipStream_t s) {
+  const RouteWs rw = carve_route(ws, d);
+  const int N = static_cast<int>(d->N);
+  if (N > 0 && d->T > 0)
+    ZC_LAUNCH(ZC_PH_TILE_OFFSETS,
+              zc::launch_tile_offsets2(r->offsets, N, zc::kGemmBM, rw.tile_off,
+                                       fwd_rows_per_tile(d), rw.tile_off2, rw.tile_exp, rw.sched,
+                                       zc::kSchedInts, s),
+              "tile offsets");
+  return do_experts<T>(d, x, wg, wu, wd, out, r, nullptr, mxq, mxs, rw, ws, s);
 }
 
 template <typename T>
@@ -798,6 +874,7 @@ size_t zc_moe_workspace_size(const zc_moe_desc* desc, int op) {
     case ZC_OP_BACKWARD: return static_cast<size_t>(bwd_ws_bytes(desc));
     case ZC_OP_LB_LOSS: return static_cast<size_t>(lb_ws_bytes(desc));
     case ZC_OP_ROUTE_STATS: return static_cast<size_t>(stats_ws_bytes(desc));
+    case ZC_OP_EXPERTS: return static_cast<size_t>(fwd_ws_bytes(desc));
     default: return 0;
   }
 }
@@ -855,6 +932,51 @@ zc_status zc_moe_forward(const zc_moe_desc* desc, const void* x, const void* w_r
                            bias, static_cast<const float*>(w_gate),
                            static_cast<const float*>(w_up), static_cast<const float*>(w_down),
                            static_cast<float*>(out), r, saved, w, s);
+}
+
+zc_status zc_moe_experts(const zc_moe_desc* desc, const void* x, const zc_route_buf* r,
+                         const void* w_gate, const void* w_up, const void* w_down,
+                         const uint8_t* x_codes, const uint8_t* x_scales, void* out, void* ws,
+                         size_t ws_bytes, void* stream) {
+  ZC_CHECK(check_desc(desc));
+  const bool none = desc->T == 0;
+  if (!r) return fail(ZC_ERR_INVALID, "route buffer is NULL");
+  ZC_CHECK(check_ptr(r->topk_idx, "r->topk_idx", none));
+  ZC_CHECK(check_ptr(r->topk_gate, "r->topk_gate", none));
+  ZC_CHECK(check_ptr(r->offsets, "r->offsets"));
+  ZC_CHECK(check_ptr(r->perm, "r->perm", none));
+  ZC_CHECK(check_ptr(r->inv, "r->inv", none));
+  ZC_CHECK(check_ptr(x, "x", none));
+  ZC_CHECK(check_weights(desc, w_gate, w_up, w_down));
+  ZC_CHECK(check_ptr(x_codes, "x_codes", true));
+  ZC_CHECK(check_ptr(x_scales, "x_scales", true));
+  if ((x_codes == nullptr) != (x_scales == nullptr))
+    return fail(ZC_ERR_INVALID, "x_codes and x_scales must both be set or both be NULL");
+  if (x_codes && desc->weight_layout != ZC_WEIGHTS_MXFP8)
+    return fail(ZC_ERR_INVALID, "x_codes go with MXFP8 weights");
+  ZC_CHECK(check_ptr(out, "out", none));
+  const int64_t need = fwd_ws_bytes(desc);
+  ZC_CHECK(check_ws(ws, ws_bytes, need));
+  const int64_t n = desc->T * desc->d, b = n * esize(desc), k = desc->T * desc->K;
+  const Range in[] = {{x, b, "x", false}, {x_codes, n, "x_codes", false},
+                      {x_scales, n / 32, "x_scales", false}, {r->topk_idx, 4 * k, "r->topk_idx", false},
+                      {r->topk_gate, 4 * k, "r->topk_gate", false},
+                      {r->offsets, 4 * (desc->N + 1), "r->offsets", false},
+                      {r->perm, 4 * k, "r->perm", false}, {r->inv, 4 * k, "r->inv", false}};
+  const Range outs[] = {{out, b, "out", false}, {ws, need, "ws", false}};
+  ZC_CHECK(check_overlap(outs, 2, in, 8));
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  char* w = static_cast<char*>(ws);
+  if (desc->dtype == ZC_BF16)
+    return do_routed_experts<bf16_t>(
+        desc, static_cast<const bf16_t*>(x), static_cast<const bf16_t*>(w_gate),
+        static_cast<const bf16_t*>(w_up), static_cast<const bf16_t*>(w_down),
+        static_cast<bf16_t*>(out), r, x_codes, x_scales, w, s);
+  return do_routed_experts<float>(desc, static_cast<const float*>(x),
+                                  static_cast<const float*>(w_gate),
+                                  static_cast<const float*>(w_up),
+                                  static_cast<const float*>(w_down), static_cast<float*>(out), r,
+                                  nullptr, nullptr, w, s);
 }
 
 zc_status zc_moe_forward_noalloc(const zc_moe_desc* desc, const void* x, const void* w_router,
@@ -946,7 +1068,7 @@ zc_status zc_moe_lb_loss(const zc_moe_desc* desc, const zc_lb_cfg* lb, const zc_
 
 size_t zc_moe_seq_balance_workspace_size(const zc_moe_desc* desc, int64_t S) {
   if (check_desc(desc) != ZC_OK || check_seqs(desc, S) != ZC_OK) return 0;
-  return zc::seq_balance_scratch_bytes(desc->T, desc->N + desc->Z, S);
+  return zc::seq_balance_scratch_bytes(desc->T, desc->N + desc->Z, desc->K, S);
 }
 
 zc_status zc_moe_seq_balance(const zc_moe_desc* desc, const zc_lb_cfg* lb, const zc_route_buf* r,
@@ -968,7 +1090,7 @@ zc_status zc_moe_seq_balance(const zc_moe_desc* desc, const zc_lb_cfg* lb, const
   ZC_CHECK(check_ptr(counts, "counts"));
   ZC_CHECK(check_ptr(dlogits, "dlogits", true));
   const int64_t E = desc->N + desc->Z, T = desc->T;
-  const int64_t need = static_cast<int64_t>(zc::seq_balance_scratch_bytes(T, E, S));
+  const int64_t need = static_cast<int64_t>(zc::seq_balance_scratch_bytes(T, E, desc->K, S));
   ZC_CHECK(check_ws(ws, ws_bytes, need));
   const Range in[] = {{r->logits, 4 * T * E, "r->logits", false},
                       {r->topk_idx, 4 * T * desc->K, "r->topk_idx", false},
@@ -1068,6 +1190,68 @@ zc_status zc_moe_quantize_weights(const zc_moe_desc* desc, int which, const void
   hipError_t e = zc::launch_mxq_weights(static_cast<const bf16_t*>(src), static_cast<uint8_t*>(dst),
                                         desc->N, R, C, static_cast<hipStream_t>(stream));
   if (e != hipSuccess) return hip_fail(e, "weight quantization launch");
+  return ZC_OK;
+}
+
+size_t zc_moe_int4_weight_bytes(const zc_moe_desc* desc) {
+  if (check_desc(desc) != ZC_OK || !int4_group(desc)) return 0;
+  const int64_t n = desc->N * desc->I * desc->d;
+  return static_cast<size_t>(n / 2 + n / int4_group(desc) * 2);
+}
+
+namespace {
+// A call on one set of 4-bit weights: its sizes R, C and G.
+zc_status int4_set(const zc_moe_desc* d, int which, int* R, int* C, int* G) {
+  ZC_CHECK(check_desc(d));
+  *G = int4_group(d);
+  if (!*G) return fail(ZC_ERR_INVALID, "weight_layout %d is no INT4 layout", d->weight_layout);
+  if (which != ZC_PACK_GATE_UP && which != ZC_PACK_DOWN)
+    return fail(ZC_ERR_INVALID, "which=%d is neither ZC_PACK_GATE_UP nor ZC_PACK_DOWN", which);
+  *R = static_cast<int>(which == ZC_PACK_GATE_UP ? d->I : d->d);
+  *C = static_cast<int>(which == ZC_PACK_GATE_UP ? d->d : d->I);
+  return ZC_OK;
+}
+}  // namespace
+
+zc_status zc_moe_int4_quantize(const zc_moe_desc* desc, int which, const void* src, uint8_t* codes,
+                               void* scales, void* stream) {
+  int R, C, G;
+  ZC_CHECK(int4_set(desc, which, &R, &C, &G));
+  const bool opt = desc->N == 0;
+  ZC_CHECK(check_ptr(src, "src", opt));
+  ZC_CHECK(check_ptr(codes, "codes", opt));
+  ZC_CHECK(check_ptr(scales, "scales", opt));
+  const int64_t n = desc->N * desc->I * desc->d;
+  const Range in[] = {{src, 2 * n, "src", false}};
+  const Range out[] = {{codes, n / 2, "codes", false}, {scales, n / G * 2, "scales", false}};
+  ZC_CHECK(check_overlap(out, 2, in, 1));
+  if (opt) return ZC_OK;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  ZC_LAUNCH(ZC_PH_QUANTIZE,
+            zc::launch_int4_quantize(static_cast<const bf16_t*>(src), codes,
+                                     static_cast<bf16_t*>(scales), desc->N, R, C, G, s),
+            "4-bit quantization launch");
+  return ZC_OK;
+}
+
+zc_status zc_moe_int4_pack(const zc_moe_desc* desc, int which, const uint8_t* codes,
+                           const void* scales, void* dst, void* stream) {
+  int R, C, G;
+  ZC_CHECK(int4_set(desc, which, &R, &C, &G));
+  const bool opt = desc->N == 0;
+  ZC_CHECK(check_ptr(codes, "codes", opt));
+  ZC_CHECK(check_ptr(scales, "scales", opt));
+  ZC_CHECK(check_ptr(dst, "dst", opt));
+  const int64_t n = desc->N * desc->I * desc->d;
+  const Range in[] = {{codes, n / 2, "codes", false}, {scales, n / G * 2, "scales", false}};
+  const Range out[] = {{dst, n / 2 + n / G * 2, "dst", false}};
+  ZC_CHECK(check_overlap(out, 1, in, 2));
+  if (opt) return ZC_OK;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  ZC_LAUNCH(ZC_PH_QUANTIZE,
+            zc::launch_int4_pack(codes, static_cast<const bf16_t*>(scales),
+                                 static_cast<uint8_t*>(dst), desc->N, R, C, G, s),
+            "4-bit packing launch");
   return ZC_OK;
 }
 

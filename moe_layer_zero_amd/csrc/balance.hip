@@ -87,25 +87,25 @@ __device__ __forceinline__ int valid_tokens(const Seqs& q, int lo, int hi, int* 
   return block_sum(n, s_red);
 }
 
-// Picks of the tokens [lo, hi) into s_hist (LDS or global), valid ones only.
+// Picks of the tokens [lo, hi) into hist (LDS or global), valid ones only.
+// A thread's loads of eight rounds go out together: the pass is otherwise
+// one round trip of a pick and its mask byte after another.
 __device__ __forceinline__ void count_picks(const Seqs& q, const int32_t* __restrict__ idx, int K,
                                             int E, int lo, int hi, int* hist) {
-  const int64_t b = static_cast<int64_t>(lo) * K;
+  const int32_t* row = idx + static_cast<int64_t>(lo) * K;
   const int n = (hi - lo) * K;  // T * K < 2^31
-  for (int i = threadIdx.x; i < n; i += blockDim.x) {
-    if (q.mask && !q.mask[lo + i / K]) continue;
-    const int e = idx[b + i];
-    if (e >= 0 && e < E) atomicAdd(hist + e, 1);
+  for (int64_t i0 = threadIdx.x; i0 < n; i0 += 8 * static_cast<int64_t>(blockDim.x)) {
+    int e[8], m[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int64_t i = i0 + u * static_cast<int64_t>(blockDim.x);
+      e[u] = i < n ? row[i] : -1;
+      m[u] = i < n && q.mask ? q.mask[lo + static_cast<uint32_t>(i) / static_cast<uint32_t>(K)] : 1;
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (m[u] && e[u] >= 0 && e[u] < E) atomicAdd(hist + e[u], 1);
   }
-}
-
-// counts, ts and the two counters behind it to zero (a kernel: a memset node in a
-// captured graph would not do)
-__global__ void balance_zero_kernel(int32_t* counts, int64_t n, int* ts, int S) {
-  const int64_t i0 = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.x;
-  for (int64_t i = i0; i < n; i += step) counts[i] = 0;
-  for (int64_t i = i0; i < S + 2; i += step) ts[i] = 0;
 }
 
 // First sequence whose end lies behind token t, S if none: the number of
@@ -125,53 +125,86 @@ __device__ __forceinline__ int find_seq(const Seqs& q, int t, int lane) {
   return lo;
 }
 
-// One workgroup counts kChunk tokens: a run of one sequence's tokens in LDS,
-// then added to the sequence's counts; a short run straight into them.
-// Whoever counts a sequence's first valid token counts the sequence as used.
-constexpr int kChunk = 256, kShortRun = 32;
-__global__ __launch_bounds__(256) void balance_count_kernel(Seqs q, const int32_t* __restrict__ idx,
-                                                            int K, int E, int32_t* counts,
-                                                            int* ts, int* used) {
-  __shared__ int s_hist[kMaxExperts];
-  __shared__ int s_red[4];
-  const int c0 = blockIdx.x * kChunk, c1 = min(c0 + kChunk, q.T);
-  for (int pos = c0; pos < c1;) {
-    const int s = find_seq(q, pos, threadIdx.x & 63);
-    if (s >= q.S) break;
-    int lo, hi;
-    seq_range(q, s, lo, hi);
-    lo = max(lo, pos);
-    hi = min(hi, c1);
-    pos = max(pos + 1, hi);
-    if (lo >= hi) continue;
-    const int live = valid_tokens(q, lo, hi, s_red);
-    if (live == 0) continue;
-    if (threadIdx.x == 0 && atomicAdd(ts + s, live) == 0) atomicAdd(used, 1);
-    int32_t* row = counts + static_cast<int64_t>(s) * E;
-    if (hi - lo < kShortRun) {
-      count_picks(q, idx, K, E, lo, hi, row);
-      continue;
-    }
-    __syncthreads();
-    for (int j = threadIdx.x; j < E; j += blockDim.x) s_hist[j] = 0;
-    __syncthreads();
-    count_picks(q, idx, K, E, lo, hi, s_hist);
-    __syncthreads();
-    for (int j = threadIdx.x; j < E; j += blockDim.x)
-      if (s_hist[j]) atomicAdd(row + j, s_hist[j]);
-  }
+// Part p of P of sequence s (workgroup s P + p): its picks of each expert and
+// its valid tokens, as a row of their own, so nothing has to be zero before.
+__global__ __launch_bounds__(kCountThreads) void balance_count_kernel(
+    Seqs q, const int32_t* __restrict__ idx, int K, int E, int P, int32_t* __restrict__ part,
+    int* __restrict__ ts) {
+  __shared__ int s_hist[kMaxExperts], s_red[kCountThreads / 64];
+  const int s = blockIdx.x / P, p = blockIdx.x % P;
+  int lo, hi;
+  seq_range(q, s, lo, hi);
+  const int64_t len = hi - lo;
+  hi = lo + static_cast<int>(len * (p + 1) / P);
+  lo = lo + static_cast<int>(len * p / P);
+  for (int j = threadIdx.x; j < E; j += blockDim.x) s_hist[j] = 0;
+  __syncthreads();
+  const int live = valid_tokens(q, lo, hi, s_red);
+  if (live) count_picks(q, idx, K, E, lo, hi, s_hist);
+  __syncthreads();
+  for (int j = threadIdx.x; j < E; j += blockDim.x)
+    part[static_cast<int64_t>(blockIdx.x) * E + j] = s_hist[j];
+  if (threadIdx.x == 0) ts[blockIdx.x] = live;
 }
 
-__global__ __launch_bounds__(256) void balance_coef_kernel(LossCfg c, const int32_t* counts,
-                                                           const int* ts, const int* n_used,
-                                                           float* coef, float* seq_scale) {
-  __shared__ int s_hist[kMaxExperts], s_group[kMaxExperts + 1];
-  const int s = blockIdx.x;
-  const int used = *n_used;
-  for (int j = threadIdx.x; j < c.E; j += blockDim.x)
-    s_hist[j] = counts[static_cast<int64_t>(s) * c.E + j];
+// Sequences among [0, S) with a valid token, and those of sequence mine, from
+// the parts' token counts (P > 1 only with S <= kMaxSplit).
+constexpr int kMaxSplit = 128;
+__device__ __forceinline__ int count_used(const int* ts, int S, int P, int mine, int* s_red,
+                                          int& live) {
+  __shared__ int s_live[kMaxSplit];
+  int n = 0;
+  if (P == 1) {
+    for (int s = threadIdx.x; s < S; s += blockDim.x) n += ts[s] != 0;
+    live = ts[mine];
+    return block_sum(n, s_red);
+  }
+  if (threadIdx.x < kMaxSplit) s_live[threadIdx.x] = 0;
   __syncthreads();
-  write_coef(c, s_hist, s_group, ts[s], used, coef + static_cast<int64_t>(s) * c.E);
+  for (int i = threadIdx.x; i < S * P; i += blockDim.x) atomicAdd(s_live + i / P, ts[i]);
+  __syncthreads();
+  live = s_live[mine];
+  return block_sum(threadIdx.x < static_cast<unsigned>(S) && s_live[threadIdx.x] != 0, s_red);
+}
+__global__ __launch_bounds__(kCountThreads) void balance_used_kernel(const int* ts, int S,
+                                                                     int* used) {
+  __shared__ int s_red[kCountThreads / 64];
+  int live;
+  const int n = count_used(ts, S, 1, 0, s_red, live);
+  if (threadIdx.x == 0) *used = n;
+}
+
+// Counts and k of a sequence from its parts.  n_used: the sequences with a
+// valid token, NULL to count them here.
+__global__ __launch_bounds__(kCountThreads) void balance_coef_kernel(
+    LossCfg c, int S, int P, const int32_t* __restrict__ part, const int* __restrict__ ts,
+    const int* __restrict__ n_used, int32_t* __restrict__ counts, float* __restrict__ coef,
+    float* __restrict__ seq_scale) {
+  __shared__ int s_hist[kMaxExperts], s_group[kMaxExperts + 1], s_red[kCountThreads / 64];
+  const int s = blockIdx.x;
+  int live, used;
+  if (n_used) {
+    used = *n_used;
+    live = ts[s];  // P == 1
+  } else {
+    used = count_used(ts, S, P, s, s_red, live);
+  }
+  const int64_t row = static_cast<int64_t>(s) * P * c.E;
+  for (int j = threadIdx.x; j < c.E; j += blockDim.x) {
+    int n = 0;
+    for (int p0 = 0; p0 < P; p0 += 16) {
+      int w[16];
+#pragma unroll
+      for (int u = 0; u < 16; ++u)
+        w[u] = p0 + u < P ? part[row + static_cast<int64_t>(p0 + u) * c.E + j] : 0;
+#pragma unroll
+      for (int u = 0; u < 16; ++u) n += w[u];
+    }
+    s_hist[j] = n;
+    counts[static_cast<int64_t>(s) * c.E + j] = n;
+  }
+  __syncthreads();
+  write_coef(c, s_hist, s_group, live, used, coef + static_cast<int64_t>(s) * c.E);
   if (threadIdx.x == 0) seq_scale[s] = static_cast<float>(used);
 }
 
@@ -180,7 +213,7 @@ __global__ __launch_bounds__(256) void balance_coef_kernel(LossCfg c, const int3
 // every workgroup again.
 __global__ __launch_bounds__(kCountThreads) void balance_count_coef_kernel(
     LossCfg c, Seqs q, const int32_t* __restrict__ idx, int32_t* counts, float* coef,
-    float* seq_scale, int* arrived) {
+    float* seq_scale) {
   __shared__ int s_hist[kMaxExperts], s_group[kMaxExperts + 1], s_red[kCountThreads / 64], s_used;
   const int s = blockIdx.x, lane = threadIdx.x & 63;
   if (threadIdx.x == 0) s_used = 0;
@@ -205,130 +238,141 @@ __global__ __launch_bounds__(kCountThreads) void balance_count_coef_kernel(
   write_coef(c, s_hist, s_group, ts, s_used, coef + static_cast<int64_t>(s) * c.E);
   for (int j = threadIdx.x; j < c.E; j += blockDim.x)
     counts[static_cast<int64_t>(s) * c.E + j] = s_hist[j];
-  if (threadIdx.x == 0) {
-    seq_scale[s] = static_cast<float>(s_used);
-    if (s == 0) *arrived = 0;
-  }
+  if (threadIdx.x == 0) seq_scale[s] = static_cast<float>(s_used);
 }
 
-// The scores' pass: a wavefront takes kRun consecutive tokens and keeps its
-// sequence's k in registers, NPER slots a lane (E <= 64 NPER).  A token
-// that is masked or behind the last sequence gets zeros, whatever it holds.
-constexpr int kRun = 4;
-template <int NPER>
+// The scores' pass: a wavefront per token, NV pieces of VEC scores a lane
+// (E <= 64 NV VEC, E a multiple of VEC).  The row's loads go out before its
+// sequence is looked up.  A token that is masked or behind the last sequence
+// gets zeros, whatever it holds.
+template <int NV, int VEC>
 __global__ __launch_bounds__(64 * kWaves) void balance_scores_kernel(
     Seqs q, const float* __restrict__ logits, int E, const float* __restrict__ coef,
     float* __restrict__ dot, float* __restrict__ dl) {
+  typedef float vec_t __attribute__((ext_vector_type(VEC)));
   const int lane = threadIdx.x & 63;
-  const int64_t t0 = (static_cast<int64_t>(blockIdx.x) * kWaves + (threadIdx.x >> 6)) * kRun;
-  if (t0 >= q.T) return;
-  const int t1 = static_cast<int>(min(t0 + kRun, static_cast<int64_t>(q.T)));
-  int s = find_seq(q, static_cast<int>(t0), lane), have = -1;
-  float k[NPER];
-  for (int t = static_cast<int>(t0); t < t1; ++t) {
-    if (s < q.S && q.cu && q.cu[s + 1] <= t) s = find_seq(q, t, lane);
-    const bool live = s < q.S && (!q.cu || q.cu[s] <= t) && (!q.mask || q.mask[t]);
-    const int64_t b = static_cast<int64_t>(t) * E;
-    if (!live) {
-      if (dl)
-        for (int j = lane; j < E; j += 64) dl[b + j] = 0.f;
-      if (lane == 0) dot[t] = 0.f;
-      continue;
-    }
-    if (s != have) {
+  const int64_t tt = static_cast<int64_t>(blockIdx.x) * kWaves + (threadIdx.x >> 6);
+  if (tt >= q.T) return;
+  const int t = static_cast<int>(tt), n = E / VEC;
+  const vec_t* row = reinterpret_cast<const vec_t*>(logits + tt * E);
+  vec_t* out = reinterpret_cast<vec_t*>(dl + tt * E);
+  vec_t p[NV], k[NV];
 #pragma unroll
-      for (int i = 0; i < NPER; ++i) {
-        const int j = lane + 64 * i;
-        k[i] = j < E ? coef[static_cast<int64_t>(s) * E + j] : 0.f;
-      }
-      have = s;
-    }
-    float p[NPER], m = -INFINITY;
+  for (int i = 0; i < NV; ++i) {
+    const int j = lane + 64 * i;
+    p[i] = j < n ? row[j] : vec_t(-INFINITY);
+  }
+  const bool valid = !q.mask || q.mask[t];
+  const int s = find_seq(q, t, lane);
+  if (!valid || s >= q.S || (q.cu && q.cu[s] > t)) {
+    if (dl)
+      for (int j = lane; j < n; j += 64) out[j] = vec_t(0.f);
+    if (lane == 0) dot[t] = 0.f;
+    return;
+  }
+  const vec_t* kr = reinterpret_cast<const vec_t*>(coef + static_cast<int64_t>(s) * E);
 #pragma unroll
-    for (int i = 0; i < NPER; ++i) {
+  for (int i = 0; i < NV; ++i) {
+    const int j = lane + 64 * i;
+    k[i] = j < n ? kr[j] : vec_t(0.f);
+  }
+  float m = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) m = fmaxf(m, p[i][e]);
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
+  float sum = 0.f, sk = 0.f;
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      p[i][e] = lane + 64 * i < n ? expf(p[i][e] - m) : 0.f;
+      sum += p[i][e];
+      sk += p[i][e] * k[i][e];
+    }
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) {
+    sum += __shfl_xor(sum, o);
+    sk += __shfl_xor(sk, o);
+  }
+  const float inv = 1.0f / sum, qt = sk * inv;
+  if (lane == 0) dot[t] = qt;
+  if (dl) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
       const int j = lane + 64 * i;
-      p[i] = j < E ? logits[b + j] : -INFINITY;
-      m = fmaxf(m, p[i]);
-    }
+      vec_t v;
 #pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
-    float sum = 0.f, sk = 0.f;
-#pragma unroll
-    for (int i = 0; i < NPER; ++i) {
-      const int j = lane + 64 * i;
-      p[i] = j < E ? expf(p[i] - m) : 0.f;
-      sum += p[i];
-      sk += p[i] * k[i];
-    }
-#pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) {
-      sum += __shfl_xor(sum, o);
-      sk += __shfl_xor(sk, o);
-    }
-    const float inv = 1.0f / sum, qt = sk * inv;
-    if (lane == 0) dot[t] = qt;
-    if (dl) {
-#pragma unroll
-      for (int i = 0; i < NPER; ++i) {
-        const int j = lane + 64 * i;
-        if (j < E) dl[b + j] = (p[i] * inv) * (k[i] - qt);
-      }
+      for (int e = 0; e < VEC; ++e) v[e] = (p[i][e] * inv) * (k[i][e] - qt);
+      if (j < n) out[j] = v;
     }
   }
 }
 
-// L_s = S' sum of q_t over the sequence, a workgroup each, in binary64; the
-// last workgroup to arrive adds the sequences' sums in order for L.
+// Workgroup s: L_s = S' sum of q_t over its sequence; workgroup S: L, the sum
+// over all tokens (q_t is 0 where none counts).  Binary64, each thread its
+// tokens ascending, eight loads at a time, then a fixed tree.
 __global__ __launch_bounds__(kCountThreads) void balance_loss_kernel(
-    Seqs q, const float* __restrict__ dot, const float* __restrict__ seq_scale, double* sums,
-    int* arrived, float* __restrict__ loss) {
+    Seqs q, const float* __restrict__ dot, const float* __restrict__ seq_scale,
+    float* __restrict__ loss) {
   __shared__ double s_red[kCountThreads / 64];
-  __shared__ int s_last;
   const int s = blockIdx.x;
-  int lo, hi;
-  seq_range(q, s, lo, hi);
-  auto total = [&](double v) {
-#pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o);
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) s_red[threadIdx.x >> 6] = v;
-    __syncthreads();
-    v = 0.0;
-    for (int w = 0; w < kCountThreads / 64; ++w) v += s_red[w];
-    return v;
-  };
-  double v = 0.0;
-  for (int t = lo + threadIdx.x; t < hi; t += kCountThreads) v += static_cast<double>(dot[t]);
-  v = total(v);
-  if (threadIdx.x == 0) {
-    loss[1 + s] = static_cast<float>(v * static_cast<double>(seq_scale[s]));
-    __hip_atomic_store(sums + s, v, __ATOMIC_RELEASE, __HIP_MEMORY_SCOPE_AGENT);
-    s_last = __hip_atomic_fetch_add(arrived, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) ==
-             static_cast<int>(gridDim.x) - 1;
+  int lo = 0, hi = q.T;
+  double scale = 1.0;
+  if (s < q.S) {
+    seq_range(q, s, lo, hi);
+    scale = static_cast<double>(seq_scale[s]);
   }
+  double v = 0.0;
+  for (int64_t t0 = lo + static_cast<int64_t>(threadIdx.x); t0 < hi; t0 += 8 * kCountThreads) {
+    float w[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) w[u] = t0 + u * kCountThreads < hi ? dot[t0 + u * kCountThreads] : 0.f;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) v += static_cast<double>(w[u]);
+  }
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o);
+  if ((threadIdx.x & 63) == 0) s_red[threadIdx.x >> 6] = v;
   __syncthreads();
-  if (!s_last) return;
+  if (threadIdx.x != 0) return;
   v = 0.0;
-  for (int o = threadIdx.x; o < q.S; o += kCountThreads)
-    v += __hip_atomic_load(sums + o, __ATOMIC_ACQUIRE, __HIP_MEMORY_SCOPE_AGENT);
-  v = total(v);
-  if (threadIdx.x == 0) loss[0] = static_cast<float>(v);
+#pragma unroll
+  for (int w = 0; w < kCountThreads / 64; ++w) v += s_red[w];
+  loss[s < q.S ? 1 + s : 0] = static_cast<float>(v * scale);
 }
 
 int64_t up256(int64_t b) { return (b + 255) & ~int64_t(255); }
 
+// Parts a sequence is counted in: about 256 workgroups in all, at most 64 a
+// sequence (their rows are added by one workgroup) and at least 1024 picks
+// each, if every sequence were the average one.
+int count_parts(int64_t Tn, int64_t K, int64_t S) {
+  int64_t p = S <= kMaxSplit ? 256 / S : 1;
+  p = p > 64 ? 64 : p;
+  const int64_t most = Tn * K / (1024 * S);
+  p = p > most ? most : p;
+  return p < 1 ? 1 : static_cast<int>(p);
+}
+
 }  // namespace
 
-// coef [S][E], scale [S], sums [S] (binary64), ts [S] and two counters, dot [T]
-size_t seq_balance_scratch_bytes(int64_t Tn, int64_t E, int64_t S) {
-  return static_cast<size_t>(up256(4 * S * E) + up256(4 * S) + up256(8 * S) + up256(4 * S + 8) +
-                             up256(4 * Tn));
+// coef [S][E], scale [S], parts' counts [S][P][E] and tokens [S][P], the
+// number of used sequences, dot [T]
+size_t seq_balance_scratch_bytes(int64_t Tn, int64_t E, int64_t K, int64_t S) {
+  const int64_t P = count_parts(Tn, K, S);
+  return static_cast<size_t>(up256(4 * S * E) + up256(4 * S) + up256(4 * S * P * E) +
+                             up256(4 * S * P + 4) + up256(4 * Tn));
 }
 
 hipError_t launch_seq_balance(const float* logits, const int32_t* topk_idx, int Tn, int N, int E,
                               int K, int D, double K_e, double alpha, int S, const int32_t* cu,
                               const uint8_t* mask, float* loss, int32_t* counts, float* dlogits,
                               void* scratch, hipStream_t s) {
+  const int P = count_parts(Tn, K, S);
+  const int64_t rows = static_cast<int64_t>(S) * P;
   char* p = static_cast<char*>(scratch);
   auto take = [&p](int64_t b) {
     char* r = p;
@@ -337,49 +381,55 @@ hipError_t launch_seq_balance(const float* logits, const int32_t* topk_idx, int 
   };
   float* coef = reinterpret_cast<float*>(take(4 * static_cast<int64_t>(S) * E));
   float* scale = reinterpret_cast<float*>(take(4 * static_cast<int64_t>(S)));
-  double* sums = reinterpret_cast<double*>(take(8 * static_cast<int64_t>(S)));
-  int* ts = reinterpret_cast<int*>(take(4 * static_cast<int64_t>(S) + 8));
-  int *used = ts + S, *arrived = used + 1;
+  int32_t* part = reinterpret_cast<int32_t*>(take(4 * rows * E));
+  int* ts = reinterpret_cast<int*>(take(4 * rows + 4));
+  int* used = ts + rows;
   float* dot = reinterpret_cast<float*>(take(4 * static_cast<int64_t>(Tn)));
   const Seqs q{cu, mask, S, Tn};
   const LossCfg c{N, E, K, D, D / K_e, E > N ? 1.0 / (K - K_e) : 0.0, alpha};
   hipError_t e;
-  // Few picks: one workgroup a sequence counts them all (at most 64 a thread)
-  // and one launch does for three.
-  if (static_cast<int64_t>(Tn) * K <= 65536 && S <= 256) {
+  // Few picks: one workgroup a sequence counts them and writes k at once.
+  if (P == 1 && S <= 256) {
     hipLaunchKernelGGL(balance_count_coef_kernel, dim3(S), dim3(kCountThreads), 0, s, c, q,
-                       topk_idx, counts, coef, scale, arrived);
+                       topk_idx, counts, coef, scale);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   } else {
-    const int64_t n = static_cast<int64_t>(S) * E;
-    const int64_t zb = (n + 1023) / 1024;
-    hipLaunchKernelGGL(balance_zero_kernel, dim3(static_cast<unsigned>(zb < 1024 ? zb : 1024)),
-                       dim3(256), 0, s, counts, n, ts, S);
+    hipLaunchKernelGGL(balance_count_kernel, dim3(static_cast<unsigned>(rows)),
+                       dim3(kCountThreads), 0, s, q, topk_idx, K, E, P, part, ts);
     if ((e = hipGetLastError()) != hipSuccess) return e;
-    hipLaunchKernelGGL(balance_count_kernel, dim3((Tn + kChunk - 1) / kChunk), dim3(256), 0, s, q,
-                       topk_idx, K, E, counts, ts, used);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-    hipLaunchKernelGGL(balance_coef_kernel, dim3(S), dim3(256), 0, s, c, counts, ts, used, coef,
-                       scale);
+    // beyond 4096 sequences each workgroup's own count of the used ones would
+    // cost more than a launch
+    const bool apart = S > 4096;
+    if (apart) {
+      hipLaunchKernelGGL(balance_used_kernel, dim3(1), dim3(kCountThreads), 0, s, ts, S, used);
+      if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+    hipLaunchKernelGGL(balance_coef_kernel, dim3(S), dim3(kCountThreads), 0, s, c, S, P, part, ts,
+                       apart ? used : nullptr, counts, coef, scale);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   if (Tn > 0) {
-    const dim3 grid((Tn + kWaves * kRun - 1) / (kWaves * kRun)), block(64 * kWaves);
-    const int nper = (E + 63) / 64;
-#define ZC_BAL(NP) \
-  hipLaunchKernelGGL((balance_scores_kernel<NP>), grid, block, 0, s, q, logits, E, coef, dot, dlogits)
-    if (nper <= 1) ZC_BAL(1);
-    else if (nper <= 2) ZC_BAL(2);
-    else if (nper <= 3) ZC_BAL(3);
-    else if (nper <= 4) ZC_BAL(4);
-    else if (nper <= 8) ZC_BAL(8);
-    else if (nper <= 12) ZC_BAL(12);
-    else ZC_BAL(16);
+    const dim3 grid((Tn + kWaves - 1) / kWaves), block(64 * kWaves);
+#define ZC_BAL(NV, VEC)                                                                            \
+  hipLaunchKernelGGL((balance_scores_kernel<NV, VEC>), grid, block, 0, s, q, logits, E, coef, dot, \
+                     dlogits)
+    if (E % 4 == 0) {
+      if (E <= 256) ZC_BAL(1, 4);
+      else if (E <= 512) ZC_BAL(2, 4);
+      else if (E <= 768) ZC_BAL(3, 4);
+      else ZC_BAL(4, 4);
+    } else {
+      if (E <= 64) ZC_BAL(1, 1);
+      else if (E <= 128) ZC_BAL(2, 1);
+      else if (E <= 256) ZC_BAL(4, 1);
+      else if (E <= 512) ZC_BAL(8, 1);
+      else ZC_BAL(16, 1);
+    }
 #undef ZC_BAL
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
-  hipLaunchKernelGGL(balance_loss_kernel, dim3(S), dim3(kCountThreads), 0, s, q, dot, scale, sums,
-                     arrived, loss);
+  hipLaunchKernelGGL(balance_loss_kernel, dim3(S + 1), dim3(kCountThreads), 0, s, q, dot, scale,
+                     loss);
   return hipGetLastError();
 }
 

@@ -54,9 +54,11 @@ __device__ __forceinline__ float load_picks(const int32_t* topk_idx, const float
 // smallest covering K, so a token's rows are in flight at once).  The
 // workgroup has one thread per 16-byte piece of a row (at most 1024), so
 // at the usual widths a token's loads all go out in one pass.
-template <typename T, int G>
+// y rows are in the layer dtype or in fp32 (Y): a piece of V values is then
+// two vectors.
+template <typename T, typename Y, int G>
 __global__ __launch_bounds__(kCombineMaxThreads) void combine_kernel(
-    const T* __restrict__ x, const T* __restrict__ y, const int32_t* __restrict__ topk_idx,
+    const T* __restrict__ x, const Y* __restrict__ y, const int32_t* __restrict__ topk_idx,
     const float* __restrict__ gate, const int32_t* __restrict__ inv, int d, int N, int K,
     float out_scale, T* __restrict__ out) {
   __shared__ float s_g[kMaxK];
@@ -64,7 +66,8 @@ __global__ __launch_bounds__(kCombineMaxThreads) void combine_kernel(
   __shared__ float s_c;
   const int64_t t = blockIdx.x;
   const float c = load_picks(topk_idx, gate, inv, t, N, K, s_g, s_inv, &s_c);
-  constexpr int V = V16<T>::n;
+  constexpr int V = V16<T>::n, YV = V16<Y>::n, YN = V / YV;
+  typedef typename V16<Y>::raw_t yraw_t;
   for (int j = threadIdx.x * V; j < d; j += blockDim.x * V) {
     float acc[V], v[V];
     V16<T>::load(x + t * d + j, v);
@@ -76,17 +79,20 @@ __global__ __launch_bounds__(kCombineMaxThreads) void combine_kernel(
       // (a slot past K or of a zero-computation pick loads nothing and is
       // skipped below; each y row is read by its one token only, so its
       // loads carry the non-temporal hint)
-      typename V16<T>::raw_t w[G];
+      yraw_t w[G][YN];
 #pragma unroll
       for (int u = 0; u < G; ++u) {
         const int q = r0 + u < K ? s_inv[r0 + u] : -1;
-        w[u] = q >= 0 ? V16<T>::ld_raw_once(y + static_cast<int64_t>(q) * d + j) : typename V16<T>::raw_t{};
+#pragma unroll
+        for (int i = 0; i < YN; ++i)
+          w[u][i] = q >= 0 ? V16<Y>::ld_raw_once(y + static_cast<int64_t>(q) * d + j + i * YV) : yraw_t{};
       }
 #pragma unroll
       for (int u = 0; u < G; ++u) {
         if (r0 + u >= K || s_inv[r0 + u] < 0) continue;
         const float g = s_g[r0 + u];
-        V16<T>::unpack(w[u], v);
+#pragma unroll
+        for (int i = 0; i < YN; ++i) V16<Y>::unpack(w[u][i], v + i * YV);
 #pragma unroll
         for (int e = 0; e < V; ++e) acc[e] += g * v[e];
       }
@@ -269,14 +275,14 @@ int combine_threads(int d, int V) {
 
 }  // namespace
 
-template <typename T>
-hipError_t launch_combine(const T* x, const T* y, const int32_t* topk_idx, const float* gate,
+template <typename T, typename Y>
+hipError_t launch_combine(const T* x, const Y* y, const int32_t* topk_idx, const float* gate,
                           const int32_t* inv, int Tn, int d, int N, int K, float out_scale, T* out,
                           hipStream_t s) {
   if (Tn == 0) return hipSuccess;
   const int threads = combine_threads(d, V16<T>::n);
 #define ZC_COMBINE(G)                                                                      \
-  hipLaunchKernelGGL((combine_kernel<T, G>), dim3(Tn), dim3(threads), 0, s, x, y, topk_idx, \
+  hipLaunchKernelGGL((combine_kernel<T, Y, G>), dim3(Tn), dim3(threads), 0, s, x, y, topk_idx, \
                      gate, inv, d, N, K, out_scale, out)
   if (K <= 4) ZC_COMBINE(4);
   else if (K <= 8) ZC_COMBINE(8);
@@ -310,9 +316,9 @@ hipError_t launch_dx_gather(const T* dout, const float* dxp, const float* dxr, c
 }
 
 #define ZC_INST(T)                                                                              \
-  template hipError_t launch_combine<T>(const T*, const T*, const int32_t*, const float*,       \
-                                        const int32_t*, int, int, int, int, float, T*,          \
-                                        hipStream_t);                                           \
+  template hipError_t launch_combine<T, T>(const T*, const T*, const int32_t*, const float*,    \
+                                           const int32_t*, int, int, int, int, float, T*,       \
+                                           hipStream_t);                                        \
   template hipError_t launch_combine_bwd<T>(const T*, const T*, const T*, const float*,         \
                                             const int32_t*, const float*, const int32_t*, int,  \
                                             int, int, int, int, int, float, const float*,       \
@@ -324,5 +330,8 @@ hipError_t launch_dx_gather(const T* dout, const float* dxp, const float* dxr, c
 ZC_INST(bf16_t)
 ZC_INST(float)
 #undef ZC_INST
+template hipError_t launch_combine<bf16_t, float>(const bf16_t*, const float*, const int32_t*,
+                                                  const float*, const int32_t*, int, int, int, int,
+                                                  float, bf16_t*, hipStream_t);
 
 }  // namespace zc

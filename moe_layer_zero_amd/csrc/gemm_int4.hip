@@ -1,0 +1,381 @@
+// Forward expert GEMMs on 4-bit weights with group scales.
+//
+//   W[r][c] = s[r][c / G] (q[r][c] - 8),  q in 0..15,  G = 32, 64 or 128
+//   gate/up: h[p][n] = silu(x[tok(p)] . W_g[e][n]) * (x[tok(p)] . W_u[e][n])
+//   down:    y[p][n] = h[p] . W_d[e][n]
+// for the rows p of expert e's segment of the dispatch order; x and h in
+// bf16, every sum in fp32, h rounded to bf16 (the operand of the next
+// product), y kept in fp32 for the combine.
+//
+// A decode step gives an expert a handful of rows, so it is bound by the
+// weights' bytes, a quarter of bf16's: the kernel is built to stream them.
+//  - The codes lie in the order in which a wavefront feeds them to the matrix
+//    cores: 1 KB holds 16 output columns and 128 reduction steps, lane l's 16
+//    bytes are column l % 16, steps 32 t + 8 (l / 16) .. + 7 of t = 0..3: the
+//    B operands of four v_mfma_f32_16x16x32_bf16.  One load a lane, no LDS.
+//  - A code becomes a bf16 without a conversion: 0x4300 | q is 128 + q
+//    exactly, so 8 codes cost 7 integer operations.  The offset is taken
+//    out by the matrix cores as well: the sum of -136 x over the group (one
+//    more step per row block, shared by all columns) is where each column's
+//    sum starts, which leaves sum of x (q - 8) of the group.  Intermediate
+//    sums are up to 136 |x| large, so a group's sum carries an error of about
+//    136 * 2^-24 sum |x|, 2^-9 of a bf16 half step of x itself.  An
+//    infinity in a row gives NaN.
+//  - The scale multiplies the group's fp32 sum, not each weight.
+//  - The four wavefronts of a workgroup split the reduction and add their
+//    sums through LDS in order, so few rows still give many workgroups with
+//    many loads in flight, and there is no barrier in the loop.
+//
+// Weights of one set (N matrices [R][C]): codes [N][R/16][C/128][1 KB], then
+// scales [N][R/16][C/128][16 columns][128/G] in bf16.  In a lane's 4 bytes of
+// a step t, the code of step 2 p is at bit 4 p, that of 2 p + 1 at 16 + 4 p:
+// (word >> 4 p) & 0x000f000f is register p of the operand.
+#include "zc_common.h"
+
+namespace zc {
+namespace {
+
+constexpr int kWaves = 4;
+constexpr int kThreads = 64 * kWaves;
+constexpr int kStep = 128;  // reduction steps of a code block
+
+enum { I4_SWIGLU = 0, I4_STORE = 1 };
+
+struct I4Params {
+  int N, ncols, K;          // experts, output columns (I or d), reduction length (d or I)
+  const int32_t* offsets;   // [N+1] rows of each expert in dispatch order
+  const int32_t* mt_off;    // [N+1] prefix of ceil(rows / tile height)
+  const int32_t* tile_exp;  // expert of each row tile
+  const bf16_t* A;          // x [T][d] gathered through perm, or h [P][I]
+  const int32_t* perm;      // gate/up only
+  int kdiv;                 // K of the layer (slot -> token)
+  const uint8_t* B;         // W_g or W_d
+  const uint8_t* B2;        // W_u (gate/up)
+  bf16_t* h;                // gate/up output [P][I]
+  float* y;                 // down output [P][d]
+};
+
+__device__ __forceinline__ float silu_f(float a) {
+  return a * __builtin_amdgcn_rcpf(1.0f + __expf(-a));
+}
+
+// Eight codes -> 128 + q in bf16.
+__device__ __forceinline__ bf16x8_t codes_bf16(uint32_t w) {
+  u32x4_t r;
+#pragma unroll
+  for (int p = 0; p < 4; ++p) r[p] = ((w >> (4 * p)) & 0x000f000fu) | 0x43004300u;
+  return __builtin_bit_cast(bf16x8_t, r);
+}
+
+// RB blocks of 16 rows and NB blocks of 16 weight columns a workgroup (gate/up:
+// the first half of them gate, the second the matching up columns).
+template <int EPI, int RB, int NB, int G>
+__global__ __launch_bounds__(kThreads) void int4_kernel(I4Params p) {
+  constexpr int NG = kStep / G;                             // groups of a code block
+  constexpr int TG = 4 / NG;                                // MFMA steps of a group
+  constexpr int OUT = (EPI == I4_SWIGLU ? NB / 2 : NB) * 16;  // output columns a workgroup
+  constexpr int TM = 16 * RB;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int l16 = lane & 15, lq = lane >> 4;
+
+  // Tiles are dealt to the 8 XCDs (workgroup b runs on XCD b mod 8) in
+  // runs of consecutive ones, row tiles of a weight panel next to each other:
+  // they read it from one L2.
+  const int NT = p.ncols / OUT;
+  const int64_t total = static_cast<int64_t>(ld_scalar(p.mt_off + p.N)) * NT;
+  const int64_t chunk = (total + 7) / 8;
+  __shared__ float s_acc[kWaves][RB * NB * 4][64];
+  for (int64_t in = blockIdx.x / 8; in < chunk; in += gridDim.x / 8) {
+  const int64_t L = (blockIdx.x % 8) * chunk + in;
+  if (L >= total) break;
+  const int e = ld_scalar(p.tile_exp + L / NT);
+  const int mt0 = ld_scalar(p.mt_off + e);
+  const int mte = ld_scalar(p.mt_off + e + 1) - mt0;
+  const int q = static_cast<int>(L - static_cast<int64_t>(mt0) * NT);
+  const int nt = q / mte;
+  const int seg1 = ld_scalar(p.offsets + e + 1);
+  const int m0 = ld_scalar(p.offsets + e) + TM * (q % mte);
+  const int mcount = min(TM, seg1 - m0);
+
+  // this lane's piece of its rows; rows past the tile read its last row again
+  const bf16_t* arow[RB];
+#pragma unroll
+  for (int rb = 0; rb < RB; ++rb) {
+    const int row = m0 + min(16 * rb + l16, mcount - 1);
+    const int src = EPI == I4_SWIGLU ? p.perm[row] / p.kdiv : row;
+    arow[rb] = p.A + static_cast<int64_t>(src) * p.K + 8 * lq;
+  }
+  const int nkb = p.K / kStep;
+  const int64_t mat = static_cast<int64_t>(p.ncols) * p.K;  // weights of one matrix
+  const u32x4_t* code[NB];
+  const bf16_t* scale[NB];
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) {
+    const bool up = EPI == I4_SWIGLU && nb >= NB / 2;
+    const uint8_t* base = up ? p.B2 : p.B;
+    const int cb = nt * (OUT / 16) + (up ? nb - NB / 2 : nb);
+    code[nb] = reinterpret_cast<const u32x4_t*>(base + e * (mat / 2) +
+                                                static_cast<int64_t>(cb) * nkb * 1024) + lane;
+    scale[nb] = reinterpret_cast<const bf16_t*>(base + p.N * (mat / 2)) + e * (mat / G) +
+                (static_cast<int64_t>(cb) * nkb * 16 + l16) * NG;
+  }
+
+  struct Buf {
+    u32x4_t b[NB];
+    bf16_t s[NB][NG];
+    bf16x8_t a[RB][4];
+  };
+  auto load = [&](int kb, Buf& f) {
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) f.b[nb] = __builtin_nontemporal_load(code[nb] + kb * 64);
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+      __builtin_memcpy(f.s[nb], scale[nb] + static_cast<int64_t>(kb) * 16 * NG, 2 * NG);
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+        f.a[rb][t] = *reinterpret_cast<const bf16x8_t*>(arow[rb] + kb * kStep + 32 * t);
+  };
+
+  f32x4_t acc[RB][NB];
+#pragma unroll
+  for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) acc[rb][nb] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  const u32x4_t off_bits = {0xc308c308u, 0xc308c308u, 0xc308c308u, 0xc308c308u};  // -136
+  const bf16x8_t off = __builtin_bit_cast(bf16x8_t, off_bits);
+
+  auto compute = [&](const Buf& f) {
+    f32x4_t start[RB][NG];
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        f32x4_t v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int t = g * TG; t < (g + 1) * TG; ++t)
+          v = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f.a[rb][t], off, v, 0, 0, 0);
+        start[rb][g] = v;
+      }
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        f32x4_t part[RB];
+#pragma unroll
+        for (int rb = 0; rb < RB; ++rb) part[rb] = start[rb][g];
+#pragma unroll
+        for (int t = g * TG; t < (g + 1) * TG; ++t) {
+          const bf16x8_t w = codes_bf16(f.b[nb][t]);
+#pragma unroll
+          for (int rb = 0; rb < RB; ++rb)
+            part[rb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f.a[rb][t], w, part[rb], 0, 0, 0);
+        }
+        const float s = bf2f(f.s[nb][g]);
+#pragma unroll
+        for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+          for (int v = 0; v < 4; ++v) acc[rb][nb][v] += s * part[rb][v];
+      }
+  };
+
+  // this wavefront's share of the reduction, one block ahead in registers
+  const int kb0 = nkb * wave / kWaves, kb1 = nkb * (wave + 1) / kWaves;
+  if (kb0 < kb1) {
+    Buf f0, f1;
+    load(kb0, f0);
+    int kb = kb0;
+    for (; kb + 2 <= kb1; kb += 2) {
+      load(kb + 1, f1);
+      compute(f0);
+      if (kb + 2 < kb1) load(kb + 2, f0);
+      compute(f1);
+    }
+    if (kb < kb1) compute(f0);
+  }
+
+  // the wavefronts' sums, added in order; wavefront w finishes its share of
+  // the tile.  Register v of block (rb, nb): row 16 rb + 4 (lane / 16) + v,
+  // column 16 nb + lane % 16.
+  __syncthreads();  // the previous tile's sums have been read
+#pragma unroll
+  for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) s_acc[wave][(rb * NB + nb) * 4 + v][lane] = acc[rb][nb][v];
+  __syncthreads();
+  auto sum = [&](int rb, int nb, int v) {
+    const int i = (rb * NB + nb) * 4 + v;
+    return ((s_acc[0][i][lane] + s_acc[1][i][lane]) + s_acc[2][i][lane]) + s_acc[3][i][lane];
+  };
+  // wavefront w takes register v = w of every block
+#pragma unroll
+  for (int rb = 0; rb < RB; ++rb) {
+    const int r = 16 * rb + 4 * lq + wave;
+    if (r >= mcount) continue;
+    const int64_t row = (static_cast<int64_t>(m0) + r) * p.ncols + nt * OUT + l16;
+    if constexpr (EPI == I4_SWIGLU) {
+#pragma unroll
+      for (int nb = 0; nb < NB / 2; ++nb)
+        p.h[row + 16 * nb] = f2bf(silu_f(sum(rb, nb, wave)) * sum(rb, nb + NB / 2, wave));
+    } else {
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) p.y[row + 16 * nb] = sum(rb, nb, wave);
+    }
+  }
+  }
+}
+
+// Natural layout (two codes a byte, the even step in the low half; scales
+// [R][C/G]) -> the layout above.  One thread per 8 codes.
+__global__ __launch_bounds__(256) void int4_pack_kernel(const uint32_t* __restrict__ codes,
+                                                        const bf16_t* __restrict__ scales,
+                                                        uint8_t* __restrict__ dst, int64_t nmat,
+                                                        int R, int C, int G) {
+  const int64_t words = nmat * R * (C / 8);
+  const int64_t i0 = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * 256;
+  for (int64_t i = i0; i < words; i += step) {
+    // i = (((mat R/16 + rb) C/128 + kb) 64 + lane) 4 + t
+    const int t = i & 3, lane = (i >> 2) & 63;
+    const int64_t blk = i >> 8;
+    const int kb = static_cast<int>(blk % (C / kStep));
+    const int64_t row = blk / (C / kStep) * 16 + (lane & 15);
+    const uint32_t w = codes[row * (C / 8) + kb * 16 + t * 4 + (lane >> 4)];
+    uint32_t v = 0;
+#pragma unroll
+    for (int p = 0; p < 4; ++p)
+      v |= ((w >> (8 * p)) & 0xfu) << (4 * p) | ((w >> (8 * p + 4)) & 0xfu) << (16 + 4 * p);
+    reinterpret_cast<uint32_t*>(dst)[i] = v;
+  }
+  const int64_t ns = nmat * R * (C / G);
+  for (int64_t i = i0; i < ns; i += step) {
+    // i = ((mat R/16 + rb) C/128 + kb) 16 NG + column NG + g
+    const int NG = kStep / G, g = static_cast<int>(i % NG);
+    const int64_t j = i / NG;
+    const int64_t blk = j >> 4;
+    const int kb = static_cast<int>(blk % (C / kStep));
+    const int64_t row = blk / (C / kStep) * 16 + (j & 15);
+    reinterpret_cast<bf16_t*>(dst + words * 4)[i] = scales[row * (C / G) + kb * NG + g];
+  }
+}
+
+// bf16 rows -> codes and scales in the natural layout: s = bf16(max|w| / 7),
+// q = nearest of w / s (ties to even) clamped to -8..7, plus 8; a group of
+// zeros (or whose scale rounds to 0) has s = 0 and q = 8, a group with a NaN
+// or an infinity the scale NaN.  One thread per 8 values.
+__global__ __launch_bounds__(256) void int4_quantize_kernel(const bf16_t* __restrict__ src,
+                                                            int64_t groups8, int G,
+                                                            uint32_t* __restrict__ codes,
+                                                            bf16_t* __restrict__ scales) {
+  // (a group's lanes take the same rounds: C is a multiple of 128)
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < groups8;
+       i += static_cast<int64_t>(gridDim.x) * 256) {
+  float f[8];
+  V16<bf16_t>::load(src + i * 8, f);
+  float m = 0.f;
+  bool bad = false;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    bad |= !(fabsf(f[e]) <= 3.402823466e38f);
+    m = fmaxf(m, fabsf(f[e]));
+  }
+  int b = bad;
+  for (int o = 1; o < G / 8; o <<= 1) {
+    m = fmaxf(m, __shfl_xor(m, o));
+    b |= __shfl_xor(b, o);
+  }
+  const bf16_t sb = b ? static_cast<bf16_t>(0x7fc0) : f2bf(m / 7.0f);
+  const float s = bf2f(sb);
+  uint32_t w = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    int q = 8;
+    if (!b && s > 0.f) q = static_cast<int>(fminf(fmaxf(rintf(f[e] / s), -8.f), 7.f)) + 8;
+    w |= static_cast<uint32_t>(q) << (4 * e);
+  }
+  codes[i] = w;
+  if (i % (G / 8) == 0) scales[i / (G / 8)] = sb;
+  }
+}
+
+// Grids beyond this many workgroups go round again (a launch holds fewer than
+// 2^32 threads).
+constexpr int64_t kMaxGrid = int64_t(1) << 20;
+unsigned grid_of(int64_t blocks) {
+  return static_cast<unsigned>(blocks < kMaxGrid ? blocks : kMaxGrid);
+}
+
+// At most this many row tiles of height tm: every one of the rows' experts has
+// one ragged tile.
+int64_t int4_max_tiles(int64_t rows, int64_t N, int tm) {
+  return rows / tm + (rows < N ? rows : N);
+}
+
+template <int EPI, int RB, int NB>
+hipError_t launch_int4(const I4Params& p, int G, int64_t rows, hipStream_t s) {
+  constexpr int OUT = (EPI == I4_SWIGLU ? NB / 2 : NB) * 16;
+  const int64_t tiles = int4_max_tiles(rows, p.N, 16 * RB) * (p.ncols / OUT);
+  const dim3 grid(grid_of((tiles + 7) / 8 * 8)), block(kThreads);
+  if (G == 32)
+    hipLaunchKernelGGL((int4_kernel<EPI, RB, NB, 32>), grid, block, 0, s, p);
+  else if (G == 64)
+    hipLaunchKernelGGL((int4_kernel<EPI, RB, NB, 64>), grid, block, 0, s, p);
+  else
+    hipLaunchKernelGGL((int4_kernel<EPI, RB, NB, 128>), grid, block, 0, s, p);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+int int4_rows_per_tile(int64_t avg_rows) {
+  if (avg_rows <= 12) return 16;
+  if (avg_rows <= 40) return 32;
+  return 64;
+}
+
+hipError_t launch_int4_gateup(const bf16_t* x, const uint8_t* wg, const uint8_t* wu, int G,
+                              const int32_t* offsets, const int32_t* perm, const int32_t* mt_off,
+                              const int32_t* tile_exp, int tm, int64_t rows, int N, int I, int d,
+                              int K, bf16_t* h, hipStream_t s) {
+  I4Params p{};
+  p.N = N; p.ncols = I; p.K = d;
+  p.offsets = offsets; p.mt_off = mt_off; p.tile_exp = tile_exp;
+  p.A = x; p.perm = perm; p.kdiv = K; p.B = wg; p.B2 = wu; p.h = h;
+  if (tm == 16) return launch_int4<I4_SWIGLU, 1, 4>(p, G, rows, s);
+  if (tm == 32) return launch_int4<I4_SWIGLU, 2, 4>(p, G, rows, s);
+  return launch_int4<I4_SWIGLU, 4, 4>(p, G, rows, s);
+}
+
+hipError_t launch_int4_down(const bf16_t* h, const uint8_t* wd, int G, const int32_t* offsets,
+                            const int32_t* mt_off, const int32_t* tile_exp, int tm, int64_t rows,
+                            int N, int I, int d, float* y, hipStream_t s) {
+  I4Params p{};
+  p.N = N; p.ncols = d; p.K = I;
+  p.offsets = offsets; p.mt_off = mt_off; p.tile_exp = tile_exp;
+  p.A = h; p.kdiv = 1; p.B = wd; p.y = y;
+  if (tm == 16) return launch_int4<I4_STORE, 1, 8>(p, G, rows, s);
+  if (tm == 32) return launch_int4<I4_STORE, 2, 8>(p, G, rows, s);
+  return launch_int4<I4_STORE, 4, 4>(p, G, rows, s);
+}
+
+hipError_t launch_int4_pack(const uint8_t* codes, const bf16_t* scales, uint8_t* dst, int64_t nmat,
+                            int R, int C, int G, hipStream_t s) {
+  const int64_t words = nmat * R * (C / 8);  // at least the scales: G >= 32
+  hipLaunchKernelGGL(int4_pack_kernel, dim3(grid_of((words + 255) / 256)), dim3(256),
+                     0, s, reinterpret_cast<const uint32_t*>(codes), scales, dst, nmat, R, C, G);
+  return hipGetLastError();
+}
+
+hipError_t launch_int4_quantize(const bf16_t* src, uint8_t* codes, bf16_t* scales, int64_t nmat,
+                                int R, int C, int G, hipStream_t s) {
+  const int64_t n = nmat * R * (C / 8);
+  hipLaunchKernelGGL(int4_quantize_kernel, dim3(grid_of((n + 255) / 256)), dim3(256),
+                     0, s, src, n, G, reinterpret_cast<uint32_t*>(codes), scales);
+  return hipGetLastError();
+}
+
+}  // namespace zc

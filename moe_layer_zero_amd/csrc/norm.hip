@@ -78,8 +78,9 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_fwd_kernel(
   constexpr int RPB = (TPR < 256 ? 256 : TPR) / TPR;
   __shared__ double s_red[TPR / 64];
   const int tid = threadIdx.x % TPR;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * RPB + threadIdx.x / TPR;
-  if (row >= Tn) return;  // whole wavefronts only: with TPR > 64 a row is the workgroup's
+  // (beyond kNormGrid workgroups the grid goes round again)
+  for (int64_t row = static_cast<int64_t>(blockIdx.x) * RPB + threadIdx.x / TPR; row < Tn;
+       row += static_cast<int64_t>(gridDim.x) * RPB) {
   const int64_t base = row * d;
   // all loads of the row first; a vector past its end counts as zeros
   typename V16<T>::raw_t wx[NV], wr[NV], wg[NV];
@@ -133,6 +134,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_fwd_kernel(
       const int b = j / 32, k = b & 3;
       if ((tid & 3) == 0) scales[base / 32 + (b & ~3) + ((k & 1) << 1 | k >> 1)] = static_cast<uint8_t>(S);
     }
+  }
   }
 }
 
@@ -251,6 +253,9 @@ __global__ __launch_bounds__(kRedCols * kRedGroups) void norm_dgamma_kernel(
   }
 }
 
+// A launch holds fewer than 2^32 threads.
+constexpr int64_t kNormGrid = int64_t(1) << 20;
+
 // Partial rows of the dgamma sum, by T alone.
 constexpr int kNormBlocks = 512;
 
@@ -291,7 +296,8 @@ hipError_t launch_norm_fwd(const T* x, const T* res, const T* gamma, T* r, T* y,
   return norm_shape<T>(d, [&](auto nv, auto tpr) {
     constexpr int NV = decltype(nv)::value, TPR = decltype(tpr)::value;
     constexpr int NT = TPR < 256 ? 256 : TPR, RPB = NT / TPR;
-    const dim3 grid(static_cast<unsigned>((Tn + RPB - 1) / RPB)), block(NT);
+    const int64_t blocks = (Tn + RPB - 1) / RPB;
+    const dim3 grid(static_cast<unsigned>(blocks < kNormGrid ? blocks : kNormGrid)), block(NT);
     if constexpr (std::is_same<T, bf16_t>::value) {
       if (codes) {
         hipLaunchKernelGGL((norm_fwd_kernel<T, NV, TPR, true>), grid, block, 0, s, x, res, gamma, r,

@@ -319,9 +319,29 @@ hipError_t launch_fwdq_down(const uint8_t* hq, const uint8_t* hs, int64_t rows,
                             const int32_t* tile_exp, int32_t* sched, int tm, int N, int I, int d,
                             bf16_t* y, int cu, hipStream_t s);
 
+// Expert GEMMs on 4-bit weights with group scales (gemm_int4.hip): group
+// size G of 32, 64 or 128, d and I multiples of 128.  Tile tables as for the
+// packed kernels, with tm = int4_rows_per_tile(T*K/N) rows a tile (16, 32 or
+// 64); rows = T*K bounds the picks.  y is fp32 [P][d].
+int int4_rows_per_tile(int64_t avg_rows);
+hipError_t launch_int4_gateup(const bf16_t* x, const uint8_t* wg, const uint8_t* wu, int G,
+                              const int32_t* offsets, const int32_t* perm, const int32_t* mt_off,
+                              const int32_t* tile_exp, int tm, int64_t rows, int N, int I, int d,
+                              int K, bf16_t* h, hipStream_t s);
+hipError_t launch_int4_down(const bf16_t* h, const uint8_t* wd, int G, const int32_t* offsets,
+                            const int32_t* mt_off, const int32_t* tile_exp, int tm, int64_t rows,
+                            int N, int I, int d, float* y, hipStream_t s);
+// nmat [R][C] matrices: natural codes and scales -> the kernels' order; bf16
+// -> natural codes and scales.
+hipError_t launch_int4_pack(const uint8_t* codes, const bf16_t* scales, uint8_t* dst, int64_t nmat,
+                            int R, int C, int G, hipStream_t s);
+hipError_t launch_int4_quantize(const bf16_t* src, uint8_t* codes, bf16_t* scales, int64_t nmat,
+                                int R, int C, int G, hipStream_t s);
+
 // Combine: out = out_scale * (c_t x_t + sum_r g_r y[inv]).
-template <typename T>
-hipError_t launch_combine(const T* x, const T* y, const int32_t* topk_idx, const float* gate,
+// y in the layer dtype, or in fp32.
+template <typename T, typename Y>
+hipError_t launch_combine(const T* x, const Y* y, const int32_t* topk_idx, const float* gate,
                           const int32_t* inv, int Tn, int d, int N, int K, float out_scale,
                           T* out, hipStream_t s);
 
@@ -345,8 +365,8 @@ hipError_t launch_dx_gather(const T* dout, const float* dxp, const float* dxr, c
 
 // Balance loss of packed sequences (balance.hip): loss [1+S], counts [S][E]
 // and the score gradient dlogits [T][E] (may be NULL).  cu [S+1] and mask [T]
-// may be NULL.  Scratch: seq_balance_scratch_bytes(T, E, S).
-size_t seq_balance_scratch_bytes(int64_t Tn, int64_t E, int64_t S);
+// may be NULL.  Scratch: seq_balance_scratch_bytes(T, E, K, S).
+size_t seq_balance_scratch_bytes(int64_t Tn, int64_t E, int64_t K, int64_t S);
 hipError_t launch_seq_balance(const float* logits, const int32_t* topk_idx, int Tn, int N, int E,
                               int K, int D, double K_e, double alpha, int S, const int32_t* cu,
                               const uint8_t* mask, float* loss, int32_t* counts, float* dlogits,

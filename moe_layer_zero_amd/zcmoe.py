@@ -20,7 +20,9 @@ LIB_PATH = os.path.join(HERE, "libzcmoe.so")
 ZC_OK, ZC_ERR_INVALID, ZC_ERR_UNSUPPORTED, ZC_ERR_WORKSPACE, ZC_ERR_HIP = range(5)
 ZC_F32, ZC_BF16 = 0, 1
 ZC_OP_ROUTE, ZC_OP_FORWARD, ZC_OP_BACKWARD, ZC_OP_LB_LOSS, ZC_OP_ROUTE_STATS = 0, 1, 2, 3, 4
+ZC_OP_EXPERTS = 5
 ZC_WEIGHTS_ROWMAJOR, ZC_WEIGHTS_PACKED, ZC_WEIGHTS_MXFP8 = 0, 1, 2
+ZC_WEIGHTS_INT4_G32, ZC_WEIGHTS_INT4_G64, ZC_WEIGHTS_INT4_G128 = 4, 5, 6
 ZC_PACK_GATE_UP, ZC_PACK_DOWN = 0, 1
 
 # Every symbol include/zc_moe.h declares.
@@ -29,6 +31,8 @@ EXPORTS = ("zc_moe_workspace_size", "zc_moe_saved_size", "zc_moe_route", "zc_moe
            "zc_moe_pid_update", "zc_moe_pack_weights", "zc_moe_quantized_weight_bytes",
            "zc_moe_quantize_weights",
            "zc_moe_backward_scores", "zc_moe_seq_balance_workspace_size", "zc_moe_seq_balance",
+           "zc_moe_experts", "zc_moe_int4_weight_bytes", "zc_moe_int4_quantize",
+           "zc_moe_int4_pack",
            "zc_rmsnorm_forward", "zc_rmsnorm_workspace_size", "zc_rmsnorm_backward",
            "zc_moe_profile",
            "zc_moe_profile_read",
@@ -98,12 +102,18 @@ def lib() -> C.CDLL:
         L.zc_moe_seq_balance_workspace_size.argtypes = [P, i64]
         L.zc_moe_seq_balance_workspace_size.restype = sz
         L.zc_moe_seq_balance.argtypes = [P, LB, D, i64, v, v, v, v, v, v, sz, v]
+        L.zc_moe_experts.argtypes = [P, v, D, v, v, v, v, v, v, v, sz, v]
+        L.zc_moe_int4_weight_bytes.argtypes = [P]
+        L.zc_moe_int4_weight_bytes.restype = sz
+        L.zc_moe_int4_quantize.argtypes = [P, C.c_int, v, v, v, v]
+        L.zc_moe_int4_pack.argtypes = [P, C.c_int, v, v, v, v]
         NP = C.POINTER(zc_norm_desc)
         L.zc_rmsnorm_forward.argtypes = [NP, v, v, v, v, v, v, v, v, v]
         L.zc_rmsnorm_workspace_size.argtypes = [NP]
         L.zc_rmsnorm_workspace_size.restype = sz
         L.zc_rmsnorm_backward.argtypes = [NP, v, v, v, v, v, v, v, v, sz, v]
-        for f in ("zc_moe_backward_scores", "zc_moe_seq_balance", "zc_rmsnorm_forward", "zc_rmsnorm_backward",
+        for f in ("zc_moe_experts", "zc_moe_int4_quantize", "zc_moe_int4_pack",
+                  "zc_moe_backward_scores", "zc_moe_seq_balance", "zc_rmsnorm_forward", "zc_rmsnorm_backward",
                   "zc_moe_route", "zc_moe_forward", "zc_moe_forward_noalloc",
                   "zc_moe_backward", "zc_moe_lb_loss",
                   "zc_moe_route_stats", "zc_moe_accumulate_counts", "zc_moe_pid_update",
@@ -278,12 +288,27 @@ def _check_layer_tensor(t, shape, dtype, name):
         raise ValueError(f"{name}: expected {tuple(shape)} {dtype}, got {tuple(t.shape)} {t.dtype}")
 
 
+def int4_layout(G: int) -> int:
+    """Weight layout of 4-bit weights with groups of G (32, 64 or 128)."""
+    try:
+        return {32: ZC_WEIGHTS_INT4_G32, 64: ZC_WEIGHTS_INT4_G64, 128: ZC_WEIGHTS_INT4_G128}[G]
+    except KeyError:
+        raise ValueError(f"groups of {G}: 32, 64 or 128 are supported") from None
+
+
+def int4_group(desc: LayerDesc) -> int:
+    """Group size of desc's 4-bit weight layout, 0 for the other layouts."""
+    return {ZC_WEIGHTS_INT4_G32: 32, ZC_WEIGHTS_INT4_G64: 64,
+            ZC_WEIGHTS_INT4_G128: 128}.get(desc.weight_layout, 0)
+
+
 def _check_weights(desc, w_router, w_gate, w_up, w_down):
     dt = desc.dtype
     _check_layer_tensor(w_router, (desc.E, desc.d), dt, "w_router")
-    if desc.weight_layout == ZC_WEIGHTS_MXFP8:
+    if desc.weight_layout == ZC_WEIGHTS_MXFP8 or int4_group(desc):
         d = desc.c()
-        n = int(lib().zc_moe_quantized_weight_bytes(C.byref(d)))
+        size = lib().zc_moe_int4_weight_bytes if int4_group(desc) else lib().zc_moe_quantized_weight_bytes
+        n = int(size(C.byref(d)))
         for t, name in ((w_gate, "w_gate"), (w_up, "w_up"), (w_down, "w_down")):
             if t is not None and (t.dtype != torch.uint8 or t.numel() < n):
                 raise ValueError(f"{name}: expected a quantized weight set of {n} uint8")
@@ -319,6 +344,31 @@ def zc_moe_forward(desc: LayerDesc, x, w_router, bias, w_gate, w_up, w_down, out
     _check(lib().zc_moe_forward(C.byref(d), _ptr(x), _ptr(w_router), _ptr(bias), _ptr(w_gate),
                                 _ptr(w_up), _ptr(w_down), _ptr(out), C.byref(r), _ptr(saved),
                                 _ptr(ws), ws.numel(), _stream(stream)), "zc_moe_forward")
+
+
+def zc_moe_experts(desc: LayerDesc, x, route: RouteBuffers, w_gate, w_up, w_down, out, xq=None,
+                   ws=None, stream=None):
+    """The experts and the combine on routing that zc_moe_route left in route.
+    xq: (codes, scales) of x from zc_rmsnorm_forward, for MXFP8 weights."""
+    T, K, N, dt = desc.T, desc.K, desc.N, desc.dtype
+    a, sh, i32, u8 = _Args("zc_moe_experts"), (desc.T, desc.d), torch.int32, torch.uint8
+    px, po = a(x, sh, dt, "x"), a(out, sh, dt, "out")
+    r = zc_route_buf(topk_idx=a(route.topk_idx, (T, K), i32, "route.topk_idx"),
+                     topk_gate=a(route.topk_gate, (T, K), torch.float32, "route.topk_gate"),
+                     offsets=a(route.offsets, (N + 1,), i32, "route.offsets"),
+                     perm=a(route.perm, (max(T * K, 1),), i32, "route.perm"),
+                     inv=a(route.inv, (max(T * K, 1),), i32, "route.inv"))
+    _check_weights(desc, None, w_gate, w_up, w_down)
+    w = [None if t is None else a(t, t.shape, t.dtype, n)
+         for t, n in ((w_gate, "w_gate"), (w_up, "w_up"), (w_down, "w_down"))]
+    codes, scales = (None, None) if xq is None else (
+        a(xq[0], sh, u8, "xq codes"), a(xq[1], (T, desc.d // 32), u8, "xq scales"))
+    scratch = None
+    if ws is None:
+        ws = scratch = workspace(desc, ZC_OP_EXPERTS, x.device)
+    n = ws.numel() * ws.element_size()
+    a.run(lib().zc_moe_experts, C.byref(desc.c()), px, C.byref(r), *w, codes, scales, po,
+          a(ws, ws.shape, ws.dtype, "ws"), n, stream=stream, scratch=scratch)
 
 
 NOALLOC_SCRATCH_BYTES = 64 << 20  # ZC_NOALLOC_SCRATCH_BYTES
@@ -518,6 +568,63 @@ def quantize_expert_weights(desc: LayerDesc, w_gate, w_up, w_down, stream=None):
     return (zc_moe_quantize_weights(desc, ZC_PACK_GATE_UP, w_gate, stream=stream),
             zc_moe_quantize_weights(desc, ZC_PACK_GATE_UP, w_up, stream=stream),
             zc_moe_quantize_weights(desc, ZC_PACK_DOWN, w_down, stream=stream))
+
+
+def _int4_shapes(desc: LayerDesc, which: int):
+    G = int4_group(desc)
+    if not G:
+        raise ValueError("desc.weight_layout is no 4-bit layout (see int4_layout)")
+    N, R, Cc = (desc.N, desc.I, desc.d) if which == ZC_PACK_GATE_UP else (desc.N, desc.d, desc.I)
+    return (N, R, Cc), (N, R, Cc // 2), (N, R, Cc // G)
+
+
+def zc_moe_int4_quantize(desc: LayerDesc, which: int, src, codes=None, scales=None, stream=None):
+    """w_gate or w_up (ZC_PACK_GATE_UP, [N][I][d]) or w_down (ZC_PACK_DOWN,
+    [N][d][I]) as 4-bit codes (uint8 [N][R][C/2]) and group scales (bf16
+    [N][R][C/G]); both are allocated when None and returned."""
+    full, cs, ss = _int4_shapes(desc, which)
+    if codes is None:
+        codes = torch.empty(cs, dtype=torch.uint8, device=src.device)
+    if scales is None:
+        scales = torch.empty(ss, dtype=torch.bfloat16, device=src.device)
+    a = _Args("zc_moe_int4_quantize")
+    a.run(lib().zc_moe_int4_quantize, C.byref(desc.c()), which, a(src, full, torch.bfloat16, "src"),
+          a(codes, cs, torch.uint8, "codes"), a(scales, ss, torch.bfloat16, "scales"), stream=stream)
+    return codes, scales
+
+
+def zc_moe_int4_pack(desc: LayerDesc, which: int, codes, scales, dst=None, stream=None):
+    """4-bit codes and scales in their natural layout (zc_moe_int4_quantize, or
+    made elsewhere) -> the weight set a forward with desc's layout takes, a
+    uint8 tensor (allocated when None).  Returns it."""
+    _, cs, ss = _int4_shapes(desc, which)
+    d = desc.c()
+    n = int(lib().zc_moe_int4_weight_bytes(C.byref(d)))
+    if dst is None:
+        dst = torch.empty(max(n, 16), dtype=torch.uint8, device=codes.device)
+    if dst.dtype != torch.uint8 or dst.numel() < n:
+        raise ValueError(f"dst: expected at least {n} uint8, got {dst.numel()} {dst.dtype}")
+    a = _Args("zc_moe_int4_pack")
+    a.run(lib().zc_moe_int4_pack, C.byref(d), which, a(codes, cs, torch.uint8, "codes"),
+          a(scales, ss, torch.bfloat16, "scales"), a(dst, dst.shape, dst.dtype, "dst"),
+          stream=stream)
+    return dst
+
+
+def pack_int4_expert_weights(desc: LayerDesc, gate, up, down, stream=None):
+    """The three weight sets of a 4-bit forward, from (codes, scales) pairs in
+    the natural layout."""
+    return (zc_moe_int4_pack(desc, ZC_PACK_GATE_UP, *gate, stream=stream),
+            zc_moe_int4_pack(desc, ZC_PACK_GATE_UP, *up, stream=stream),
+            zc_moe_int4_pack(desc, ZC_PACK_DOWN, *down, stream=stream))
+
+
+def int4_expert_weights(desc: LayerDesc, w_gate, w_up, w_down, stream=None):
+    """The three weight sets of a 4-bit forward, quantized from bf16 weights."""
+    return tuple(zc_moe_int4_pack(desc, which, *zc_moe_int4_quantize(desc, which, w, stream=stream),
+                                  stream=stream)
+                 for w, which in ((w_gate, ZC_PACK_GATE_UP), (w_up, ZC_PACK_GATE_UP),
+                                  (w_down, ZC_PACK_DOWN)))
 
 
 @dataclass

@@ -1,0 +1,112 @@
+"""Host-side checks of the 4-bit weight calls and of zc_moe_experts, before any
+work is queued."""
+import ctypes as C
+
+import pytest
+import torch
+
+from moe_layer_zero_amd import zcmoe
+
+A = [C.c_void_p((i + 1) << 40) for i in range(20)]  # distinct, aligned, never dereferenced
+BF = torch.bfloat16
+
+
+def desc(G=128, **kw):
+    base = dict(T=64, d=256, N=8, Z=4, I=128, K=2, dtype=BF, weight_layout=zcmoe.int4_layout(G))
+    base.update(kw)
+    return zcmoe.LayerDesc(**base)
+
+
+def test_layouts_and_sizes():
+    L = zcmoe.lib()
+    for G in (32, 64, 128):
+        d = desc(G).c()
+        assert L.zc_moe_int4_weight_bytes(C.byref(d)) == 8 * 256 * 128 // 2 + 8 * 256 * 128 // G * 2
+        assert L.zc_moe_workspace_size(C.byref(d), zcmoe.ZC_OP_FORWARD) > 0
+    assert L.zc_moe_int4_weight_bytes(C.byref(desc(weight_layout=0).c())) == 0
+    with pytest.raises(ValueError):
+        zcmoe.int4_layout(16)
+    # the experts alone need no more than the forward
+    for lay in (0, 4):
+        d = desc(weight_layout=lay).c()
+        assert 0 < L.zc_moe_workspace_size(C.byref(d), zcmoe.ZC_OP_EXPERTS) <= \
+            L.zc_moe_workspace_size(C.byref(d), zcmoe.ZC_OP_FORWARD)
+
+
+@pytest.mark.parametrize("kw", [dict(dtype=torch.float32), dict(d=192), dict(I=64)])
+def test_unsupported_layers(kw):
+    L = zcmoe.lib()
+    d = desc(**kw).c()
+    assert L.zc_moe_int4_weight_bytes(C.byref(d)) == 0
+    assert L.zc_moe_int4_pack(C.byref(d), 0, A[0], A[1], A[2], None) == zcmoe.ZC_ERR_UNSUPPORTED
+    assert L.zc_moe_int4_quantize(C.byref(d), 0, A[0], A[1], A[2], None) == zcmoe.ZC_ERR_UNSUPPORTED
+
+
+def test_quantize_and_pack_arguments():
+    L = zcmoe.lib()
+    d = desc().c()
+    for f in (L.zc_moe_int4_pack, L.zc_moe_int4_quantize):
+        assert f(C.byref(d), 2, A[0], A[1], A[2], None) == zcmoe.ZC_ERR_INVALID
+        assert f(None, 0, A[0], A[1], A[2], None) == zcmoe.ZC_ERR_INVALID
+        for k in range(3):
+            a = [A[0], A[1], A[2]]
+            a[k] = None
+            assert f(C.byref(d), 0, *a, None) == zcmoe.ZC_ERR_INVALID
+        assert f(C.byref(d), 0, A[0], A[1], A[0], None) == zcmoe.ZC_ERR_INVALID
+        assert "overlap" in L.zc_last_error().decode()
+        row = desc(weight_layout=0).c()
+        assert f(C.byref(row), 0, A[0], A[1], A[2], None) == zcmoe.ZC_ERR_INVALID
+
+
+def test_int4_serves_inference_only():
+    L = zcmoe.lib()
+    d = desc().c()
+    r = zcmoe.zc_route_buf(*A[:7])
+    st = L.zc_moe_forward(C.byref(d), *A[7:14], C.byref(r), A[14], A[15], 1 << 39, None)
+    assert st == zcmoe.ZC_ERR_UNSUPPORTED and "row-major" in L.zc_last_error().decode()
+    st = L.zc_moe_backward(C.byref(d), *A[7:12], C.byref(r), *A[12:19], None, A[19], 1 << 39, None)
+    assert st == zcmoe.ZC_ERR_UNSUPPORTED
+
+
+def experts(d, ws_bytes=1 << 30, **over):
+    a = dict(x=A[7], wg=A[8], wu=A[9], wd=A[10], xc=None, xs=None, out=A[11], ws=A[12], r=True)
+    ro = dict(logits=None, topk_idx=A[0], topk_gate=A[1], counts=None, offsets=A[2], perm=A[3],
+              inv=A[4])
+    for k, v in over.items():
+        (a if k in a else ro)[k] = v
+    c, r = d.c(), zcmoe.zc_route_buf(**ro)
+    return zcmoe.lib().zc_moe_experts(C.byref(c), a["x"], C.byref(r) if a["r"] else None, a["wg"],
+                                      a["wu"], a["wd"], a["xc"], a["xs"], a["out"], a["ws"],
+                                      ws_bytes, None)
+
+
+def test_experts_arguments():
+    d = desc()
+    for k in ("x", "wg", "wu", "wd", "out", "r", "topk_idx", "topk_gate", "offsets", "perm", "inv"):
+        assert experts(d, **{k: None}) == zcmoe.ZC_ERR_INVALID, k
+    need = zcmoe.zc_moe_workspace_size(d, zcmoe.ZC_OP_EXPERTS)
+    assert experts(d, ws_bytes=need - 1) == zcmoe.ZC_ERR_WORKSPACE
+    assert experts(d, out=A[7]) == zcmoe.ZC_ERR_INVALID     # not in place
+    assert experts(d, ws=A[3]) == zcmoe.ZC_ERR_INVALID
+    # quantized rows come in pairs, with MXFP8 weights
+    assert experts(d, xc=A[13]) == zcmoe.ZC_ERR_INVALID
+    assert experts(d, xc=A[13], xs=A[14]) == zcmoe.ZC_ERR_INVALID
+    assert "MXFP8" in zcmoe.lib().zc_last_error().decode()
+    assert experts(desc(weight_layout=3)) == zcmoe.ZC_ERR_INVALID
+
+
+def test_bindings_reject():
+    d = desc()
+    w = torch.zeros((8, 128, 256), dtype=BF)
+    with pytest.raises(ValueError):      # host tensor
+        zcmoe.zc_moe_int4_quantize(d, zcmoe.ZC_PACK_GATE_UP, w)
+    with pytest.raises(ValueError):      # the other matrix' shape
+        zcmoe.zc_moe_int4_quantize(d, zcmoe.ZC_PACK_DOWN, w)
+    with pytest.raises(ValueError):      # a layout without groups
+        zcmoe.zc_moe_int4_quantize(desc(weight_layout=0), zcmoe.ZC_PACK_GATE_UP, w)
+    with pytest.raises(ValueError):      # too small a destination
+        zcmoe.zc_moe_int4_pack(d, 0, torch.zeros((8, 128, 128), dtype=torch.uint8),
+                               torch.zeros((8, 128, 2), dtype=BF), torch.zeros(16, dtype=torch.uint8))
+    with pytest.raises(ValueError):      # weights that are no 4-bit set
+        zcmoe.zc_moe_experts(d, torch.zeros((64, 256), dtype=BF), zcmoe.RouteBuffers(d, "cpu"), w, w,
+                             w, torch.zeros((64, 256), dtype=BF))
