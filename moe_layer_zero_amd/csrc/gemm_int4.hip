@@ -59,25 +59,37 @@ __device__ __forceinline__ float silu_f(float a) {
   return a * __builtin_amdgcn_rcpf(1.0f + __expf(-a));
 }
 
+// The lane number, taken anew for each tile: what is computed from it would
+// otherwise be moved out of the tile loop, and fill the registers for good.
+__device__ __forceinline__ int tile_lane() {
+  int lane = threadIdx.x & 63;
+  asm volatile("" : "+v"(lane));
+  return lane;
+}
+
+// Keeps the scaling of a group's sums where it is written: moved behind the
+// next loads, the sums of every column and group are live at once.
+__device__ __forceinline__ void settle(f32x4_t& v) { asm volatile("" : "+v"(v)); }
+
 // Eight codes -> 128 + q in bf16.
-__device__ __forceinline__ bf16x8_t codes_bf16(uint32_t w) {
+// (The two constants come in registers, one of them a vector one, so that
+// each pair is a shift and one and-or.)
+__device__ __forceinline__ bf16x8_t codes_bf16(uint32_t w, uint32_t mask, uint32_t exponent) {
   u32x4_t r;
 #pragma unroll
-  for (int p = 0; p < 4; ++p) r[p] = ((w >> (4 * p)) & 0x000f000fu) | 0x43004300u;
+  for (int p = 0; p < 4; ++p) r[p] = ((w >> (4 * p)) & mask) | exponent;
   return __builtin_bit_cast(bf16x8_t, r);
 }
 
 // RB blocks of 16 rows and NB blocks of 16 weight columns a workgroup (gate/up:
 // the first half of them gate, the second the matching up columns).
 template <int EPI, int RB, int NB, int G>
-__global__ __launch_bounds__(kThreads) void int4_kernel(I4Params p) {
+__global__ __launch_bounds__(kThreads, 2) void int4_kernel(I4Params p) {
   constexpr int NG = kStep / G;                             // groups of a code block
   constexpr int TG = 4 / NG;                                // MFMA steps of a group
   constexpr int OUT = (EPI == I4_SWIGLU ? NB / 2 : NB) * 16;  // output columns a workgroup
   constexpr int TM = 16 * RB;
-  const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int l16 = lane & 15, lq = lane >> 4;
 
   // Tiles are dealt to the 8 XCDs (workgroup b runs on XCD b mod 8) in
   // runs of consecutive ones, row tiles of a weight panel next to each other:
@@ -89,6 +101,7 @@ __global__ __launch_bounds__(kThreads) void int4_kernel(I4Params p) {
   for (int64_t in = blockIdx.x / 8; in < chunk; in += gridDim.x / 8) {
   const int64_t L = (blockIdx.x % 8) * chunk + in;
   if (L >= total) break;
+  const int lane = tile_lane(), l16 = lane & 15, lq = lane >> 4;
   const int e = ld_scalar(p.tile_exp + L / NT);
   const int mt0 = ld_scalar(p.mt_off + e);
   const int mte = ld_scalar(p.mt_off + e + 1) - mt0;
@@ -108,18 +121,17 @@ __global__ __launch_bounds__(kThreads) void int4_kernel(I4Params p) {
   }
   const int nkb = p.K / kStep;
   const int64_t mat = static_cast<int64_t>(p.ncols) * p.K;  // weights of one matrix
-  const u32x4_t* code[NB];
-  const bf16_t* scale[NB];
+  const uint8_t* code[NB];  // wave-uniform
+  const uint8_t* scale[NB];
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb) {
     const bool up = EPI == I4_SWIGLU && nb >= NB / 2;
     const uint8_t* base = up ? p.B2 : p.B;
     const int cb = nt * (OUT / 16) + (up ? nb - NB / 2 : nb);
-    code[nb] = reinterpret_cast<const u32x4_t*>(base + e * (mat / 2) +
-                                                static_cast<int64_t>(cb) * nkb * 1024) + lane;
-    scale[nb] = reinterpret_cast<const bf16_t*>(base + p.N * (mat / 2)) + e * (mat / G) +
-                (static_cast<int64_t>(cb) * nkb * 16 + l16) * NG;
+    code[nb] = base + e * (mat / 2) + static_cast<int64_t>(cb) * nkb * 1024;
+    scale[nb] = base + p.N * (mat / 2) + (e * (mat / G) + static_cast<int64_t>(cb) * nkb * 16 * NG) * 2;
   }
+  const uint32_t code_lane = lane * 16, scale_lane = l16 * NG * 2;
 
   struct Buf {
     u32x4_t b[NB];
@@ -128,10 +140,12 @@ __global__ __launch_bounds__(kThreads) void int4_kernel(I4Params p) {
   };
   auto load = [&](int kb, Buf& f) {
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb) f.b[nb] = __builtin_nontemporal_load(code[nb] + kb * 64);
+    for (int nb = 0; nb < NB; ++nb)
+      f.b[nb] = __builtin_nontemporal_load(
+          reinterpret_cast<const u32x4_t*>(code[nb] + kb * 1024 + code_lane));
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
-      __builtin_memcpy(f.s[nb], scale[nb] + static_cast<int64_t>(kb) * 16 * NG, 2 * NG);
+      __builtin_memcpy(f.s[nb], scale[nb] + kb * (32 * NG) + scale_lane, 2 * NG);
 #pragma unroll
     for (int rb = 0; rb < RB; ++rb)
 #pragma unroll
@@ -146,29 +160,28 @@ __global__ __launch_bounds__(kThreads) void int4_kernel(I4Params p) {
     for (int nb = 0; nb < NB; ++nb) acc[rb][nb] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   const u32x4_t off_bits = {0xc308c308u, 0xc308c308u, 0xc308c308u, 0xc308c308u};  // -136
   const bf16x8_t off = __builtin_bit_cast(bf16x8_t, off_bits);
+  uint32_t mask = 0x000f000fu, exponent = 0x43004300u;
+  asm volatile("" : "+s"(mask), "+v"(exponent));
 
   auto compute = [&](const Buf& f) {
-    f32x4_t start[RB][NG];
 #pragma unroll
-    for (int rb = 0; rb < RB; ++rb)
+    for (int g = 0; g < NG; ++g) {
+      f32x4_t start[RB];
 #pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        f32x4_t v = {0.f, 0.f, 0.f, 0.f};
+      for (int rb = 0; rb < RB; ++rb) {
+        start[rb] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int t = g * TG; t < (g + 1) * TG; ++t)
-          v = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f.a[rb][t], off, v, 0, 0, 0);
-        start[rb][g] = v;
+          start[rb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f.a[rb][t], off, start[rb], 0, 0, 0);
       }
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-      for (int g = 0; g < NG; ++g) {
+      for (int nb = 0; nb < NB; ++nb) {
         f32x4_t part[RB];
 #pragma unroll
-        for (int rb = 0; rb < RB; ++rb) part[rb] = start[rb][g];
+        for (int rb = 0; rb < RB; ++rb) part[rb] = start[rb];
 #pragma unroll
         for (int t = g * TG; t < (g + 1) * TG; ++t) {
-          const bf16x8_t w = codes_bf16(f.b[nb][t]);
+          const bf16x8_t w = codes_bf16(f.b[nb][t], mask, exponent);
 #pragma unroll
           for (int rb = 0; rb < RB; ++rb)
             part[rb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f.a[rb][t], w, part[rb], 0, 0, 0);
@@ -179,6 +192,11 @@ __global__ __launch_bounds__(kThreads) void int4_kernel(I4Params p) {
 #pragma unroll
           for (int v = 0; v < 4; ++v) acc[rb][nb][v] += s * part[rb][v];
       }
+#pragma unroll
+      for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) settle(acc[rb][nb]);
+    }
   };
 
   // this wavefront's share of the reduction, one block ahead in registers
@@ -226,6 +244,236 @@ __global__ __launch_bounds__(kThreads) void int4_kernel(I4Params p) {
       for (int nb = 0; nb < NB; ++nb) p.y[row + 16 * nb] = sum(rb, nb, wave);
     }
   }
+  }
+}
+
+// ------------------------------------------------------------- many rows
+// With more than some 32 rows an expert the matrix cores are what bounds the
+// products, and each decoded weight has to feed many rows.  A workgroup then
+// takes 64 or 128 rows and 256 weight columns over the whole reduction, a
+// wavefront 64 rows and 64 columns (gate/up: 32 gate and the matching 32 up
+// columns); 64 x 64 sums and as many of the group at hand fill half of a
+// SIMD's registers, so two wavefronts share it and one's vector work (codes
+// decoded, sums scaled) runs under the other's matrix steps.
+//  - The rows' 128-step slabs come through a ring of four LDS slots, copied
+//    by the loads themselves (16 bytes a lane, gathered rows); chunk c
+//    (16 bytes) of row r lies at chunk c ^ (r & 15), so the 16 lanes of a
+//    read phase hit 16 different bank groups.
+//  - The sums of -136 x that start each column's sum are shared out: a
+//    wavefront makes those of one row block for the next slab and leaves them
+//    in LDS, 1 matrix step beside 16.
+//  - A group's sums are scaled into the accumulators under the first step of
+//    the next group.
+// Loads return in issue order: when the codes of slab k have been used, the
+// rows of slab k + 2, issued before them, have landed.  So the barrier at the
+// head of slab k shows every wavefront slabs k and k + 1, and frees the slot of
+// slab k - 1 for slab k + 3.
+typedef __attribute__((address_space(3))) void lds_void;
+typedef __attribute__((address_space(1))) const void global_void;
+__device__ __forceinline__ void copy_to_lds16(const void* src, lds_void* dst) {
+  __builtin_amdgcn_global_load_lds((global_void*)src, dst, 16, 0, 0);
+}
+constexpr int kAllLoads = 0x0f70;  // s_waitcnt vmcnt(0)
+// Keeps the LDS reads of one matrix step behind the step before: hoisted
+// together, a slab's fragments do not fit the registers.
+__device__ __forceinline__ void step_end() { asm volatile("" ::: "memory"); }
+// Barrier for LDS alone: loads stay in flight.
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0)
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// WR groups of 64 rows a workgroup, four wavefronts each.
+template <int EPI, int WR, int G>
+__global__ __launch_bounds__(kThreads * WR, 2) void int4_wide_kernel(I4Params p) {
+  constexpr int RB = 4, NB = 4, NG = kStep / G, TG = 4 / NG;
+  constexpr int TM = 64 * WR;
+  constexpr int SLOT = TM * kStep;  // bf16 of a ring slot
+  constexpr int OUT = EPI == I4_SWIGLU ? 128 : 256;
+  constexpr int CP = 4;             // copies a wavefront and slab: 4 rows each
+  __shared__ __align__(16) bf16_t ring[4 * SLOT];
+  __shared__ f32x4_t s_start[2 * NG * (TM / 4)];  // [slab parity][group][row / 4]
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int rw = wave >> 2, cw = wave & 3;  // row group, column group
+  const int nkb = p.K / kStep;
+  const int NT = (p.ncols + OUT - 1) / OUT;
+  const int64_t total = static_cast<int64_t>(ld_scalar(p.mt_off + p.N)) * NT;
+  const int64_t chunk = (total + 7) / 8;
+  for (int64_t in = blockIdx.x / 8; in < chunk; in += gridDim.x / 8) {
+    const int64_t L = (blockIdx.x % 8) * chunk + in;
+    if (L >= total) break;
+    const int lane = tile_lane(), l16 = lane & 15, lq = lane >> 4;
+    const int e = ld_scalar(p.tile_exp + L / NT);
+    const int mt0 = ld_scalar(p.mt_off + e);
+    const int mte = ld_scalar(p.mt_off + e + 1) - mt0;
+    const int q = static_cast<int>(L - static_cast<int64_t>(mt0) * NT);
+    const int nt = q / mte;
+    const int seg1 = ld_scalar(p.offsets + e + 1);
+    const int m0 = ld_scalar(p.offsets + e) + TM * (q % mte);
+    const int mcount = min(TM, seg1 - m0);
+
+    // copies: instruction i of this wavefront fills rows 4 (CP wave + i) + lq
+    const bf16_t* src[CP];
+#pragma unroll
+    for (int i = 0; i < CP; ++i) {
+      const int r = 4 * (CP * wave + i) + lq;
+      const int row = m0 + min(r, mcount - 1);  // past the tile: its last row again
+      const int tok = EPI == I4_SWIGLU ? p.perm[row] / p.kdiv : row;
+      src[i] = p.A + static_cast<int64_t>(tok) * p.K + 8 * (l16 ^ (r & 15));
+    }
+    auto copy = [&](int kb) {
+#pragma unroll
+      for (int i = 0; i < CP; ++i)
+        copy_to_lds16(src[i] + kb * kStep,
+                      (lds_void*)(ring + (kb & 3) * SLOT + 4 * (CP * wave + i) * kStep));
+    };
+
+    // this wavefront's columns; past the matrix (the last tile of a width that
+    // is no multiple of 256) its last ones again, not stored
+    const int64_t mat = static_cast<int64_t>(p.ncols) * p.K;
+    const uint8_t* code[NB];  // wave-uniform
+    const uint8_t* scale[NB];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+      const bool up = EPI == I4_SWIGLU && nb >= NB / 2;
+      const uint8_t* base = up ? p.B2 : p.B;
+      const int cb = EPI == I4_SWIGLU ? nt * 8 + 2 * cw + (nb & 1)
+                                      : min(nt * 16 + 4 * cw + nb, p.ncols / 16 - 1);
+      code[nb] = base + e * (mat / 2) + static_cast<int64_t>(cb) * nkb * 1024;
+      scale[nb] =
+          base + p.N * (mat / 2) + (e * (mat / G) + static_cast<int64_t>(cb) * nkb * 16 * NG) * 2;
+    }
+    const uint32_t code_lane = lane * 16, scale_lane = l16 * NG * 2;
+    struct Buf {
+      u32x4_t b[NB];
+      bf16_t s[NB][NG];
+    };
+    auto load = [&](int kb, Buf& f) {
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+        f.b[nb] = *reinterpret_cast<const u32x4_t*>(code[nb] + kb * 1024 + code_lane);
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+        __builtin_memcpy(f.s[nb], scale[nb] + kb * (32 * NG) + scale_lane, 2 * NG);
+    };
+
+    const u32x4_t off_bits = {0xc308c308u, 0xc308c308u, 0xc308c308u, 0xc308c308u};  // -136
+    const bf16x8_t off = __builtin_bit_cast(bf16x8_t, off_bits);
+  uint32_t mask = 0x000f000fu, exponent = 0x43004300u;
+  asm volatile("" : "+s"(mask), "+v"(exponent));
+    auto frag = [&](int kb, int rb, int t) {  // row block rb of the whole tile
+      return *reinterpret_cast<const bf16x8_t*>(ring + (kb & 3) * SLOT + (16 * rb + l16) * kStep +
+                                                8 * ((4 * t + lq) ^ l16));
+    };
+    // Sums of -136 x over slab kb's groups, of row block `wave` of the tile
+    auto starts = [&](int kb) {
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        f32x4_t v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int t = g * TG; t < (g + 1) * TG; ++t)
+          v = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag(kb, wave, t), off, v, 0, 0, 0);
+        if (l16 == 0) s_start[((kb & 1) * NG + g) * (TM / 4) + 4 * wave + lq] = v;
+      }
+    };
+
+    f32x4_t acc[RB][NB], part[RB][NB];
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb) acc[rb][nb] = part[rb][nb] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    float sp[NB] = {0.f, 0.f, 0.f, 0.f};  // scales of the group in part
+
+    auto compute = [&](int kb, const Buf& f) {
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        bf16x8_t a[RB];
+#pragma unroll
+        for (int rb = 0; rb < RB; ++rb) a[rb] = frag(kb, RB * rw + rb, t);
+        const bool first = t % TG == 0;
+        f32x4_t st[RB];
+        if (first) {
+#pragma unroll
+          for (int rb = 0; rb < RB; ++rb)
+            st[rb] = s_start[((kb & 1) * NG + t / TG) * (TM / 4) + 4 * (RB * rw + rb) + lq];
+        }
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+          const bf16x8_t w = codes_bf16(f.b[nb][t], mask, exponent);
+#pragma unroll
+          for (int rb = 0; rb < RB; ++rb) {
+            if (first) {
+#pragma unroll
+              for (int v = 0; v < 4; ++v) acc[rb][nb][v] += sp[nb] * part[rb][nb][v];
+              part[rb][nb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[rb], w, st[rb], 0, 0, 0);
+            } else {
+              part[rb][nb] =
+                  __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[rb], w, part[rb][nb], 0, 0, 0);
+            }
+          }
+          if (first) sp[nb] = bf2f(f.s[nb][t / TG]);
+        }
+        if (first) {
+#pragma unroll
+          for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) settle(acc[rb][nb]);
+        }
+        step_end();
+      }
+    };
+
+    Buf f0, f1;
+    lds_barrier();  // the ring is free: the previous tile's reads are done
+    copy(0);
+    if (nkb > 1) copy(1);
+    if (nkb > 2) copy(2);
+    load(0, f0);
+    __builtin_amdgcn_s_waitcnt(kAllLoads);
+    lds_barrier();
+    starts(0);
+    const bool rows = 64 * rw < mcount;  // this row group holds rows
+    auto slab = [&](int kb, const Buf& cur, Buf& next) {
+      if (kb + 2 >= nkb) __builtin_amdgcn_s_waitcnt(kAllLoads);  // no younger loads used before
+      lds_barrier();
+      if (kb + 3 < nkb) copy(kb + 3);
+      if (kb + 1 < nkb) {
+        load(kb + 1, next);
+        starts(kb + 1);
+      }
+      if (rows) compute(kb, cur);
+    };
+    int kb = 0;
+    for (; kb + 2 <= nkb; kb += 2) {
+      slab(kb, f0, f1);
+      slab(kb + 1, f1, f0);
+    }
+    if (kb < nkb) slab(kb, f0, f1);
+
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) acc[rb][nb][v] += sp[nb] * part[rb][nb][v];
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        const int r = 16 * (RB * rw + rb) + 4 * lq + v;
+        if (r >= mcount) continue;
+        const int64_t row = (static_cast<int64_t>(m0) + r) * p.ncols + nt * OUT + l16;
+        if constexpr (EPI == I4_SWIGLU) {
+#pragma unroll
+          for (int nb = 0; nb < 2; ++nb)
+            p.h[row + 32 * cw + 16 * nb] = f2bf(silu_f(acc[rb][nb][v]) * acc[rb][nb + 2][v]);
+        } else if (nt * OUT + 64 * cw < p.ncols) {
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) p.y[row + 64 * cw + 16 * nb] = acc[rb][nb][v];
+        }
+      }
   }
 }
 
@@ -329,12 +577,26 @@ hipError_t launch_int4(const I4Params& p, int G, int64_t rows, hipStream_t s) {
   return hipGetLastError();
 }
 
+template <int EPI, int WR>
+hipError_t launch_int4_wide(const I4Params& p, int G, int64_t rows, hipStream_t s) {
+  constexpr int OUT = EPI == I4_SWIGLU ? 128 : 256;
+  const int64_t tiles = int4_max_tiles(rows, p.N, 64 * WR) * ((p.ncols + OUT - 1) / OUT);
+  const dim3 grid(grid_of((tiles + 7) / 8 * 8)), block(kThreads * WR);
+  if (G == 32)
+    hipLaunchKernelGGL((int4_wide_kernel<EPI, WR, 32>), grid, block, 0, s, p);
+  else if (G == 64)
+    hipLaunchKernelGGL((int4_wide_kernel<EPI, WR, 64>), grid, block, 0, s, p);
+  else
+    hipLaunchKernelGGL((int4_wide_kernel<EPI, WR, 128>), grid, block, 0, s, p);
+  return hipGetLastError();
+}
+
 }  // namespace
 
 int int4_rows_per_tile(int64_t avg_rows) {
   if (avg_rows <= 12) return 16;
-  if (avg_rows <= 40) return 32;
-  return 64;
+  if (avg_rows <= 32) return 32;
+  return avg_rows <= 64 ? 64 : 128;
 }
 
 hipError_t launch_int4_gateup(const bf16_t* x, const uint8_t* wg, const uint8_t* wu, int G,
@@ -347,7 +609,8 @@ hipError_t launch_int4_gateup(const bf16_t* x, const uint8_t* wg, const uint8_t*
   p.A = x; p.perm = perm; p.kdiv = K; p.B = wg; p.B2 = wu; p.h = h;
   if (tm == 16) return launch_int4<I4_SWIGLU, 1, 4>(p, G, rows, s);
   if (tm == 32) return launch_int4<I4_SWIGLU, 2, 4>(p, G, rows, s);
-  return launch_int4<I4_SWIGLU, 4, 4>(p, G, rows, s);
+  if (tm == 64) return launch_int4_wide<I4_SWIGLU, 1>(p, G, rows, s);
+  return launch_int4_wide<I4_SWIGLU, 2>(p, G, rows, s);
 }
 
 hipError_t launch_int4_down(const bf16_t* h, const uint8_t* wd, int G, const int32_t* offsets,
@@ -358,8 +621,9 @@ hipError_t launch_int4_down(const bf16_t* h, const uint8_t* wd, int G, const int
   p.offsets = offsets; p.mt_off = mt_off; p.tile_exp = tile_exp;
   p.A = h; p.kdiv = 1; p.B = wd; p.y = y;
   if (tm == 16) return launch_int4<I4_STORE, 1, 8>(p, G, rows, s);
-  if (tm == 32) return launch_int4<I4_STORE, 2, 8>(p, G, rows, s);
-  return launch_int4<I4_STORE, 4, 4>(p, G, rows, s);
+  if (tm == 32) return launch_int4<I4_STORE, 2, 4>(p, G, rows, s);
+  if (tm == 64) return launch_int4_wide<I4_STORE, 1>(p, G, rows, s);
+  return launch_int4_wide<I4_STORE, 2>(p, G, rows, s);
 }
 
 hipError_t launch_int4_pack(const uint8_t* codes, const bf16_t* scales, uint8_t* dst, int64_t nmat,

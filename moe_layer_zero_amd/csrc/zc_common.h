@@ -321,8 +321,8 @@ hipError_t launch_fwdq_down(const uint8_t* hq, const uint8_t* hs, int64_t rows,
 
 // Expert GEMMs on 4-bit weights with group scales (gemm_int4.hip): group
 // size G of 32, 64 or 128, d and I multiples of 128.  Tile tables as for the
-// packed kernels, with tm = int4_rows_per_tile(T*K/N) rows a tile (16, 32 or
-// 64); rows = T*K bounds the picks.  y is fp32 [P][d].
+// packed kernels, with tm = int4_rows_per_tile(T*K/N) rows a tile (16, 32, 64
+// or 128); rows = T*K bounds the picks.  y is fp32 [P][d].
 int int4_rows_per_tile(int64_t avg_rows);
 hipError_t launch_int4_gateup(const bf16_t* x, const uint8_t* wg, const uint8_t* wu, int G,
                               const int32_t* offsets, const int32_t* perm, const int32_t* mt_off,
