@@ -242,10 +242,8 @@ struct RouteWs {
   void* dispatch;
 };
 // Row tiles of the second prefix, at most: every FFN pick in a tile of its
-// own expert, tiles at least 32 rows high (16 with 4-bit weights).
-int64_t max_tiles2(const zc_moe_desc* d) {
-  return d->T * d->K / (int4_group(d) ? 16 : 32) + d->N + 1;
-}
+// own expert, tiles at least 32 rows high.
+int64_t max_tiles2(const zc_moe_desc* d) { return d->T * d->K / 32 + d->N + 1; }
 int64_t rpart_bytes(const zc_moe_desc* d) {
   const int64_t E = d->N + d->Z;
   const int s = zc::router_gemm_splits(d->T, E, d->d);
@@ -300,6 +298,7 @@ int64_t fwd_ws_bytes(const zc_moe_desc* d) {
   const int64_t ys = int4_group(d) ? 4 : es;
   int64_t b = route_ws_bytes(d) + a256(rows * d->I * es) + a256(rows * d->d * ys);
   if (d->weight_layout == ZC_WEIGHTS_MXFP8) b += a256(d->T * d->d) + a256(d->T * d->d / 32);
+  if (int4_group(d)) b += a256(zc::int4_tiles_bytes(rows, d->N));
   return b;
 }
 
@@ -458,8 +457,7 @@ bool use_dense_router(const zc_moe_desc* d) {
 // kernels of gemm_rmw.hip likewise but at least 64 rows, the other row-major
 // bf16 forward kernels use 256.
 int fwd_rows_per_tile(const zc_moe_desc* d) {
-  if (d->N == 0) return zc::kFwdBM;
-  if (int4_group(d)) return zc::int4_rows_per_tile(d->T * d->K / d->N);
+  if (d->N == 0 || int4_group(d)) return zc::kFwdBM;  // (4-bit layers list their own tiles)
   const int tm = zc::fwdp_rows_per_tile(d->T * d->K / d->N);
   if (d->weight_layout != ZC_WEIGHTS_ROWMAJOR) return tm;
   return rmw_layer(d) ? (tm < 64 ? 64 : tm) : zc::kFwdBM;
@@ -543,18 +541,21 @@ zc_status do_experts(const zc_moe_desc* d, const T* x, const T* wg, const T* wu,
     } else if (const int G = int4_group(d)) {
       // 4-bit weights (validated: bf16, no saved buffer); y is fp32
       float* yf = reinterpret_cast<float*>(y);
-      const int tm = fwd_rows_per_tile(d);
+      void* tiles = ws + fwd_ws_bytes(d) - a256(zc::int4_tiles_bytes(rows, N));
+      // (picks spread over all N + Z experts)
+      const int tm = zc::int4_rows_per_tile(rows / (d->N + d->Z), d->T, rows, d->d, d->I);
+      ZC_LAUNCH(ZC_PH_TILE_OFFSETS, zc::launch_int4_tiles(r->offsets, N, tm, tiles, s),
+                "tile list launch");
       ZC_LAUNCH(ZC_PH_GATE_UP,
-                zc::launch_int4_gateup(reinterpret_cast<const bf16_t*>(x),
+                zc::launch_int4_gateup(reinterpret_cast<const bf16_t*>(x), d->T,
                                        reinterpret_cast<const uint8_t*>(wg),
-                                       reinterpret_cast<const uint8_t*>(wu), G, r->offsets, r->perm,
-                                       rw.tile_off2, rw.tile_exp, tm, rows, N, I, dd, K,
-                                       reinterpret_cast<bf16_t*>(h), s),
+                                       reinterpret_cast<const uint8_t*>(wu), G, tiles, r->perm, tm,
+                                       rows, N, I, dd, K, reinterpret_cast<bf16_t*>(h), s),
                 "gate/up GEMM launch");
       ZC_LAUNCH(ZC_PH_DOWN,
                 zc::launch_int4_down(reinterpret_cast<const bf16_t*>(h),
-                                     reinterpret_cast<const uint8_t*>(wd), G, r->offsets,
-                                     rw.tile_off2, rw.tile_exp, tm, rows, N, I, dd, yf, s),
+                                     reinterpret_cast<const uint8_t*>(wd), G, tiles, tm, rows, N, I,
+                                     dd, yf, s),
                 "down GEMM launch");
     } else if (d->weight_layout == ZC_WEIGHTS_PACKED) {
       // bf16 inference on packed weights (validated: bf16, no saved buffer)
@@ -645,7 +646,7 @@ zc_status do_routed_experts(const zc_moe_desc* d, const T* x, const T* wg, const
                             char* ws, hipStream_t s) {
   const RouteWs rw = carve_route(ws, d);
   const int N = static_cast<int>(d->N);
-  if (N > 0 && d->T > 0)
+  if (N > 0 && d->T > 0 && !int4_group(d))
     ZC_LAUNCH(ZC_PH_TILE_OFFSETS,
               zc::launch_tile_offsets2(r->offsets, N, zc::kGemmBM, rw.tile_off,
                                        fwd_rows_per_tile(d), rw.tile_off2, rw.tile_exp, rw.sched,

@@ -41,18 +41,27 @@ constexpr int kStep = 128;  // reduction steps of a code block
 
 enum { I4_SWIGLU = 0, I4_STORE = 1 };
 
+// What a workgroup has to know of its row tile, in one load: the expert, the
+// first of the expert's row tiles and their number, its first row and the end
+// of its rows.
+struct __align__(32) Tile {
+  int32_t e, mt0, mte, seg0, seg1, pad[3];
+};
+static_assert(sizeof(Tile) == kInt4TileBytes, "the workspace holds them");
+
 struct I4Params {
   int N, ncols, K;          // experts, output columns (I or d), reduction length (d or I)
-  const int32_t* offsets;   // [N+1] rows of each expert in dispatch order
-  const int32_t* mt_off;    // [N+1] prefix of ceil(rows / tile height)
-  const int32_t* tile_exp;  // expert of each row tile
+  const int32_t* total;     // number of row tiles
+  const Tile* tiles;        // one of each (as many as the grid has row tiles)
   const bf16_t* A;          // x [T][d] gathered through perm, or h [P][I]
+  uint32_t a_bytes;         // its size where 31 bits hold it
   const int32_t* perm;      // gate/up only
   int kdiv;                 // K of the layer (slot -> token)
   const uint8_t* B;         // W_g or W_d
   const uint8_t* B2;        // W_u (gate/up)
   bf16_t* h;                // gate/up output [P][I]
   float* y;                 // down output [P][d]
+  int64_t per_xcd;          // tiles of an XCD, at most
 };
 
 __device__ __forceinline__ float silu_f(float a) {
@@ -67,9 +76,61 @@ __device__ __forceinline__ int tile_lane() {
   return lane;
 }
 
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ u32x4_t load16(__amdgpu_buffer_rsrc_t r, uint32_t voff, int soff) {
+  return __builtin_amdgcn_raw_buffer_load_b128(r, voff, soff, 0);
+}
+
+// The bf16 scales of one column's NG groups of a code block, in whole registers:
+// with one group a lane loads the word that holds its column's scale and its
+// neighbour's (a 16-bit load is widened where it lands, so it would be waited
+// for a slab early).
+template <int NG>
+struct Scales {
+  uint32_t w[(NG + 1) / 2];
+  static __device__ __forceinline__ uint32_t lane_offset(int column) {
+    return NG == 1 ? (column & ~1) * 2 : column * NG * 2;
+  }
+  __device__ __forceinline__ void load(const uint8_t* p) {
+    constexpr int n = NG == 1 ? 4 : 2 * NG;
+    __builtin_memcpy(w, __builtin_assume_aligned(p, n), n);
+  }
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t voff, int soff) {
+    if constexpr (NG == 4) {
+      const u32x2_t v = __builtin_amdgcn_raw_buffer_load_b64(r, voff, soff, 0);
+      w[0] = v[0];
+      w[1] = v[1];
+    } else {
+      w[0] = __builtin_amdgcn_raw_buffer_load_b32(r, voff, soff, 0);
+    }
+  }
+  // upper: 16 where the lane's column is even, else 0 (one group)
+  __device__ __forceinline__ float get(int g, int upper) const {
+    const uint32_t v = NG == 1 ? w[0] << upper : g & 1 ? w[g / 2] : w[g / 2] << 16;
+    return __uint_as_float(v & 0xffff0000u);
+  }
+};
+
 // Keeps the scaling of a group's sums where it is written: moved behind the
 // next loads, the sums of every column and group are live at once.
 __device__ __forceinline__ void settle(f32x4_t& v) { asm volatile("" : "+v"(v)); }
+
+// A wave-uniform read of a table written before this kernel, as scalar loads.
+__device__ __forceinline__ Tile ld_tile(const Tile* t) {
+  typedef int32_t i32x8_t __attribute__((ext_vector_type(8)));
+  const i32x8_t v = *(const __attribute__((address_space(4))) i32x8_t*)t;
+  return Tile{v[0], v[1], v[2], v[3], v[4], {0, 0, 0}};
+}
+
+// Tile number of the in-th tile of XCD x: runs of kRun consecutive tiles are
+// dealt to the 8 XCDs (workgroup b runs on XCD b mod 8), so that the row
+// tiles of a weight panel, next to each other, read it from one L2.  (By
+// the number of tiles alone: a workgroup's record and the count of tiles
+// are loaded together.)
+constexpr int kRun = 8;
+__device__ __forceinline__ int64_t tile_of(int x, int64_t in) {
+  return (in / kRun * 8 + x) * kRun + in % kRun;
+}
 
 // Eight codes -> 128 + q in bf16.
 // (The two constants come in registers, one of them a vector one, so that
@@ -91,25 +152,20 @@ __global__ __launch_bounds__(kThreads, 2) void int4_kernel(I4Params p) {
   constexpr int TM = 16 * RB;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 
-  // Tiles are dealt to the 8 XCDs (workgroup b runs on XCD b mod 8) in
-  // runs of consecutive ones, row tiles of a weight panel next to each other:
-  // they read it from one L2.
   const int NT = p.ncols / OUT;
-  const int64_t total = static_cast<int64_t>(ld_scalar(p.mt_off + p.N)) * NT;
-  const int64_t chunk = (total + 7) / 8;
+  const int64_t total = static_cast<int64_t>(ld_scalar(p.total)) * NT;
   __shared__ float s_acc[kWaves][RB * NB * 4][64];
-  for (int64_t in = blockIdx.x / 8; in < chunk; in += gridDim.x / 8) {
-  const int64_t L = (blockIdx.x % 8) * chunk + in;
+  for (int64_t in = blockIdx.x / 8;; in += gridDim.x / 8) {
+  const int64_t L = tile_of(blockIdx.x % 8, in);
+  if (in >= p.per_xcd) break;
+  const Tile tile = ld_tile(p.tiles + L / NT);
   if (L >= total) break;
   const int lane = tile_lane(), l16 = lane & 15, lq = lane >> 4;
-  const int e = ld_scalar(p.tile_exp + L / NT);
-  const int mt0 = ld_scalar(p.mt_off + e);
-  const int mte = ld_scalar(p.mt_off + e + 1) - mt0;
-  const int q = static_cast<int>(L - static_cast<int64_t>(mt0) * NT);
-  const int nt = q / mte;
-  const int seg1 = ld_scalar(p.offsets + e + 1);
-  const int m0 = ld_scalar(p.offsets + e) + TM * (q % mte);
-  const int mcount = min(TM, seg1 - m0);
+  const int e = tile.e;
+  const int q = static_cast<int>(L - static_cast<int64_t>(tile.mt0) * NT);
+  const int nt = q / tile.mte;
+  const int m0 = tile.seg0 + TM * (q % tile.mte);
+  const int mcount = min(TM, tile.seg1 - m0);
 
   // this lane's piece of its rows; rows past the tile read its last row again
   const bf16_t* arow[RB];
@@ -131,11 +187,12 @@ __global__ __launch_bounds__(kThreads, 2) void int4_kernel(I4Params p) {
     code[nb] = base + e * (mat / 2) + static_cast<int64_t>(cb) * nkb * 1024;
     scale[nb] = base + p.N * (mat / 2) + (e * (mat / G) + static_cast<int64_t>(cb) * nkb * 16 * NG) * 2;
   }
-  const uint32_t code_lane = lane * 16, scale_lane = l16 * NG * 2;
+  const uint32_t code_lane = lane * 16, scale_lane = Scales<NG>::lane_offset(l16);
+  const int upper = l16 & 1 ? 0 : 16;
 
   struct Buf {
     u32x4_t b[NB];
-    bf16_t s[NB][NG];
+    Scales<NG> s[NB];
     bf16x8_t a[RB][4];
   };
   auto load = [&](int kb, Buf& f) {
@@ -145,7 +202,7 @@ __global__ __launch_bounds__(kThreads, 2) void int4_kernel(I4Params p) {
           reinterpret_cast<const u32x4_t*>(code[nb] + kb * 1024 + code_lane));
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
-      __builtin_memcpy(f.s[nb], scale[nb] + kb * (32 * NG) + scale_lane, 2 * NG);
+      f.s[nb].load(scale[nb] + kb * (32 * NG) + scale_lane);
 #pragma unroll
     for (int rb = 0; rb < RB; ++rb)
 #pragma unroll
@@ -186,7 +243,7 @@ __global__ __launch_bounds__(kThreads, 2) void int4_kernel(I4Params p) {
           for (int rb = 0; rb < RB; ++rb)
             part[rb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f.a[rb][t], w, part[rb], 0, 0, 0);
         }
-        const float s = bf2f(f.s[nb][g]);
+        const float s = f.s[nb].get(g, upper);
 #pragma unroll
         for (int rb = 0; rb < RB; ++rb)
 #pragma unroll
@@ -250,11 +307,11 @@ __global__ __launch_bounds__(kThreads, 2) void int4_kernel(I4Params p) {
 // ------------------------------------------------------------- many rows
 // With more than some 32 rows an expert the matrix cores are what bounds the
 // products, and each decoded weight has to feed many rows.  A workgroup then
-// takes 64 or 128 rows and 256 weight columns over the whole reduction, a
+// takes 64 rows and 256 weight columns over the whole reduction, a
 // wavefront 64 rows and 64 columns (gate/up: 32 gate and the matching 32 up
 // columns); 64 x 64 sums and as many of the group at hand fill half of a
-// SIMD's registers, so two wavefronts share it and one's vector work (codes
-// decoded, sums scaled) runs under the other's matrix steps.
+// SIMD's registers, so two workgroups share a CU and one's vector work (codes
+// decoded, sums scaled), copies and stores run under the other's matrix steps.
 //  - The rows' 128-step slabs come through a ring of four LDS slots, copied
 //    by the loads themselves (16 bytes a lane, gathered rows); chunk c
 //    (16 bytes) of row r lies at chunk c ^ (r & 15), so the 16 lanes of a
@@ -262,18 +319,23 @@ __global__ __launch_bounds__(kThreads, 2) void int4_kernel(I4Params p) {
 //  - The sums of -136 x that start each column's sum are shared out: a
 //    wavefront makes those of one row block for the next slab and leaves them
 //    in LDS, 1 matrix step beside 16.
-//  - A group's sums are scaled into the accumulators under the first step of
-//    the next group.
-// Loads return in issue order: when the codes of slab k have been used, the
-// rows of slab k + 2, issued before them, have landed.  So the barrier at the
-// head of slab k shows every wavefront slabs k and k + 1, and frees the slot of
-// slab k - 1 for slab k + 3.
+//  - A group's sums are scaled into the accumulators column block by column
+//    block, behind the matrix steps of the next one.
+// Each slab issues the copies of the slab three ahead and the codes of the next.
+// Loads return in issue order, so where slab k waits until only the issues of
+// slab k - 1 are in flight, the rows of slab k + 1 have landed; the barrier
+// then shows them to every wavefront, and frees the slot of slab k - 1 for
+// slab k + 3.
 typedef __attribute__((address_space(3))) void lds_void;
-typedef __attribute__((address_space(1))) const void global_void;
-__device__ __forceinline__ void copy_to_lds16(const void* src, lds_void* dst) {
-  __builtin_amdgcn_global_load_lds((global_void*)src, dst, 16, 0, 0);
+// (A buffer load: the compiler would have every LDS read wait for all copies in
+// flight if they were global loads into LDS.)
+__device__ __forceinline__ void copy_to_lds16(__amdgpu_buffer_rsrc_t r, lds_void* dst,
+                                              uint32_t voff, int soff) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, dst, 16, voff, soff, 0, 0);
 }
-constexpr int kAllLoads = 0x0f70;  // s_waitcnt vmcnt(0)
+// s_waitcnt immediate for "vmcnt <= n" (expcnt and lgkmcnt not waited)
+constexpr int vmcnt_imm(int n) { return 0x0f70 | (n & 15) | ((n >> 4) << 14); }
+constexpr int kAllLoads = vmcnt_imm(0);
 // Keeps the LDS reads of one matrix step behind the step before: hoisted
 // together, a slab's fragments do not fit the registers.
 __device__ __forceinline__ void step_end() { asm volatile("" ::: "memory"); }
@@ -285,78 +347,86 @@ __device__ __forceinline__ void lds_barrier() {
   asm volatile("" ::: "memory");
 }
 
-// WR groups of 64 rows a workgroup, four wavefronts each.
-template <int EPI, int WR, int G>
-__global__ __launch_bounds__(kThreads * WR, 2) void int4_wide_kernel(I4Params p) {
+template <int EPI, int G>
+__global__ __launch_bounds__(kThreads, 2) void int4_wide_kernel(I4Params p) {
   constexpr int RB = 4, NB = 4, NG = kStep / G, TG = 4 / NG;
-  constexpr int TM = 64 * WR;
+  constexpr int TM = 16 * RB;
   constexpr int SLOT = TM * kStep;  // bf16 of a ring slot
   constexpr int OUT = EPI == I4_SWIGLU ? 128 : 256;
   constexpr int CP = 4;             // copies a wavefront and slab: 4 rows each
-  __shared__ __align__(16) bf16_t ring[4 * SLOT];
-  __shared__ f32x4_t s_start[2 * NG * (TM / 4)];  // [slab parity][group][row / 4]
+  // the ring, then the starts [slab parity][group][row / 4] (one LDS object: with
+  // two, the compiler has LDS reads wait for copies in flight)
+  constexpr int kStartWords = 2 * NG * (TM / 4) * 8;  // bf16 of LDS they take
+  __shared__ __align__(16) bf16_t ring[4 * SLOT + 2 * kStartWords + 256 * 8];
+  f32x4_t* const s_start = reinterpret_cast<f32x4_t*>(ring + 4 * SLOT);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int rw = wave >> 2, cw = wave & 3;  // row group, column group
   const int nkb = p.K / kStep;
   const int NT = (p.ncols + OUT - 1) / OUT;
-  const int64_t total = static_cast<int64_t>(ld_scalar(p.mt_off + p.N)) * NT;
-  const int64_t chunk = (total + 7) / 8;
-  for (int64_t in = blockIdx.x / 8; in < chunk; in += gridDim.x / 8) {
-    const int64_t L = (blockIdx.x % 8) * chunk + in;
+  const __amdgpu_buffer_rsrc_t rows = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<bf16_t*>(p.A), (short)0, p.a_bytes, 0x00020000);
+  const int64_t total = static_cast<int64_t>(ld_scalar(p.total)) * NT;
+  for (int64_t in = blockIdx.x / 8;; in += gridDim.x / 8) {
+    const int64_t L = tile_of(blockIdx.x % 8, in);
+    if (in >= p.per_xcd) break;
+    const Tile tile = ld_tile(p.tiles + L / NT);
     if (L >= total) break;
     const int lane = tile_lane(), l16 = lane & 15, lq = lane >> 4;
-    const int e = ld_scalar(p.tile_exp + L / NT);
-    const int mt0 = ld_scalar(p.mt_off + e);
-    const int mte = ld_scalar(p.mt_off + e + 1) - mt0;
-    const int q = static_cast<int>(L - static_cast<int64_t>(mt0) * NT);
-    const int nt = q / mte;
-    const int seg1 = ld_scalar(p.offsets + e + 1);
-    const int m0 = ld_scalar(p.offsets + e) + TM * (q % mte);
-    const int mcount = min(TM, seg1 - m0);
+    const int e = tile.e;
+    const int q = static_cast<int>(L - static_cast<int64_t>(tile.mt0) * NT);
+    const int nt = q / tile.mte;
+    const int m0 = tile.seg0 + TM * (q % tile.mte);
+    const int mcount = min(TM, tile.seg1 - m0);
 
     // copies: instruction i of this wavefront fills rows 4 (CP wave + i) + lq
-    const bf16_t* src[CP];
+    // (rows past the tile with its last row); byte offsets fit 31 bits, the
+    // launch made sure
+    uint32_t src[CP];
 #pragma unroll
     for (int i = 0; i < CP; ++i) {
       const int r = 4 * (CP * wave + i) + lq;
-      const int row = m0 + min(r, mcount - 1);  // past the tile: its last row again
+      const int row = m0 + min(r, mcount - 1);
       const int tok = EPI == I4_SWIGLU ? p.perm[row] / p.kdiv : row;
-      src[i] = p.A + static_cast<int64_t>(tok) * p.K + 8 * (l16 ^ (r & 15));
+      src[i] = (static_cast<uint32_t>(tok) * static_cast<uint32_t>(p.K) + 8 * (l16 ^ (r & 15))) * 2;
     }
-    auto copy = [&](int kb) {
+    auto copy = [&](int kb, int slot) {
 #pragma unroll
       for (int i = 0; i < CP; ++i)
-        copy_to_lds16(src[i] + kb * kStep,
-                      (lds_void*)(ring + (kb & 3) * SLOT + 4 * (CP * wave + i) * kStep));
+        copy_to_lds16(rows, (lds_void*)(ring + (slot & 3) * SLOT + 4 * (CP * wave + i) * kStep),
+                      src[i], kb * (2 * kStep));
     };
 
     // this wavefront's columns; past the matrix (the last tile of a width that
-    // is no multiple of 256) its last ones again, not stored
+    // is no multiple of 256) its last ones again, not stored.  Loaded through
+    // buffer resources: a base, a scalar offset and one lane offset, where
+    // eight pairs of address registers would not fit.
     const int64_t mat = static_cast<int64_t>(p.ncols) * p.K;
-    const uint8_t* code[NB];  // wave-uniform
-    const uint8_t* scale[NB];
+    __amdgpu_buffer_rsrc_t codes[2], scales[2];  // gate (or down) and up
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-      const bool up = EPI == I4_SWIGLU && nb >= NB / 2;
-      const uint8_t* base = up ? p.B2 : p.B;
-      const int cb = EPI == I4_SWIGLU ? nt * 8 + 2 * cw + (nb & 1)
-                                      : min(nt * 16 + 4 * cw + nb, p.ncols / 16 - 1);
-      code[nb] = base + e * (mat / 2) + static_cast<int64_t>(cb) * nkb * 1024;
-      scale[nb] =
-          base + p.N * (mat / 2) + (e * (mat / G) + static_cast<int64_t>(cb) * nkb * 16 * NG) * 2;
+    for (int m = 0; m < 2; ++m) {
+      uint8_t* base = const_cast<uint8_t*>(EPI == I4_SWIGLU && m ? p.B2 : p.B);
+      codes[m] = __builtin_amdgcn_make_buffer_rsrc(base + e * (mat / 2), (short)0, 0xffffffffu,
+                                                   0x00020000);
+      scales[m] = __builtin_amdgcn_make_buffer_rsrc(base + p.N * (mat / 2) + e * (mat / G) * 2,
+                                                    (short)0, 0xffffffffu, 0x00020000);
     }
-    const uint32_t code_lane = lane * 16, scale_lane = l16 * NG * 2;
+    uint32_t col[NB];  // first code block of each column block
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+      col[nb] = (EPI == I4_SWIGLU ? nt * 8 + 2 * wave + (nb & 1)
+                                  : min(nt * 16 + 4 * wave + nb, p.ncols / 16 - 1)) * nkb;
+    const uint32_t code_lane = lane * 16, scale_lane = Scales<NG>::lane_offset(l16);
+    const int upper = l16 & 1 ? 0 : 16;
     struct Buf {
       u32x4_t b[NB];
-      bf16_t s[NB][NG];
+      Scales<NG> s[NB];
     };
     auto load = [&](int kb, Buf& f) {
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
-        f.b[nb] = *reinterpret_cast<const u32x4_t*>(code[nb] + kb * 1024 + code_lane);
+        f.b[nb] = load16(codes[EPI == I4_SWIGLU ? nb / 2 : 0], code_lane, (col[nb] + kb) * 1024);
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
-        __builtin_memcpy(f.s[nb], scale[nb] + kb * (32 * NG) + scale_lane, 2 * NG);
+        f.s[nb].load(scales[EPI == I4_SWIGLU ? nb / 2 : 0], scale_lane, (col[nb] + kb) * (32 * NG));
     };
 
     const u32x4_t off_bits = {0xc308c308u, 0xc308c308u, 0xc308c308u, 0xc308c308u};  // -136
@@ -367,7 +437,12 @@ __global__ __launch_bounds__(kThreads * WR, 2) void int4_wide_kernel(I4Params p)
       return *reinterpret_cast<const bf16x8_t*>(ring + (kb & 3) * SLOT + (16 * rb + l16) * kStep +
                                                 8 * ((4 * t + lq) ^ l16));
     };
-    // Sums of -136 x over slab kb's groups, of row block `wave` of the tile
+    // Sums of -136 x over slab kb's groups, of row block `wave` of the tile (past
+    // the last slab: of what the slot holds, and unused).  The 16 lanes of a
+    // row quad hold the same sums: the first leaves them in LDS, the others write
+    // to a place of their own that nobody reads (no branch).
+    bf16_t* const start_out =
+        ring + 4 * SLOT + 8 * (l16 == 0 ? 4 * wave + lq : kStartWords / 8 + (threadIdx.x & 255));
     auto starts = [&](int kb) {
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
@@ -375,75 +450,78 @@ __global__ __launch_bounds__(kThreads * WR, 2) void int4_wide_kernel(I4Params p)
 #pragma unroll
         for (int t = g * TG; t < (g + 1) * TG; ++t)
           v = __builtin_amdgcn_mfma_f32_16x16x32_bf16(frag(kb, wave, t), off, v, 0, 0, 0);
-        if (l16 == 0) s_start[((kb & 1) * NG + g) * (TM / 4) + 4 * wave + lq] = v;
+        *reinterpret_cast<f32x4_t*>(start_out + ((kb & 1) * NG + g) * (TM / 4) * 8) = v;
       }
     };
 
-    f32x4_t acc[RB][NB], part[RB][NB];
+    f32x4_t acc[RB][NB];
 #pragma unroll
     for (int rb = 0; rb < RB; ++rb)
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb) acc[rb][nb] = part[rb][nb] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    float sp[NB] = {0.f, 0.f, 0.f, 0.f};  // scales of the group in part
+      for (int nb = 0; nb < NB; ++nb) acc[rb][nb] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
+    // Slab kb.  A column block's group sums are scaled into the accumulators
+    // behind the last matrix steps of the next column block.
     auto compute = [&](int kb, const Buf& f) {
+      f32x4_t part[RB][NB];
+      auto fold = [&](int nb, int g) {
+        const float s = f.s[nb].get(g, upper);
+#pragma unroll
+        for (int rb = 0; rb < RB; ++rb) {
+#pragma unroll
+          for (int v = 0; v < 4; ++v) acc[rb][nb][v] += s * part[rb][nb][v];
+          settle(acc[rb][nb]);
+        }
+      };
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
+        const int g = t / TG;
+        const bool first = t % TG == 0, last = t % TG == TG - 1;
         bf16x8_t a[RB];
 #pragma unroll
-        for (int rb = 0; rb < RB; ++rb) a[rb] = frag(kb, RB * rw + rb, t);
-        const bool first = t % TG == 0;
+        for (int rb = 0; rb < RB; ++rb) a[rb] = frag(kb, rb, t);
         f32x4_t st[RB];
         if (first) {
 #pragma unroll
           for (int rb = 0; rb < RB; ++rb)
-            st[rb] = s_start[((kb & 1) * NG + t / TG) * (TM / 4) + 4 * (RB * rw + rb) + lq];
+            st[rb] = s_start[((kb & 1) * NG + g) * (TM / 4) + 4 * rb + lq];
         }
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
           const bf16x8_t w = codes_bf16(f.b[nb][t], mask, exponent);
 #pragma unroll
-          for (int rb = 0; rb < RB; ++rb) {
-            if (first) {
-#pragma unroll
-              for (int v = 0; v < 4; ++v) acc[rb][nb][v] += sp[nb] * part[rb][nb][v];
-              part[rb][nb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[rb], w, st[rb], 0, 0, 0);
-            } else {
-              part[rb][nb] =
-                  __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[rb], w, part[rb][nb], 0, 0, 0);
-            }
-          }
-          if (first) sp[nb] = bf2f(f.s[nb][t / TG]);
-        }
-        if (first) {
-#pragma unroll
           for (int rb = 0; rb < RB; ++rb)
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb) settle(acc[rb][nb]);
+            part[rb][nb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                a[rb], w, first ? st[rb] : part[rb][nb], 0, 0, 0);
+          if (last && nb > 0) fold(nb - 1, g);
         }
+        if (last) fold(NB - 1, g);
         step_end();
       }
     };
 
     Buf f0, f1;
     lds_barrier();  // the ring is free: the previous tile's reads are done
-    copy(0);
-    if (nkb > 1) copy(1);
-    if (nkb > 2) copy(2);
+    const int last = nkb - 1;
+    copy(0, 0);
+    copy(min(1, last), 1);
+    copy(min(2, last), 2);
     load(0, f0);
     __builtin_amdgcn_s_waitcnt(kAllLoads);
     lds_barrier();
     starts(0);
-    const bool rows = 64 * rw < mcount;  // this row group holds rows
+    // Slab kb.  No branch in it: past the end the last slab is copied and
+    // loaded again, so that the number of loads in flight is known.
     auto slab = [&](int kb, const Buf& cur, Buf& next) {
-      if (kb + 2 >= nkb) __builtin_amdgcn_s_waitcnt(kAllLoads);  // no younger loads used before
+      // slab kb + 1 has landed: younger are only the copies and loads of the slab
+      // before this one
+      __builtin_amdgcn_s_waitcnt(vmcnt_imm(CP + 2 * NB));
       lds_barrier();
-      if (kb + 3 < nkb) copy(kb + 3);
-      if (kb + 1 < nkb) {
-        load(kb + 1, next);
-        starts(kb + 1);
-      }
-      if (rows) compute(kb, cur);
+      copy(min(kb + 3, last), kb + 3);
+      load(min(kb + 1, last), next);
+      __builtin_amdgcn_sched_barrier(0);
+      starts(kb + 1);
+      compute(kb, cur);
     };
     int kb = 0;
     for (; kb + 2 <= nkb; kb += 2) {
@@ -451,27 +529,22 @@ __global__ __launch_bounds__(kThreads * WR, 2) void int4_wide_kernel(I4Params p)
       slab(kb + 1, f1, f0);
     }
     if (kb < nkb) slab(kb, f0, f1);
+    __builtin_amdgcn_s_waitcnt(kAllLoads);  // no copy of this tile lands in the next one's ring
 
 #pragma unroll
     for (int rb = 0; rb < RB; ++rb)
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-        for (int v = 0; v < 4; ++v) acc[rb][nb][v] += sp[nb] * part[rb][nb][v];
-#pragma unroll
-    for (int rb = 0; rb < RB; ++rb)
-#pragma unroll
       for (int v = 0; v < 4; ++v) {
-        const int r = 16 * (RB * rw + rb) + 4 * lq + v;
+        const int r = 16 * rb + 4 * lq + v;
         if (r >= mcount) continue;
         const int64_t row = (static_cast<int64_t>(m0) + r) * p.ncols + nt * OUT + l16;
         if constexpr (EPI == I4_SWIGLU) {
 #pragma unroll
           for (int nb = 0; nb < 2; ++nb)
-            p.h[row + 32 * cw + 16 * nb] = f2bf(silu_f(acc[rb][nb][v]) * acc[rb][nb + 2][v]);
-        } else if (nt * OUT + 64 * cw < p.ncols) {
+            p.h[row + 32 * wave + 16 * nb] = f2bf(silu_f(acc[rb][nb][v]) * acc[rb][nb + 2][v]);
+        } else if (nt * OUT + 64 * wave < p.ncols) {
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb) p.y[row + 64 * cw + 16 * nb] = acc[rb][nb][v];
+          for (int nb = 0; nb < NB; ++nb) p.y[row + 64 * wave + 16 * nb] = acc[rb][nb][v];
         }
       }
   }
@@ -557,73 +630,114 @@ unsigned grid_of(int64_t blocks) {
   return static_cast<unsigned>(blocks < kMaxGrid ? blocks : kMaxGrid);
 }
 
-// At most this many row tiles of height tm: every one of the rows' experts has
-// one ragged tile.
-int64_t int4_max_tiles(int64_t rows, int64_t N, int tm) {
-  return rows / tm + (rows < N ? rows : N);
+// The records of the row tiles of height tm, in expert order, and their number.
+// One workgroup: inclusive scan of the experts' tile counts by wavefront, then
+// over the 16 wavefronts' sums.
+__global__ __launch_bounds__(kMaxExperts) void int4_tiles_kernel(
+    const int32_t* __restrict__ offsets, int N, int tm, int32_t* __restrict__ total,
+    Tile* __restrict__ tiles) {
+  __shared__ int32_t s_sum[kMaxExperts / 64];
+  const int e = threadIdx.x, lane = e & 63, wave = e >> 6;
+  const int lo = e < N ? offsets[e] : 0, hi = e < N ? offsets[e + 1] : 0;
+  const int n = (hi - lo + tm - 1) / tm;
+  int scan = n;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int v = __shfl_up(scan, o);
+    if (lane >= o) scan += v;
+  }
+  if (lane == 63) s_sum[wave] = scan;
+  __syncthreads();
+  int first = scan - n;
+  for (int w = 0; w < wave; ++w) first += s_sum[w];
+  if (e == kMaxExperts - 1) *total = first + n;
+  Tile t{e, first, n, lo, hi, {0, 0, 0}};
+  for (int i = 0; i < n; ++i) tiles[first + i] = t;
 }
 
+// At most this many column tiles of OUT columns by row tiles of height tm; the
+// row tiles rounded up so that the runs of tile_of stay inside the records.
+template <typename K>
+hipError_t launch_tiles(K kernel32, K kernel64, K kernel128, I4Params p, int G, int64_t rows, int tm,
+                        int OUT, hipStream_t s) {
+  const int64_t NT = (p.ncols + OUT - 1) / OUT;
+  const int64_t most = int4_max_tiles(rows, p.N, tm) * NT;
+  const int64_t runs = (most + 8 * kRun - 1) / (8 * kRun);
+  p.per_xcd = runs * kRun;
+  const dim3 grid(grid_of(p.per_xcd * 8)), block(kThreads);
+  hipLaunchKernelGGL(G == 32 ? kernel32 : G == 64 ? kernel64 : kernel128, grid, block, 0, s, p);
+  return hipGetLastError();
+}
 template <int EPI, int RB, int NB>
 hipError_t launch_int4(const I4Params& p, int G, int64_t rows, hipStream_t s) {
-  constexpr int OUT = (EPI == I4_SWIGLU ? NB / 2 : NB) * 16;
-  const int64_t tiles = int4_max_tiles(rows, p.N, 16 * RB) * (p.ncols / OUT);
-  const dim3 grid(grid_of((tiles + 7) / 8 * 8)), block(kThreads);
-  if (G == 32)
-    hipLaunchKernelGGL((int4_kernel<EPI, RB, NB, 32>), grid, block, 0, s, p);
-  else if (G == 64)
-    hipLaunchKernelGGL((int4_kernel<EPI, RB, NB, 64>), grid, block, 0, s, p);
-  else
-    hipLaunchKernelGGL((int4_kernel<EPI, RB, NB, 128>), grid, block, 0, s, p);
-  return hipGetLastError();
+  return launch_tiles(int4_kernel<EPI, RB, NB, 32>, int4_kernel<EPI, RB, NB, 64>,
+                      int4_kernel<EPI, RB, NB, 128>, p, G, rows, 16 * RB,
+                      (EPI == I4_SWIGLU ? NB / 2 : NB) * 16, s);
 }
-
-template <int EPI, int WR>
+template <int EPI>
 hipError_t launch_int4_wide(const I4Params& p, int G, int64_t rows, hipStream_t s) {
-  constexpr int OUT = EPI == I4_SWIGLU ? 128 : 256;
-  const int64_t tiles = int4_max_tiles(rows, p.N, 64 * WR) * ((p.ncols + OUT - 1) / OUT);
-  const dim3 grid(grid_of((tiles + 7) / 8 * 8)), block(kThreads * WR);
-  if (G == 32)
-    hipLaunchKernelGGL((int4_wide_kernel<EPI, WR, 32>), grid, block, 0, s, p);
-  else if (G == 64)
-    hipLaunchKernelGGL((int4_wide_kernel<EPI, WR, 64>), grid, block, 0, s, p);
-  else
-    hipLaunchKernelGGL((int4_wide_kernel<EPI, WR, 128>), grid, block, 0, s, p);
-  return hipGetLastError();
+  return launch_tiles(int4_wide_kernel<EPI, 32>, int4_wide_kernel<EPI, 64>,
+                      int4_wide_kernel<EPI, 128>, p, G, rows, 64, EPI == I4_SWIGLU ? 128 : 256, s);
 }
 
 }  // namespace
 
-int int4_rows_per_tile(int64_t avg_rows) {
-  if (avg_rows <= 12) return 16;
-  if (avg_rows <= 32) return 32;
-  return avg_rows <= 64 ? 64 : 128;
+int int4_rows_per_tile(int64_t avg_rows, int64_t Tn, int64_t rows, int64_t d, int64_t I) {
+  if (avg_rows <= 13) return 16;
+  // (the 64-row kernel takes byte offsets of 31 bits into x, h and a matrix)
+  const int64_t limit = int64_t(1) << 30;
+  if (avg_rows <= 20 || Tn * d >= limit || rows * I >= limit || d * I >= limit) return 32;
+  return 64;
 }
 
-hipError_t launch_int4_gateup(const bf16_t* x, const uint8_t* wg, const uint8_t* wu, int G,
-                              const int32_t* offsets, const int32_t* perm, const int32_t* mt_off,
-                              const int32_t* tile_exp, int tm, int64_t rows, int N, int I, int d,
-                              int K, bf16_t* h, hipStream_t s) {
+// Row tiles of height tm at most: every one of the rows' experts has one ragged
+// tile.
+int64_t int4_max_tiles(int64_t rows, int64_t N, int tm) {
+  return rows / tm + (rows < N ? rows : N);
+}
+// Bytes of their records and count.  tile_of reaches up to 8 kRun - 1 column
+// tiles, so fewer than 8 kRun row tiles, past the last.
+int64_t int4_tiles_bytes(int64_t rows, int64_t N) {
+  return kInt4TileBytes * (1 + int4_max_tiles(rows, N, 16) + 8 * kRun);
+}
+
+hipError_t launch_int4_tiles(const int32_t* offsets, int N, int tm, void* tiles, hipStream_t s) {
+  hipLaunchKernelGGL(int4_tiles_kernel, dim3(1), dim3(kMaxExperts), 0, s, offsets, N, tm,
+                     static_cast<int32_t*>(tiles), static_cast<Tile*>(tiles) + 1);
+  return hipGetLastError();
+}
+
+hipError_t launch_int4_gateup(const bf16_t* x, int64_t Tn, const uint8_t* wg, const uint8_t* wu,
+                              int G, const void* tiles, const int32_t* perm, int tm, int64_t rows,
+                              int N, int I, int d, int K, bf16_t* h, hipStream_t s) {
   I4Params p{};
   p.N = N; p.ncols = I; p.K = d;
-  p.offsets = offsets; p.mt_off = mt_off; p.tile_exp = tile_exp;
-  p.A = x; p.perm = perm; p.kdiv = K; p.B = wg; p.B2 = wu; p.h = h;
+  p.total = static_cast<const int32_t*>(tiles);
+  p.tiles = static_cast<const Tile*>(tiles) + 1;
+  p.A = x; p.a_bytes = static_cast<uint32_t>(Tn * d * 2); p.perm = perm; p.kdiv = K;
+  p.B = wg; p.B2 = wu; p.h = h;
+  // 16-row tiles: 32 columns of h a workgroup, 16 where that gives too few
+  // workgroups to fill the card
+  if (tm == 16 && int4_max_tiles(rows, N, 16) * (I / 32) < 1024)
+    return launch_int4<I4_SWIGLU, 1, 2>(p, G, rows, s);
   if (tm == 16) return launch_int4<I4_SWIGLU, 1, 4>(p, G, rows, s);
   if (tm == 32) return launch_int4<I4_SWIGLU, 2, 4>(p, G, rows, s);
-  if (tm == 64) return launch_int4_wide<I4_SWIGLU, 1>(p, G, rows, s);
-  return launch_int4_wide<I4_SWIGLU, 2>(p, G, rows, s);
+  return launch_int4_wide<I4_SWIGLU>(p, G, rows, s);
 }
 
-hipError_t launch_int4_down(const bf16_t* h, const uint8_t* wd, int G, const int32_t* offsets,
-                            const int32_t* mt_off, const int32_t* tile_exp, int tm, int64_t rows,
-                            int N, int I, int d, float* y, hipStream_t s) {
+hipError_t launch_int4_down(const bf16_t* h, const uint8_t* wd, int G, const void* tiles, int tm,
+                            int64_t rows, int N, int I, int d, float* y, hipStream_t s) {
   I4Params p{};
   p.N = N; p.ncols = d; p.K = I;
-  p.offsets = offsets; p.mt_off = mt_off; p.tile_exp = tile_exp;
-  p.A = h; p.kdiv = 1; p.B = wd; p.y = y;
+  p.total = static_cast<const int32_t*>(tiles);
+  p.tiles = static_cast<const Tile*>(tiles) + 1;
+  p.A = h; p.a_bytes = static_cast<uint32_t>(rows * I * 2); p.kdiv = 1; p.B = wd; p.y = y;
+  // 16-row tiles: 128 columns of y a workgroup, 64 where that gives too few
+  if (tm == 16 && int4_max_tiles(rows, N, 16) * (d / 128) < 4096)
+    return launch_int4<I4_STORE, 1, 4>(p, G, rows, s);
   if (tm == 16) return launch_int4<I4_STORE, 1, 8>(p, G, rows, s);
   if (tm == 32) return launch_int4<I4_STORE, 2, 4>(p, G, rows, s);
-  if (tm == 64) return launch_int4_wide<I4_STORE, 1>(p, G, rows, s);
-  return launch_int4_wide<I4_STORE, 2>(p, G, rows, s);
+  return launch_int4_wide<I4_STORE>(p, G, rows, s);
 }
 
 hipError_t launch_int4_pack(const uint8_t* codes, const bf16_t* scales, uint8_t* dst, int64_t nmat,

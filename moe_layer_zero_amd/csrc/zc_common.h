@@ -320,17 +320,20 @@ hipError_t launch_fwdq_down(const uint8_t* hq, const uint8_t* hs, int64_t rows,
                             bf16_t* y, int cu, hipStream_t s);
 
 // Expert GEMMs on 4-bit weights with group scales (gemm_int4.hip): group
-// size G of 32, 64 or 128, d and I multiples of 128.  Tile tables as for the
-// packed kernels, with tm = int4_rows_per_tile(T*K/N) rows a tile (16, 32, 64
-// or 128); rows = T*K bounds the picks.  y is fp32 [P][d].
-int int4_rows_per_tile(int64_t avg_rows);
-hipError_t launch_int4_gateup(const bf16_t* x, const uint8_t* wg, const uint8_t* wu, int G,
-                              const int32_t* offsets, const int32_t* perm, const int32_t* mt_off,
-                              const int32_t* tile_exp, int tm, int64_t rows, int N, int I, int d,
-                              int K, bf16_t* h, hipStream_t s);
-hipError_t launch_int4_down(const bf16_t* h, const uint8_t* wd, int G, const int32_t* offsets,
-                            const int32_t* mt_off, const int32_t* tile_exp, int tm, int64_t rows,
-                            int N, int I, int d, float* y, hipStream_t s);
+// size G of 32, 64 or 128, d and I multiples of 128.  launch_int4_tiles lists
+// the row tiles, tm = int4_rows_per_tile(...) rows each (16, 32 or 64, by the
+// average rows an expert), in tiles: int4_tiles_bytes(rows, N) bytes, 32-byte
+// aligned.  rows = T*K bounds the picks.  y is fp32 [P][d].
+constexpr int64_t kInt4TileBytes = 32;
+int int4_rows_per_tile(int64_t avg_rows, int64_t Tn, int64_t rows, int64_t d, int64_t I);
+int64_t int4_max_tiles(int64_t rows, int64_t N, int tm);
+int64_t int4_tiles_bytes(int64_t rows, int64_t N);
+hipError_t launch_int4_tiles(const int32_t* offsets, int N, int tm, void* tiles, hipStream_t s);
+hipError_t launch_int4_gateup(const bf16_t* x, int64_t Tn, const uint8_t* wg, const uint8_t* wu,
+                              int G, const void* tiles, const int32_t* perm, int tm, int64_t rows,
+                              int N, int I, int d, int K, bf16_t* h, hipStream_t s);
+hipError_t launch_int4_down(const bf16_t* h, const uint8_t* wd, int G, const void* tiles, int tm,
+                            int64_t rows, int N, int I, int d, float* y, hipStream_t s);
 // nmat [R][C] matrices: natural codes and scales -> the kernels' order; bf16
 // -> natural codes and scales.
 hipError_t launch_int4_pack(const uint8_t* codes, const bf16_t* scales, uint8_t* dst, int64_t nmat,
