@@ -62,6 +62,7 @@ struct I4Params {
   bf16_t* h;                // gate/up output [P][I]
   float* y;                 // down output [P][d]
   int64_t per_xcd;          // tiles of an XCD, at most
+  int log_run;              // runs of consecutive tiles on one XCD
 };
 
 __device__ __forceinline__ float silu_f(float a) {
@@ -122,14 +123,14 @@ __device__ __forceinline__ Tile ld_tile(const Tile* t) {
   return Tile{v[0], v[1], v[2], v[3], v[4], {0, 0, 0}};
 }
 
-// Tile number of the in-th tile of XCD x: runs of kRun consecutive tiles are
-// dealt to the 8 XCDs (workgroup b runs on XCD b mod 8), so that the row
-// tiles of a weight panel, next to each other, read it from one L2.  (By
-// the number of tiles alone: a workgroup's record and the count of tiles
-// are loaded together.)
-constexpr int kRun = 8;
-__device__ __forceinline__ int64_t tile_of(int x, int64_t in) {
-  return (in / kRun * 8 + x) * kRun + in % kRun;
+// Tile number of the in-th tile of XCD x: runs of 2^log_run consecutive tiles
+// are dealt to the 8 XCDs (workgroup b runs on XCD b mod 8), so that the row
+// tiles of a weight panel, next to each other, read it from one L2.  (Without
+// the number of tiles: a workgroup's record and that number are loaded
+// together.)
+constexpr int kMaxLogRun = 6;
+__device__ __forceinline__ int64_t tile_of(int x, int64_t in, int log_run) {
+  return (((in >> log_run) * 8 + x) << log_run) + (in & ((1 << log_run) - 1));
 }
 
 // Eight codes -> 128 + q in bf16.
@@ -156,7 +157,7 @@ __global__ __launch_bounds__(kThreads, 2) void int4_kernel(I4Params p) {
   const int64_t total = static_cast<int64_t>(ld_scalar(p.total)) * NT;
   __shared__ float s_acc[kWaves][RB * NB * 4][64];
   for (int64_t in = blockIdx.x / 8;; in += gridDim.x / 8) {
-  const int64_t L = tile_of(blockIdx.x % 8, in);
+  const int64_t L = tile_of(blockIdx.x % 8, in, p.log_run);
   if (in >= p.per_xcd) break;
   const Tile tile = ld_tile(p.tiles + L / NT);
   if (L >= total) break;
@@ -366,7 +367,7 @@ __global__ __launch_bounds__(kThreads, 2) void int4_wide_kernel(I4Params p) {
       const_cast<bf16_t*>(p.A), (short)0, p.a_bytes, 0x00020000);
   const int64_t total = static_cast<int64_t>(ld_scalar(p.total)) * NT;
   for (int64_t in = blockIdx.x / 8;; in += gridDim.x / 8) {
-    const int64_t L = tile_of(blockIdx.x % 8, in);
+    const int64_t L = tile_of(blockIdx.x % 8, in, p.log_run);
     if (in >= p.per_xcd) break;
     const Tile tile = ld_tile(p.tiles + L / NT);
     if (L >= total) break;
@@ -662,8 +663,11 @@ hipError_t launch_tiles(K kernel32, K kernel64, K kernel128, I4Params p, int G, 
                         int OUT, hipStream_t s) {
   const int64_t NT = (p.ncols + OUT - 1) / OUT;
   const int64_t most = int4_max_tiles(rows, p.N, tm) * NT;
-  const int64_t runs = (most + 8 * kRun - 1) / (8 * kRun);
-  p.per_xcd = runs * kRun;
+  // runs of 8 tiles, longer ones while every XCD has at least 32 of them
+  p.log_run = 3;
+  while (p.log_run < kMaxLogRun && (most >> p.log_run) >= 8 * 64) ++p.log_run;
+  const int64_t round = int64_t(8) << p.log_run;
+  p.per_xcd = (most + round - 1) / round << p.log_run;
   const dim3 grid(grid_of(p.per_xcd * 8)), block(kThreads);
   hipLaunchKernelGGL(G == 32 ? kernel32 : G == 64 ? kernel64 : kernel128, grid, block, 0, s, p);
   return hipGetLastError();
@@ -695,10 +699,10 @@ int int4_rows_per_tile(int64_t avg_rows, int64_t Tn, int64_t rows, int64_t d, in
 int64_t int4_max_tiles(int64_t rows, int64_t N, int tm) {
   return rows / tm + (rows < N ? rows : N);
 }
-// Bytes of their records and count.  tile_of reaches up to 8 kRun - 1 column
-// tiles, so fewer than 8 kRun row tiles, past the last.
+// Bytes of their records and count.  tile_of reaches fewer than 8 runs of column
+// tiles, so fewer row tiles than that, past the last.
 int64_t int4_tiles_bytes(int64_t rows, int64_t N) {
-  return kInt4TileBytes * (1 + int4_max_tiles(rows, N, 16) + 8 * kRun);
+  return kInt4TileBytes * (1 + int4_max_tiles(rows, N, 16) + (8 << kMaxLogRun));
 }
 
 hipError_t launch_int4_tiles(const int32_t* offsets, int N, int tm, void* tiles, hipStream_t s) {
