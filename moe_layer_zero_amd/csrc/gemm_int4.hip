@@ -69,6 +69,11 @@ __device__ __forceinline__ float silu_f(float a) {
   return a * __builtin_amdgcn_rcpf(1.0f + __expf(-a));
 }
 
+// Keeps memory reads in the order written (the LDS reads of one matrix step
+// behind the step before: hoisted together, a slab's fragments do not fit the
+// registers).
+__device__ __forceinline__ void step_end() { asm volatile("" ::: "memory"); }
+
 // The lane number, taken anew for each tile: what is computed from it would
 // otherwise be moved out of the tile loop, and fill the registers for good.
 __device__ __forceinline__ int tile_lane() {
@@ -168,13 +173,12 @@ __global__ __launch_bounds__(kThreads, 2) void int4_kernel(I4Params p) {
   const int m0 = tile.seg0 + TM * (q % tile.mte);
   const int mcount = min(TM, tile.seg1 - m0);
 
-  // this lane's piece of its rows; rows past the tile read its last row again
-  const bf16_t* arow[RB];
+  // this lane's rows; rows past the tile read its last row again
+  int src[RB];
 #pragma unroll
   for (int rb = 0; rb < RB; ++rb) {
-    const int row = m0 + min(16 * rb + l16, mcount - 1);
-    const int src = EPI == I4_SWIGLU ? p.perm[row] / p.kdiv : row;
-    arow[rb] = p.A + static_cast<int64_t>(src) * p.K + 8 * lq;
+    src[rb] = m0 + min(16 * rb + l16, mcount - 1);
+    if (EPI == I4_SWIGLU) src[rb] = p.perm[src[rb]];
   }
   const int nkb = p.K / kStep;
   const int64_t mat = static_cast<int64_t>(p.ncols) * p.K;  // weights of one matrix
@@ -196,7 +200,8 @@ __global__ __launch_bounds__(kThreads, 2) void int4_kernel(I4Params p) {
     Scales<NG> s[NB];
     bf16x8_t a[RB][4];
   };
-  auto load = [&](int kb, Buf& f) {
+  const bf16_t* arow[RB];
+  auto load_codes = [&](int kb, Buf& f) {
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
       f.b[nb] = __builtin_nontemporal_load(
@@ -204,11 +209,17 @@ __global__ __launch_bounds__(kThreads, 2) void int4_kernel(I4Params p) {
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
       f.s[nb].load(scale[nb] + kb * (32 * NG) + scale_lane);
+  };
+  auto load_rows = [&](int kb, Buf& f) {
 #pragma unroll
     for (int rb = 0; rb < RB; ++rb)
 #pragma unroll
       for (int t = 0; t < 4; ++t)
         f.a[rb][t] = *reinterpret_cast<const bf16x8_t*>(arow[rb] + kb * kStep + 32 * t);
+  };
+  auto load = [&](int kb, Buf& f) {
+    load_codes(kb, f);
+    load_rows(kb, f);
   };
 
   f32x4_t acc[RB][NB];
@@ -261,7 +272,13 @@ __global__ __launch_bounds__(kThreads, 2) void int4_kernel(I4Params p) {
   const int kb0 = nkb * wave / kWaves, kb1 = nkb * (wave + 1) / kWaves;
   if (kb0 < kb1) {
     Buf f0, f1;
-    load(kb0, f0);
+    // the first codes are under way before the rows' tokens are known
+    load_codes(kb0, f0);
+    step_end();
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb)
+      arow[rb] = p.A + static_cast<int64_t>(EPI == I4_SWIGLU ? src[rb] / p.kdiv : src[rb]) * p.K + 8 * lq;
+    load_rows(kb0, f0);
     int kb = kb0;
     for (; kb + 2 <= kb1; kb += 2) {
       load(kb + 1, f1);
@@ -337,9 +354,6 @@ __device__ __forceinline__ void copy_to_lds16(__amdgpu_buffer_rsrc_t r, lds_void
 // s_waitcnt immediate for "vmcnt <= n" (expcnt and lgkmcnt not waited)
 constexpr int vmcnt_imm(int n) { return 0x0f70 | (n & 15) | ((n >> 4) << 14); }
 constexpr int kAllLoads = vmcnt_imm(0);
-// Keeps the LDS reads of one matrix step behind the step before: hoisted
-// together, a slab's fragments do not fit the registers.
-__device__ __forceinline__ void step_end() { asm volatile("" ::: "memory"); }
 // Barrier for LDS alone: loads stay in flight.
 __device__ __forceinline__ void lds_barrier() {
   asm volatile("" ::: "memory");
