@@ -206,7 +206,8 @@ zc_status zc_moe_experts(const zc_moe_desc* desc, const void* x, const zc_route_
  * the first call with that device current).  Layers whose
  * zc_moe_workspace_size(desc, ZC_OP_FORWARD) exceeds it are rejected with
  * ZC_ERR_WORKSPACE before anything is queued; the LongCat-Flash layer at a
- * 256-token decode batch (57 MB) fits.  The caller still owns x, the
+ * 256-token decode batch (57 MB) fits (with 4-bit weights, whose expert
+ * outputs are fp32, at 128 tokens).  The caller still owns x, the
  * weights, out and r, with the same contract as zc_moe_forward.  Every call
  * on a GPU shares that GPU's scratch: calls that overlap on one GPU (other
  * streams, other threads) race and give undefined results; calls queued on
@@ -292,7 +293,7 @@ zc_status zc_moe_lb_loss(const zc_moe_desc* desc, const zc_lb_cfg* lb,
  * is overwritten.  Only logits and topk_idx of r are read; a pick outside
  * 0..E-1 counts nowhere.  Offsets outside 0..T are clamped; with descending
  * ones the results mean nothing, but no access leaves its buffer.  1 <= S <=
- * 2^20.  No output may overlap an input or another output.
+ * 2^20, T <= 2^25.  No output may overlap an input or another output.
  * ws: zc_moe_seq_balance_workspace_size(desc, S) bytes. */
 size_t zc_moe_seq_balance_workspace_size(const zc_moe_desc* desc, int64_t S);
 zc_status zc_moe_seq_balance(const zc_moe_desc* desc, const zc_lb_cfg* lb, const zc_route_buf* r,
@@ -413,7 +414,8 @@ zc_status zc_moe_int4_pack(const zc_moe_desc* desc, int which, const uint8_t* co
  * r may be x or res, and y may be x or res, in place (r and y are two
  * buffers); any other overlap of an output with an input, or of two outputs,
  * is ZC_ERR_INVALID.  Needs eps > 0, d at most 32768 and a multiple of
- * 8 (bf16) or 4 (fp32). */
+ * 8 (bf16) or 4 (fp32).  Squares are taken in fp32: a row with |r| above
+ * 1.8e19 has rstd = 0. */
 typedef struct {
   int64_t T;     /* rows (0 allowed: nothing is done) */
   int64_t d;

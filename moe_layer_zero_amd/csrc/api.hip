@@ -829,6 +829,8 @@ zc_status check_overlap(const Range* out, int nout, const Range* in, int nin) {
 zc_status check_seqs(const zc_moe_desc* d, int64_t S) {
   if (S < 1 || S > (int64_t(1) << 20))
     return fail(ZC_ERR_INVALID, "S=%lld sequences outside 1..2^20", (long long)S);
+  if (d->T > (int64_t(1) << 25))
+    return fail(ZC_ERR_UNSUPPORTED, "T=%lld tokens above 2^25", (long long)d->T);
   return ZC_OK;
 }
 

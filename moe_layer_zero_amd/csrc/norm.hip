@@ -43,8 +43,10 @@ __device__ __forceinline__ S row_sum(S v, S* s_red) {
 // m^-1/2 rounded to fp32 (m > 0): the hardware's fp32 estimate and one Newton
 // step in binary64.  Every value of the row is scaled by it, so its last bit
 // counts; the threads' fp32 sums are joined in binary64 for the same reason.
-// m beyond fp32 gives 0, NaN stays NaN.
+// m beyond fp32 gives 0, NaN stays NaN; where fp32 would be subnormal (eps and
+// the row both next to nothing) all of it runs in binary64.
 __device__ __forceinline__ float rsqrt_f64(double m) {
+  if (m < 1e-36) return static_cast<float>(1.0 / sqrt(m));
   const float e = __frsqrt_rn(static_cast<float>(m));
   if (!(e > 0.f) || isinf(e)) return e;
   const double y = e;

@@ -40,6 +40,8 @@ def test_pointers_sequences_and_workspace():
     need = zcmoe.lib().zc_moe_seq_balance_workspace_size(C.byref(d), 3)
     assert need > 0 and call(ws_bytes=need - 1) == zcmoe.ZC_ERR_WORKSPACE
     assert zcmoe.lib().zc_moe_seq_balance_workspace_size(C.byref(d), 0) == 0
+    big = zcmoe.LayerDesc((1 << 25) + 1, 128, 8, 4, 64, 2, torch.float32)
+    assert call(big, ws_bytes=1 << 40) == zcmoe.ZC_ERR_UNSUPPORTED
     assert call(mask=C.c_void_p((1 << 32) + 4)) == zcmoe.ZC_ERR_INVALID
     # no output over an input or another output
     for k, at in (("loss", 0), ("counts", 1), ("dl", 0), ("ws", 2), ("dl", 5), ("counts", 4)):

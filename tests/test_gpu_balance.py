@@ -206,6 +206,32 @@ def test_bad_offsets_stay_in_their_buffers():
     assert (counts >= 0).all() and counts.sum() <= 4 * 100
 
 
+def test_offsets_beyond_32_bits():
+    """Scores past the 2^31st: the last sequence's counts, loss and gradient are
+    those of the same tokens with as many sequences in front of them."""
+    N, Z, K, n = 512, 256, 2, 40
+    T = (1 << 31) // (N + Z) + 1000
+    g = torch.Generator(device="cuda").manual_seed(5)
+    desc = zcmoe.LayerDesc(T, 64, N, Z, 64, K, BF)
+    route = zcmoe.RouteBuffers(desc)
+    route.logits.normal_(generator=g)
+    route.topk_idx.copy_(torch.randint(0, N + Z, (T, 1), generator=g, device="cuda")
+                         + torch.tensor([0, 1], device="cuda"))
+    route.topk_idx.remainder_(N + Z)
+    lb = zcmoe.LoadBalance(8, 1.3, 1.0)
+    cu = torch.tensor([0, T // 3, T - n, T], dtype=torch.int32, device="cuda")
+    loss = torch.empty(4, device="cuda")
+    counts = torch.empty((3, N + Z), dtype=torch.int32, device="cuda")
+    dl = torch.empty((T, N + Z), device="cuda")
+    zcmoe.zc_moe_seq_balance(desc, lb, route, loss, counts, dl, cu_seqlens=cu)
+    torch.cuda.synchronize()
+    assert (counts.long().sum(1) == torch.tensor([T // 3, T - n - T // 3, n], device="cuda") * K).all()
+    l, idx = route.logits[-n - 2:].cpu(), route.topk_idx[-n - 2:].cpu()
+    small = run(l, idx, N, K, lb, [0, 1, 2, n + 2])
+    assert torch.equal(counts[2].cpu(), small[1][2]) and torch.equal(dl[-n:].cpu(), small[2][2:])
+    assert abs(loss[3].item() - small[0][3].item()) <= 2 * U * abs(small[0][3].item())
+
+
 def test_loss_without_gradient_and_reproducible():
     T, N, Z, K = 20000, 128, 64, 8
     l = scores(T, N + Z, 61)

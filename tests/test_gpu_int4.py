@@ -69,10 +69,10 @@ def product(v, W, s, G):
     return z, za, 2 * (G / 32) * 33 * U * 279 * groups + (C / G + 4) * U * za
 
 
-def reference(desc, x, w, route, G):
+def reference(desc, x, w, route, G, pick=slice(None)):
     T, N, K, I = desc.T, desc.N, desc.K, desc.I
-    xd = x.double().numpy()
-    idx, gate = route.topk_idx.cpu().numpy(), route.topk_gate.cpu().double().numpy()
+    xd = x[pick].double().numpy()
+    idx, gate = route.topk_idx[pick].cpu().numpy(), route.topk_gate[pick].cpu().double().numpy()
     ident = np.where(idx >= N, gate, 0).sum(1, keepdims=True)
     out, tol, terms = ident * xd, np.zeros_like(xd), np.abs(ident * xd)
     W = [values(c, s, G) for c, s in w]
@@ -139,6 +139,22 @@ def test_one_expert_takes_every_token(T):
     average, the rest nearly empty."""
     print(f"[int4 skew] T={T}", flush=True)
     check(*make(T, 256, 32, 8, 128, 2, 64, seed=7, skew=5), 64)
+
+
+def test_offsets_beyond_32_bits():
+    """Rows of h past the 2^32nd element, more tiles than one grid has
+    workgroups, and more rows than the 64-row kernel takes: tokens all over the
+    batch against the reference."""
+    T, d, N, Z, I, K, G = 600_000, 128, 8, 4, 2048, 8, 64
+    desc, x, w, route, packed = make(T, d, N, Z, I, K, G, seed=11)
+    assert int(route.offsets[-1]) * I > 1 << 32
+    out = torch.full((T, d), float("nan"), dtype=BF, device="cuda")
+    zcmoe.zc_moe_experts(desc, x.cuda(), route, *packed, out)
+    pick = torch.tensor([0, 1, 77_777, 299_999, 450_001, T - 2, T - 1])
+    ref, tol = reference(desc, x, w, route, G, pick)
+    err = np.abs(out[pick].cpu().double().numpy() - ref)
+    assert (err <= tol * (1 + HB) + HB * np.abs(ref) + 2.0 ** -133).all()
+    assert torch.isfinite(out[::997].float()).all()
 
 
 def test_all_picks_on_zero_computation_experts():

@@ -141,6 +141,62 @@ def test_non_finite_rows_stay_in_their_row():
     assert (y[4] == 0).all() and torch.isfinite(rstd[4]) and (scales[4] == 0).all()
 
 
+@pytest.mark.parametrize("eps", [1e-45, 1e-38, 1e-20, 4.0])
+def test_rows_next_to_nothing_and_their_eps(eps):
+    x, res, gamma = inputs(4, 264, F32)
+    x[0], res[0] = 0, 0
+    x[1] *= 1e-22   # squares of the order of the smallest fp32 numbers vanish
+    res[1] = 0
+    r, y, rstd, _, _ = forward(x, res, gamma, eps)
+    ro, yo, so = reference(x, res, gamma, float(np.float32(eps)))
+    assert torch.equal(r.cpu(), ro)
+    for t in (0, 2, 3):
+        assert abs(rstd[t].item() - so[t].item()) <= 48 * U * so[t].item()
+    assert (y[0] == 0).all() and torch.isfinite(y).all()
+
+
+def test_many_narrow_rows():
+    """More rows than one grid's workgroups: the grid goes round again."""
+    T, d = (1 << 22) + 4099, 8
+    x = torch.randn((T, d), generator=torch.Generator(device="cuda").manual_seed(1), device="cuda").to(BF)
+    gamma = torch.ones(d, dtype=BF, device="cuda")
+    y, rstd = torch.full_like(x, float("nan")), torch.empty(T, device="cuda")
+    zcmoe.zc_rmsnorm_forward(zcmoe.NormDesc(T, d, BF), x, gamma, y, rstd=rstd)
+    xd = x.double()
+    s = 1.0 / torch.sqrt((xd * xd).mean(-1) + 1e-6)
+    assert ((rstd.double() - s).abs() <= 48 * U * s).all()
+    yo = xd * s[:, None]
+    assert ((y.double() - yo).abs() <= (HALF[BF] + 50 * U) * yo.abs()).all()
+
+
+def test_offsets_beyond_32_bits():
+    """Rows whose elements lie past 2^31: the last ones against the formula,
+    forward (with codes) and backward."""
+    T, d, n = 360_000, 6144, 5
+    assert T * d > 1 << 31
+    x = torch.zeros((T, d), dtype=BF, device="cuda")
+    tail, res, gamma = inputs(n, d, BF, 120)
+    x[-n:] = tail.cuda()
+    desc = zcmoe.NormDesc(T, d, BF)
+    y, rstd = torch.empty_like(x), torch.empty(T, device="cuda")
+    codes, scales = zcmoe.mx_buffers(T, d)
+    zcmoe.zc_rmsnorm_forward(desc, x, gamma.cuda(), y, rstd=rstd, codes=codes, scales=scales)
+    want = forward(tail, None, gamma, mx=True)
+    for a, b in zip((y, rstd, codes, scales), want[1:]):
+        assert torch.equal(a[-n:], b)
+    assert (y[:-n:1000] == 0).all()
+    # backward: the rows in front give nothing but rstd * 0 * gamma = 0
+    dy = torch.zeros_like(x)
+    dyt = randn((n, d), 121, BF)
+    dy[-n:] = dyt.cuda()
+    dr, dg = y, torch.empty_like(gamma.cuda())
+    zcmoe.zc_rmsnorm_backward(desc, dy, x, gamma.cuda(), rstd, dr, dg)
+    ro, tol, go, ga = backward_reference(dyt, tail, gamma, rstd[-n:].cpu(), None)
+    assert ((dr[-n:].cpu().double() - ro).abs() <= tol + (HALF[BF] + 2 * U) * ro.abs()).all()
+    assert ((dg.cpu().double() - go).abs() <= 90 * U * ga + HALF[BF] * go.abs()).all()
+    assert (dr[:-n:1000] == 0).all()
+
+
 def test_in_place_and_no_kept_sum():
     x, res, gamma = inputs(33, 2056, BF)
     r0, y0, s0, _, _ = forward(x, res, gamma)

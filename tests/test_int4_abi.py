@@ -26,6 +26,9 @@ def test_layouts_and_sizes():
     assert L.zc_moe_int4_weight_bytes(C.byref(desc(weight_layout=0).c())) == 0
     with pytest.raises(ValueError):
         zcmoe.int4_layout(16)
+    # the LongCat-Flash layer's decode forward without a workspace argument
+    dec = desc(T=128, d=6144, N=512, Z=256, I=2048, K=12)
+    assert zcmoe.zc_moe_workspace_size(dec, zcmoe.ZC_OP_FORWARD) <= zcmoe.NOALLOC_SCRATCH_BYTES
     # the experts alone need no more than the forward
     for lay in (0, 4):
         d = desc(weight_layout=lay).c()
