@@ -186,7 +186,7 @@ class _Args:
         stream is that device's current one; scratch is a workspace the
         binding allocated itself, kept until a given stream is done with it."""
         if stream is None:
-            handle = torch.cuda.current_stream(self.dev).cuda_stream
+            handle = torch._C._cuda_getCurrentRawStream(self.dev)  # the handle alone
         elif stream.device_index != self.dev:
             raise ValueError(f"{self.where}: stream of GPU {stream.device_index}, tensors on GPU {self.dev}")
         else:
