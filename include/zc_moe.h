@@ -404,7 +404,7 @@ zc_status zc_moe_int4_pack(const zc_moe_desc* desc, int which, const uint8_t* co
  * the layer.  Row by row (T rows of d values, dtype a zc_dtype):
  *   r     = x + res, rounded to dtype (res NULL: r = x);
  *   rstd  = 1 / sqrt(mean(r^2) + eps), fp32, from the rounded r;
- *   y     = r * rstd * gamma in fp32, rounded once to dtype.
+ *   y     = r * gamma * rstd in fp32, rounded once to dtype.
  * r, rstd (fp32 [T]) and codes may be NULL: then they are not written.
  * codes and scales (both or neither; bf16, d a multiple of 128) receive y
  * as MXFP8, the operand that zc_moe_experts takes in place of quantizing x

@@ -6,7 +6,7 @@
 //          next block reads it); r = x without res
 //   rstd = 1 / sqrt(mean(r^2) + eps), from the rounded r, so that a backward
 //          pass that reads r differentiates what was computed
-//   y    = r * rstd * gamma in fp32, rounded once to the layer dtype
+//   y    = r * gamma * rstd in fp32, rounded once to the layer dtype
 //   codes, scales = MXFP8 of the rounded y: bit for bit what the FP8 expert
 //          kernels' own quantizer makes of y.
 // Backward, with a = dy * gamma and n = r * rstd:
@@ -40,17 +40,16 @@ __device__ __forceinline__ S row_sum(S v, S* s_red) {
   return v;
 }
 
-// m^-1/2 rounded to fp32 (m > 0): the hardware's fp32 estimate and one Newton
-// step in binary64.  Every value of the row is scaled by it, so its last bit
-// counts; the threads' fp32 sums are joined in binary64 for the same reason.
-// m beyond fp32 gives 0, NaN stays NaN; where fp32 would be subnormal (eps and
-// the row both next to nothing) all of it runs in binary64.
-__device__ __forceinline__ float rsqrt_f64(double m) {
-  if (m < 1e-36) return static_cast<float>(1.0 / sqrt(m));
+// m^-1/2 (m > 0): the hardware's fp32 estimate and one Newton step in binary64.
+// Every value of the row is scaled by it, so the threads' fp32 sums are joined
+// in binary64 too.  m beyond fp32 gives 0, NaN stays NaN; where fp32 would be
+// subnormal (eps and the row both next to nothing) all of it runs in binary64.
+__device__ __forceinline__ double rsqrt_f64(double m) {
+  if (m < 1e-36) return 1.0 / sqrt(m);
   const float e = __frsqrt_rn(static_cast<float>(m));
   if (!(e > 0.f) || isinf(e)) return e;
   const double y = e;
-  return static_cast<float>(y * (1.5 - 0.5 * m * y * y));
+  return y * (1.5 - 0.5 * m * y * y);
 }
 
 // MXFP8 of one thread's 8 values of a block of 32 held by 4 consecutive
@@ -117,7 +116,11 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_fwd_kernel(
 #pragma unroll
     for (int e = 0; e < V; ++e) ss += f[i][e] * f[i][e];
   }
-  const float rs = rsqrt_f64(row_sum<TPR>(static_cast<double>(ss), s_red) * inv_d + eps);
+  // r * gamma is exact in fp32 for bf16 rows; times rstd as a sum of two fp32
+  // (hi + lo), so that y is rounded once to fp32 and once to its type: a bf16
+  // y next to a rounding border, and the codes made of it, seldom cross it
+  const double rd = rsqrt_f64(row_sum<TPR>(static_cast<double>(ss), s_red) * inv_d + eps);
+  const float rs = static_cast<float>(rd), rs_lo = static_cast<float>(rd - rs);
   if (rstd && tid == 0) rstd[row] = rs;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
@@ -127,7 +130,10 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_fwd_kernel(
     V16<T>::unpack(wg[i], g);
     if (r) V16<T>::store(r + base + j, f[i]);
 #pragma unroll
-    for (int e = 0; e < V; ++e) f[i][e] = V16<T>::round(f[i][e] * rs * g[e]);
+    for (int e = 0; e < V; ++e) {
+      const float p = f[i][e] * g[e];
+      f[i][e] = V16<T>::round(__builtin_fmaf(p, rs, p * rs_lo));
+    }
     V16<T>::store(y + base + j, f[i]);
     if constexpr (MX) {
       int S;
