@@ -181,10 +181,9 @@ class _Args:
             raise ValueError("tensors passed to the HIP library must be contiguous")
         return t.data_ptr()
 
-    def run(self, fn, *args, stream=None, scratch=None):
+    def run(self, fn, *args, stream=None):
         """fn(*args, stream) with the tensors' device current.  The default
-        stream is that device's current one; scratch is a workspace the
-        binding allocated itself, kept until a given stream is done with it."""
+        stream is that device's current one."""
         if stream is None:
             handle = torch._C._cuda_getCurrentRawStream(self.dev)  # the handle alone
         elif stream.device_index != self.dev:
@@ -198,8 +197,16 @@ class _Args:
                 st = fn(*args, handle)
         if st != ZC_OK:
             _check(st, self.where)
-        if scratch is not None and stream is not None:
-            scratch.record_stream(stream)
+
+
+def _alloc(stream, make, *args, **kw):
+    """make(*args, **kw), its memory taken from the stream that will use it: a
+    block of another stream's may still be in use there, and goes back to that
+    stream, not to this one, when it is dropped."""
+    if stream is None:
+        return make(*args, **kw)
+    with torch.cuda.stream(stream):
+        return make(*args, **kw)
 
 
 @dataclass
@@ -363,12 +370,11 @@ def zc_moe_experts(desc: LayerDesc, x, route: RouteBuffers, w_gate, w_up, w_down
          for t, n in ((w_gate, "w_gate"), (w_up, "w_up"), (w_down, "w_down"))]
     codes, scales = (None, None) if xq is None else (
         a(xq[0], sh, u8, "xq codes"), a(xq[1], (T, desc.d // 32), u8, "xq scales"))
-    scratch = None
     if ws is None:
-        ws = scratch = workspace(desc, ZC_OP_EXPERTS, x.device)
+        ws = _alloc(stream, workspace, desc, ZC_OP_EXPERTS, x.device)
     n = ws.numel() * ws.element_size()
     a.run(lib().zc_moe_experts, C.byref(desc.c()), px, C.byref(r), *w, codes, scales, po,
-          a(ws, ws.shape, ws.dtype, "ws"), n, stream=stream, scratch=scratch)
+          a(ws, ws.shape, ws.dtype, "ws"), n, stream=stream)
 
 
 NOALLOC_SCRATCH_BYTES = 64 << 20  # ZC_NOALLOC_SCRATCH_BYTES
@@ -463,13 +469,12 @@ def zc_moe_seq_balance(desc: LayerDesc, lb: LoadBalance, route: RouteBuffers, lo
            "mask"),
          a(loss, (1 + S,), f32, "loss"), a(counts, (S, E), i32, "counts"),
          a(dlogits, (T, E), f32, "dlogits"))
-    scratch = None
     if ws is None:
-        ws = scratch = seq_balance_workspace(desc, S, loss.device)
+        ws = _alloc(stream, seq_balance_workspace, desc, S, loss.device)
     n = ws.numel() * ws.element_size()
     r = zc_route_buf(logits=lg, topk_idx=ti)
     a.run(lib().zc_moe_seq_balance, C.byref(desc.c()), C.byref(lb.c()), C.byref(r), S, *p,
-          a(ws, ws.shape, ws.dtype, "ws"), n, stream=stream, scratch=scratch)
+          a(ws, ws.shape, ws.dtype, "ws"), n, stream=stream)
 
 
 def zc_moe_route_stats(desc: LayerDesc, route: RouteBuffers, hist=None, moments=None, ws=None,
@@ -581,12 +586,13 @@ def _int4_shapes(desc: LayerDesc, which: int):
 def zc_moe_int4_quantize(desc: LayerDesc, which: int, src, codes=None, scales=None, stream=None):
     """w_gate or w_up (ZC_PACK_GATE_UP, [N][I][d]) or w_down (ZC_PACK_DOWN,
     [N][d][I]) as 4-bit codes (uint8 [N][R][C/2]) and group scales (bf16
-    [N][R][C/G]); both are allocated when None and returned."""
+    [N][R][C/G]); both are allocated when None and returned.  (What a call on
+    a given stream allocates belongs to that stream.)"""
     full, cs, ss = _int4_shapes(desc, which)
     if codes is None:
-        codes = torch.empty(cs, dtype=torch.uint8, device=src.device)
+        codes = _alloc(stream, torch.empty, cs, dtype=torch.uint8, device=src.device)
     if scales is None:
-        scales = torch.empty(ss, dtype=torch.bfloat16, device=src.device)
+        scales = _alloc(stream, torch.empty, ss, dtype=torch.bfloat16, device=src.device)
     a = _Args("zc_moe_int4_quantize")
     a.run(lib().zc_moe_int4_quantize, C.byref(desc.c()), which, a(src, full, torch.bfloat16, "src"),
           a(codes, cs, torch.uint8, "codes"), a(scales, ss, torch.bfloat16, "scales"), stream=stream)
@@ -601,7 +607,7 @@ def zc_moe_int4_pack(desc: LayerDesc, which: int, codes, scales, dst=None, strea
     d = desc.c()
     n = int(lib().zc_moe_int4_weight_bytes(C.byref(d)))
     if dst is None:
-        dst = torch.empty(max(n, 16), dtype=torch.uint8, device=codes.device)
+        dst = _alloc(stream, torch.empty, max(n, 16), dtype=torch.uint8, device=codes.device)
     if dst.dtype != torch.uint8 or dst.numel() < n:
         raise ValueError(f"dst: expected at least {n} uint8, got {dst.numel()} {dst.dtype}")
     a = _Args("zc_moe_int4_pack")
@@ -677,9 +683,8 @@ def zc_rmsnorm_backward(desc: NormDesc, dy, r, gamma, rstd, dr, dgamma, dres=Non
     p = (a(dy, sh, dt, "dy"), a(r, sh, dt, "r"), a(gamma, (d,), dt, "gamma"),
          a(rstd, (T,), torch.float32, "rstd"), a(dres, sh, dt, "dres"), a(dr, sh, dt, "dr"),
          a(dgamma, (d,), dt, "dgamma"))
-    scratch = None
     if ws is None:
-        ws = scratch = norm_workspace(desc, gamma.device)
+        ws = _alloc(stream, norm_workspace, desc, gamma.device)
     n = ws.numel() * ws.element_size()
     a.run(lib().zc_rmsnorm_backward, C.byref(desc.c()), *p, a(ws, ws.shape, ws.dtype, "ws"), n,
-          stream=stream, scratch=scratch)
+          stream=stream)
