@@ -15,9 +15,12 @@
 //          a fixed order, rounded once).
 //
 // Both passes are bound by HBM: a row is read once, kept in registers and
-// written once.  A row of up to 64 * NV vectors of 16 bytes belongs to one
-// wavefront (no LDS, no barrier), a longer one to a workgroup of 256 or
-// 1024 threads.
+// written once.  A short row belongs to one wavefront (no LDS, no barrier), a
+// longer one to a workgroup of 256 or 1024 threads (norm_shape).  Measured
+// (bf16): forward with MXFP8 output, 16384 x 6144, 167 us for 909 MB, 5.4 TB/s,
+// where a large copy moves 4.8; backward, 8192 x 2048, 25 + 4 us for 134 MB.  Calls
+// of a few rows are bound by the launch: 1 x 6144 takes 5 us on the card, 7 us to
+// issue.
 #include "zc_common.h"
 
 namespace zc {
@@ -146,7 +149,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_fwd_kernel(
   }
 }
 
-// Rows are dealt to nblk workgroups (nblk fixed by T alone): workgroup b
+// Rows are dealt to nblk workgroups (nblk by T and d alone): workgroup b
 // takes rows b * RPB + sub, then every nblk * RPB further, and keeps the
 // dgamma sums of its columns in registers.
 template <typename T, int NV, int TPR>
@@ -264,24 +267,40 @@ __global__ __launch_bounds__(kRedCols * kRedGroups) void norm_dgamma_kernel(
 // A launch holds fewer than 2^32 threads.
 constexpr int64_t kNormGrid = int64_t(1) << 20;
 
-// Partial rows of the dgamma sum, by T alone.
+// Partial rows of the dgamma sum at most (8192 rows of 2048 and of 6144, us: 256
+// 29 and 88, 512 24 and 61, 1024 27 and 68).
 constexpr int kNormBlocks = 512;
 
 // One row's threads and vectors per thread: f(NV, TPR) with NV * TPR
-// vectors covering the row (d <= kNormMaxD).
-template <typename T, typename F>
+// vectors covering the row (d <= kNormMaxD).  By d alone: a row's result does not
+// depend on how many others the call has.  Measured, bf16, us:
+//  - 768 to 1024 columns on a wavefront against 256 threads: 16 rows 4.4 and 3.6,
+//    8192 rows 14.0 and 18.8.
+//  - 2048 columns: forward, 16 rows 6.3 and 3.7, 8192 rows 26.2 and 24.3 (1544
+//    columns, 32768 rows: 79 and 83); backward, 16 rows 7.2 and 5.3, 8192 rows 24.5
+//    and 26.2.  So the forward's wavefronts end at 128 vectors, the backward's,
+//    which would join as many more partial rows, at 256.
+//  - 4096 columns on 256 threads against a wavefront: 8192 rows, forward 43 and 60,
+//    backward 40 and 58.
+//  - 6144 columns (forward with MXFP8) on 256 threads against 512: one row 6.7 and
+//    5.6, 16384 rows 166 and 192; against 1024: 6.5 and 5.2, 168 and 190.
+template <typename T, bool BWD, typename F>
 hipError_t norm_shape(int d, F&& f) {
   const int vecs = (d + V16<T>::n - 1) / V16<T>::n;
   using std::integral_constant;
   if (vecs <= 64) return f(integral_constant<int, 1>{}, integral_constant<int, 64>{});
   if (vecs <= 128) return f(integral_constant<int, 2>{}, integral_constant<int, 64>{});
-  if (vecs <= 256) return f(integral_constant<int, 4>{}, integral_constant<int, 64>{});
+  if (vecs <= 256) {
+    if constexpr (BWD) return f(integral_constant<int, 4>{}, integral_constant<int, 64>{});
+    else return f(integral_constant<int, 1>{}, integral_constant<int, 256>{});
+  }
   if (vecs <= 512) return f(integral_constant<int, 2>{}, integral_constant<int, 256>{});
   if (vecs <= 768) return f(integral_constant<int, 3>{}, integral_constant<int, 256>{});
   if (vecs <= 1024) return f(integral_constant<int, 4>{}, integral_constant<int, 256>{});
   if (vecs <= 2048) return f(integral_constant<int, 2>{}, integral_constant<int, 1024>{});
-  if (vecs <= 4096) return f(integral_constant<int, 4>{}, integral_constant<int, 1024>{});
-  return f(integral_constant<int, 8>{}, integral_constant<int, 1024>{});
+  if constexpr (kNormMaxD > 4096 * V16<T>::n)  // (fp32 rows)
+    if (vecs > 4096) return f(integral_constant<int, 8>{}, integral_constant<int, 1024>{});
+  return f(integral_constant<int, 4>{}, integral_constant<int, 1024>{});
 }
 
 int64_t norm_bwd_blocks(int64_t Tn, int rpb) {
@@ -301,7 +320,7 @@ hipError_t launch_norm_fwd(const T* x, const T* res, const T* gamma, T* r, T* y,
                            uint8_t* codes, uint8_t* scales, int64_t Tn, int d, float eps,
                            hipStream_t s) {
   if (Tn == 0) return hipSuccess;
-  return norm_shape<T>(d, [&](auto nv, auto tpr) {
+  return norm_shape<T, false>(d, [&](auto nv, auto tpr) {
     constexpr int NV = decltype(nv)::value, TPR = decltype(tpr)::value;
     constexpr int NT = TPR < 256 ? 256 : TPR, RPB = NT / TPR;
     const int64_t blocks = (Tn + RPB - 1) / RPB;
@@ -330,7 +349,7 @@ hipError_t launch_norm_bwd(const T* dy, const T* r, const T* gamma, const float*
                            hipStream_t s) {
   const int np = static_cast<int>(norm_bwd_parts<T>(Tn, d));
   if (Tn > 0) {
-    const hipError_t e = norm_shape<T>(d, [&](auto nv, auto tpr) {
+    const hipError_t e = norm_shape<T, true>(d, [&](auto nv, auto tpr) {
       constexpr int NV = decltype(nv)::value, TPR = decltype(tpr)::value;
       constexpr int NT = TPR < 256 ? 256 : TPR, RPB = NT / TPR;
       hipLaunchKernelGGL((norm_bwd_kernel<T, NV, TPR>),
