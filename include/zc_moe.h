@@ -415,7 +415,8 @@ zc_status zc_moe_int4_pack(const zc_moe_desc* desc, int which, const uint8_t* co
  * buffers); any other overlap of an output with an input, or of two outputs,
  * is ZC_ERR_INVALID.  Needs eps > 0, d at most 32768 and a multiple of
  * 8 (bf16) or 4 (fp32).  Squares are taken in fp32: a row with |r| above
- * 1.8e19 has rstd = 0. */
+ * 1.8e19 has rstd = 0; r * gamma is taken in fp32 too, before rstd.  A row's
+ * result does not depend on T. */
 typedef struct {
   int64_t T;     /* rows (0 allowed: nothing is done) */
   int64_t d;

@@ -354,10 +354,11 @@ int64_t up256(int64_t b) { return (b + 255) & ~int64_t(255); }
 // if every sequence were the average one (one sequence of 1024 tokens, K = 8:
 // 9.5 us, with parts of 1024 picks 12.8; 16384 tokens, K = 12: 35 and 36, 55 in
 // one part).  But enough that a sequence which holds the whole batch, the
-// others empty, is counted in parts of at most 65536.
+// others empty, is counted in parts of at most 32768
+// (16381 tokens in 37 ragged sequences, K = 12, the call: 39.1 us, with 65536 41.2).
 int count_parts(int64_t Tn, int64_t K, int64_t S) {
   if (S > kMaxSplit) return 1;
-  const int64_t even = Tn * K / (8192 * S), least = (Tn * K + 65535) / 65536;
+  const int64_t even = Tn * K / (8192 * S), least = (Tn * K + 32767) / 32768;
   int64_t p = 256 / S < even ? 256 / S : even;
   if (p < least) p = least;
   return p < 1 ? 1 : p > 64 ? 64 : static_cast<int>(p);

@@ -26,7 +26,7 @@ def test_balance_at_the_splits_in_the_number_of_sequences(S):
     B.check(l, B.topk(l, K), N, K, 4, 1.8, 0.3, cu, mask)
 
 
-@pytest.mark.parametrize("picks", [8191, 8192, 16384, 65536, 65537, 140000])
+@pytest.mark.parametrize("picks", [8191, 8192, 16384, 32768, 32769, 65536, 65537, 140000])
 @pytest.mark.parametrize("S", [1, 40])
 def test_balance_of_one_sequence_that_holds_the_batch(picks, S):
     # the others are empty; parts end inside the sequence
