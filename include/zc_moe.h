@@ -287,8 +287,11 @@ zc_status zc_moe_lb_loss(const zc_moe_desc* desc, const zc_lb_cfg* lb,
  *   dlogits[t][j] = dL/dl_{t,j} = p_j (k_j - sum_i p_i k_i),
  *                   k_j = alpha f_{s,g(j)} / (S' T_s), f held fixed,
  * and 0 for a masked token or one of no sequence, whatever its scores hold.
- * lb->D = N balances expert by expert.  The softmax, k and dlogits are fp32;
- * sums over tokens binary64.  loss: fp32 [1+S], L then L_s.  counts: int32
+ * lb->D = N balances expert by expert.  The exponentials of the softmax and
+ * dlogits are fp32; k, as k_j - k_0, and every sum are binary64, so that the
+ * gradient keeps its precision close to balance, where k_j - sum_i p_i k_i is
+ * small, and is 0 where all k_j agree (with zero-computation experts: for a K_e
+ * whose products with the counts are exact).  loss: fp32 [1+S], L then L_s.  counts: int32
  * [S][E].  dlogits: fp32 [T][E], or NULL (loss and counts only); every entry
  * is overwritten.  Only logits and topk_idx of r are read; a pick outside
  * 0..E-1 counts nowhere.  Offsets outside 0..T are clamped; with descending

@@ -16,12 +16,25 @@
 // that the gradient needs anyway.  No column sums of the softmax, and one
 // pass over the scores for loss and gradient together.
 //
+// k_sj - q_t is a difference of nearly equal numbers in every sequence that is
+// close to balance, which is where the loss drives them, and zero in one that
+// is balanced.  So what is kept of k is k_sj - k_s0, the difference taken of
+// the counts in binary64 (0 exactly where they agree), and the sums over a
+// token's scores run in binary64 too:
+//   u_t = sum_j e_tj (k_sj - k_s0) / sum_j e_tj,   q_t = k_s0 + u_t,
+//   dL/dl_tj = p_tj ((k_sj - k_s0) - u_t).
+// The error is then that of the fp32 exponentials e, relative to
+// |k_sj - q_t| and the spread of k about q_t: in an emulation of E = 192 scores
+// 6e-8 of the gradient at any imbalance, where fp32 k and sums lose 6e-7 at 10%
+// and 1e-3 at 0.01%.
+//
 // Passes: picks counted (integer sums, so their order is free), k from the
 // counts, the scores' pass, the tokens' q summed in a fixed order.  The
 // scores' pass is bound by HBM (4 bytes read and 4 written a score).  Measured:
-// 16381 tokens of 768 scores in 37 sequences, masked: that pass 24 us, 4.2 TB/s,
-// the counts, k and loss some 6 us each; at 64 tokens of 12 scores three kernels of
-// 2 to 4 us, less than their launches cost the host.
+// 16381 tokens of 768 scores in 37 sequences, masked: that pass 25 us, 4.0 TB/s
+// (the call 40.3 us, 39.2 with k and its sums in fp32), the counts, k and loss 5 to
+// 6 us each; at 64 tokens of 12 scores three kernels of 2 to 4 us, less than their
+// launches cost the host.
 #include "zc_common.h"
 
 namespace zc {
@@ -45,14 +58,18 @@ __device__ __forceinline__ void seq_range(const Seqs& q, int s, int& lo, int& hi
 
 struct LossCfg {
   int N, E, K, D;
-  double ffn;    // D / K_e
-  double zero;   // 1 / (K - K_e), 0 without zero-computation experts
+  // f = ffn / (den T_s) picks of an FFN group, zero / (den T_s) of the others
+  double ffn, zero, den;
   double alpha;
 };
 
-// k_sj of one sequence from its counts (s_hist, in LDS), by the workgroup.
+// k_sj - k_s0 and k_s0 of one sequence from its counts (s_hist, in LDS), by the
+// workgroup.  With Z > 0 both groups' f are brought to the denominator K_e (K -
+// K_e) T_s first, so that equal f (of a K_e with few bits) differ by 0.
 __device__ __forceinline__ void write_coef(const LossCfg& c, const int* s_hist, int* s_group,
-                                           int ts, int used, float* __restrict__ coef) {
+                                           int ts, int used, double* __restrict__ coef,
+                                           double* __restrict__ k0) {
+#pragma clang fp contract(off)  // (a fused product would differ from the rounded one it is taken from)
   const int G = c.N / c.D;
   for (int g = threadIdx.x; g <= c.D; g += blockDim.x) s_group[g] = 0;
   __syncthreads();
@@ -60,15 +77,13 @@ __device__ __forceinline__ void write_coef(const LossCfg& c, const int* s_hist, 
     if (s_hist[j]) atomicAdd(s_group + (j < c.N ? j / G : c.D), s_hist[j]);
   __syncthreads();
   const double t = static_cast<double>(ts);
+  const double first = c.ffn * static_cast<double>(s_group[0]);
+  const double scale = ts > 0 ? c.alpha / (c.den * static_cast<double>(used) * t * t) : 0.0;
   for (int j = threadIdx.x; j < c.E; j += blockDim.x) {
-    double k = 0.0;
-    if (ts > 0) {
-      const int g = j < c.N ? j / G : c.D;
-      const double f = (g < c.D ? c.ffn : c.zero) * static_cast<double>(s_group[g]) / t;
-      k = c.alpha * f / (static_cast<double>(used) * t);
-    }
-    coef[j] = static_cast<float>(k);
+    const int g = j < c.N ? j / G : c.D;
+    coef[j] = scale * ((g < c.D ? c.ffn : c.zero) * static_cast<double>(s_group[g]) - first);
   }
+  if (threadIdx.x == 0) *k0 = scale * first;
 }
 
 // Integer sum over the workgroup; every thread gets it.
@@ -181,8 +196,8 @@ __global__ __launch_bounds__(kCountThreads) void balance_used_kernel(const int* 
 // valid token, NULL to count them here.
 __global__ __launch_bounds__(kCountThreads) void balance_coef_kernel(
     LossCfg c, int S, int P, const int32_t* __restrict__ part, const int* __restrict__ ts,
-    const int* __restrict__ n_used, int32_t* __restrict__ counts, float* __restrict__ coef,
-    float* __restrict__ seq_scale) {
+    const int* __restrict__ n_used, int32_t* __restrict__ counts, double* __restrict__ coef,
+    double* __restrict__ k0, float* __restrict__ seq_scale) {
   __shared__ int s_hist[kMaxExperts], s_group[kMaxExperts + 1], s_red[kCountThreads / 64];
   const int s = blockIdx.x;
   int live, used;
@@ -207,7 +222,7 @@ __global__ __launch_bounds__(kCountThreads) void balance_coef_kernel(
     counts[static_cast<int64_t>(s) * c.E + j] = n;
   }
   __syncthreads();
-  write_coef(c, s_hist, s_group, live, used, coef + static_cast<int64_t>(s) * c.E);
+  write_coef(c, s_hist, s_group, live, used, coef + static_cast<int64_t>(s) * c.E, k0 + s);
   if (threadIdx.x == 0) seq_scale[s] = static_cast<float>(used);
 }
 
@@ -215,7 +230,7 @@ __global__ __launch_bounds__(kCountThreads) void balance_coef_kernel(
 // and k at once.  The number of sequences with a valid token is counted by
 // every workgroup again.
 __global__ __launch_bounds__(kCountThreads) void balance_count_coef_kernel(
-    LossCfg c, Seqs q, const int32_t* __restrict__ idx, int32_t* counts, float* coef,
+    LossCfg c, Seqs q, const int32_t* __restrict__ idx, int32_t* counts, double* coef, double* k0,
     float* seq_scale) {
   __shared__ int s_hist[kMaxExperts], s_group[kMaxExperts + 1], s_red[kCountThreads / 64], s_used;
   const int s = blockIdx.x, lane = threadIdx.x & 63;
@@ -238,7 +253,7 @@ __global__ __launch_bounds__(kCountThreads) void balance_count_coef_kernel(
   const int ts = valid_tokens(q, lo, hi, s_red);
   count_picks(q, idx, c.K, c.E, lo, hi, s_hist);
   __syncthreads();
-  write_coef(c, s_hist, s_group, ts, s_used, coef + static_cast<int64_t>(s) * c.E);
+  write_coef(c, s_hist, s_group, ts, s_used, coef + static_cast<int64_t>(s) * c.E, k0 + s);
   for (int j = threadIdx.x; j < c.E; j += blockDim.x)
     counts[static_cast<int64_t>(s) * c.E + j] = s_hist[j];
   if (threadIdx.x == 0) seq_scale[s] = static_cast<float>(s_used);
@@ -250,16 +265,18 @@ __global__ __launch_bounds__(kCountThreads) void balance_count_coef_kernel(
 // gets zeros, whatever it holds.
 template <int NV, int VEC>
 __global__ __launch_bounds__(64 * kWaves) void balance_scores_kernel(
-    Seqs q, const float* __restrict__ logits, int E, const float* __restrict__ coef,
-    float* __restrict__ dot, float* __restrict__ dl) {
+    Seqs q, const float* __restrict__ logits, int E, const double* __restrict__ coef,
+    const double* __restrict__ k0, float* __restrict__ dot, float* __restrict__ dl) {
   typedef float vec_t __attribute__((ext_vector_type(VEC)));
+  typedef double dvec_t __attribute__((ext_vector_type(VEC)));
   const int lane = threadIdx.x & 63;
   const int64_t tt = static_cast<int64_t>(blockIdx.x) * kWaves + (threadIdx.x >> 6);
   if (tt >= q.T) return;
   const int t = static_cast<int>(tt), n = E / VEC;
   const vec_t* row = reinterpret_cast<const vec_t*>(logits + tt * E);
   vec_t* out = reinterpret_cast<vec_t*>(dl + tt * E);
-  vec_t p[NV], k[NV];
+  vec_t p[NV];
+  dvec_t k[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int j = lane + 64 * i;
@@ -273,11 +290,11 @@ __global__ __launch_bounds__(64 * kWaves) void balance_scores_kernel(
     if (lane == 0) dot[t] = 0.f;
     return;
   }
-  const vec_t* kr = reinterpret_cast<const vec_t*>(coef + static_cast<int64_t>(s) * E);
+  const dvec_t* kr = reinterpret_cast<const dvec_t*>(coef + static_cast<int64_t>(s) * E);
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int j = lane + 64 * i;
-    k[i] = j < n ? kr[j] : vec_t(0.f);
+    k[i] = j < n ? kr[j] : dvec_t(0.0);
   }
   float m = -INFINITY;
 #pragma unroll
@@ -286,29 +303,30 @@ __global__ __launch_bounds__(64 * kWaves) void balance_scores_kernel(
     for (int e = 0; e < VEC; ++e) m = fmaxf(m, p[i][e]);
 #pragma unroll
   for (int o = 32; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
-  float sum = 0.f, sk = 0.f;
+  double sum = 0.0, sk = 0.0;
 #pragma unroll
   for (int i = 0; i < NV; ++i)
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
       p[i][e] = lane + 64 * i < n ? expf(p[i][e] - m) : 0.f;
-      sum += p[i][e];
-      sk += p[i][e] * k[i][e];
+      sum += static_cast<double>(p[i][e]);
+      sk += static_cast<double>(p[i][e]) * k[i][e];
     }
 #pragma unroll
   for (int o = 32; o >= 1; o >>= 1) {
     sum += __shfl_xor(sum, o);
     sk += __shfl_xor(sk, o);
   }
-  const float inv = 1.0f / sum, qt = sk * inv;
-  if (lane == 0) dot[t] = qt;
+  const float inv = 1.0f / static_cast<float>(sum);
+  const double u = sk / sum;
+  if (lane == 0) dot[t] = static_cast<float>(k0[s] + u);
   if (dl) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int j = lane + 64 * i;
       vec_t v;
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) v[e] = (p[i][e] * inv) * (k[i][e] - qt);
+      for (int e = 0; e < VEC; ++e) v[e] = (p[i][e] * inv) * static_cast<float>(k[i][e] - u);
       if (j < n) out[j] = v;
     }
   }
@@ -366,12 +384,12 @@ int count_parts(int64_t Tn, int64_t K, int64_t S) {
 
 }  // namespace
 
-// coef [S][E], scale [S], parts' counts [S][P][E] and tokens [S][P], the
-// number of used sequences, dot [T]
+// coef [S][E] and k_s0 [S] (binary64), scale [S], parts' counts [S][P][E] and
+// tokens [S][P], the number of used sequences, dot [T]
 size_t seq_balance_scratch_bytes(int64_t Tn, int64_t E, int64_t K, int64_t S) {
   const int64_t P = count_parts(Tn, K, S);
-  return static_cast<size_t>(up256(4 * S * E) + up256(4 * S) + up256(4 * S * P * E) +
-                             up256(4 * S * P + 4) + up256(4 * Tn));
+  return static_cast<size_t>(up256(8 * S * E) + up256(8 * S) + up256(4 * S) +
+                             up256(4 * S * P * E) + up256(4 * S * P + 4) + up256(4 * Tn));
 }
 
 hipError_t launch_seq_balance(const float* logits, const int32_t* topk_idx, int Tn, int N, int E,
@@ -386,21 +404,23 @@ hipError_t launch_seq_balance(const float* logits, const int32_t* topk_idx, int 
     p += up256(b);
     return r;
   };
-  float* coef = reinterpret_cast<float*>(take(4 * static_cast<int64_t>(S) * E));
+  double* coef = reinterpret_cast<double*>(take(8 * static_cast<int64_t>(S) * E));
+  double* k0 = reinterpret_cast<double*>(take(8 * static_cast<int64_t>(S)));
   float* scale = reinterpret_cast<float*>(take(4 * static_cast<int64_t>(S)));
   int32_t* part = reinterpret_cast<int32_t*>(take(4 * rows * E));
   int* ts = reinterpret_cast<int*>(take(4 * rows + 4));
   int* used = ts + rows;
   float* dot = reinterpret_cast<float*>(take(4 * static_cast<int64_t>(Tn)));
   const Seqs q{cu, mask, S, Tn};
-  const LossCfg c{N, E, K, D, D / K_e, E > N ? 1.0 / (K - K_e) : 0.0, alpha};
+  const bool z = E > N;
+  const LossCfg c{N, E, K, D, z ? D * (K - K_e) : D, z ? K_e : 0.0, z ? K_e * (K - K_e) : K_e, alpha};
   hipError_t e;
   // Sequences not split: one workgroup each counts the picks and writes k at once
   // (1024 tokens, 32 sequences: 9.7 us, two launches 12.8; 256 sequences 13.5 and
   // 14.7; 1024, each looking through all: 45 and 27).
   if (P == 1 && S <= 256) {
     hipLaunchKernelGGL(balance_count_coef_kernel, dim3(S), dim3(kCountThreads), 0, s, c, q,
-                       topk_idx, counts, coef, scale);
+                       topk_idx, counts, coef, k0, scale);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   } else {
     hipLaunchKernelGGL(balance_count_kernel, dim3(static_cast<unsigned>(rows)),
@@ -414,14 +434,14 @@ hipError_t launch_seq_balance(const float* logits, const int32_t* topk_idx, int 
       if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     hipLaunchKernelGGL(balance_coef_kernel, dim3(S), dim3(kCountThreads), 0, s, c, S, P, part, ts,
-                       apart ? used : nullptr, counts, coef, scale);
+                       apart ? used : nullptr, counts, coef, k0, scale);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   if (Tn > 0) {
     const dim3 grid((Tn + kWaves - 1) / kWaves), block(64 * kWaves);
 #define ZC_BAL(NV, VEC)                                                                            \
-  hipLaunchKernelGGL((balance_scores_kernel<NV, VEC>), grid, block, 0, s, q, logits, E, coef, dot, \
-                     dlogits)
+  hipLaunchKernelGGL((balance_scores_kernel<NV, VEC>), grid, block, 0, s, q, logits, E, coef, k0, \
+                     dot, dlogits)
     if (E % 4 == 0) {
       if (E <= 256) ZC_BAL(1, 4);
       else if (E <= 512) ZC_BAL(2, 4);
