@@ -11,8 +11,8 @@
 //          kernels' own quantizer makes of y.
 // Backward, with a = dy * gamma and n = r * rstd:
 //   dr     = rstd * (a - n * mean(a n)) + dres, rounded once
-//   dgamma = sum over rows of dy * n (fp32 partials per workgroup, added in
-//          a fixed order, rounded once).
+//   dgamma = sum over rows of dy * n (fp32 partials of up to 512 workgroups,
+//          joined in binary64 in a fixed order, rounded once).
 //
 // Both passes are bound by HBM: a row is read once, kept in registers and
 // written once.  A short row belongs to one wavefront (no LDS, no barrier), a
@@ -236,31 +236,35 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_bwd_kernel(
 }
 
 // dgamma[j] = the np partial rows' column j: 32 groups of consecutive rows,
-// each summed ascending, added in group order.  32 columns a workgroup: the
-// sum is bound by the latency of its loads, so 16 go out at once a thread.
+// each summed ascending, added in group order, all in binary64 (in fp32 the join
+// of up to 512 rows costs more than the partials' own sums; it is bound by
+// the latency of its loads either way).  32 columns a workgroup, and 16 loads go
+// out at once a thread.
 constexpr int kRedCols = 32, kRedGroups = 32;
 template <typename T>
 __global__ __launch_bounds__(kRedCols * kRedGroups) void norm_dgamma_kernel(
     const float* __restrict__ part, int np, int d, T* __restrict__ dgamma) {
-  __shared__ float s_p[kRedGroups][kRedCols];
+  __shared__ double s_p[kRedGroups][kRedCols];
   const int c = threadIdx.x % kRedCols, g = threadIdx.x / kRedCols;
   const int j = blockIdx.x * kRedCols + c;
   const int per = (np + kRedGroups - 1) / kRedGroups;
   const int hi = j < d ? min(np, (g + 1) * per) : 0;
-  float v = 0.f;
+  double v = 0.0;
   for (int b0 = g * per; b0 < hi; b0 += 16) {
+    // (past the group its last row again, and not added: with a load behind a
+    // branch the compiler widens the value there, and waits for each)
     float w[16];
 #pragma unroll
-    for (int u = 0; u < 16; ++u) w[u] = b0 + u < hi ? part[static_cast<int64_t>(b0 + u) * d + j] : 0.f;
+    for (int u = 0; u < 16; ++u) w[u] = part[static_cast<int64_t>(min(b0 + u, hi - 1)) * d + j];
 #pragma unroll
-    for (int u = 0; u < 16; ++u) v += w[u];
+    for (int u = 0; u < 16; ++u) v += b0 + u < hi ? static_cast<double>(w[u]) : 0.0;
   }
   s_p[g][c] = v;
   __syncthreads();
   if (g == 0 && j < d) {
 #pragma unroll
     for (int k = 1; k < kRedGroups; ++k) v += s_p[k][c];
-    Elem<T>::st(dgamma + j, v);
+    Elem<T>::st(dgamma + j, static_cast<float>(v));
   }
 }
 
