@@ -407,7 +407,8 @@ zc_status zc_moe_int4_pack(const zc_moe_desc* desc, int which, const uint8_t* co
  * the layer.  Row by row (T rows of d values, dtype a zc_dtype):
  *   r     = x + res, rounded to dtype (res NULL: r = x);
  *   rstd  = 1 / sqrt(mean(r^2) + eps), fp32, from the rounded r;
- *   y     = r * gamma * rstd in fp32, rounded once to dtype.
+ *   y     = r * gamma * rstd in fp32, rounded once to dtype (rstd before gamma
+ *           where r * gamma is beyond fp32).
  * r, rstd (fp32 [T]) and codes may be NULL: then they are not written.
  * codes and scales (both or neither; bf16, d a multiple of 128) receive y
  * as MXFP8, the operand that zc_moe_experts takes in place of quantizing x
@@ -418,8 +419,7 @@ zc_status zc_moe_int4_pack(const zc_moe_desc* desc, int which, const uint8_t* co
  * buffers); any other overlap of an output with an input, or of two outputs,
  * is ZC_ERR_INVALID.  Needs eps > 0, d at most 32768 and a multiple of
  * 8 (bf16) or 4 (fp32).  Squares are taken in fp32: a row with |r| above
- * 1.8e19 has rstd = 0; r * gamma is taken in fp32 too, before rstd.  A row's
- * result does not depend on T. */
+ * 1.8e19 has rstd = 0.  A row's result does not depend on T. */
 typedef struct {
   int64_t T;     /* rows (0 allowed: nothing is done) */
   int64_t d;

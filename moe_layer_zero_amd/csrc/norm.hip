@@ -17,7 +17,7 @@
 // Both passes are bound by HBM: a row is read once, kept in registers and
 // written once.  A short row belongs to one wavefront (no LDS, no barrier), a
 // longer one to a workgroup of 256 or 1024 threads (norm_shape).  Measured
-// (bf16): forward with MXFP8 output, 16384 x 6144, 167 us for 909 MB, 5.4 TB/s,
+// (bf16): forward with MXFP8 output, 16384 x 6144, 168 us for 909 MB, 5.4 TB/s,
 // where a large copy moves 4.8; backward, 8192 x 2048, 25 + 4 us for 134 MB.  Calls
 // of a few rows are bound by the launch: 1 x 6144 takes 5 us on the card, 7 us to
 // issue.
@@ -121,7 +121,9 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_fwd_kernel(
   }
   // r * gamma is exact in fp32 for bf16 rows; times rstd as a sum of two fp32
   // (hi + lo), so that y is rounded once to fp32 and once to its type: a bf16
-  // y next to a rounding border, and the codes made of it, seldom cross it
+  // y next to a rounding border, and the codes made of it, seldom cross it.
+  // Where r * gamma or y leave fp32 the sum could be inf - inf: there rstd comes
+  // first, which gives an infinity, or y where only r * gamma is too large
   const double rd = rsqrt_f64(row_sum<TPR>(static_cast<double>(ss), s_red) * inv_d + eps);
   const float rs = static_cast<float>(rd), rs_lo = static_cast<float>(rd - rs);
   if (rstd && tid == 0) rstd[row] = rs;
@@ -132,11 +134,20 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_fwd_kernel(
     float g[V];
     V16<T>::unpack(wg[i], g);
     if (r) V16<T>::store(r + base + j, f[i]);
+    float v[V], finite = 0.f;  // NaN with a NaN or an infinity among v
 #pragma unroll
     for (int e = 0; e < V; ++e) {
       const float p = f[i][e] * g[e];
-      f[i][e] = V16<T>::round(__builtin_fmaf(p, rs, p * rs_lo));
+      v[e] = __builtin_fmaf(p, rs, p * rs_lo);
+      finite = __builtin_fmaf(v[e], 0.f, finite);
     }
+    if (finite != finite) {  // (16384 x 6144: 166.4 -> 167.9 us; chosen value by value, 171)
+#pragma unroll
+      for (int e = 0; e < V; ++e)
+        if (!(fabsf(v[e]) <= 3.402823466e38f)) v[e] = (f[i][e] * rs) * g[e];
+    }
+#pragma unroll
+    for (int e = 0; e < V; ++e) f[i][e] = V16<T>::round(v[e]);
     V16<T>::store(y + base + j, f[i]);
     if constexpr (MX) {
       int S;
