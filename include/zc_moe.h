@@ -363,7 +363,9 @@ zc_status zc_moe_pack_weights(const zc_moe_desc* desc, int which, const void* sr
  * 2^(S-127), S an 8-bit exponent (E8M0), and each value is stored as an
  * FP8 E4M3 code of value / 2^(S-127):
  *   S = floor(log2 max|v|) - 8 + 127 (at least 0; 0 for an all-zero run);
- *   code = nearest E4M3 value, ties to even, magnitudes above 448 clamped.
+ *   code = nearest E4M3 value, ties to even, magnitudes above 448 clamped (an
+ *          infinity saturates); a NaN becomes the E4M3 NaN, and the maximum is
+ *          that of the run's other values.
  * A forward with desc->weight_layout = ZC_WEIGHTS_MXFP8 quantizes x the
  * same way per token (runs of 32 along d) and h per pick (runs of 32 along
  * I, from h rounded to fp32), multiplies on the scaled FP8 matrix cores with
@@ -414,7 +416,7 @@ zc_status zc_moe_int4_pack(const zc_moe_desc* desc, int which, const uint8_t* co
  * as MXFP8, the operand that zc_moe_experts takes in place of quantizing x
  * itself: codes [T][d] E4M3; scales [T][d/32] E8M0, block b of a row at
  * 4*(b/4) + {0,2,1,3}[b%4].  The rule is that of zc_moe_quantize_weights,
- * on the rounded y; a NaN becomes the E4M3 NaN, an infinity saturates.
+ * on the rounded y.
  * r may be x or res, and y may be x or res, in place (r and y are two
  * buffers); any other overlap of an output with an input, or of two outputs,
  * is ZC_ERR_INVALID.  Needs eps > 0, d at most 32768 and a multiple of

@@ -17,7 +17,8 @@
 //       2^(floor(log2 max|v|) - 8), 0 for an all-zero block);
 //   code_i = E4M3 of v_i * 2^(127 - S), nearest with ties to even, after
 //            clamping to +-448 (the conversion instruction rounds to nearest
-//            even; without the clamp it returns NaN past 464).
+//            even; without the clamp it returns NaN past 464); a NaN is the E4M3
+//            NaN and does not enter the maximum, an infinity saturates.
 //
 // Matrix-core operand layout of one 32x32x64 step (measured on MI355X):
 // lane l feeds row (or column) l % 32; with h = l / 32, its bytes 0..15 are

@@ -56,7 +56,7 @@ __device__ __forceinline__ double rsqrt_f64(double m) {
 }
 
 // MXFP8 of one thread's 8 values of a block of 32 held by 4 consecutive
-// lanes.  A NaN gets the NaN code; infinities saturate.
+// lanes.
 __device__ __forceinline__ uint64_t mx_quad(const float* f, int& S) {
   float amax = 0.f;
 #pragma unroll
@@ -67,8 +67,7 @@ __device__ __forceinline__ uint64_t mx_quad(const float* f, int& S) {
   uint64_t q = 0;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    const uint32_t c = f[e] != f[e] ? 0x7fu : mx_code(f[e], S);
-    q |= static_cast<uint64_t>(c) << (8 * e);
+    q |= static_cast<uint64_t>(mx_code(f[e], S)) << (8 * e);
   }
   return q;
 }

@@ -105,11 +105,13 @@ __device__ __forceinline__ int mx_scale(float amax) {
   return be > 8 ? be - 8 : 0;
 }
 
-// E4M3 code of v at scale S.
+// E4M3 code of v at scale S.  A NaN keeps being one (the clamp alone would make
+// it a number); an infinity saturates.
 __device__ __forceinline__ uint32_t mx_code(float v, int S) {
   float q = __builtin_ldexpf(v, 127 - S);
   q = fminf(fmaxf(q, -448.f), 448.f);
-  return static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(q, 0.f, 0, false)) & 0xffu;
+  const uint32_t c = static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(q, 0.f, 0, false)) & 0xffu;
+  return v != v ? 0x7fu : c;
 }
 
 // Row-tile height of the grouped GEMMs; the dispatch step publishes the
