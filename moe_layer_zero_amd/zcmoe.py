@@ -202,7 +202,8 @@ class _Args:
 def _alloc(stream, make, *args, **kw):
     """make(*args, **kw), its memory taken from the stream that will use it: a
     block of another stream's may still be in use there, and goes back to that
-    stream, not to this one, when it is dropped."""
+    stream, not to this one, when it is dropped.  (So it is with everything that
+    a call here allocates, outputs too.)"""
     if stream is None:
         return make(*args, **kw)
     with torch.cuda.stream(stream):
@@ -333,7 +334,7 @@ def zc_moe_route(desc: LayerDesc, x, w_router, bias, route: RouteBuffers, ws=Non
         _check_weights(desc, w_router, None, None, None)
     _check_layer_tensor(bias, (desc.E,), torch.float32, "bias")
     if ws is None:
-        ws = workspace(desc, ZC_OP_ROUTE, bias.device)
+        ws = _alloc(stream, workspace, desc, ZC_OP_ROUTE, bias.device)
     d, r = desc.c(), route.c()
     _check(lib().zc_moe_route(C.byref(d), _ptr(x), _ptr(w_router), _ptr(bias), C.byref(r),
                               _ptr(ws), ws.numel(), _stream(stream)), "zc_moe_route")
@@ -346,7 +347,7 @@ def zc_moe_forward(desc: LayerDesc, x, w_router, bias, w_gate, w_up, w_down, out
     _check_layer_tensor(bias, (desc.E,), torch.float32, "bias")
     _check_weights(desc, w_router, w_gate, w_up, w_down)
     if ws is None:
-        ws = workspace(desc, ZC_OP_FORWARD, x.device)
+        ws = _alloc(stream, workspace, desc, ZC_OP_FORWARD, x.device)
     d, r = desc.c(), route.c()
     _check(lib().zc_moe_forward(C.byref(d), _ptr(x), _ptr(w_router), _ptr(bias), _ptr(w_gate),
                                 _ptr(w_up), _ptr(w_down), _ptr(out), C.byref(r), _ptr(saved),
@@ -418,7 +419,7 @@ def zc_moe_backward(desc: LayerDesc, x, w_router, w_gate, w_up, w_down, route: R
     _check_weights(desc, w_router, w_gate, w_up, w_down)
     _check_weights(desc, dw_router, dw_gate, dw_up, dw_down)
     if ws is None:
-        ws = workspace(desc, ZC_OP_BACKWARD, x.device)
+        ws = _alloc(stream, workspace, desc, ZC_OP_BACKWARD, x.device)
     d, r = desc.c(), route.c()
     lbc = None if lb is None else C.byref(lb.c())
     a = (C.byref(d), _ptr(x), _ptr(w_router), _ptr(w_gate), _ptr(w_up), _ptr(w_down), C.byref(r),
@@ -437,10 +438,11 @@ def zc_moe_lb_loss(desc: LayerDesc, lb: LoadBalance, route: RouteBuffers, out=No
     """Queues the device-level load-balance loss of the routed batch; returns
     out, a float64 GPU tensor [1 + 2(D+1)]: L, f_1..f_{D+1}, P_1..P_{D+1}."""
     if out is None:
-        out = torch.empty(1 + 2 * (lb.D + 1), dtype=torch.float64, device=route.counts.device)
+        out = _alloc(stream, torch.empty, 1 + 2 * (lb.D + 1), dtype=torch.float64,
+                     device=route.counts.device)
     _check_layer_tensor(out, (1 + 2 * (lb.D + 1),), torch.float64, "out")
     if ws is None:
-        ws = workspace(desc, ZC_OP_LB_LOSS, route.counts.device)
+        ws = _alloc(stream, workspace, desc, ZC_OP_LB_LOSS, route.counts.device)
     d, r, c = desc.c(), route.c(), lb.c()
     _check(lib().zc_moe_lb_loss(C.byref(d), C.byref(c), C.byref(r), _ptr(out), _ptr(ws),
                                 ws.numel(), _stream(stream)), "zc_moe_lb_loss")
@@ -483,13 +485,13 @@ def zc_moe_route_stats(desc: LayerDesc, route: RouteBuffers, hist=None, moments=
     (hist [K+1] int32, moments [2] float64 = mean, std), both on the GPU."""
     dev = route.counts.device
     if hist is None:
-        hist = torch.empty(desc.K + 1, dtype=torch.int32, device=dev)
+        hist = _alloc(stream, torch.empty, desc.K + 1, dtype=torch.int32, device=dev)
     if moments is None:
-        moments = torch.empty(2, dtype=torch.float64, device=dev)
+        moments = _alloc(stream, torch.empty, 2, dtype=torch.float64, device=dev)
     _check_layer_tensor(hist, (desc.K + 1,), torch.int32, "hist")
     _check_layer_tensor(moments, (2,), torch.float64, "moments")
     if ws is None:
-        ws = workspace(desc, ZC_OP_ROUTE_STATS, dev)
+        ws = _alloc(stream, workspace, desc, ZC_OP_ROUTE_STATS, dev)
     d, r = desc.c(), route.c()
     _check(lib().zc_moe_route_stats(C.byref(d), C.byref(r), _ptr(hist), _ptr(moments), _ptr(ws),
                                     ws.numel(), _stream(stream)), "zc_moe_route_stats")
@@ -530,7 +532,7 @@ def pack_expert_weights(desc: LayerDesc, w_gate, w_up, w_down, stream=None):
     """Packed copies (new tensors) of the three expert weight tensors."""
     out = []
     for w, which in ((w_gate, ZC_PACK_GATE_UP), (w_up, ZC_PACK_GATE_UP), (w_down, ZC_PACK_DOWN)):
-        p = torch.empty_like(w)
+        p = _alloc(stream, torch.empty_like, w)
         zc_moe_pack_weights(desc, which, w, p, stream)
         out.append(p)
     return tuple(out)
@@ -560,7 +562,7 @@ def zc_moe_quantize_weights(desc: LayerDesc, which: int, src, dst=None, stream=N
     d = desc.c()
     n = int(lib().zc_moe_quantized_weight_bytes(C.byref(d)))
     if dst is None:
-        dst = torch.empty(max(n, 16), dtype=torch.uint8, device=src.device)
+        dst = _alloc(stream, torch.empty, max(n, 16), dtype=torch.uint8, device=src.device)
     if dst.dtype != torch.uint8 or dst.numel() < n:
         raise ValueError(f"dst: expected at least {n} uint8, got {dst.numel()} {dst.dtype}")
     _check(lib().zc_moe_quantize_weights(C.byref(d), which, _ptr(src), _ptr(dst), _stream(stream)),
