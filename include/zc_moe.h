@@ -296,7 +296,9 @@ zc_status zc_moe_lb_loss(const zc_moe_desc* desc, const zc_lb_cfg* lb,
  * is overwritten.  Only logits and topk_idx of r are read; a pick outside
  * 0..E-1 counts nowhere.  Offsets outside 0..T are clamped; with descending
  * ones the results mean nothing, but no access leaves its buffer.  1 <= S <=
- * 2^20, T <= 2^25.  No output may overlap an input or another output.
+ * 2^20, T <= 2^25.  cu_seqlens and mask are 16-byte aligned like every other
+ * buffer: a slice of a larger batch may need a copy.  No output may overlap an
+ * input or another output.
  * ws: zc_moe_seq_balance_workspace_size(desc, S) bytes. */
 size_t zc_moe_seq_balance_workspace_size(const zc_moe_desc* desc, int64_t S);
 zc_status zc_moe_seq_balance(const zc_moe_desc* desc, const zc_lb_cfg* lb, const zc_route_buf* r,

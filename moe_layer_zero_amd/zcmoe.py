@@ -210,6 +210,12 @@ def _alloc(stream, make, *args, **kw):
         return make(*args, **kw)
 
 
+def _aligned(stream, t):
+    """t, or a copy of it (made on the call's stream) where it does not start at a
+    multiple of 16 bytes, as the library wants it: a slice of a larger batch."""
+    return t if t is None or t.data_ptr() % 16 == 0 else _alloc(stream, torch.clone, t)
+
+
 @dataclass
 class LayerDesc:
     T: int
@@ -460,7 +466,9 @@ def zc_moe_seq_balance(desc: LayerDesc, lb: LoadBalance, route: RouteBuffers, lo
     """Balance loss of the packed sequences of a routed batch: loss fp32 [1+S]
     (L, then each sequence's), counts int32 [S][E] and, where given, the
     gradient of the router scores dlogits fp32 [T][E].  cu_seqlens int32
-    [S+1]; mask uint8 or bool [T], nonzero for valid tokens."""
+    [S+1]; mask uint8 or bool [T], nonzero for valid tokens; both may be slices
+    that start anywhere (one not at a multiple of 16 bytes is copied first)."""
+    cu_seqlens, mask = _aligned(stream, cu_seqlens), _aligned(stream, mask)
     S = 1 if cu_seqlens is None else cu_seqlens.numel() - 1
     T, E, i32, f32 = desc.T, desc.E, torch.int32, torch.float32
     a = _Args("zc_moe_seq_balance")
