@@ -857,6 +857,13 @@ int64_t norm_ws_bytes(const zc_norm_desc* d) {
   return a256(np * d->d * 4);
 }
 
+// Bytes of one set of expert weights in the layer's layout.
+int64_t weight_set_bytes(const zc_moe_desc* d) {
+  const int64_t n = d->N * d->I * d->d;
+  if (const int G = int4_group(d)) return n / 2 + n / G * 2;
+  return d->weight_layout == ZC_WEIGHTS_MXFP8 ? n + n / 32 : n * esize(d);
+}
+
 zc_status check_weights(const zc_moe_desc* d, const void* wg, const void* wu, const void* wd) {
   const bool opt = d->N == 0;
   ZC_CHECK(check_ptr(wg, "w_gate", opt));
@@ -961,13 +968,15 @@ zc_status zc_moe_experts(const zc_moe_desc* desc, const void* x, const zc_route_
   const int64_t need = fwd_ws_bytes(desc);
   ZC_CHECK(check_ws(ws, ws_bytes, need));
   const int64_t n = desc->T * desc->d, b = n * esize(desc), k = desc->T * desc->K;
-  const Range in[] = {{x, b, "x", false}, {x_codes, n, "x_codes", false},
+  const int64_t wb = weight_set_bytes(desc);
+  const Range in[] = {{w_gate, wb, "w_gate", false}, {w_up, wb, "w_up", false},
+                      {w_down, wb, "w_down", false}, {x, b, "x", false}, {x_codes, n, "x_codes", false},
                       {x_scales, n / 32, "x_scales", false}, {r->topk_idx, 4 * k, "r->topk_idx", false},
                       {r->topk_gate, 4 * k, "r->topk_gate", false},
                       {r->offsets, 4 * (desc->N + 1), "r->offsets", false},
                       {r->perm, 4 * k, "r->perm", false}, {r->inv, 4 * k, "r->inv", false}};
   const Range outs[] = {{out, b, "out", false}, {ws, need, "ws", false}};
-  ZC_CHECK(check_overlap(outs, 2, in, 8));
+  ZC_CHECK(check_overlap(outs, 2, in, 11));
   hipStream_t s = static_cast<hipStream_t>(stream);
   char* w = static_cast<char*>(ws);
   if (desc->dtype == ZC_BF16)
@@ -1198,8 +1207,7 @@ zc_status zc_moe_quantize_weights(const zc_moe_desc* desc, int which, const void
 
 size_t zc_moe_int4_weight_bytes(const zc_moe_desc* desc) {
   if (check_desc(desc) != ZC_OK || !int4_group(desc)) return 0;
-  const int64_t n = desc->N * desc->I * desc->d;
-  return static_cast<size_t>(n / 2 + n / int4_group(desc) * 2);
+  return static_cast<size_t>(weight_set_bytes(desc));
 }
 
 namespace {
