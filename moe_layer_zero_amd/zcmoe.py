@@ -150,12 +150,6 @@ def _ptr(t):
     return C.c_void_p(t.data_ptr())
 
 
-def _stream(stream):
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return C.c_void_p(stream.cuda_stream)
-
-
 class _Args:
     """Device addresses of one call's tensors, checked: shape, dtype, contiguity,
     and that all of them live on one GPU.  (Calls of a few microseconds go
@@ -197,6 +191,14 @@ class _Args:
                 st = fn(*args, handle)
         if st != ZC_OK:
             _check(st, self.where)
+
+
+def _call(where, t, stream, fn, *args):
+    """fn(*args, stream), as _Args.run, for the GPU of tensor t (the library
+    refuses the call if there is none)."""
+    a = _Args(where)
+    a.dev = torch.cuda.current_device() if t is None else t.get_device()
+    a.run(fn, *args, stream=stream)
 
 
 def _alloc(stream, make, *args, **kw):
@@ -342,8 +344,8 @@ def zc_moe_route(desc: LayerDesc, x, w_router, bias, route: RouteBuffers, ws=Non
     if ws is None:
         ws = _alloc(stream, workspace, desc, ZC_OP_ROUTE, bias.device)
     d, r = desc.c(), route.c()
-    _check(lib().zc_moe_route(C.byref(d), _ptr(x), _ptr(w_router), _ptr(bias), C.byref(r),
-                              _ptr(ws), ws.numel(), _stream(stream)), "zc_moe_route")
+    _call("zc_moe_route", bias, stream, lib().zc_moe_route, C.byref(d), _ptr(x), _ptr(w_router),
+          _ptr(bias), C.byref(r), _ptr(ws), ws.numel())
 
 
 def zc_moe_forward(desc: LayerDesc, x, w_router, bias, w_gate, w_up, w_down, out,
@@ -355,9 +357,9 @@ def zc_moe_forward(desc: LayerDesc, x, w_router, bias, w_gate, w_up, w_down, out
     if ws is None:
         ws = _alloc(stream, workspace, desc, ZC_OP_FORWARD, x.device)
     d, r = desc.c(), route.c()
-    _check(lib().zc_moe_forward(C.byref(d), _ptr(x), _ptr(w_router), _ptr(bias), _ptr(w_gate),
-                                _ptr(w_up), _ptr(w_down), _ptr(out), C.byref(r), _ptr(saved),
-                                _ptr(ws), ws.numel(), _stream(stream)), "zc_moe_forward")
+    _call("zc_moe_forward", bias, stream, lib().zc_moe_forward, C.byref(d), _ptr(x), _ptr(w_router),
+          _ptr(bias), _ptr(w_gate), _ptr(w_up), _ptr(w_down), _ptr(out), C.byref(r), _ptr(saved),
+          _ptr(ws), ws.numel())
 
 
 def zc_moe_experts(desc: LayerDesc, x, route: RouteBuffers, w_gate, w_up, w_down, out, xq=None,
@@ -397,9 +399,8 @@ def zc_moe_forward_noalloc(desc: LayerDesc, x, w_router, bias, w_gate, w_up, w_d
     _check_layer_tensor(bias, (desc.E,), torch.float32, "bias")
     _check_weights(desc, w_router, w_gate, w_up, w_down)
     d, r = desc.c(), route.c()
-    _check(lib().zc_moe_forward_noalloc(C.byref(d), _ptr(x), _ptr(w_router), _ptr(bias),
-                                        _ptr(w_gate), _ptr(w_up), _ptr(w_down), _ptr(out),
-                                        C.byref(r), _stream(stream)), "zc_moe_forward_noalloc")
+    _call("zc_moe_forward_noalloc", bias, stream, lib().zc_moe_forward_noalloc, C.byref(d), _ptr(x),
+          _ptr(w_router), _ptr(bias), _ptr(w_gate), _ptr(w_up), _ptr(w_down), _ptr(out), C.byref(r))
 
 
 @dataclass
@@ -432,11 +433,11 @@ def zc_moe_backward(desc: LayerDesc, x, w_router, w_gate, w_up, w_down, route: R
          _ptr(saved), _ptr(dout), _ptr(dx), _ptr(dw_router), _ptr(dw_gate), _ptr(dw_up),
          _ptr(dw_down), lbc)
     if dlogits is None:
-        _check(lib().zc_moe_backward(*a, _ptr(ws), ws.numel(), _stream(stream)), "zc_moe_backward")
+        _call("zc_moe_backward", w_router, stream, lib().zc_moe_backward, *a, _ptr(ws), ws.numel())
     else:
         _check_layer_tensor(dlogits, (desc.T, desc.E), torch.float32, "dlogits")
-        _check(lib().zc_moe_backward_scores(*a, _ptr(dlogits), _ptr(ws), ws.numel(),
-                                            _stream(stream)), "zc_moe_backward_scores")
+        _call("zc_moe_backward_scores", w_router, stream, lib().zc_moe_backward_scores, *a,
+              _ptr(dlogits), _ptr(ws), ws.numel())
 
 
 def zc_moe_lb_loss(desc: LayerDesc, lb: LoadBalance, route: RouteBuffers, out=None, ws=None,
@@ -450,8 +451,8 @@ def zc_moe_lb_loss(desc: LayerDesc, lb: LoadBalance, route: RouteBuffers, out=No
     if ws is None:
         ws = _alloc(stream, workspace, desc, ZC_OP_LB_LOSS, route.counts.device)
     d, r, c = desc.c(), route.c(), lb.c()
-    _check(lib().zc_moe_lb_loss(C.byref(d), C.byref(c), C.byref(r), _ptr(out), _ptr(ws),
-                                ws.numel(), _stream(stream)), "zc_moe_lb_loss")
+    _call("zc_moe_lb_loss", out, stream, lib().zc_moe_lb_loss, C.byref(d), C.byref(c), C.byref(r),
+          _ptr(out), _ptr(ws), ws.numel())
     return out
 
 
@@ -501,8 +502,8 @@ def zc_moe_route_stats(desc: LayerDesc, route: RouteBuffers, hist=None, moments=
     if ws is None:
         ws = _alloc(stream, workspace, desc, ZC_OP_ROUTE_STATS, dev)
     d, r = desc.c(), route.c()
-    _check(lib().zc_moe_route_stats(C.byref(d), C.byref(r), _ptr(hist), _ptr(moments), _ptr(ws),
-                                    ws.numel(), _stream(stream)), "zc_moe_route_stats")
+    _call("zc_moe_route_stats", hist, stream, lib().zc_moe_route_stats, C.byref(d), C.byref(r),
+          _ptr(hist), _ptr(moments), _ptr(ws), ws.numel())
     return hist, moments
 
 
@@ -512,16 +513,16 @@ def zc_moe_accumulate_counts(counts, acc, stream=None):
     E = counts.numel()
     _check_layer_tensor(counts, (E,), torch.int32, "counts")
     _check_layer_tensor(acc, (E,), torch.int32, "acc")
-    _check(lib().zc_moe_accumulate_counts(E, _ptr(counts), _ptr(acc), _stream(stream)),
-           "zc_moe_accumulate_counts")
+    _call("zc_moe_accumulate_counts", acc, stream, lib().zc_moe_accumulate_counts, E, _ptr(counts),
+          _ptr(acc))
 
 
 def zc_moe_pid_update(N: int, Z: int, K: int, counts, T_all: int, mu: float, K_e: float, bias,
                       stream=None):
     _check_layer_tensor(counts, (N + Z,), torch.int32, "counts")
     _check_layer_tensor(bias, (N + Z,), torch.float32, "bias")
-    _check(lib().zc_moe_pid_update(N, Z, K, _ptr(counts), T_all, float(mu), float(K_e),
-                                   _ptr(bias), _stream(stream)), "zc_moe_pid_update")
+    _call("zc_moe_pid_update", bias, stream, lib().zc_moe_pid_update, N, Z, K, _ptr(counts), T_all,
+          float(mu), float(K_e), _ptr(bias))
 
 
 def zc_moe_pack_weights(desc: LayerDesc, which: int, src, dst, stream=None):
@@ -532,8 +533,8 @@ def zc_moe_pack_weights(desc: LayerDesc, which: int, src, dst, stream=None):
     _check_layer_tensor(src, shape, desc.dtype, "src")
     _check_layer_tensor(dst, shape, desc.dtype, "dst")
     d = desc.c()
-    _check(lib().zc_moe_pack_weights(C.byref(d), which, _ptr(src), _ptr(dst), _stream(stream)),
-           "zc_moe_pack_weights")
+    _call("zc_moe_pack_weights", dst, stream, lib().zc_moe_pack_weights, C.byref(d), which, _ptr(src),
+          _ptr(dst))
 
 
 def pack_expert_weights(desc: LayerDesc, w_gate, w_up, w_down, stream=None):
@@ -573,8 +574,8 @@ def zc_moe_quantize_weights(desc: LayerDesc, which: int, src, dst=None, stream=N
         dst = _alloc(stream, torch.empty, max(n, 16), dtype=torch.uint8, device=src.device)
     if dst.dtype != torch.uint8 or dst.numel() < n:
         raise ValueError(f"dst: expected at least {n} uint8, got {dst.numel()} {dst.dtype}")
-    _check(lib().zc_moe_quantize_weights(C.byref(d), which, _ptr(src), _ptr(dst), _stream(stream)),
-           "zc_moe_quantize_weights")
+    _call("zc_moe_quantize_weights", dst, stream, lib().zc_moe_quantize_weights, C.byref(d), which,
+          _ptr(src), _ptr(dst))
     return dst
 
 

@@ -40,7 +40,6 @@ def taken(monkeypatch):
 
     monkeypatch.setattr(zcmoe, "_LIB", NoLibrary())
     monkeypatch.setattr(zcmoe, "_ptr", lambda t: None)
-    monkeypatch.setattr(zcmoe, "_stream", lambda s: None)
     monkeypatch.setattr(zcmoe._Args, "__call__", lambda self, t, *a: None)
     monkeypatch.setattr(zcmoe._Args, "run", lambda self, *a, **kw: None)
     monkeypatch.setattr(torch.cuda, "stream", stream)
