@@ -399,7 +399,8 @@ zc_status zc_moe_quantize_weights(const zc_moe_desc* desc, int which,
  *  zc_moe_int4_pack: natural -> dst, zc_moe_int4_weight_bytes(desc) bytes, in
  *      an order private to this library: what the forward takes.
  * The products keep x and h in bf16 and every sum, and the experts' outputs
- * y, in fp32; an infinity in a row of x gives NaN.  Their grids are not
+ * y, in fp32, the codes' offset among them: an infinity in a row of x or h gives
+ * NaN, and so does a group whose sum of 136 |x| is beyond fp32.  Their grids are not
  * persistent: cu_limit does not size them.  No output may overlap an input. */
 size_t zc_moe_int4_weight_bytes(const zc_moe_desc* desc);
 zc_status zc_moe_int4_quantize(const zc_moe_desc* desc, int which, const void* src, uint8_t* codes,

@@ -17,10 +17,10 @@
 // Both passes are bound by HBM: a row is read once, kept in registers and
 // written once.  A short row belongs to one wavefront (no LDS, no barrier), a
 // longer one to a workgroup of 256 or 1024 threads (norm_shape).  Measured
-// (bf16): forward with MXFP8 output, 16384 x 6144, 168 us for 909 MB, 5.4 TB/s,
-// where a large copy moves 4.8; backward, 8192 x 2048, 25 + 4 us for 134 MB.  Calls
-// of a few rows are bound by the launch: 1 x 6144 takes 5 us on the card, 7 us to
-// issue.
+// (three input sets in turn): forward with MXFP8 output, bf16, 16384 x 6144, 165 to
+// 168 us for 909 MB, 5.4 TB/s, where a large copy moves 4.8, fp32, 16384 x 2048, 90 us,
+// 5.9 TB/s; backward, bf16, 8192 x 2048, 28 + 5 us for 134 MB.  Calls of a few rows are
+// bound by the launch: 1 x 6144 takes 5 us on the card, 7 us to issue.
 #include "zc_common.h"
 
 namespace zc {
@@ -281,23 +281,25 @@ __global__ __launch_bounds__(kRedCols * kRedGroups) void norm_dgamma_kernel(
 // A launch holds fewer than 2^32 threads.
 constexpr int64_t kNormGrid = int64_t(1) << 20;
 
-// Partial rows of the dgamma sum at most (8192 rows of 2048 and of 6144, us: 256
-// 29 and 88, 512 24 and 61, 1024 27 and 68).
+// Partial rows of the dgamma sum at most (a call on 8192 rows of 2048 and of 6144,
+// three input sets in turn, us: 256 38 and 103, 512 31 and 81, 1024 35 and 91).
 constexpr int kNormBlocks = 512;
 
 // One row's threads and vectors per thread: f(NV, TPR) with NV * TPR
 // vectors covering the row (d <= kNormMaxD).  By d alone: a row's result does not
-// depend on how many others the call has.  Measured, bf16, us:
-//  - 768 to 1024 columns on a wavefront against 256 threads: 16 rows 4.4 and 3.6,
-//    8192 rows 14.0 and 18.8.
-//  - 2048 columns: forward, 16 rows 6.3 and 3.7, 8192 rows 26.2 and 24.3 (1544
-//    columns, 32768 rows: 79 and 83); backward, 16 rows 7.2 and 5.3, 8192 rows 24.5
-//    and 26.2.  So the forward's wavefronts end at 128 vectors, the backward's,
+// depend on how many others the call has.  Measured, bf16, us; 8192 rows and more as
+// calls on three input sets in turn, so that a set is not in the caches from the
+// call before, 16 rows and fewer as calls in a graph:
+//  - 768 columns on a wavefront against 256 threads: 16 rows 4.4 and 3.6, 8192 rows
+//    14.9 and 20.8 (1024 columns 17.6 and 21.4, backward 19.0 and 30.4).
+//  - 2048 columns: forward, 16 rows 6.3 and 3.7, 8192 rows 30.0 and 28.2 (1544
+//    columns, 32768 rows: 80 and 86); backward, 16 rows 7.2 and 5.3, 8192 rows 30.8
+//    and 33.6.  So the forward's wavefronts end at 128 vectors, the backward's,
 //    which would join as many more partial rows, at 256.
-//  - 4096 columns on 256 threads against a wavefront: 8192 rows, forward 43 and 60,
-//    backward 40 and 58.
+//  - 4096 columns on 256 threads against a wavefront: 8192 rows, forward 49.7 and
+//    67.8, backward 54.2 and 77.1.
 //  - 6144 columns (forward with MXFP8) on 256 threads against 512: one row 6.7 and
-//    5.6, 16384 rows 166 and 192; against 1024: 6.5 and 5.2, 168 and 190.
+//    5.6, 16384 rows 165 and 184; against 1024: 6.5 and 5.2, 165 and 184.
 template <typename T, bool BWD, typename F>
 hipError_t norm_shape(int d, F&& f) {
   const int vecs = (d + V16<T>::n - 1) / V16<T>::n;
