@@ -448,6 +448,78 @@ zc_status zc_rmsnorm_backward(const zc_norm_desc* desc, const void* dy, const vo
                               const void* gamma, const float* rstd, const void* dres, void* dr,
                               void* dgamma, void* ws, size_t ws_bytes, void* stream);
 
+/* The weights' step: what follows zc_moe_backward and zc_rmsnorm_backward.
+ *
+ * Norm of all gradients (`count` tensors of n elements each, all of g_dtype) and
+ * the factor that clips them, on the device:
+ *   norm   = sqrt(sum of g^2), squares and sums in binary64, in a fixed order;
+ *   factor = max_norm / norm where norm > max_norm, else 1; 0 where norm is not
+ *            finite: zc_adamw_step then leaves everything as it is.
+ * out (device, fp32 [2]): norm, factor.  step (device, int64, nullable): one more
+ * where norm is finite.  max_norm > 0, infinity for no clipping.  tensors is a
+ * host array, read during the call; its pointers are device pointers (NULL where
+ * n is 0).  n < 2^36, count <= 2^20.  ws: zc_grad_norm_workspace_size bytes (0
+ * for invalid arguments).  No output may overlap an input or another output. */
+typedef struct {
+  const void* g;
+  int64_t n;
+} zc_grad_tensor;
+size_t zc_grad_norm_workspace_size(const zc_grad_tensor* tensors, int64_t count, int g_dtype);
+zc_status zc_grad_norm(const zc_grad_tensor* tensors, int64_t count, int g_dtype, double max_norm,
+                       float* out, int64_t* step, void* ws, size_t ws_bytes, void* stream);
+
+/* An AdamW step (decoupled weight decay) over many tensors, in place.  With g' =
+ * factor * g and t the step, counted from 1, element by element in fp32:
+ *   m = beta1 m + (1 - beta1) g'         v = beta2 v + (1 - beta2) g'^2
+ *   p = p (1 - lr wd) - lr / (1 - beta1^t) * m / (sqrt(v / (1 - beta2^t)) + eps)
+ * Weights: p of p_dtype; with master (bf16 weights, fp32 [n]; for all tensors or
+ * none) the step is made on master and p receives its rounding.
+ * Gradients: g of g_dtype, p_dtype or fp32.
+ * States, both zeros before the first step:
+ *   ZC_STATE_F32:  m, v fp32 [n].
+ *   ZC_STATE_8BIT: m, v E4M3 codes [n] and m_scale, v_scale fp32 [ceil(n / 128)],
+ *     one for each 128 values: m = code * scale; v = (code * scale)^2, so that the
+ *     codes span its range; scale = max / 448 over the new values, at least
+ *     2^-120; no positive v becomes 0 but the smallest code.
+ * rounding: how what has fewer than 32 bits is rounded.  ZC_ROUND_NEAREST: ties to
+ * even.  ZC_ROUND_STOCHASTIC: 8-bit codes, and bf16 weights without master, go to
+ * one of their two neighbours with the odds that keep the mean (down after adding
+ * a multiple of 2^-16 of their distance), by bits that seed, t, the tensor's place
+ * in the list and the element's place in it determine.  Without it a state or
+ * weight that a step changes by less than half its codes' distance stays.
+ * factor, lr, step (device, nullable; else 1, cfg->lr, cfg->step) are read when
+ * the step runs, so that nothing has to come to the host between zc_grad_norm
+ * and the step, and a captured step goes on when it is replayed; lr >= 0.  Where factor
+ * is 0 nothing is written.  A gradient that is not finite makes what it touches NaN
+ * or infinite (with 8-bit states all its 128 values).  No buffer may overlap
+ * another, and none be in the list twice.  The scales, factor, lr and step are
+ * aligned like their elements, the other buffers to 16 bytes.  tensors: host array,
+ * as above; n < 2^36, count <= 2^20. */
+enum { ZC_STATE_F32 = 0, ZC_STATE_8BIT = 1 };
+enum { ZC_ROUND_NEAREST = 0, ZC_ROUND_STOCHASTIC = 1 };
+typedef struct {
+  void* p;
+  const void* g;
+  float* master;            /* NULL: none */
+  void* m;
+  void* v;
+  float* m_scale;           /* 8-bit states only, else NULL */
+  float* v_scale;
+  int64_t n;
+  double weight_decay;      /* wd of this tensor */
+} zc_adamw_tensor;
+typedef struct {
+  int32_t p_dtype, g_dtype; /* zc_dtype */
+  int32_t state;            /* ZC_STATE_F32 or ZC_STATE_8BIT */
+  int32_t rounding;
+  double lr, beta1, beta2;  /* lr >= 0; 0 <= beta < 1 */
+  double eps;               /* > 0 in fp32 */
+  int64_t step;             /* >= 1 where it counts */
+  uint32_t seed;
+} zc_adamw_cfg;
+zc_status zc_adamw_step(const zc_adamw_cfg* cfg, const zc_adamw_tensor* tensors, int64_t count,
+                        const float* factor, const float* lr, const int64_t* step, void* stream);
+
 /* Kernel timing for benchmarks.  While profiling is on, every entry point
  * brackets each of its kernel launches with a pair of HIP events recorded on
  * the call's own stream, tagged with one of the phases below.  The events
@@ -462,7 +534,7 @@ enum {
   ZC_PH_BWD_GATE_UP_DW, ZC_PH_BWD_ROUTER_DW, ZC_PH_BWD_ROUTER_DX, ZC_PH_BWD_DX_GATHER,
   ZC_PH_BIAS_UPDATE, ZC_PH_TILE_OFFSETS, ZC_PH_LB_LOSS, ZC_PH_LB_COEF, ZC_PH_ROUTE_STATS,
   ZC_PH_ACCUMULATE, ZC_PH_QUANTIZE, ZC_PH_BWD_GATHER, ZC_PH_NORM, ZC_PH_NORM_BWD,
-  ZC_PH_SEQ_BALANCE, ZC_NUM_PHASES
+  ZC_PH_SEQ_BALANCE, ZC_PH_GRAD_NORM, ZC_PH_ADAMW, ZC_NUM_PHASES
 };
 zc_status zc_moe_profile(int on);
 zc_status zc_moe_profile_read(double* total_ms, int32_t* count);

@@ -1,5 +1,6 @@
 // C ABI of libzcmoe: argument checks, workspace carving and the launch
 // sequence of each entry point.  See include/zc_moe.h for the contract.
+#include <algorithm>
 #include <atomic>
 #include <cstdarg>
 #include <cmath>
@@ -857,6 +858,187 @@ int64_t norm_ws_bytes(const zc_norm_desc* d) {
   return a256(np * d->d * 4);
 }
 
+// ---- lists of tensors (gradient norm, AdamW)
+constexpr int64_t kMaxTensors = int64_t(1) << 20, kMaxElems = int64_t(1) << 36;
+int64_t dtype_size(int dtype) { return dtype == ZC_F32 ? 4 : 2; }
+zc_status check_dtype(int dtype, const char* name) {
+  if (dtype != ZC_F32 && dtype != ZC_BF16)
+    return fail(ZC_ERR_INVALID, "%s %d is neither ZC_F32 nor ZC_BF16", name, dtype);
+  return ZC_OK;
+}
+zc_status check_elems(int64_t n, int64_t i) {
+  if (n < 0) return fail(ZC_ERR_INVALID, "tensor %lld has n=%lld", (long long)i, (long long)n);
+  if (n >= kMaxElems)
+    return fail(ZC_ERR_UNSUPPORTED, "tensor %lld: n=%lld is not below 2^36", (long long)i, (long long)n);
+  return ZC_OK;
+}
+zc_status check_count(const void* tensors, int64_t count) {
+  if (count < 0 || count > kMaxTensors)
+    return fail(ZC_ERR_INVALID, "count=%lld outside 0..2^20", (long long)count);
+  if (count && !tensors) return fail(ZC_ERR_INVALID, "tensors is NULL");
+  return ZC_OK;
+}
+
+// The buffers of a list: no written one may share bytes with any other.
+struct Span {
+  uintptr_t begin, end;
+  int64_t tensor;
+  const char* name;
+  bool written;
+};
+zc_status check_spans(std::vector<Span>& v) {
+  std::sort(v.begin(), v.end(), [](const Span& a, const Span& b) { return a.begin < b.begin; });
+  const Span *far = nullptr, *far_written = nullptr;  // the one that ends last so far
+  for (const Span& x : v) {
+    const Span* hit = x.written ? far : far_written;
+    if (hit && x.begin < hit->end)
+      return fail(ZC_ERR_INVALID, "%s of tensor %lld overlaps %s of tensor %lld", x.name,
+                  (long long)x.tensor, hit->name, (long long)hit->tensor);
+    if (!far || x.end > far->end) far = &x;
+    if (x.written && (!far_written || x.end > far_written->end)) far_written = &x;
+  }
+  return ZC_OK;
+}
+void add_span(std::vector<Span>& v, const void* p, int64_t bytes, int64_t tensor, const char* name,
+              bool written) {
+  const uintptr_t b = reinterpret_cast<uintptr_t>(p);
+  if (p && bytes > 0) v.push_back(Span{b, b + static_cast<uintptr_t>(bytes), tensor, name, written});
+}
+
+// Read and written one by one: aligned like an element.
+zc_status check_scalar(const void* p, size_t align, const char* name) {
+  if (reinterpret_cast<uintptr_t>(p) % align)
+    return fail(ZC_ERR_INVALID, "%s is not %zu-byte aligned", name, align);
+  return ZC_OK;
+}
+
+zc_status check_grads(const zc_grad_tensor* t, int64_t count, int g_dtype) {
+  ZC_CHECK(check_dtype(g_dtype, "g_dtype"));
+  ZC_CHECK(check_count(t, count));
+  for (int64_t i = 0; i < count; ++i) {
+    ZC_CHECK(check_elems(t[i].n, i));
+    ZC_CHECK(check_ptr(t[i].g, "g", t[i].n == 0));
+  }
+  return ZC_OK;
+}
+// The list as two arrays, and the workspace it takes.
+struct Grads {
+  std::vector<const void*> g;
+  std::vector<int64_t> n;
+  int64_t ws_bytes;
+  Grads(const zc_grad_tensor* t, int64_t count, bool bf16) {
+    for (int64_t i = 0; i < count; ++i) {
+      g.push_back(t[i].g);
+      n.push_back(t[i].n);
+    }
+    ws_bytes = a256(8 * zc::grad_norm_parts(n.data(), count, bf16));
+  }
+};
+
+zc_status do_grad_norm(const zc_grad_tensor* t, int64_t count, int g_dtype, double max_norm,
+                       float* out, int64_t* step, void* ws, size_t ws_bytes, hipStream_t s) {
+  const bool bf16 = g_dtype == ZC_BF16;
+  const Grads l(t, count, bf16);
+  ZC_CHECK(check_ws(ws, ws_bytes, l.ws_bytes));
+  std::vector<Span> spans;
+  for (int64_t i = 0; i < count; ++i)
+    add_span(spans, t[i].g, t[i].n * dtype_size(g_dtype), i, "g", false);
+  add_span(spans, out, 8, -1, "out", true);
+  add_span(spans, step, 8, -1, "step", true);
+  add_span(spans, ws, l.ws_bytes, -1, "ws", true);
+  ZC_CHECK(check_spans(spans));
+  ZC_LAUNCH(ZC_PH_GRAD_NORM,
+            zc::launch_grad_norm(l.g.data(), l.n.data(), count, bf16, max_norm,
+                                 static_cast<double*>(ws), out, step, s),
+            "gradient norm launch");
+  return ZC_OK;
+}
+
+zc_status check_adamw(const zc_adamw_cfg* c, bool device_step) {
+  if (!c) return fail(ZC_ERR_INVALID, "cfg is NULL");
+  ZC_CHECK(check_dtype(c->p_dtype, "p_dtype"));
+  ZC_CHECK(check_dtype(c->g_dtype, "g_dtype"));
+  if (c->g_dtype != c->p_dtype && c->g_dtype != ZC_F32)
+    return fail(ZC_ERR_UNSUPPORTED, "bf16 gradients of fp32 weights");
+  if (c->state != ZC_STATE_F32 && c->state != ZC_STATE_8BIT)
+    return fail(ZC_ERR_INVALID, "state %d is neither ZC_STATE_F32 nor ZC_STATE_8BIT", c->state);
+  if (c->rounding != ZC_ROUND_NEAREST && c->rounding != ZC_ROUND_STOCHASTIC)
+    return fail(ZC_ERR_INVALID, "rounding %d is neither ZC_ROUND_NEAREST nor ZC_ROUND_STOCHASTIC",
+                c->rounding);
+  if (!std::isfinite(c->lr) || c->lr < 0.0) return fail(ZC_ERR_INVALID, "lr=%g", c->lr);
+  if (!(c->beta1 >= 0.0 && c->beta1 < 1.0) || !(c->beta2 >= 0.0 && c->beta2 < 1.0))
+    return fail(ZC_ERR_INVALID, "beta1=%g beta2=%g outside [0, 1)", c->beta1, c->beta2);
+  const float eps = static_cast<float>(c->eps);
+  if (!std::isfinite(eps) || !(eps >= 1.17549435e-38f))
+    return fail(ZC_ERR_INVALID, "eps=%g is no positive fp32 number", c->eps);
+  if (!device_step && c->step < 1)
+    return fail(ZC_ERR_INVALID, "step=%lld, counted from 1", (long long)c->step);
+  return ZC_OK;
+}
+
+zc_status do_adamw(const zc_adamw_cfg* c, const zc_adamw_tensor* t, int64_t count,
+                   const float* factor, const float* lr, const int64_t* step, hipStream_t s) {
+  const bool b8 = c->state == ZC_STATE_8BIT;
+  const bool master = count > 0 && t[0].master != nullptr;
+  if (master && c->p_dtype != ZC_BF16)
+    return fail(ZC_ERR_INVALID, "master weights go with bf16 weights");
+  std::vector<zc::AdamwTensor> list(static_cast<size_t>(count));
+  std::vector<Span> spans;
+  spans.reserve(static_cast<size_t>(count) * (b8 ? 7 : 5) + 3);
+  const int64_t ss = b8 ? 1 : 4;
+  for (int64_t i = 0; i < count; ++i) {
+    const zc_adamw_tensor& x = t[i];
+    const bool none = x.n == 0;
+    ZC_CHECK(check_elems(x.n, i));
+    if (!std::isfinite(x.weight_decay))
+      return fail(ZC_ERR_INVALID, "weight_decay of tensor %lld is not finite", (long long)i);
+    if ((x.master != nullptr) != master && !none)
+      return fail(ZC_ERR_INVALID, "tensor %lld: master weights are for all tensors or none", (long long)i);
+    ZC_CHECK(check_ptr(x.p, "p", none));
+    ZC_CHECK(check_ptr(x.g, "g", none));
+    ZC_CHECK(check_ptr(x.master, "master", true));
+    ZC_CHECK(check_ptr(x.m, "m", none));
+    ZC_CHECK(check_ptr(x.v, "v", none));
+    if (b8 && !none && (!x.m_scale || !x.v_scale))
+      return fail(ZC_ERR_INVALID, "tensor %lld: 8-bit states without scales", (long long)i);
+    ZC_CHECK(check_scalar(x.m_scale, 4, "m_scale"));
+    ZC_CHECK(check_scalar(x.v_scale, 4, "v_scale"));
+    if (!b8 && (x.m_scale || x.v_scale))
+      return fail(ZC_ERR_INVALID, "tensor %lld: scales go with 8-bit states", (long long)i);
+    list[static_cast<size_t>(i)] = zc::AdamwTensor{x.p, x.g, x.master, x.m, x.v, x.m_scale, x.v_scale,
+                                                   x.n, x.weight_decay};
+    const int64_t blocks = (x.n + 127) / 128 * 4;
+    add_span(spans, x.p, x.n * dtype_size(c->p_dtype), i, "p", true);
+    add_span(spans, x.g, x.n * dtype_size(c->g_dtype), i, "g", false);
+    add_span(spans, x.master, x.n * 4, i, "master", true);
+    add_span(spans, x.m, x.n * ss, i, "m", true);
+    add_span(spans, x.v, x.n * ss, i, "v", true);
+    add_span(spans, x.m_scale, blocks, i, "m_scale", true);
+    add_span(spans, x.v_scale, blocks, i, "v_scale", true);
+  }
+  add_span(spans, factor, 4, -1, "factor", false);
+  add_span(spans, lr, 4, -1, "lr", false);
+  add_span(spans, step, 8, -1, "step", false);
+  ZC_CHECK(check_spans(spans));
+  const zc::AdamwScalars sc{c->lr, c->beta1, c->beta2, c->step, factor, lr, step,
+                            static_cast<float>(c->eps), c->seed};
+  ZC_LAUNCH(ZC_PH_ADAMW,
+            zc::launch_adamw(list.data(), count, c->p_dtype == ZC_BF16, c->g_dtype == ZC_BF16, master,
+                             b8, c->rounding == ZC_ROUND_STOCHASTIC, sc, s),
+            "AdamW launch");
+  return ZC_OK;
+}
+
+// A list too long for the host's memory is refused, not thrown through C.
+template <typename F>
+zc_status no_throw(F&& f) {
+  try {
+    return f();
+  } catch (...) {
+    return fail(ZC_ERR_INVALID, "no host memory for a list of tensors");
+  }
+}
+
 // Bytes of one set of expert weights in the layer's layout.
 int64_t weight_set_bytes(const zc_moe_desc* d) {
   const int64_t n = d->N * d->I * d->d;
@@ -1368,6 +1550,43 @@ zc_status zc_rmsnorm_backward(const zc_norm_desc* desc, const void* dy, const vo
   return ZC_OK;
 }
 
+size_t zc_grad_norm_workspace_size(const zc_grad_tensor* tensors, int64_t count, int g_dtype) {
+  size_t bytes = 0;
+  no_throw([&]() -> zc_status {
+    ZC_CHECK(check_dtype(g_dtype, "g_dtype"));
+    ZC_CHECK(check_count(tensors, count));
+    for (int64_t i = 0; i < count; ++i) ZC_CHECK(check_elems(tensors[i].n, i));
+    bytes = static_cast<size_t>(Grads(tensors, count, g_dtype == ZC_BF16).ws_bytes);
+    return ZC_OK;
+  });
+  return bytes;
+}
+
+zc_status zc_grad_norm(const zc_grad_tensor* tensors, int64_t count, int g_dtype, double max_norm,
+                       float* out, int64_t* step, void* ws, size_t ws_bytes, void* stream) {
+  ZC_CHECK(check_grads(tensors, count, g_dtype));
+  if (!(max_norm > 0.0)) return fail(ZC_ERR_INVALID, "max_norm=%g is not positive", max_norm);
+  if (!out) return fail(ZC_ERR_INVALID, "out is NULL");
+  ZC_CHECK(check_scalar(out, 4, "out"));
+  ZC_CHECK(check_scalar(step, 8, "step"));
+  return no_throw([&] {
+    return do_grad_norm(tensors, count, g_dtype, max_norm, out, step, ws, ws_bytes,
+                        static_cast<hipStream_t>(stream));
+  });
+}
+
+zc_status zc_adamw_step(const zc_adamw_cfg* cfg, const zc_adamw_tensor* tensors, int64_t count,
+                        const float* factor, const float* lr, const int64_t* step, void* stream) {
+  ZC_CHECK(check_adamw(cfg, step != nullptr));
+  ZC_CHECK(check_count(tensors, count));
+  ZC_CHECK(check_scalar(factor, 4, "factor"));
+  ZC_CHECK(check_scalar(lr, 4, "lr"));
+  ZC_CHECK(check_scalar(step, 8, "step"));
+  return no_throw([&] {
+    return do_adamw(cfg, tensors, count, factor, lr, step, static_cast<hipStream_t>(stream));
+  });
+}
+
 zc_status zc_moe_profile(int on) {
   std::lock_guard<std::mutex> lk(g_prof_mu);
   if (!on) drop_records();
@@ -1404,7 +1623,7 @@ const char* zc_moe_phase_name(int phase) {
       "bwd_combine", "bwd_down_dh", "bwd_down_dw", "bwd_gate_up_dx", "bwd_gate_up_dw",
       "bwd_router_dw", "bwd_router_dx", "bwd_dx_gather", "bias_update", "tile_offsets",
       "lb_loss", "lb_coef", "route_stats", "accumulate_counts", "quantize", "bwd_gather",
-      "norm", "norm_bwd", "seq_balance"};
+      "norm", "norm_bwd", "seq_balance", "grad_norm", "adamw"};
   return (phase >= 0 && phase < ZC_NUM_PHASES) ? names[phase] : "";
 }
 

@@ -1,0 +1,485 @@
+// What follows a backward pass: the norm of all gradients with the factor that
+// clips them, and an AdamW step over many tensors, states in 32 or in 8 bits.
+//
+//   norm   = sqrt(sum of g^2), factor = min(1, max_norm / norm)
+//   g'     = factor g
+//   m      = b1 m + (1 - b1) g'            v = b2 v + (1 - b2) g'^2
+//   p      = p (1 - lr wd) - lr / (1 - b1^t) m / (sqrt(v / (1 - b2^t)) + eps)
+// all in fp32 (the sum of squares in binary64), each result rounded once to where
+// it is kept.
+//
+// 8-bit states: 128 values share an fp32 scale s = max / 448, and a state is an
+// E4M3 code times s; for v the codes are of sqrt(v), which halves the range of
+// exponents they have to span, and no positive v becomes 0 (the smallest code
+// instead: m / sqrt(v) would leave all bounds).  Rounded to nearest a state moves
+// only where a step changes it by half a code's distance, 3 to 6 %, which at b2
+// near 1 it hardly ever does; rounded stochastically (down after adding a random
+// part of a code's distance) it follows on average.  bf16 weights without an fp32
+// copy lose small steps alike and are rounded alike.  The random bits are a
+// function of seed, step, tensor and element.
+//
+// Both are bound by HBM: every array goes through once, nothing is reused.
+#include "zc_common.h"
+
+namespace zc {
+namespace {
+
+constexpr int kThreads = 256;
+
+// Tensors of one launch, passed by value: nothing has to be copied to the device
+// before it, and a captured launch holds them.
+constexpr int kNormTensors = 128;
+constexpr int kAdamTensors = 46;
+
+struct NormArgs {
+  const void* g[kNormTensors];
+  int64_t n[kNormTensors];
+  int32_t first[kNormTensors + 1];  // first chunk of each
+  int32_t count;
+  double* part;                     // a sum for each chunk
+};
+
+struct AdamArgs {
+  AdamwTensor t[kAdamTensors];
+  int32_t first[kAdamTensors + 1];
+  int32_t count;
+  int32_t passes;  // rounds of kThreads vectors in a chunk
+  int32_t base;    // number of t[0] in the whole list
+  AdamwScalars s;
+};
+static_assert(sizeof(NormArgs) <= 4096 && sizeof(AdamArgs) <= 4096, "kernel arguments");
+
+// The tensor that chunk b belongs to.
+template <typename A>
+__device__ __forceinline__ int tensor_of(const A& a, int b) {
+  int lo = 0, hi = a.count;  // first[lo] <= b < first[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (a.first[mid] <= b) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+// ------------------------------------------------------------------ norm
+// Sum over the threads of a workgroup in a fixed order (thread 0 gets it).
+template <int NT>
+__device__ __forceinline__ double block_sum(double v, double* s_red) {
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o);
+  if ((threadIdx.x & 63) == 0) s_red[threadIdx.x >> 6] = v;
+  __syncthreads();
+  v = s_red[0];
+#pragma unroll
+  for (int w = 1; w < NT / 64; ++w) v += s_red[w];
+  return v;
+}
+
+template <typename T>
+__global__ __launch_bounds__(kThreads) void sqsum_kernel(NormArgs a, int chunk) {
+  constexpr int V = V16<T>::n;
+  __shared__ double s_red[kThreads / 64];
+  const int i = tensor_of(a, blockIdx.x);
+  const T* g = static_cast<const T*>(a.g[i]);
+  const int64_t n = a.n[i];
+  const int64_t begin = static_cast<int64_t>(blockIdx.x - a.first[i]) * chunk;
+  const int64_t end = begin + chunk < n ? begin + chunk : n;
+  double sum = 0.0;
+  int64_t j = begin + threadIdx.x * V;
+  for (; j + 3 * kThreads * V + V <= end; j += 4 * kThreads * V) {
+    typename V16<T>::raw_t w[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) w[u] = V16<T>::ld_raw_once(g + j + u * kThreads * V);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      float f[V];
+      V16<T>::unpack(w[u], f);
+#pragma unroll
+      for (int e = 0; e < V; ++e) sum = fma(static_cast<double>(f[e]), static_cast<double>(f[e]), sum);
+    }
+  }
+  for (; j < end; j += kThreads * V) {
+    for (int e = 0; e < V && j + e < end; ++e) {
+      const double f = Elem<T>::ld(g + j + e);
+      sum = fma(f, f, sum);
+    }
+  }
+  sum = block_sum<kThreads>(sum, s_red);
+  if (threadIdx.x == 0) a.part[blockIdx.x] = sum;
+}
+
+// out = [norm, factor]; one more step where the norm is finite.
+__global__ __launch_bounds__(1024) void norm_finish_kernel(const double* __restrict__ part,
+                                                           int64_t n, double max_norm,
+                                                           float* __restrict__ out,
+                                                           int64_t* __restrict__ step) {
+  __shared__ double s_red[1024 / 64];
+  double sum = 0.0;
+  for (int64_t i = threadIdx.x; i < n; i += 1024) sum += part[i];
+  sum = block_sum<1024>(sum, s_red);
+  if (threadIdx.x != 0) return;
+  const double norm = sqrt(sum);
+  const bool fine = norm <= 1.7976931348623157e308;
+  out[0] = static_cast<float>(norm);
+  out[1] = !fine ? 0.f : norm > max_norm ? static_cast<float>(max_norm / norm) : 1.f;
+  if (step && fine) *step += 1;
+}
+
+// ----------------------------------------------------------------- AdamW
+__device__ __forceinline__ uint32_t mix(uint32_t x) {
+  x *= 0x9E3779B1u;
+  x ^= x >> 15;
+  x *= 0x85EBCA77u;
+  return x ^ (x >> 13);
+}
+
+// Largest of the 16 lanes of a row (a block of 128 values), in every lane.
+__device__ __forceinline__ float row_max(float v) {
+  auto turn = [](float f, auto c) {
+    return __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(f), decltype(c)::value, 0xf,
+                                                       0xf, true));
+  };
+  v = fmaxf(v, turn(v, std::integral_constant<int, 0x128>{}));  // row_ror 8, 4, 2, 1
+  v = fmaxf(v, turn(v, std::integral_constant<int, 0x124>{}));
+  v = fmaxf(v, turn(v, std::integral_constant<int, 0x122>{}));
+  return fmaxf(v, turn(v, std::integral_constant<int, 0x121>{}));
+}
+
+// E4M3 code of |q| <= 448 rounded down after r of a code's distance is added,
+// 0 <= r < 1.
+__device__ __forceinline__ uint32_t e4m3_down(float q, float r) {
+  const uint32_t a = __float_as_uint(q) & 0x7fffffffu;
+  const uint32_t eb = max(a >> 23, 121u);  // below 2^-6 the distance stays 2^-9
+  const float n = __uint_as_float(a) * __uint_as_float((257u - eb) << 23) + r;
+  uint32_t c = min(8u * (eb - 121u) + static_cast<uint32_t>(n), 0x7eu);
+  if (a > 0x7f800000u) c = 0x7fu;
+  return c | (__float_as_uint(q) >> 24 & 0x80u);
+}
+
+// Eight values of a block as codes and the block's scale.
+template <bool SR, bool ROOT>
+__device__ __forceinline__ uint2 encode(const float* f, const uint32_t* noise, float& scale) {
+  float amax = 0.f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(f[e]));
+  scale = fmaxf(row_max(amax) * (1.f / 448.f), 0x1p-120f);
+  // f / scale, correctly rounded, with one division for the eight: the quotient by
+  // the reciprocal, then its remainder
+  const float inv = 1.f / scale;
+  float q[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float t = f[e] * inv;
+    q[e] = fmaf(fmaf(-t, scale, f[e]), inv, t);
+  }
+  uint32_t w[2] = {0u, 0u};
+  if constexpr (SR) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const uint32_t bits = ROOT ? noise[e] >> 16 : noise[e] & 0xffffu;
+      uint32_t c = e4m3_down(q[e], static_cast<float>(bits) * 0x1p-16f);
+      if (ROOT && c == 0u && f[e] > 0.f) c = 1u;
+      w[e / 4] |= c << (8 * (e % 4));
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; e += 4) {
+      int c = __builtin_amdgcn_cvt_pk_fp8_f32(q[e], q[e + 1], 0, false);
+      w[e / 4] = __builtin_amdgcn_cvt_pk_fp8_f32(q[e + 2], q[e + 3], c, true);
+    }
+    if constexpr (ROOT) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if ((w[e / 4] >> (8 * (e % 4)) & 0xffu) == 0u && f[e] > 0.f) w[e / 4] |= 1u << (8 * (e % 4));
+    }
+  }
+  return make_uint2(w[0], w[1]);
+}
+
+__device__ __forceinline__ void decode(uint2 w, float scale, float* f) {
+  const uint32_t v[2] = {w.x, w.y};
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8(v[i], false);
+    const auto hi = __builtin_amdgcn_cvt_pk_f32_fp8(v[i], true);
+    f[4 * i] = lo[0] * scale;
+    f[4 * i + 1] = lo[1] * scale;
+    f[4 * i + 2] = hi[0] * scale;
+    f[4 * i + 3] = hi[1] * scale;
+  }
+}
+
+// W consecutive elements, or the first `left` of them.
+template <typename T, int W>
+__device__ __forceinline__ void load(const T* p, int left, float* f) {
+  if (left >= W) {
+    if constexpr (sizeof(T) == 2 && W == 4) {
+      const uint2 w = *reinterpret_cast<const uint2*>(p);
+      f[0] = __uint_as_float(w.x << 16);
+      f[1] = __uint_as_float(w.x & 0xffff0000u);
+      f[2] = __uint_as_float(w.y << 16);
+      f[3] = __uint_as_float(w.y & 0xffff0000u);
+    } else {
+#pragma unroll
+      for (int i = 0; i < W / V16<T>::n; ++i)
+        V16<T>::unpack(V16<T>::ld_raw_once(p + i * V16<T>::n), f + i * V16<T>::n);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < W; ++e) f[e] = e < left ? Elem<T>::ld(p + e) : 0.f;
+  }
+}
+template <typename T, int W>
+__device__ __forceinline__ void store(T* p, int left, const float* f) {
+  if (left >= W) {
+    if constexpr (sizeof(T) == 2 && W == 4) {
+      *reinterpret_cast<uint2*>(p) =
+          make_uint2(f2bf(f[0]) | static_cast<uint32_t>(f2bf(f[1])) << 16,
+                     f2bf(f[2]) | static_cast<uint32_t>(f2bf(f[3])) << 16);
+    } else {
+#pragma unroll
+      for (int i = 0; i < W / V16<T>::n; ++i) V16<T>::store(p + i * V16<T>::n, f + i * V16<T>::n);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < W; ++e)
+      if (e < left) Elem<T>::st(p + e, f[e]);
+  }
+}
+__device__ __forceinline__ uint2 load_codes(const uint8_t* p, int left) {
+  if (left >= 8) return *reinterpret_cast<const uint2*>(p);
+  uint32_t w[2] = {0u, 0u};
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (e < left) w[e / 4] |= static_cast<uint32_t>(p[e]) << (8 * (e % 4));
+  return make_uint2(w[0], w[1]);
+}
+__device__ __forceinline__ void store_codes(uint8_t* p, int left, uint2 c) {
+  if (left >= 8) {
+    *reinterpret_cast<uint2*>(p) = c;
+    return;
+  }
+  const uint32_t w[2] = {c.x, c.y};
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (e < left) p[e] = static_cast<uint8_t>(w[e / 4] >> (8 * (e % 4)));
+}
+
+// 1 - b^t in binary64 (relative error 2^-53 / (1 - b) at most, from the
+// subtraction).
+__device__ __forceinline__ double one_minus_power(double b, int64_t t) {
+  double r = 1.0;
+  for (; t > 0; t >>= 1) {
+    if (t & 1) r *= b;
+    b *= b;
+  }
+  return 1.0 - r;
+}
+
+// P weights, G gradients; MASTER: fp32 weights with bf16 copies; B8: 8-bit
+// states; SR: stochastic rounding of what has fewer than 32 bits.
+template <typename P, typename G, bool MASTER, bool B8, bool SR>
+__global__ __launch_bounds__(kThreads) void adamw_kernel(AdamArgs a) {
+  constexpr int W = B8 ? 8 : 4;  // elements of a thread and pass
+  const AdamwScalars& s = a.s;
+  const float factor = s.factor ? *s.factor : 1.f;
+  if (factor == 0.f) return;
+  const int64_t t = s.step_ptr ? *s.step_ptr : s.step;
+  const double lr = s.lr_ptr ? static_cast<double>(*s.lr_ptr) : s.lr;
+  const float rate = static_cast<float>(lr / one_minus_power(s.beta1, t > 1 ? t : 1));
+  const float root = static_cast<float>(1.0 / sqrt(one_minus_power(s.beta2, t > 1 ? t : 1)));
+  const float b1 = static_cast<float>(s.beta1), c1 = static_cast<float>(1.0 - s.beta1);
+  const float b2 = static_cast<float>(s.beta2), c2 = static_cast<float>(1.0 - s.beta2);
+  const float eps = s.eps;
+
+  const int i = tensor_of(a, blockIdx.x);
+  const AdamwTensor& x = a.t[i];
+  const float keep = static_cast<float>(1.0 - lr * x.weight_decay);
+  const int64_t n = x.n;
+  int64_t j = (static_cast<int64_t>(blockIdx.x - a.first[i]) * a.passes * kThreads + threadIdx.x) * W;
+  const uint32_t key0 = (s.seed + 0x9E3779B9u * static_cast<uint32_t>(a.base + i)) ^
+                        static_cast<uint32_t>(t) * 0x85EBCA77u;
+  for (int pass = 0; pass < a.passes; ++pass, j += kThreads * W) {
+    // (a block of 8-bit states lies in one row of lanes: all of it is here, or none)
+    if (j >= n && (!B8 || (j & ~int64_t(127)) >= n)) break;
+    const int left = j >= n ? 0 : n - j < W ? static_cast<int>(n - j) : W;
+    float g[W], p[W], m[W], v[W];
+    load<G, W>(static_cast<const G*>(x.g) + j, left, g);
+    if constexpr (MASTER)
+      load<float, W>(x.master + j, left, p);
+    else
+      load<P, W>(static_cast<const P*>(x.p) + j, left, p);
+    if constexpr (B8) {
+      const int64_t blk = j >> 7;
+      decode(load_codes(static_cast<const uint8_t*>(x.m) + j, left), x.m_scale[blk], m);
+      decode(load_codes(static_cast<const uint8_t*>(x.v) + j, left), x.v_scale[blk], v);
+#pragma unroll
+      for (int e = 0; e < W; ++e) v[e] *= v[e];
+    } else {
+      load<float, W>(static_cast<const float*>(x.m) + j, left, m);
+      load<float, W>(static_cast<const float*>(x.v) + j, left, v);
+    }
+#pragma unroll
+    for (int e = 0; e < W; ++e) {
+      // (each operation rounded by itself, so that a state does not depend on what
+      // the compiler fuses: the codes of two builds are the same)
+#pragma clang fp contract(off)
+      g[e] *= factor;
+      m[e] = b1 * m[e] + c1 * g[e];
+      v[e] = b2 * v[e] + c2 * (g[e] * g[e]);
+      const float r = sqrtf(v[e]);
+      p[e] = p[e] * keep - rate * (m[e] / (r * root + eps));
+      if constexpr (B8) v[e] = r;
+    }
+    uint32_t noise[W];
+    if constexpr (SR) {
+      const uint32_t key = key0 + 0xC2B2AE3Du * static_cast<uint32_t>(j >> 32);
+#pragma unroll
+      for (int e = 0; e < W; ++e) noise[e] = mix((static_cast<uint32_t>(j) + e) ^ key);
+    }
+    if constexpr (MASTER) store<float, W>(x.master + j, left, p);
+    if constexpr (SR && sizeof(P) == 2 && !MASTER) {
+#pragma unroll
+      for (int e = 0; e < W; ++e) {
+        const uint32_t bits = __float_as_uint(p[e]);
+        if ((bits & 0x7f800000u) != 0x7f800000u)
+          p[e] = __uint_as_float(bits + ((noise[e] * 0xC2B2AE3Du) >> 16) & 0xffff0000u);
+      }
+    }
+    store<P, W>(static_cast<P*>(x.p) + j, left, p);
+    if constexpr (B8) {
+      const int64_t blk = j >> 7;
+      float sm, sv;
+      const uint2 cm = encode<SR, false>(m, noise, sm), cv = encode<SR, true>(v, noise, sv);
+      store_codes(static_cast<uint8_t*>(x.m) + j, left, cm);
+      store_codes(static_cast<uint8_t*>(x.v) + j, left, cv);
+      if ((j & 127) == 0) {
+        x.m_scale[blk] = sm;
+        x.v_scale[blk] = sv;
+      }
+    } else {
+      store<float, W>(static_cast<float*>(x.m) + j, left, m);
+      store<float, W>(static_cast<float*>(x.v) + j, left, v);
+    }
+  }
+}
+
+template <typename P, typename G, bool MASTER>
+void adamw_pick(bool b8, bool sr, dim3 grid, hipStream_t s, const AdamArgs& a) {
+  if (b8 && sr)
+    hipLaunchKernelGGL((adamw_kernel<P, G, MASTER, true, true>), grid, dim3(kThreads), 0, s, a);
+  else if (b8)
+    hipLaunchKernelGGL((adamw_kernel<P, G, MASTER, true, false>), grid, dim3(kThreads), 0, s, a);
+  else if (sr && sizeof(P) == 2 && !MASTER)
+    hipLaunchKernelGGL((adamw_kernel<P, G, MASTER, false, sizeof(P) == 2 && !MASTER>), grid,
+                       dim3(kThreads), 0, s, a);
+  else  // nothing to round stochastically
+    hipLaunchKernelGGL((adamw_kernel<P, G, MASTER, false, false>), grid, dim3(kThreads), 0, s, a);
+}
+
+// Elements of a chunk of the norm: large ones where there are enough of them for
+// the card.
+int norm_chunk(int64_t total, bool bf16) {
+  const int step = 4 * kThreads * (bf16 ? 8 : 4);
+  int c = step;
+  while (c < 32 * step && total / (2 * c) >= 2048) c *= 2;
+  return c;
+}
+
+}  // namespace
+
+int64_t grad_norm_parts(const int64_t* n, int64_t count, bool bf16) {
+  int64_t total = 0, parts = 0;
+  for (int64_t i = 0; i < count; ++i) total += n[i];
+  const int64_t chunk = norm_chunk(total, bf16);
+  for (int64_t i = 0; i < count; ++i) parts += (n[i] + chunk - 1) / chunk;
+  return parts;
+}
+
+hipError_t launch_grad_norm(const void* const* g, const int64_t* n, int64_t count, bool bf16,
+                            double max_norm, double* part, float* out, int64_t* step,
+                            hipStream_t s) {
+  int64_t total = 0;
+  for (int64_t i = 0; i < count; ++i) total += n[i];
+  const int chunk = norm_chunk(total, bf16);
+  NormArgs a;
+  int64_t parts = 0;
+  a.count = 0;
+  a.first[0] = 0;
+  auto flush = [&]() -> hipError_t {
+    const int blocks = a.first[a.count];
+    if (blocks) {
+      a.part = part + parts;
+      if (bf16)
+        hipLaunchKernelGGL(sqsum_kernel<bf16_t>, dim3(blocks), dim3(kThreads), 0, s, a, chunk);
+      else
+        hipLaunchKernelGGL(sqsum_kernel<float>, dim3(blocks), dim3(kThreads), 0, s, a, chunk);
+    }
+    parts += blocks;
+    a.count = 0;
+    return hipGetLastError();
+  };
+  for (int64_t i = 0; i < count; ++i) {
+    if (n[i] == 0) continue;
+    const int64_t blocks = (n[i] + chunk - 1) / chunk;
+    if (a.count == kNormTensors || (a.count && a.first[a.count] + blocks >= (int64_t(1) << 24))) {
+      const hipError_t e = flush();
+      if (e != hipSuccess) return e;
+    }
+    a.g[a.count] = g[i];
+    a.n[a.count] = n[i];
+    a.first[a.count + 1] = static_cast<int32_t>(a.first[a.count] + blocks);
+    ++a.count;
+  }
+  const hipError_t e = flush();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(norm_finish_kernel, dim3(1), dim3(1024), 0, s, part, parts, max_norm, out, step);
+  return hipGetLastError();
+}
+
+hipError_t launch_adamw(const AdamwTensor* t, int64_t count, bool bf16, bool g_bf16, bool master,
+                        bool b8, bool sr, const AdamwScalars& scalars, hipStream_t s) {
+  const int W = b8 ? 8 : 4;
+  int64_t total = 0;
+  for (int64_t i = 0; i < count; ++i) total += t[i].n;
+  AdamArgs a;
+  a.s = scalars;
+  a.passes = 1;
+  while (a.passes < 8 && total / (int64_t(2) * a.passes * kThreads * W) >= 4096) a.passes *= 2;
+  const int64_t chunk = int64_t(a.passes) * kThreads * W;
+  a.count = 0;
+  a.first[0] = 0;
+  auto flush = [&]() -> hipError_t {
+    const dim3 grid(a.first[a.count]);
+    if (a.count) {
+      if (!bf16)
+        adamw_pick<float, float, false>(b8, sr, grid, s, a);
+      else if (g_bf16 && master)
+        adamw_pick<bf16_t, bf16_t, true>(b8, sr, grid, s, a);
+      else if (g_bf16)
+        adamw_pick<bf16_t, bf16_t, false>(b8, sr, grid, s, a);
+      else if (master)
+        adamw_pick<bf16_t, float, true>(b8, sr, grid, s, a);
+      else
+        adamw_pick<bf16_t, float, false>(b8, sr, grid, s, a);
+    }
+    a.count = 0;
+    return hipGetLastError();
+  };
+  for (int64_t i = 0; i < count; ++i) {
+    if (t[i].n == 0) continue;
+    const int64_t blocks = (t[i].n + chunk - 1) / chunk;
+    // (a launch holds consecutive tensors, so that base + index is a tensor's number)
+    if (a.count && (a.count == kAdamTensors || a.base + a.count != i ||
+                    a.first[a.count] + blocks >= (int64_t(1) << 24))) {
+      const hipError_t e = flush();
+      if (e != hipSuccess) return e;
+    }
+    if (a.count == 0) a.base = static_cast<int32_t>(i);
+    a.t[a.count] = t[i];
+    a.first[a.count + 1] = static_cast<int32_t>(a.first[a.count] + blocks);
+    ++a.count;
+  }
+  return flush();
+}
+
+}  // namespace zc

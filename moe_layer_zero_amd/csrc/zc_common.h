@@ -393,6 +393,37 @@ hipError_t launch_norm_bwd(const T* dy, const T* r, const T* gamma, const float*
                            const T* dres, T* dr, T* dgamma, float* part, int64_t Tn, int d,
                            hipStream_t s);
 
+// Norm of all gradients and the factor that clips them (optim.hip): out = [norm,
+// factor], step (nullable) advanced where the norm is finite; part:
+// grad_norm_parts(...) doubles.
+int64_t grad_norm_parts(const int64_t* n, int64_t count, bool bf16);
+hipError_t launch_grad_norm(const void* const* g, const int64_t* n, int64_t count, bool bf16,
+                            double max_norm, double* part, float* out, int64_t* step,
+                            hipStream_t s);
+
+// An AdamW step over `count` tensors of fewer than 2^36 elements each (optim.hip).
+// master: fp32 weights, p their bf16 copies; b8: m and v E4M3 codes with a scale
+// for each 128; sr: stochastic rounding.
+struct AdamwTensor {
+  void* p;
+  const void* g;
+  float* master;
+  void *m, *v;
+  float *m_scale, *v_scale;
+  int64_t n;
+  double weight_decay;
+};
+struct AdamwScalars {
+  double lr, beta1, beta2;
+  int64_t step;
+  const float *factor, *lr_ptr;  // device, nullable
+  const int64_t* step_ptr;       // device, nullable
+  float eps;
+  uint32_t seed;
+};
+hipError_t launch_adamw(const AdamwTensor* t, int64_t count, bool bf16, bool g_bf16, bool master,
+                        bool b8, bool sr, const AdamwScalars& scalars, hipStream_t s);
+
 // Bias update, Eq.(2) of section 2.1.1.
 hipError_t launch_pid(int N, int K, const int32_t* counts, int64_t T_all, double mu, double K_e,
                       float* bias, hipStream_t s);

@@ -24,6 +24,9 @@ ZC_OP_EXPERTS = 5
 ZC_WEIGHTS_ROWMAJOR, ZC_WEIGHTS_PACKED, ZC_WEIGHTS_MXFP8 = 0, 1, 2
 ZC_WEIGHTS_INT4_G32, ZC_WEIGHTS_INT4_G64, ZC_WEIGHTS_INT4_G128 = 4, 5, 6
 ZC_PACK_GATE_UP, ZC_PACK_DOWN = 0, 1
+ZC_STATE_F32, ZC_STATE_8BIT = 0, 1
+ZC_ROUND_NEAREST, ZC_ROUND_STOCHASTIC = 0, 1
+STATE_BLOCK = 128  # values that share a scale of the 8-bit states
 
 # Every symbol include/zc_moe.h declares.
 EXPORTS = ("zc_moe_workspace_size", "zc_moe_saved_size", "zc_moe_route", "zc_moe_forward",
@@ -34,10 +37,11 @@ EXPORTS = ("zc_moe_workspace_size", "zc_moe_saved_size", "zc_moe_route", "zc_moe
            "zc_moe_experts", "zc_moe_int4_weight_bytes", "zc_moe_int4_quantize",
            "zc_moe_int4_pack",
            "zc_rmsnorm_forward", "zc_rmsnorm_workspace_size", "zc_rmsnorm_backward",
+           "zc_grad_norm_workspace_size", "zc_grad_norm", "zc_adamw_step",
            "zc_moe_profile",
            "zc_moe_profile_read",
            "zc_moe_phase_name", "zc_status_string", "zc_last_error")
-ZC_NUM_PHASES = 25
+ZC_NUM_PHASES = 27
 
 
 class ZcError(RuntimeError):
@@ -65,6 +69,23 @@ class zc_route_buf(C.Structure):
 
 class zc_norm_desc(C.Structure):
     _fields_ = [("T", C.c_int64), ("d", C.c_int64), ("dtype", C.c_int32), ("eps", C.c_float)]
+
+
+class zc_grad_tensor(C.Structure):
+    _fields_ = [("g", C.c_void_p), ("n", C.c_int64)]
+
+
+class zc_adamw_tensor(C.Structure):
+    _fields_ = [("p", C.c_void_p), ("g", C.c_void_p), ("master", C.c_void_p), ("m", C.c_void_p),
+                ("v", C.c_void_p), ("m_scale", C.c_void_p), ("v_scale", C.c_void_p),
+                ("n", C.c_int64), ("weight_decay", C.c_double)]
+
+
+class zc_adamw_cfg(C.Structure):
+    _fields_ = [("p_dtype", C.c_int32), ("g_dtype", C.c_int32), ("state", C.c_int32),
+                ("rounding", C.c_int32), ("lr", C.c_double), ("beta1", C.c_double),
+                ("beta2", C.c_double), ("eps", C.c_double), ("step", C.c_int64),
+                ("seed", C.c_uint32)]
 
 
 _LIB = None
@@ -112,7 +133,13 @@ def lib() -> C.CDLL:
         L.zc_rmsnorm_workspace_size.argtypes = [NP]
         L.zc_rmsnorm_workspace_size.restype = sz
         L.zc_rmsnorm_backward.argtypes = [NP, v, v, v, v, v, v, v, v, sz, v]
-        for f in ("zc_moe_experts", "zc_moe_int4_quantize", "zc_moe_int4_pack",
+        GT = C.POINTER(zc_grad_tensor)
+        L.zc_grad_norm_workspace_size.argtypes = [GT, i64, C.c_int]
+        L.zc_grad_norm_workspace_size.restype = sz
+        L.zc_grad_norm.argtypes = [GT, i64, C.c_int, C.c_double, v, v, v, sz, v]
+        L.zc_adamw_step.argtypes = [C.POINTER(zc_adamw_cfg), C.POINTER(zc_adamw_tensor), i64, v, v, v,
+                                    v]
+        for f in ("zc_grad_norm", "zc_adamw_step", "zc_moe_experts", "zc_moe_int4_quantize", "zc_moe_int4_pack",
                   "zc_moe_backward_scores", "zc_moe_seq_balance", "zc_rmsnorm_forward", "zc_rmsnorm_backward",
                   "zc_moe_route", "zc_moe_forward", "zc_moe_forward_noalloc",
                   "zc_moe_backward", "zc_moe_lb_loss",
@@ -699,3 +726,168 @@ def zc_rmsnorm_backward(desc: NormDesc, dy, r, gamma, rstd, dr, dgamma, dres=Non
     n = ws.numel() * ws.element_size()
     a.run(lib().zc_rmsnorm_backward, C.byref(desc.c()), *p, a(ws, ws.shape, ws.dtype, "ws"), n,
           stream=stream)
+
+
+# ------------------------------------------------------- the weights' step
+def _list_of(tensors, name, dtypes, like=None):
+    """tensors as a list of contiguous GPU tensors of one dtype (among dtypes) on
+    one GPU; like: another list, whose sizes they have."""
+    out = list(tensors)
+    if like is not None and len(out) != len(like):
+        raise ValueError(f"{name}: {len(out)} tensors, expected {len(like)}")
+    for i, t in enumerate(out):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name}[{i}]: expected a torch.Tensor")
+        if t.dtype not in dtypes or t.dtype != out[0].dtype:
+            raise ValueError(f"{name}[{i}]: dtype {t.dtype}, expected one of {dtypes} and the same for all")
+        if not t.is_cuda:
+            raise ValueError("tensors passed to the HIP library must live on the GPU")
+        if not t.is_contiguous():
+            raise ValueError("tensors passed to the HIP library must be contiguous")
+        if like is not None and t.numel() != like[i]:
+            raise ValueError(f"{name}[{i}]: {t.numel()} elements, expected {like[i]}")
+    return out
+
+
+def _one_gpu(where, tensors):
+    dev = None
+    for t in tensors:
+        if dev is not None and t.get_device() != dev:
+            raise ValueError(f"{where}: tensors on GPU {dev} and on GPU {t.get_device()}")
+        dev = t.get_device()
+    return dev
+
+
+class TensorList:
+    """The gradients that zc_grad_norm takes: contiguous GPU tensors of one dtype
+    (bf16 or fp32).  Holds the tensors; their contents may change between calls."""
+
+    def __init__(self, tensors):
+        self.tensors = _list_of(tensors, "tensors", (torch.float32, torch.bfloat16))
+        self.device_index = _one_gpu("TensorList", self.tensors)
+        self.sizes = [t.numel() for t in self.tensors]
+        self.dtype = ZC_BF16 if self.tensors and self.tensors[0].dtype == torch.bfloat16 else ZC_F32
+        self._c = (zc_grad_tensor * len(self.tensors))(
+            *(zc_grad_tensor(t.data_ptr() or None, t.numel()) for t in self.tensors))
+
+    def __len__(self):
+        return len(self.tensors)
+
+
+def grad_norm_workspace(grads: TensorList, device=None) -> torch.Tensor:
+    n = int(lib().zc_grad_norm_workspace_size(grads._c, len(grads), grads.dtype))
+    if device is None:
+        device = "cuda" if grads.device_index is None else f"cuda:{grads.device_index}"
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=device)
+
+
+def zc_grad_norm(grads: TensorList, max_norm: float, out, step=None, ws=None, stream=None):
+    """Norm of all gradients and the factor that clips it to max_norm (inf: no
+    clipping) into out, fp32 [2]; the factor is 0 where the norm is not finite.
+    step (int64 [1]): one more unless it is.  out[1:] is what zc_adamw_step takes."""
+    a = _Args("zc_grad_norm")
+    a.dev = grads.device_index
+    p = a(out, (2,), torch.float32, "out"), a(step, (1,), torch.int64, "step")
+    if ws is None:
+        ws = _alloc(stream, grad_norm_workspace, grads, out.device)
+    n = ws.numel() * ws.element_size()
+    a.run(lib().zc_grad_norm, grads._c, len(grads), grads.dtype, float(max_norm), *p,
+          a(ws, ws.shape, ws.dtype, "ws"), n, stream=stream)
+
+
+@dataclass
+class AdamW:
+    """Settings of zc_adamw_step.  rounding: of 8-bit states, and of bf16 weights
+    without a copy in fp32."""
+    lr: float = 1e-3
+    beta1: float = 0.9
+    beta2: float = 0.95
+    eps: float = 1e-8
+    rounding: int = ZC_ROUND_NEAREST
+    seed: int = 0
+
+
+class AdamWTensors:
+    """The tensors of an AdamW step: weights (bf16 or fp32), gradients (the same
+    or fp32), states m and v, for bf16 weights where wanted their fp32 copies
+    master, and a weight decay for all or for each.  States: fp32, or
+    torch.float8_e4m3fn with m_scale and v_scale, fp32 [ceil(n / 128)] (v's codes
+    are of its square root); see adamw_tensors for a set that starts at zero.
+    Holds the tensors; gradients may be written anew between steps."""
+
+    def __init__(self, params, grads, m, v, master=None, m_scale=None, v_scale=None,
+                 weight_decay=0.0):
+        f32, bf, f8 = torch.float32, torch.bfloat16, torch.float8_e4m3fn
+        self.params = _list_of(params, "params", (f32, bf))
+        n = [t.numel() for t in self.params]
+        bf16 = bool(n) and self.params[0].dtype == bf
+        self.grads = TensorList(_list_of(grads, "grads", (bf, f32) if bf16 else (f32,), n))
+        self.m, self.v = _list_of(m, "m", (f32, f8), n), _list_of(v, "v", (f32, f8), n)
+        self.bits = 8 if n and self.m[0].dtype == f8 else 32
+        if n and self.v[0].dtype != self.m[0].dtype:
+            raise ValueError("m and v: both fp32 or both float8_e4m3fn")
+        blocks = [-(-k // STATE_BLOCK) for k in n]
+        if n and (self.bits == 8) != (m_scale is not None and v_scale is not None):
+            raise ValueError("m_scale and v_scale go with float8_e4m3fn states")
+        self.m_scale = None if m_scale is None else _list_of(m_scale, "m_scale", (f32,), blocks)
+        self.v_scale = None if v_scale is None else _list_of(v_scale, "v_scale", (f32,), blocks)
+        if master is not None and n and not bf16:
+            raise ValueError("master goes with bf16 weights")
+        self.master = None if master is None else _list_of(master, "master", (f32,), n)
+        decay = [float(weight_decay)] * len(n) if isinstance(weight_decay, (int, float)) \
+            else [float(w) for w in weight_decay]
+        if len(decay) != len(n):
+            raise ValueError(f"weight_decay: {len(decay)} values, expected {len(n)}")
+        every = [self.params, self.grads.tensors, self.master, self.m, self.v, self.m_scale, self.v_scale]
+        self.device_index = _one_gpu("AdamWTensors", [t for ts in every if ts is not None for t in ts])
+        none = [None] * len(n)
+        self._c = (zc_adamw_tensor * len(n))(
+            *(zc_adamw_tensor(*(None if t is None else t.data_ptr() or None for t in ts), k, w)
+              for *ts, k, w in zip(*(none if ts is None else ts for ts in every), n, decay)))
+        self._cfg = (ZC_BF16 if bf16 else ZC_F32, self.grads.dtype,
+                     ZC_STATE_8BIT if self.bits == 8 else ZC_STATE_F32)
+
+    def __len__(self):
+        return len(self.params)
+
+
+def adamw_tensors(params, grads, bits: int = 32, master: bool = False, weight_decay=0.0, stream=None):
+    """AdamWTensors with states of zeros in `bits` (32 or 8); master: with fp32
+    copies of the bf16 weights, made here."""
+    if bits not in (8, 32):
+        raise ValueError(f"states of {bits} bits: 8 or 32 are supported")
+    params = list(params)
+
+    def make():
+        f32 = torch.float32
+        zeros = lambda dt: [torch.zeros(p.shape, dtype=dt, device=p.device) for p in params]  # noqa: E731
+        kw = {}
+        if bits == 8:
+            # zeros of float8: bytes of zero
+            m, v = ([t.view(torch.float8_e4m3fn) for t in zeros(torch.uint8)] for _ in range(2))
+            for k in ("m_scale", "v_scale"):
+                kw[k] = [torch.zeros(-(-p.numel() // STATE_BLOCK), dtype=f32, device=p.device)
+                         for p in params]
+        else:
+            m, v = zeros(f32), zeros(f32)
+        if master:
+            kw["master"] = [p.to(f32) for p in params]
+        return AdamWTensors(params, grads, m, v, weight_decay=weight_decay, **kw)
+
+    return _alloc(stream, make)
+
+
+def zc_adamw_step(cfg: AdamW, tensors: AdamWTensors, step, factor=None, lr=None, stream=None):
+    """One AdamW step, in place.  step: an int, counted from 1, or int64 [1] on the
+    GPU; factor, lr (fp32 [1] on the GPU, or None): the gradients' factor, and a
+    learning rate in place of cfg's."""
+    a = _Args("zc_adamw_step")
+    a.dev = tensors.device_index
+    if not len(tensors):
+        return
+    on_gpu = isinstance(step, torch.Tensor)
+    p = (a(factor, (1,), torch.float32, "factor"), a(lr, (1,), torch.float32, "lr"),
+         a(step, (1,), torch.int64, "step") if on_gpu else None)
+    c = zc_adamw_cfg(*tensors._cfg, cfg.rounding, cfg.lr, cfg.beta1, cfg.beta2, cfg.eps,
+                     0 if on_gpu else int(step), cfg.seed & 0xFFFFFFFF)
+    a.run(lib().zc_adamw_step, C.byref(c), tensors._c, len(tensors), *p, stream=stream)
