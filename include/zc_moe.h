@@ -99,10 +99,14 @@ typedef struct {
  *      expert weights with a scale for each group of 32, 64 or 128 (see
  *      there).  Accepted by zc_moe_forward, zc_moe_forward_noalloc and
  *      zc_moe_experts for bf16 layers with d and I multiples of 128 and no
- *      saved buffer. */
+ *      saved buffer.
+ *  ZC_WEIGHTS_MXFP4_A8, _A4: the output of zc_moe_mxfp4_pack (the same for both):
+ *      MXFP4 expert weights, rows of x and h in MXFP8 (A8) or MXFP4 (A4) (see
+ *      there).  Accepted by the same calls for the same layers. */
 typedef enum {
   ZC_WEIGHTS_ROWMAJOR = 0, ZC_WEIGHTS_PACKED = 1, ZC_WEIGHTS_MXFP8 = 2,
-  ZC_WEIGHTS_INT4_G32 = 4, ZC_WEIGHTS_INT4_G64 = 5, ZC_WEIGHTS_INT4_G128 = 6
+  ZC_WEIGHTS_INT4_G32 = 4, ZC_WEIGHTS_INT4_G64 = 5, ZC_WEIGHTS_INT4_G128 = 6,
+  ZC_WEIGHTS_MXFP4_A8 = 8, ZC_WEIGHTS_MXFP4_A4 = 9
 } zc_weight_layout;
 
 /* Routing state: written by zc_moe_route / zc_moe_forward, read by
@@ -187,9 +191,9 @@ zc_status zc_moe_forward(const zc_moe_desc* desc, const void* x,
  * already: r as zc_moe_route wrote it for a layer of the same T, N, Z and K
  * (topk_idx, topk_gate, offsets, perm and inv are read, and trusted to be
  * consistent).  Inference: nothing is saved; any weight layout.  With MXFP8
- * weights, x_codes and x_scales (both or neither; NULL otherwise) are x as
- * zc_rmsnorm_forward quantized it, and the call's own quantization of x is
- * left out; the zero-computation experts return x itself.  Neither out nor ws
+ * or MXFP4_A8 weights, x_codes and x_scales (both or neither; NULL otherwise) are
+ * x as zc_rmsnorm_forward quantized it, with MXFP4_A4 weights as zc_mxfp4_quantize
+ * did, and the call's own quantization of x is left out; the zero-computation experts return x itself.  Neither out nor ws
  * (ZC_OP_EXPERTS bytes) may overlap an input or the other.  out is bit for bit
  * what zc_moe_forward gives on the same routing. */
 zc_status zc_moe_experts(const zc_moe_desc* desc, const void* x, const zc_route_buf* r,
@@ -407,6 +411,38 @@ zc_status zc_moe_int4_quantize(const zc_moe_desc* desc, int which, const void* s
                                void* scales, void* stream);
 zc_status zc_moe_int4_pack(const zc_moe_desc* desc, int which, const uint8_t* codes,
                            const void* scales, void* dst, void* stream);
+
+/* MXFP4, the 4-bit Microscaling format that the matrix cores take as it is: each
+ * run of 32 consecutive values of a row shares a scale 2^(S-127), S an 8-bit
+ * exponent (E8M0), and each value is a 4-bit E2M1 code (a sign, and 0, 0.5, 1, 1.5,
+ * 2, 3, 4 or 6) of value / 2^(S-127):
+ *   S = floor(log2 max|v|) - 2 + 127 (at least 0; 0 for an all-zero run);
+ *   code = nearest E2M1 value, ties to even, magnitudes above 6 clamped (an
+ *          infinity saturates).  A run that holds a NaN has S = 255 (NaN), codes 0.
+ * Natural layout: codes [R][C/2], two a byte, the even c in the low half; scales
+ * [R][C/32].
+ *  zc_mxfp4_quantize: R rows of C values (of dtype, a zc_dtype; C a multiple of 32,
+ *      R*C < 2^40) -> natural codes and scales; values (nullable, as src): what
+ *      they stand for, exactly (but for what dtype cannot hold: beyond its largest
+ *      value, infinity; below its smallest, rounded).  values may be src, in place. */
+zc_status zc_mxfp4_quantize(int64_t R, int64_t C, int dtype, const void* src, uint8_t* codes,
+                            uint8_t* scales, void* values, void* stream);
+
+/* MXFP4 expert weights (desc->weight_layout ZC_WEIGHTS_MXFP4_A8 or _A4, which take
+ * the same packed weights; dtype bf16, d and I multiples of 128): the matrix cores
+ * multiply them by rows x and h in MXFP8 (A8; the rules of zc_moe_quantize_weights)
+ * or in MXFP4 too (A4, at up to twice the rate, h and x in 4 bits), sums in fp32.  x
+ * is quantized once for each token, h from its fp32 values; the router, gates, the
+ * combine and the zero-computation experts (which return the unquantized x) stay in
+ * bf16/fp32.  Grids are not persistent: cu_limit does not size them.
+ *  zc_moe_mxfp4_pack: natural codes [N][R][C/2] and scales [N][R][C/32]
+ *      (zc_mxfp4_quantize of a weight set as N * R rows, or made elsewhere; which and
+ *      the matrix sizes are those of zc_moe_pack_weights) -> dst,
+ *      zc_moe_mxfp4_weight_bytes(desc, which) bytes, in an order private to this
+ *      library: what the forward takes.  No output may overlap an input. */
+size_t zc_moe_mxfp4_weight_bytes(const zc_moe_desc* desc, int which);
+zc_status zc_moe_mxfp4_pack(const zc_moe_desc* desc, int which, const uint8_t* codes,
+                            const uint8_t* scales, void* dst, void* stream);
 
 /* Root-mean-square norm with the residual's addition: the step in front of
  * the layer.  Row by row (T rows of d values, dtype a zc_dtype):

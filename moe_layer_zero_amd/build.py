@@ -22,7 +22,7 @@ OUT = os.path.join(HERE, "libzcmoe.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 SOURCES = ["api.hip", "router.hip", "dispatch.hip", "gemm.hip", "gemm_fwd.hip", "gemm_fwdp.hip",
-           "gemm_fwdq.hip", "gemm_int4.hip", "gemm_dw.hip", "gemm_rmw.hip", "combine.hip", "norm.hip",
+           "gemm_fwdq.hip", "gemm_int4.hip", "gemm_mx4.hip", "gemm_dw.hip", "gemm_rmw.hip", "combine.hip", "norm.hip",
            "balance.hip", "optim.hip", "pid.hip"]
 STRICT_FP = {"router.hip", "pid.hip"}
 # The persistent GEMMs claim tiles with one lane's atomic whose result is used

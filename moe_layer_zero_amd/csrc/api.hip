@@ -177,6 +177,21 @@ zc_status check_int4(const zc_moe_desc* d) {
   return ZC_OK;
 }
 
+// MXFP4 weights; their rows are MXFP4 too (A4) or MXFP8 (A8).
+bool mxfp4(const zc_moe_desc* d) {
+  return d->weight_layout == ZC_WEIGHTS_MXFP4_A8 || d->weight_layout == ZC_WEIGHTS_MXFP4_A4;
+}
+bool mxfp4_a4(const zc_moe_desc* d) { return d->weight_layout == ZC_WEIGHTS_MXFP4_A4; }
+zc_status check_mxfp4(const zc_moe_desc* d) {
+  if (d->dtype != ZC_BF16) return fail(ZC_ERR_UNSUPPORTED, "MXFP4 weights need a bf16 layer");
+  if (d->d % 128 || d->I % 128)
+    return fail(ZC_ERR_UNSUPPORTED, "MXFP4 weights need d and I multiples of 128 (d=%lld I=%lld)",
+                (long long)d->d, (long long)d->I);
+  return ZC_OK;
+}
+// Layers whose row tiles the experts' kernels list themselves.
+bool own_tiles(const zc_moe_desc* d) { return int4_group(d) || mxfp4(d); }
+
 zc_status check_desc(const zc_moe_desc* d) {
   if (!d) return fail(ZC_ERR_INVALID, "desc is NULL");
   const int64_t E = d->N + d->Z;
@@ -192,8 +207,8 @@ zc_status check_desc(const zc_moe_desc* d) {
     return fail(ZC_ERR_INVALID, "gate_norm %d is neither 0 nor 1", d->gate_norm);
   if (!std::isfinite(d->out_scale)) return fail(ZC_ERR_INVALID, "out_scale is not finite");
   if (d->weight_layout != ZC_WEIGHTS_ROWMAJOR && d->weight_layout != ZC_WEIGHTS_PACKED &&
-      d->weight_layout != ZC_WEIGHTS_MXFP8 && !int4_group(d))
-    return fail(ZC_ERR_INVALID, "weight_layout %d is not ROWMAJOR, PACKED, MXFP8 or INT4",
+      d->weight_layout != ZC_WEIGHTS_MXFP8 && !int4_group(d) && !mxfp4(d))
+    return fail(ZC_ERR_INVALID, "weight_layout %d is not ROWMAJOR, PACKED, MXFP8, INT4 or MXFP4",
                 d->weight_layout);
   if (d->cu_limit < 0 || d->cu_limit % 8)
     return fail(ZC_ERR_INVALID, "cu_limit %d is neither 0 nor a positive multiple of 8",
@@ -208,6 +223,7 @@ zc_status check_desc(const zc_moe_desc* d) {
   if (d->weight_layout == ZC_WEIGHTS_PACKED) ZC_CHECK(check_packable(d));
   if (d->weight_layout == ZC_WEIGHTS_MXFP8) ZC_CHECK(check_mxfp8(d));
   if (int4_group(d)) ZC_CHECK(check_int4(d));
+  if (mxfp4(d)) ZC_CHECK(check_mxfp4(d));
   return ZC_OK;
 }
 
@@ -291,15 +307,16 @@ Saved carve_saved(char* p, const zc_moe_desc* d) {
 
 // Forward scratch: routing scratch, h in the layer dtype (operand of the
 // down GEMM) and y when no saved buffer takes it.
-// MXFP8 layers add x' (codes T*d, scales T*d/32); h' (codes and scales)
-// fits in the h piece.
+// MXFP8 and MXFP4 layers add x' (codes and scales); h' (codes and scales)
+// fits in the h piece.  Layers that list their own row tiles add the list.
+int64_t xq_bytes(const zc_moe_desc* d) { return a256(mxfp4_a4(d) ? d->T * d->d / 2 : d->T * d->d); }
 int64_t fwd_ws_bytes(const zc_moe_desc* d) {
   const int64_t rows = d->T * d->K, es = esize(d);
   // y is fp32 with 4-bit weights
-  const int64_t ys = int4_group(d) ? 4 : es;
+  const int64_t ys = own_tiles(d) ? 4 : es;
   int64_t b = route_ws_bytes(d) + a256(rows * d->I * es) + a256(rows * d->d * ys);
-  if (d->weight_layout == ZC_WEIGHTS_MXFP8) b += a256(d->T * d->d) + a256(d->T * d->d / 32);
-  if (int4_group(d)) b += a256(zc::int4_tiles_bytes(rows, d->N));
+  if (d->weight_layout == ZC_WEIGHTS_MXFP8 || mxfp4(d)) b += xq_bytes(d) + a256(d->T * d->d / 32);
+  if (own_tiles(d)) b += a256(zc::row_tiles_bytes(rows, d->N));
   return b;
 }
 
@@ -458,7 +475,7 @@ bool use_dense_router(const zc_moe_desc* d) {
 // kernels of gemm_rmw.hip likewise but at least 64 rows, the other row-major
 // bf16 forward kernels use 256.
 int fwd_rows_per_tile(const zc_moe_desc* d) {
-  if (d->N == 0 || int4_group(d)) return zc::kFwdBM;  // (4-bit layers list their own tiles)
+  if (d->N == 0 || own_tiles(d)) return zc::kFwdBM;  // (4-bit layers list their own tiles)
   const int tm = zc::fwdp_rows_per_tile(d->T * d->K / d->N);
   if (d->weight_layout != ZC_WEIGHTS_ROWMAJOR) return tm;
   return rmw_layer(d) ? (tm < 64 ? 64 : tm) : zc::kFwdBM;
@@ -542,10 +559,10 @@ zc_status do_experts(const zc_moe_desc* d, const T* x, const T* wg, const T* wu,
     } else if (const int G = int4_group(d)) {
       // 4-bit weights (validated: bf16, no saved buffer); y is fp32
       float* yf = reinterpret_cast<float*>(y);
-      void* tiles = ws + fwd_ws_bytes(d) - a256(zc::int4_tiles_bytes(rows, N));
+      void* tiles = ws + fwd_ws_bytes(d) - a256(zc::row_tiles_bytes(rows, N));
       // (picks spread over all N + Z experts)
       const int tm = zc::int4_rows_per_tile(rows / (d->N + d->Z), d->T, rows, d->d, d->I);
-      ZC_LAUNCH(ZC_PH_TILE_OFFSETS, zc::launch_int4_tiles(r->offsets, N, tm, tiles, s),
+      ZC_LAUNCH(ZC_PH_TILE_OFFSETS, zc::launch_row_tiles(r->offsets, N, tm, tiles, s),
                 "tile list launch");
       ZC_LAUNCH(ZC_PH_GATE_UP,
                 zc::launch_int4_gateup(reinterpret_cast<const bf16_t*>(x), d->T,
@@ -557,6 +574,34 @@ zc_status do_experts(const zc_moe_desc* d, const T* x, const T* wg, const T* wu,
                 zc::launch_int4_down(reinterpret_cast<const bf16_t*>(h),
                                      reinterpret_cast<const uint8_t*>(wd), G, tiles, tm, rows, N, I,
                                      dd, yf, s),
+                "down GEMM launch");
+    } else if (mxfp4(d)) {
+      // MXFP4 weights (validated: bf16, no saved buffer); y is fp32
+      const bool a4 = mxfp4_a4(d);
+      float* yf = reinterpret_cast<float*>(y);
+      char* tiles = ws + fwd_ws_bytes(d) - a256(zc::row_tiles_bytes(rows, N));
+      uint8_t* xs = reinterpret_cast<uint8_t*>(tiles - a256(d->T * d->d / 32));
+      uint8_t* xq = xs - xq_bytes(d);
+      uint8_t* hq = reinterpret_cast<uint8_t*>(h);
+      uint8_t* hs = hq + a256(a4 ? rows * d->I / 2 : rows * d->I);
+      const int tm = zc::mx4_rows_per_tile(rows / (d->N + d->Z));
+      ZC_LAUNCH(ZC_PH_TILE_OFFSETS, zc::launch_row_tiles(r->offsets, N, tm, tiles, s),
+                "tile list launch");
+      if (!mxq)
+        ZC_LAUNCH(ZC_PH_QUANTIZE,
+                  a4 ? zc::launch_mx4_rows<bf16_t>(reinterpret_cast<const bf16_t*>(x), d->T, dd, xq,
+                                                   xs, nullptr, s)
+                     : zc::launch_mxq_rows(reinterpret_cast<const bf16_t*>(x), d->T, dd, xq, xs, s),
+                  "activation quantization launch");
+      ZC_LAUNCH(ZC_PH_GATE_UP,
+                zc::launch_mx4_gateup(a4, mxq ? mxq : xq, mxq ? mxs : xs,
+                                      reinterpret_cast<const uint8_t*>(wg),
+                                      reinterpret_cast<const uint8_t*>(wu), tiles, r->perm, tm, rows,
+                                      N, I, dd, K, hq, hs, s),
+                "gate/up GEMM launch");
+      ZC_LAUNCH(ZC_PH_DOWN,
+                zc::launch_mx4_down(a4, hq, hs, reinterpret_cast<const uint8_t*>(wd), tiles, tm, rows,
+                                    N, I, dd, yf, s),
                 "down GEMM launch");
     } else if (d->weight_layout == ZC_WEIGHTS_PACKED) {
       // bf16 inference on packed weights (validated: bf16, no saved buffer)
@@ -616,7 +661,7 @@ zc_status do_experts(const zc_moe_desc* d, const T* x, const T* wg, const T* wu,
     }
   }
   if constexpr (std::is_same<T, bf16_t>::value) {
-    if (int4_group(d)) {
+    if (own_tiles(d)) {
       ZC_LAUNCH(ZC_PH_COMBINE,
                 (zc::launch_combine<T, float>(x, reinterpret_cast<const float*>(y), r->topk_idx,
                                               r->topk_gate, r->inv, Tn, dd, N, K, d->out_scale, out,
@@ -647,7 +692,7 @@ zc_status do_routed_experts(const zc_moe_desc* d, const T* x, const T* wg, const
                             char* ws, hipStream_t s) {
   const RouteWs rw = carve_route(ws, d);
   const int N = static_cast<int>(d->N);
-  if (N > 0 && d->T > 0 && !int4_group(d))
+  if (N > 0 && d->T > 0 && !own_tiles(d))
     ZC_LAUNCH(ZC_PH_TILE_OFFSETS,
               zc::launch_tile_offsets2(r->offsets, N, zc::kGemmBM, rw.tile_off,
                                        fwd_rows_per_tile(d), rw.tile_off2, rw.tile_exp, rw.sched,
@@ -1040,8 +1085,11 @@ zc_status no_throw(F&& f) {
 }
 
 // Bytes of one set of expert weights in the layer's layout.
-int64_t weight_set_bytes(const zc_moe_desc* d) {
+int64_t weight_set_bytes(const zc_moe_desc* d, int which) {
   const int64_t n = d->N * d->I * d->d;
+  if (mxfp4(d))
+    return which == ZC_PACK_GATE_UP ? zc::mx4_weight_bytes(d->N, d->I, d->d)
+                                    : zc::mx4_weight_bytes(d->N, d->d, d->I);
   if (const int G = int4_group(d)) return n / 2 + n / G * 2;
   return d->weight_layout == ZC_WEIGHTS_MXFP8 ? n + n / 32 : n * esize(d);
 }
@@ -1144,15 +1192,16 @@ zc_status zc_moe_experts(const zc_moe_desc* desc, const void* x, const zc_route_
   ZC_CHECK(check_ptr(x_scales, "x_scales", true));
   if ((x_codes == nullptr) != (x_scales == nullptr))
     return fail(ZC_ERR_INVALID, "x_codes and x_scales must both be set or both be NULL");
-  if (x_codes && desc->weight_layout != ZC_WEIGHTS_MXFP8)
-    return fail(ZC_ERR_INVALID, "x_codes go with MXFP8 weights");
+  if (x_codes && desc->weight_layout != ZC_WEIGHTS_MXFP8 && !mxfp4(desc))
+    return fail(ZC_ERR_INVALID, "x_codes go with MXFP8 or MXFP4 weights");
   ZC_CHECK(check_ptr(out, "out", none));
   const int64_t need = fwd_ws_bytes(desc);
   ZC_CHECK(check_ws(ws, ws_bytes, need));
   const int64_t n = desc->T * desc->d, b = n * esize(desc), k = desc->T * desc->K;
-  const int64_t wb = weight_set_bytes(desc);
+  const int64_t wb = weight_set_bytes(desc, ZC_PACK_GATE_UP);
   const Range in[] = {{w_gate, wb, "w_gate", false}, {w_up, wb, "w_up", false},
-                      {w_down, wb, "w_down", false}, {x, b, "x", false}, {x_codes, n, "x_codes", false},
+                      {w_down, weight_set_bytes(desc, ZC_PACK_DOWN), "w_down", false},
+                      {x, b, "x", false}, {x_codes, mxfp4_a4(desc) ? n / 2 : n, "x_codes", false},
                       {x_scales, n / 32, "x_scales", false}, {r->topk_idx, 4 * k, "r->topk_idx", false},
                       {r->topk_gate, 4 * k, "r->topk_gate", false},
                       {r->offsets, 4 * (desc->N + 1), "r->offsets", false},
@@ -1389,7 +1438,7 @@ zc_status zc_moe_quantize_weights(const zc_moe_desc* desc, int which, const void
 
 size_t zc_moe_int4_weight_bytes(const zc_moe_desc* desc) {
   if (check_desc(desc) != ZC_OK || !int4_group(desc)) return 0;
-  return static_cast<size_t>(weight_set_bytes(desc));
+  return static_cast<size_t>(weight_set_bytes(desc, ZC_PACK_GATE_UP));
 }
 
 namespace {
@@ -1445,6 +1494,64 @@ zc_status zc_moe_int4_pack(const zc_moe_desc* desc, int which, const uint8_t* co
             zc::launch_int4_pack(codes, static_cast<const bf16_t*>(scales),
                                  static_cast<uint8_t*>(dst), desc->N, R, C, G, s),
             "4-bit packing launch");
+  return ZC_OK;
+}
+
+zc_status zc_mxfp4_quantize(int64_t R, int64_t C, int dtype, const void* src, uint8_t* codes,
+                            uint8_t* scales, void* values, void* stream) {
+  ZC_CHECK(check_dtype(dtype, "dtype"));
+  if (R < 0 || C < 1) return fail(ZC_ERR_INVALID, "bad sizes R=%lld C=%lld", (long long)R, (long long)C);
+  if (C % 32 || C >= (int64_t(1) << 31) || R >= (int64_t(1) << 40) / C)
+    return fail(ZC_ERR_UNSUPPORTED, "MXFP4 rows need C a multiple of 32 and R*C below 2^40 (R=%lld C=%lld)",
+                (long long)R, (long long)C);
+  const bool none = R == 0;
+  ZC_CHECK(check_ptr(src, "src", none));
+  ZC_CHECK(check_ptr(codes, "codes", none));
+  ZC_CHECK(check_ptr(scales, "scales", none));
+  ZC_CHECK(check_ptr(values, "values", true));
+  const int64_t n = R * C, b = n * dtype_size(dtype);
+  const Range in[] = {{src, b, "src", true}};
+  const Range out[] = {{codes, n / 2, "codes", false}, {scales, n / 32, "scales", false},
+                       {values, b, "values", true}};
+  ZC_CHECK(check_overlap(out, 3, in, 1));
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  ZC_LAUNCH(ZC_PH_QUANTIZE,
+            dtype == ZC_BF16
+                ? zc::launch_mx4_rows(static_cast<const bf16_t*>(src), R, C, codes, scales,
+                                      static_cast<bf16_t*>(values), s)
+                : zc::launch_mx4_rows(static_cast<const float*>(src), R, C, codes, scales,
+                                      static_cast<float*>(values), s),
+            "MXFP4 quantization launch");
+  return ZC_OK;
+}
+
+size_t zc_moe_mxfp4_weight_bytes(const zc_moe_desc* desc, int which) {
+  if (check_desc(desc) != ZC_OK || !mxfp4(desc) || (which != ZC_PACK_GATE_UP && which != ZC_PACK_DOWN))
+    return 0;
+  return static_cast<size_t>(weight_set_bytes(desc, which));
+}
+
+zc_status zc_moe_mxfp4_pack(const zc_moe_desc* desc, int which, const uint8_t* codes,
+                            const uint8_t* scales, void* dst, void* stream) {
+  ZC_CHECK(check_desc(desc));
+  if (!mxfp4(desc)) return fail(ZC_ERR_INVALID, "weight_layout %d is no MXFP4 layout", desc->weight_layout);
+  if (which != ZC_PACK_GATE_UP && which != ZC_PACK_DOWN)
+    return fail(ZC_ERR_INVALID, "which=%d is neither ZC_PACK_GATE_UP nor ZC_PACK_DOWN", which);
+  const bool opt = desc->N == 0;
+  ZC_CHECK(check_ptr(codes, "codes", opt));
+  ZC_CHECK(check_ptr(scales, "scales", opt));
+  ZC_CHECK(check_ptr(dst, "dst", opt));
+  const int64_t n = desc->N * desc->I * desc->d;
+  const Range in[] = {{codes, n / 2, "codes", false}, {scales, n / 32, "scales", false}};
+  const Range out[] = {{dst, weight_set_bytes(desc, which), "dst", false}};
+  ZC_CHECK(check_overlap(out, 1, in, 2));
+  if (opt) return ZC_OK;
+  const int R = static_cast<int>(which == ZC_PACK_GATE_UP ? desc->I : desc->d);
+  const int C = static_cast<int>(which == ZC_PACK_GATE_UP ? desc->d : desc->I);
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  ZC_LAUNCH(ZC_PH_QUANTIZE,
+            zc::launch_mx4_pack(codes, scales, static_cast<uint8_t*>(dst), desc->N, R, C, s),
+            "MXFP4 packing launch");
   return ZC_OK;
 }
 

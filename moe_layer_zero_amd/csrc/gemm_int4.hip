@@ -44,18 +44,10 @@ constexpr int kStep = 128;  // reduction steps of a code block
 
 enum { I4_SWIGLU = 0, I4_STORE = 1 };
 
-// What a workgroup has to know of its row tile, in one load: the expert, the
-// first of the expert's row tiles and their number, its first row and the end
-// of its rows.
-struct __align__(32) Tile {
-  int32_t e, mt0, mte, seg0, seg1, pad[3];
-};
-static_assert(sizeof(Tile) == kInt4TileBytes, "the workspace holds them");
-
 struct I4Params {
   int N, ncols, K;          // experts, output columns (I or d), reduction length (d or I)
   const int32_t* total;     // number of row tiles
-  const Tile* tiles;        // one of each (as many as the grid has row tiles)
+  const RowTile* tiles;        // one of each (as many as the grid has row tiles)
   const bf16_t* A;          // x [T][d] gathered through perm, or h [P][I]
   uint32_t a_bytes;         // its size where 31 bits hold it
   const int32_t* perm;      // gate/up only
@@ -124,23 +116,6 @@ struct Scales {
 // next loads, the sums of every column and group are live at once.
 __device__ __forceinline__ void settle(f32x4_t& v) { asm volatile("" : "+v"(v)); }
 
-// A wave-uniform read of a table written before this kernel, as scalar loads.
-__device__ __forceinline__ Tile ld_tile(const Tile* t) {
-  typedef int32_t i32x8_t __attribute__((ext_vector_type(8)));
-  const i32x8_t v = *(const __attribute__((address_space(4))) i32x8_t*)t;
-  return Tile{v[0], v[1], v[2], v[3], v[4], {0, 0, 0}};
-}
-
-// Tile number of the in-th tile of XCD x: runs of 2^log_run consecutive tiles
-// are dealt to the 8 XCDs (workgroup b runs on XCD b mod 8), so that the row
-// tiles of a weight panel, next to each other, read it from one L2.  (Without
-// the number of tiles: a workgroup's record and that number are loaded
-// together.)
-constexpr int kMaxLogRun = 6;
-__device__ __forceinline__ int64_t tile_of(int x, int64_t in, int log_run) {
-  return (((in >> log_run) * 8 + x) << log_run) + (in & ((1 << log_run) - 1));
-}
-
 // Eight codes -> 128 + q in bf16.
 // (The two constants come in registers, one of them a vector one, so that
 // each pair is a shift and one and-or.)
@@ -167,7 +142,7 @@ __global__ __launch_bounds__(kThreads, 2) void int4_kernel(I4Params p) {
   for (int64_t in = blockIdx.x / 8;; in += gridDim.x / 8) {
   const int64_t L = tile_of(blockIdx.x % 8, in, p.log_run);
   if (in >= p.per_xcd) break;
-  const Tile tile = ld_tile(p.tiles + L / NT);
+  const RowTile tile = ld_tile(p.tiles + L / NT);
   if (L >= total) break;
   const int lane = tile_lane(), l16 = lane & 15, lq = lane >> 4;
   const int e = tile.e;
@@ -389,7 +364,7 @@ __global__ __launch_bounds__(kThreads, 2) void int4_wide_kernel(I4Params p) {
   for (int64_t in = blockIdx.x / 8;; in += gridDim.x / 8) {
     const int64_t L = tile_of(blockIdx.x % 8, in, p.log_run);
     if (in >= p.per_xcd) break;
-    const Tile tile = ld_tile(p.tiles + L / NT);
+    const RowTile tile = ld_tile(p.tiles + L / NT);
     if (L >= total) break;
     const int lane = tile_lane(), l16 = lane & 15, lq = lane >> 4;
     const int e = tile.e;
@@ -644,19 +619,12 @@ __global__ __launch_bounds__(256) void int4_quantize_kernel(const bf16_t* __rest
   }
 }
 
-// Grids beyond this many workgroups go round again (a launch holds fewer than
-// 2^32 threads).
-constexpr int64_t kMaxGrid = int64_t(1) << 20;
-unsigned grid_of(int64_t blocks) {
-  return static_cast<unsigned>(blocks < kMaxGrid ? blocks : kMaxGrid);
-}
-
 // The records of the row tiles of height tm, in expert order, and their number.
 // One workgroup: inclusive scan of the experts' tile counts by wavefront, then
 // over the 16 wavefronts' sums.
-__global__ __launch_bounds__(kMaxExperts) void int4_tiles_kernel(
+__global__ __launch_bounds__(kMaxExperts) void row_tiles_kernel(
     const int32_t* __restrict__ offsets, int N, int tm, int32_t* __restrict__ total,
-    Tile* __restrict__ tiles) {
+    RowTile* __restrict__ tiles) {
   __shared__ int32_t s_sum[kMaxExperts / 64];
   const int e = threadIdx.x, lane = e & 63, wave = e >> 6;
   const int lo = e < N ? offsets[e] : 0, hi = e < N ? offsets[e + 1] : 0;
@@ -672,7 +640,7 @@ __global__ __launch_bounds__(kMaxExperts) void int4_tiles_kernel(
   int first = scan - n;
   for (int w = 0; w < wave; ++w) first += s_sum[w];
   if (e == kMaxExperts - 1) *total = first + n;
-  Tile t{e, first, n, lo, hi, {0, 0, 0}};
+  RowTile t{e, first, n, lo, hi, {0, 0, 0}};
   for (int i = 0; i < n; ++i) tiles[first + i] = t;
 }
 
@@ -682,12 +650,8 @@ template <typename K>
 hipError_t launch_tiles(K kernel32, K kernel64, K kernel128, I4Params p, int G, int64_t rows, int tm,
                         int OUT, hipStream_t s) {
   const int64_t NT = (p.ncols + OUT - 1) / OUT;
-  const int64_t most = int4_max_tiles(rows, p.N, tm) * NT;
-  // runs of 8 tiles, longer ones while every XCD has at least 32 of them
-  p.log_run = 3;
-  while (p.log_run < kMaxLogRun && (most >> p.log_run) >= 8 * 64) ++p.log_run;
-  const int64_t round = int64_t(8) << p.log_run;
-  p.per_xcd = (most + round - 1) / round << p.log_run;
+  const int64_t most = max_row_tiles(rows, p.N, tm) * NT;
+  deal_tiles(most, &p.per_xcd, &p.log_run);
   const dim3 grid(grid_of(p.per_xcd * 8)), block(kThreads);
   hipLaunchKernelGGL(G == 32 ? kernel32 : G == 64 ? kernel64 : kernel128, grid, block, 0, s, p);
   return hipGetLastError();
@@ -719,18 +683,18 @@ int int4_rows_per_tile(int64_t avg_rows, int64_t Tn, int64_t rows, int64_t d, in
 
 // Row tiles of height tm at most: every one of the rows' experts has one ragged
 // tile.
-int64_t int4_max_tiles(int64_t rows, int64_t N, int tm) {
+int64_t max_row_tiles(int64_t rows, int64_t N, int tm) {
   return rows / tm + (rows < N ? rows : N);
 }
 // Bytes of their records and count.  tile_of reaches fewer than 8 runs of column
 // tiles, so fewer row tiles than that, past the last.
-int64_t int4_tiles_bytes(int64_t rows, int64_t N) {
-  return kInt4TileBytes * (1 + int4_max_tiles(rows, N, 16) + (8 << kMaxLogRun));
+int64_t row_tiles_bytes(int64_t rows, int64_t N) {
+  return static_cast<int64_t>(sizeof(RowTile)) * (1 + max_row_tiles(rows, N, 16) + (8 << kMaxLogRun));
 }
 
-hipError_t launch_int4_tiles(const int32_t* offsets, int N, int tm, void* tiles, hipStream_t s) {
-  hipLaunchKernelGGL(int4_tiles_kernel, dim3(1), dim3(kMaxExperts), 0, s, offsets, N, tm,
-                     static_cast<int32_t*>(tiles), static_cast<Tile*>(tiles) + 1);
+hipError_t launch_row_tiles(const int32_t* offsets, int N, int tm, void* tiles, hipStream_t s) {
+  hipLaunchKernelGGL(row_tiles_kernel, dim3(1), dim3(kMaxExperts), 0, s, offsets, N, tm,
+                     static_cast<int32_t*>(tiles), static_cast<RowTile*>(tiles) + 1);
   return hipGetLastError();
 }
 
@@ -740,14 +704,14 @@ hipError_t launch_int4_gateup(const bf16_t* x, int64_t Tn, const uint8_t* wg, co
   I4Params p{};
   p.N = N; p.ncols = I; p.K = d;
   p.total = static_cast<const int32_t*>(tiles);
-  p.tiles = static_cast<const Tile*>(tiles) + 1;
+  p.tiles = static_cast<const RowTile*>(tiles) + 1;
   p.A = x; p.a_bytes = static_cast<uint32_t>(Tn * d * 2); p.perm = perm; p.kdiv = K;
   p.B = wg; p.B2 = wu; p.h = h;
   // 16-row tiles: 32 columns of h a workgroup; 16 where that gives too few
   // workgroups to fill the card (one token of d = 6144, I = 2048, K = 12: 18 us
   // against 20); 64 where tiles are so full that their rows' loads count
   // (512 tokens of N = 512: 1.02 ms against 1.09; 64 tokens: 0.63 against 0.59)
-  if (tm == 16 && int4_max_tiles(rows, N, 16) * (I / 32) < 1024)
+  if (tm == 16 && max_row_tiles(rows, N, 16) * (I / 32) < 1024)
     return launch_int4<I4_SWIGLU, 1, 2>(p, G, rows, s);
   if (tm == 16 && rows > 8 * N) return launch_int4<I4_SWIGLU, 1, 8>(p, G, rows, s);
   if (tm == 16) return launch_int4<I4_SWIGLU, 1, 4>(p, G, rows, s);
@@ -760,11 +724,11 @@ hipError_t launch_int4_down(const bf16_t* h, const uint8_t* wd, int G, const voi
   I4Params p{};
   p.N = N; p.ncols = d; p.K = I;
   p.total = static_cast<const int32_t*>(tiles);
-  p.tiles = static_cast<const Tile*>(tiles) + 1;
+  p.tiles = static_cast<const RowTile*>(tiles) + 1;
   p.A = h; p.a_bytes = static_cast<uint32_t>(rows * I * 2); p.kdiv = 1; p.B = wd; p.y = y;
   // 16-row tiles: 128 columns of y a workgroup, 64 where that gives too few (one
   // token: 11 us against 15; 256 tokens: 0.57 ms against 0.54)
-  if (tm == 16 && int4_max_tiles(rows, N, 16) * (d / 128) < 4096)
+  if (tm == 16 && max_row_tiles(rows, N, 16) * (d / 128) < 4096)
     return launch_int4<I4_STORE, 1, 4>(p, G, rows, s);
   if (tm == 16) return launch_int4<I4_STORE, 1, 8>(p, G, rows, s);
   if (tm == 32) return launch_int4<I4_STORE, 2, 4>(p, G, rows, s);

@@ -122,6 +122,44 @@ constexpr int kMaxExperts = 1024;
 // Row-tile height of the bf16 forward expert GEMMs (gemm_fwd.hip).
 constexpr int kFwdBM = 256;
 
+// Row tiles listed with what a workgroup has to know of each, in one load: the
+// expert, the first of the expert's row tiles and their number, its first row and
+// the end of its rows (launch_row_tiles).
+struct __align__(32) RowTile {
+  int32_t e, mt0, mte, seg0, seg1, pad[3];
+};
+
+// A wave-uniform read of a table written before this kernel, as scalar loads.
+__device__ __forceinline__ RowTile ld_tile(const RowTile* t) {
+  typedef int32_t i32x8_t __attribute__((ext_vector_type(8)));
+  const i32x8_t v = *(const __attribute__((address_space(4))) i32x8_t*)t;
+  return RowTile{v[0], v[1], v[2], v[3], v[4], {0, 0, 0}};
+}
+
+// Tile number of the in-th tile of XCD x: runs of 2^log_run consecutive tiles
+// are dealt to the 8 XCDs (workgroup b runs on XCD b mod 8), so that the row
+// tiles of a weight panel, next to each other, read it from one L2.  (Without
+// the number of tiles: a workgroup's record and that number are loaded
+// together.)
+constexpr int kMaxLogRun = 6;
+__device__ __forceinline__ int64_t tile_of(int x, int64_t in, int log_run) {
+  return (((in >> log_run) * 8 + x) << log_run) + (in & ((1 << log_run) - 1));
+}
+// The runs for `most` tiles at most: of 8 tiles, longer ones while every XCD has
+// at least 32 of them; and the tiles of an XCD, at most.
+inline void deal_tiles(int64_t most, int64_t* per_xcd, int* log_run) {
+  *log_run = 3;
+  while (*log_run < kMaxLogRun && (most >> *log_run) >= 8 * 64) ++*log_run;
+  const int64_t round = int64_t(8) << *log_run;
+  *per_xcd = (most + round - 1) / round << *log_run;
+}
+// Grids beyond this many workgroups go round again (a launch holds fewer than
+// 2^32 threads).
+constexpr int64_t kMaxGrid = int64_t(1) << 20;
+inline unsigned grid_of(int64_t blocks) {
+  return static_cast<unsigned>(blocks < kMaxGrid ? blocks : kMaxGrid);
+}
+
 // ---------------------------------------------------------------- launchers
 // Every launcher queues work on `s` and returns the hipError_t of the launch.
 
@@ -321,16 +359,18 @@ hipError_t launch_fwdq_down(const uint8_t* hq, const uint8_t* hs, int64_t rows,
                             const int32_t* tile_exp, int32_t* sched, int tm, int N, int I, int d,
                             bf16_t* y, int cu, hipStream_t s);
 
+// Row tiles of height tm for the rows' experts (gemm_int4.hip): their number, then
+// their records, in tiles: row_tiles_bytes(rows, N) bytes, 32-byte aligned, tm at
+// least 16.  rows = T*K bounds the picks; max_row_tiles(rows, N, tm) the tiles.
+int64_t max_row_tiles(int64_t rows, int64_t N, int tm);
+int64_t row_tiles_bytes(int64_t rows, int64_t N);
+hipError_t launch_row_tiles(const int32_t* offsets, int N, int tm, void* tiles, hipStream_t s);
+
 // Expert GEMMs on 4-bit weights with group scales (gemm_int4.hip): group
-// size G of 32, 64 or 128, d and I multiples of 128.  launch_int4_tiles lists
-// the row tiles, tm = int4_rows_per_tile(...) rows each (16, 32 or 64, by the
-// average rows an expert), in tiles: int4_tiles_bytes(rows, N) bytes, 32-byte
-// aligned.  rows = T*K bounds the picks.  y is fp32 [P][d].
-constexpr int64_t kInt4TileBytes = 32;
+// size G of 32, 64 or 128, d and I multiples of 128.  tiles: row tiles of
+// tm = int4_rows_per_tile(...) rows each (16, 32 or 64, by the average rows an
+// expert).  y is fp32 [P][d].
 int int4_rows_per_tile(int64_t avg_rows, int64_t Tn, int64_t rows, int64_t d, int64_t I);
-int64_t int4_max_tiles(int64_t rows, int64_t N, int tm);
-int64_t int4_tiles_bytes(int64_t rows, int64_t N);
-hipError_t launch_int4_tiles(const int32_t* offsets, int N, int tm, void* tiles, hipStream_t s);
 hipError_t launch_int4_gateup(const bf16_t* x, int64_t Tn, const uint8_t* wg, const uint8_t* wu,
                               int G, const void* tiles, const int32_t* perm, int tm, int64_t rows,
                               int N, int I, int d, int K, bf16_t* h, hipStream_t s);
@@ -342,6 +382,30 @@ hipError_t launch_int4_pack(const uint8_t* codes, const bf16_t* scales, uint8_t*
                             int R, int C, int G, hipStream_t s);
 hipError_t launch_int4_quantize(const bf16_t* src, uint8_t* codes, bf16_t* scales, int64_t nmat,
                                 int R, int C, int G, hipStream_t s);
+
+// Expert GEMMs on MXFP4 weights (gemm_mx4.hip): E2M1 codes with one E8M0 scale per
+// 32 reduction steps; rows of x and h in MXFP8 (a4 = false: codes and slab-ordered
+// scales, as launch_mxq_rows leaves them) or MXFP4 (a4 = true: natural order, as
+// launch_mx4_rows leaves them).  d and I multiples of 128.  tiles: row tiles of tm
+// = mx4_rows_per_tile(...) rows.
+int mx4_rows_per_tile(int64_t avg_rows);
+hipError_t launch_mx4_gateup(bool a4, const uint8_t* xq, const uint8_t* xs, const uint8_t* wg,
+                             const uint8_t* wu, const void* tiles, const int32_t* perm, int tm,
+                             int64_t rows, int N, int I, int d, int K, uint8_t* hq, uint8_t* hs,
+                             hipStream_t s);
+hipError_t launch_mx4_down(bool a4, const uint8_t* hq, const uint8_t* hs, const uint8_t* wd,
+                           const void* tiles, int tm, int64_t rows, int N, int I, int d, float* y,
+                           hipStream_t s);
+// Bytes of nmat [R][C] matrices in the kernels' order, and the packer from natural
+// codes [R][C/2] and scales [R][C/32].
+int64_t mx4_weight_bytes(int64_t nmat, int64_t R, int64_t C);
+hipError_t launch_mx4_pack(const uint8_t* codes, const uint8_t* scales, uint8_t* dst, int64_t nmat,
+                           int R, int C, hipStream_t s);
+// R rows of C values (a multiple of 32) -> natural codes and scales, and the values
+// they stand for (nullable).
+template <typename T>
+hipError_t launch_mx4_rows(const T* src, int64_t R, int64_t C, uint8_t* codes, uint8_t* scales,
+                           T* values, hipStream_t s);
 
 // Combine: out = out_scale * (c_t x_t + sum_r g_r y[inv]).
 // y in the layer dtype, or in fp32.

@@ -23,6 +23,7 @@ ZC_OP_ROUTE, ZC_OP_FORWARD, ZC_OP_BACKWARD, ZC_OP_LB_LOSS, ZC_OP_ROUTE_STATS = 0
 ZC_OP_EXPERTS = 5
 ZC_WEIGHTS_ROWMAJOR, ZC_WEIGHTS_PACKED, ZC_WEIGHTS_MXFP8 = 0, 1, 2
 ZC_WEIGHTS_INT4_G32, ZC_WEIGHTS_INT4_G64, ZC_WEIGHTS_INT4_G128 = 4, 5, 6
+ZC_WEIGHTS_MXFP4_A8, ZC_WEIGHTS_MXFP4_A4 = 8, 9
 ZC_PACK_GATE_UP, ZC_PACK_DOWN = 0, 1
 ZC_STATE_F32, ZC_STATE_8BIT = 0, 1
 ZC_ROUND_NEAREST, ZC_ROUND_STOCHASTIC = 0, 1
@@ -36,6 +37,7 @@ EXPORTS = ("zc_moe_workspace_size", "zc_moe_saved_size", "zc_moe_route", "zc_moe
            "zc_moe_backward_scores", "zc_moe_seq_balance_workspace_size", "zc_moe_seq_balance",
            "zc_moe_experts", "zc_moe_int4_weight_bytes", "zc_moe_int4_quantize",
            "zc_moe_int4_pack",
+           "zc_mxfp4_quantize", "zc_moe_mxfp4_weight_bytes", "zc_moe_mxfp4_pack",
            "zc_rmsnorm_forward", "zc_rmsnorm_workspace_size", "zc_rmsnorm_backward",
            "zc_grad_norm_workspace_size", "zc_grad_norm", "zc_adamw_step",
            "zc_moe_profile",
@@ -128,6 +130,10 @@ def lib() -> C.CDLL:
         L.zc_moe_int4_weight_bytes.restype = sz
         L.zc_moe_int4_quantize.argtypes = [P, C.c_int, v, v, v, v]
         L.zc_moe_int4_pack.argtypes = [P, C.c_int, v, v, v, v]
+        L.zc_mxfp4_quantize.argtypes = [i64, i64, C.c_int, v, v, v, v, v]
+        L.zc_moe_mxfp4_weight_bytes.argtypes = [P, C.c_int]
+        L.zc_moe_mxfp4_weight_bytes.restype = sz
+        L.zc_moe_mxfp4_pack.argtypes = [P, C.c_int, v, v, v, v]
         NP = C.POINTER(zc_norm_desc)
         L.zc_rmsnorm_forward.argtypes = [NP, v, v, v, v, v, v, v, v, v]
         L.zc_rmsnorm_workspace_size.argtypes = [NP]
@@ -139,7 +145,7 @@ def lib() -> C.CDLL:
         L.zc_grad_norm.argtypes = [GT, i64, C.c_int, C.c_double, v, v, v, sz, v]
         L.zc_adamw_step.argtypes = [C.POINTER(zc_adamw_cfg), C.POINTER(zc_adamw_tensor), i64, v, v, v,
                                     v]
-        for f in ("zc_grad_norm", "zc_adamw_step", "zc_moe_experts", "zc_moe_int4_quantize", "zc_moe_int4_pack",
+        for f in ("zc_grad_norm", "zc_adamw_step", "zc_mxfp4_quantize", "zc_moe_mxfp4_pack", "zc_moe_experts", "zc_moe_int4_quantize", "zc_moe_int4_pack",
                   "zc_moe_backward_scores", "zc_moe_seq_balance", "zc_rmsnorm_forward", "zc_rmsnorm_backward",
                   "zc_moe_route", "zc_moe_forward", "zc_moe_forward_noalloc",
                   "zc_moe_backward", "zc_moe_lb_loss",
@@ -345,14 +351,30 @@ def int4_group(desc: LayerDesc) -> int:
             ZC_WEIGHTS_INT4_G128: 128}.get(desc.weight_layout, 0)
 
 
+def mxfp4_layout(row_bits: int) -> int:
+    """Weight layout of MXFP4 weights whose rows are MXFP8 (8) or MXFP4 (4)."""
+    try:
+        return {8: ZC_WEIGHTS_MXFP4_A8, 4: ZC_WEIGHTS_MXFP4_A4}[row_bits]
+    except KeyError:
+        raise ValueError(f"rows of {row_bits} bits: 8 or 4 are supported") from None
+
+
+def _is_mxfp4(desc: LayerDesc) -> bool:
+    return desc.weight_layout in (ZC_WEIGHTS_MXFP4_A8, ZC_WEIGHTS_MXFP4_A4)
+
+
 def _check_weights(desc, w_router, w_gate, w_up, w_down):
     dt = desc.dtype
     _check_layer_tensor(w_router, (desc.E, desc.d), dt, "w_router")
-    if desc.weight_layout == ZC_WEIGHTS_MXFP8 or int4_group(desc):
+    if desc.weight_layout == ZC_WEIGHTS_MXFP8 or int4_group(desc) or _is_mxfp4(desc):
         d = desc.c()
-        size = lib().zc_moe_int4_weight_bytes if int4_group(desc) else lib().zc_moe_quantized_weight_bytes
-        n = int(size(C.byref(d)))
-        for t, name in ((w_gate, "w_gate"), (w_up, "w_up"), (w_down, "w_down")):
+        if _is_mxfp4(desc):
+            sizes = [int(lib().zc_moe_mxfp4_weight_bytes(C.byref(d), w))
+                     for w in (ZC_PACK_GATE_UP, ZC_PACK_GATE_UP, ZC_PACK_DOWN)]
+        else:
+            size = lib().zc_moe_int4_weight_bytes if int4_group(desc) else lib().zc_moe_quantized_weight_bytes
+            sizes = [int(size(C.byref(d)))] * 3
+        for t, name, n in zip((w_gate, w_up, w_down), ("w_gate", "w_up", "w_down"), sizes):
             if t is not None and (t.dtype != torch.uint8 or t.numel() < n):
                 raise ValueError(f"{name}: expected a quantized weight set of {n} uint8")
         return
@@ -392,7 +414,8 @@ def zc_moe_forward(desc: LayerDesc, x, w_router, bias, w_gate, w_up, w_down, out
 def zc_moe_experts(desc: LayerDesc, x, route: RouteBuffers, w_gate, w_up, w_down, out, xq=None,
                    ws=None, stream=None):
     """The experts and the combine on routing that zc_moe_route left in route.
-    xq: (codes, scales) of x from zc_rmsnorm_forward, for MXFP8 weights."""
+    xq: (codes, scales) of x, from zc_rmsnorm_forward for MXFP8 and MXFP4_A8 weights,
+    from zc_mxfp4_quantize for MXFP4_A4 weights."""
     T, K, N, dt = desc.T, desc.K, desc.N, desc.dtype
     a, sh, i32, u8 = _Args("zc_moe_experts"), (desc.T, desc.d), torch.int32, torch.uint8
     px, po = a(x, sh, dt, "x"), a(out, sh, dt, "out")
@@ -404,8 +427,9 @@ def zc_moe_experts(desc: LayerDesc, x, route: RouteBuffers, w_gate, w_up, w_down
     _check_weights(desc, None, w_gate, w_up, w_down)
     w = [None if t is None else a(t, t.shape, t.dtype, n)
          for t, n in ((w_gate, "w_gate"), (w_up, "w_up"), (w_down, "w_down"))]
+    cols = desc.d // 2 if desc.weight_layout == ZC_WEIGHTS_MXFP4_A4 else desc.d
     codes, scales = (None, None) if xq is None else (
-        a(xq[0], sh, u8, "xq codes"), a(xq[1], (T, desc.d // 32), u8, "xq scales"))
+        a(xq[0], (T, cols), u8, "xq codes"), a(xq[1], (T, desc.d // 32), u8, "xq scales"))
     if ws is None:
         ws = _alloc(stream, workspace, desc, ZC_OP_EXPERTS, x.device)
     n = ws.numel() * ws.element_size()
@@ -669,6 +693,76 @@ def int4_expert_weights(desc: LayerDesc, w_gate, w_up, w_down, stream=None):
                                   stream=stream)
                  for w, which in ((w_gate, ZC_PACK_GATE_UP), (w_up, ZC_PACK_GATE_UP),
                                   (w_down, ZC_PACK_DOWN)))
+
+
+def mxfp4_buffers(R: int, C: int, device="cuda"):
+    """(codes [R][C/2], scales [R][C/32]) uint8: the rows zc_mxfp4_quantize writes."""
+    return (torch.empty((R, C // 2), dtype=torch.uint8, device=device),
+            torch.empty((R, C // 32), dtype=torch.uint8, device=device))
+
+
+def zc_mxfp4_quantize(src, codes=None, scales=None, values=None, stream=None):
+    """Rows [..., C] (bf16 or fp32, C a multiple of 32) as MXFP4: codes uint8 [..., C/2]
+    (two a byte, the even column in the low half) and scales uint8 [..., C/32] (E8M0);
+    both are allocated when None and returned.  values (as src; may be src): what
+    they stand for."""
+    if src.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"src: expected float32 or bfloat16, got {src.dtype}")
+    if src.dim() < 1 or src.shape[-1] < 32 or src.shape[-1] % 32:
+        raise ValueError(f"src: rows of {tuple(src.shape)[-1:]} values, a multiple of 32 is needed")
+    Cc, lead = src.shape[-1], tuple(src.shape[:-1])
+    R = src.numel() // Cc
+    if codes is None:
+        codes = _alloc(stream, torch.empty, lead + (Cc // 2,), dtype=torch.uint8, device=src.device)
+    if scales is None:
+        scales = _alloc(stream, torch.empty, lead + (Cc // 32,), dtype=torch.uint8, device=src.device)
+    a, u8 = _Args("zc_mxfp4_quantize"), torch.uint8
+    p = (a(src, src.shape, src.dtype, "src"), a(codes, lead + (Cc // 2,), u8, "codes"),
+         a(scales, lead + (Cc // 32,), u8, "scales"), a(values, src.shape, src.dtype, "values"))
+    a.run(lib().zc_mxfp4_quantize, R, Cc, ZC_BF16 if src.dtype == torch.bfloat16 else ZC_F32, *p,
+          stream=stream)
+    return codes, scales
+
+
+def _mxfp4_shape(desc: LayerDesc, which: int):
+    if not _is_mxfp4(desc):
+        raise ValueError("desc.weight_layout is no MXFP4 layout (see mxfp4_layout)")
+    return (desc.N, desc.I, desc.d) if which == ZC_PACK_GATE_UP else (desc.N, desc.d, desc.I)
+
+
+def zc_moe_mxfp4_pack(desc: LayerDesc, which: int, codes, scales, dst=None, stream=None):
+    """MXFP4 codes [N][R][C/2] and scales [N][R][C/32] of w_gate or w_up
+    (ZC_PACK_GATE_UP, [N][I][d]) or w_down (ZC_PACK_DOWN, [N][d][I]), from
+    zc_mxfp4_quantize or made elsewhere -> the weight set a forward with desc's
+    layout takes, a uint8 tensor (allocated when None).  Returns it."""
+    N, R, Cc = _mxfp4_shape(desc, which)
+    d = desc.c()
+    n = int(lib().zc_moe_mxfp4_weight_bytes(C.byref(d), which))
+    if dst is None:
+        dst = _alloc(stream, torch.empty, max(n, 16), dtype=torch.uint8, device=codes.device)
+    if dst.dtype != torch.uint8 or dst.numel() < n:
+        raise ValueError(f"dst: expected at least {n} uint8, got {dst.numel()} {dst.dtype}")
+    a, u8 = _Args("zc_moe_mxfp4_pack"), torch.uint8
+    a.run(lib().zc_moe_mxfp4_pack, C.byref(d), which, a(codes, (N, R, Cc // 2), u8, "codes"),
+          a(scales, (N, R, Cc // 32), u8, "scales"), a(dst, dst.shape, dst.dtype, "dst"), stream=stream)
+    return dst
+
+
+def pack_mxfp4_expert_weights(desc: LayerDesc, gate, up, down, stream=None):
+    """The three weight sets of an MXFP4 forward, from (codes, scales) pairs."""
+    return (zc_moe_mxfp4_pack(desc, ZC_PACK_GATE_UP, *gate, stream=stream),
+            zc_moe_mxfp4_pack(desc, ZC_PACK_GATE_UP, *up, stream=stream),
+            zc_moe_mxfp4_pack(desc, ZC_PACK_DOWN, *down, stream=stream))
+
+
+def mxfp4_expert_weights(desc: LayerDesc, w_gate, w_up, w_down, stream=None):
+    """The three weight sets of an MXFP4 forward, quantized from bf16 weights."""
+    out = []
+    for w, which, name in ((w_gate, ZC_PACK_GATE_UP, "w_gate"), (w_up, ZC_PACK_GATE_UP, "w_up"),
+                           (w_down, ZC_PACK_DOWN, "w_down")):
+        _check_layer_tensor(w, _mxfp4_shape(desc, which), desc.dtype, name)
+        out.append(zc_moe_mxfp4_pack(desc, which, *zc_mxfp4_quantize(w, stream=stream), stream=stream))
+    return tuple(out)
 
 
 @dataclass
