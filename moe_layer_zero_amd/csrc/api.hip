@@ -309,11 +309,19 @@ Saved carve_saved(char* p, const zc_moe_desc* d) {
 // down GEMM) and y when no saved buffer takes it.
 // MXFP8 and MXFP4 layers add x' (codes and scales); h' (codes and scales)
 // fits in the h piece.  Layers that list their own row tiles add the list.
+// Row-tile height of an MXFP4 layer (picks spread over all N + Z experts).
+int mxfp4_rows_per_tile(const zc_moe_desc* d) {
+  const int64_t rows = d->T * d->K;
+  return zc::mx4_rows_per_tile(rows / (d->N + d->Z), d->T, rows, d->d, d->I);
+}
+bool fp32_y(const zc_moe_desc* d) {
+  return int4_group(d) || (mxfp4(d) && mxfp4_rows_per_tile(d) != zc::kMx4WideRows);
+}
 int64_t xq_bytes(const zc_moe_desc* d) { return a256(mxfp4_a4(d) ? d->T * d->d / 2 : d->T * d->d); }
 int64_t fwd_ws_bytes(const zc_moe_desc* d) {
   const int64_t rows = d->T * d->K, es = esize(d);
-  // y is fp32 with 4-bit weights
-  const int64_t ys = own_tiles(d) ? 4 : es;
+  // y is fp32 with 4-bit weights (but for many rows of MXFP4 ones)
+  const int64_t ys = fp32_y(d) ? 4 : es;
   int64_t b = route_ws_bytes(d) + a256(rows * d->I * es) + a256(rows * d->d * ys);
   if (d->weight_layout == ZC_WEIGHTS_MXFP8 || mxfp4(d)) b += xq_bytes(d) + a256(d->T * d->d / 32);
   if (own_tiles(d)) b += a256(zc::row_tiles_bytes(rows, d->N));
@@ -576,15 +584,14 @@ zc_status do_experts(const zc_moe_desc* d, const T* x, const T* wg, const T* wu,
                                      dd, yf, s),
                 "down GEMM launch");
     } else if (mxfp4(d)) {
-      // MXFP4 weights (validated: bf16, no saved buffer); y is fp32
+      // MXFP4 weights (validated: bf16, no saved buffer)
       const bool a4 = mxfp4_a4(d);
-      float* yf = reinterpret_cast<float*>(y);
       char* tiles = ws + fwd_ws_bytes(d) - a256(zc::row_tiles_bytes(rows, N));
       uint8_t* xs = reinterpret_cast<uint8_t*>(tiles - a256(d->T * d->d / 32));
       uint8_t* xq = xs - xq_bytes(d);
       uint8_t* hq = reinterpret_cast<uint8_t*>(h);
       uint8_t* hs = hq + a256(a4 ? rows * d->I / 2 : rows * d->I);
-      const int tm = zc::mx4_rows_per_tile(rows / (d->N + d->Z));
+      const int tm = mxfp4_rows_per_tile(d);
       ZC_LAUNCH(ZC_PH_TILE_OFFSETS, zc::launch_row_tiles(r->offsets, N, tm, tiles, s),
                 "tile list launch");
       if (!mxq)
@@ -594,14 +601,14 @@ zc_status do_experts(const zc_moe_desc* d, const T* x, const T* wg, const T* wu,
                      : zc::launch_mxq_rows(reinterpret_cast<const bf16_t*>(x), d->T, dd, xq, xs, s),
                   "activation quantization launch");
       ZC_LAUNCH(ZC_PH_GATE_UP,
-                zc::launch_mx4_gateup(a4, mxq ? mxq : xq, mxq ? mxs : xs,
+                zc::launch_mx4_gateup(a4, mxq ? mxq : xq, mxq ? mxs : xs, d->T,
                                       reinterpret_cast<const uint8_t*>(wg),
                                       reinterpret_cast<const uint8_t*>(wu), tiles, r->perm, tm, rows,
                                       N, I, dd, K, hq, hs, s),
                 "gate/up GEMM launch");
       ZC_LAUNCH(ZC_PH_DOWN,
                 zc::launch_mx4_down(a4, hq, hs, reinterpret_cast<const uint8_t*>(wd), tiles, tm, rows,
-                                    N, I, dd, yf, s),
+                                    N, I, dd, y, s),
                 "down GEMM launch");
     } else if (d->weight_layout == ZC_WEIGHTS_PACKED) {
       // bf16 inference on packed weights (validated: bf16, no saved buffer)
@@ -661,7 +668,7 @@ zc_status do_experts(const zc_moe_desc* d, const T* x, const T* wg, const T* wu,
     }
   }
   if constexpr (std::is_same<T, bf16_t>::value) {
-    if (own_tiles(d)) {
+    if (fp32_y(d)) {
       ZC_LAUNCH(ZC_PH_COMBINE,
                 (zc::launch_combine<T, float>(x, reinterpret_cast<const float*>(y), r->topk_idx,
                                               r->topk_gate, r->inv, Tn, dd, N, K, d->out_scale, out,

@@ -49,6 +49,8 @@ struct Mx4Params {
   uint8_t* hq;              // gate/up output: codes [P][I] or [P][I/2] ...
   uint8_t* hs;              // ... and scales [P][I/32]
   float* y;                 // down output [P][d]
+  bf16_t* yb;               // the same of many rows' kernel
+  uint32_t a_bytes, as_bytes;  // sizes of A and As where 31 bits hold them
   int64_t per_xcd;          // tiles of an XCD, at most
   int log_run;              // runs of consecutive tiles on one XCD
 };
@@ -293,6 +295,251 @@ hipError_t launch_mx4(bool a4, Mx4Params p, int64_t rows, hipStream_t s) {
   return hipGetLastError();
 }
 
+// ------------------------------------------------------------- many rows
+typedef __attribute__((address_space(3))) void lds_void;
+// (Buffer loads: the compiler would have every LDS read wait for all copies in
+// flight if they were global loads into LDS.)
+__device__ __forceinline__ void copy_to_lds16(__amdgpu_buffer_rsrc_t r, lds_void* dst,
+                                              uint32_t voff, int soff) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, dst, 16, voff, soff, 0, 0);
+}
+__device__ __forceinline__ void copy_to_lds4(__amdgpu_buffer_rsrc_t r, lds_void* dst, uint32_t voff,
+                                             int soff) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, dst, 4, voff, soff, 0, 0);
+}
+// s_waitcnt immediate for "vmcnt <= n" (expcnt and lgkmcnt not waited)
+constexpr int vmcnt_imm(int n) { return 0x0f70 | (n & 15) | ((n >> 4) << 14); }
+// Barrier for LDS alone: loads stay in flight.
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0)
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+template <int EPI, bool A4>
+__global__ __launch_bounds__(kThreads, 2) void mx4_wide_kernel(Mx4Params p) {
+  constexpr int TM = kMx4WideRows;
+  constexpr int CB = A4 ? kStep / 2 : kStep;   // bytes of a row's slab of 128 steps
+  constexpr int SLOT = TM * CB;                // bytes of a ring slot
+  constexpr int CP = SLOT / 1024 / kWaves;     // copies a wavefront and slab
+  constexpr int RPC = 1024 / CB;               // rows of a copy
+  constexpr int SC = TM * 16;                  // bytes of the rows' scales of 512 steps
+  constexpr int OUT = EPI == MX_SWIGLU ? 128 : 256;
+  constexpr int V = CP + 4, VS = 2 + 4;        // loads of a slab; of 512 steps' scales
+  __shared__ __align__(16) uint8_t ring[4 * SLOT + 2 * SC];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int nkb = p.K / kStep, nq = nkb / 4;
+  const int NT = p.ncols / OUT;
+  const __amdgpu_buffer_rsrc_t rows = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<uint8_t*>(p.A), (short)0, p.a_bytes, 0x00020000);
+  const __amdgpu_buffer_rsrc_t rscale = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<uint8_t*>(p.As), (short)0, p.as_bytes, 0x00020000);
+  const int64_t total = static_cast<int64_t>(ld_scalar(p.total)) * NT;
+  for (int64_t in = blockIdx.x / 8;; in += gridDim.x / 8) {
+    const int64_t L = tile_of(blockIdx.x % 8, in, p.log_run);
+    if (in >= p.per_xcd) break;
+    const RowTile tile = ld_tile(p.tiles + L / NT);
+    if (L >= total) break;
+    const int lane = tile_lane(), l16 = lane & 15, lq = lane >> 4;
+    const int e = tile.e;
+    const int q = static_cast<int>(L - static_cast<int64_t>(tile.mt0) * NT);
+    const int nt = q / tile.mte, mt = q % tile.mte;
+    // the expert's blocks of 16 rows spread evenly over its row tiles
+    const int nbe = (tile.seg1 - tile.seg0 + 15) >> 4;
+    const int blo = nbe * mt / tile.mte, bhi = nbe * (mt + 1) / tile.mte;
+    const int m0 = tile.seg0 + 16 * blo;
+    const int mcount = min(tile.seg0 + 16 * bhi, tile.seg1) - m0;
+
+    uint32_t src[CP], ssrc[2];
+#pragma unroll
+    for (int i = 0; i < CP; ++i) {
+      const int r = (CP * wave + i) * RPC + lane / (CB / 16);
+      const int row = m0 + min(r, mcount - 1);
+      const int tok = EPI == MX_SWIGLU ? p.perm[row] / p.kdiv : row;
+      const int chunk = A4 ? (lane & 3) ^ ((r >> 2) & 3) : (lane & 7) ^ ((r >> 1) & 7);
+      src[i] = static_cast<uint32_t>(tok) * static_cast<uint32_t>(A4 ? p.K / 2 : p.K) + 16 * chunk;
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = (2 * wave + i) * 16 + (lane >> 2);
+      const int row = m0 + min(r, mcount - 1);
+      const int tok = EPI == MX_SWIGLU ? p.perm[row] / p.kdiv : row;
+      ssrc[i] = static_cast<uint32_t>(tok) * static_cast<uint32_t>(p.K / 32) + 4 * (lane & 3);
+    }
+
+    const int64_t cmat = static_cast<int64_t>(p.ncols) * p.K / 2, smat = cmat / 16;
+    __amdgpu_buffer_rsrc_t codes[2], scales[2];  // gate (or down) and up
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      uint8_t* base = const_cast<uint8_t*>(EPI == MX_SWIGLU && m ? p.B2 : p.B);
+      codes[m] = __builtin_amdgcn_make_buffer_rsrc(base + e * cmat, (short)0,
+                                                   static_cast<uint32_t>(cmat), 0x00020000);
+      scales[m] = __builtin_amdgcn_make_buffer_rsrc(base + p.N * cmat + e * smat, (short)0,
+                                                    static_cast<uint32_t>(smat), 0x00020000);
+    }
+    int col[4];  // the wavefront's column blocks
+#pragma unroll
+    for (int nb = 0; nb < 4; ++nb)
+      col[nb] = EPI == MX_SWIGLU ? nt * 8 + 2 * wave + (nb & 1) : nt * 16 + 4 * wave + nb;
+    const uint32_t code_lane = lane * 16, scale_lane = lane * 4;
+
+    auto run = [&](auto nrb_c) {
+      constexpr int NRB = decltype(nrb_c)::value;
+      i32x4_t b[4][4];  // [slab % 4][column block]
+      int sb[2][4];     // [quad % 2][column block]
+      auto issue = [&](int kb, auto slot_c) {
+        constexpr int slot = decltype(slot_c)::value;
+#pragma unroll
+        for (int i = 0; i < CP; ++i)
+          copy_to_lds16(rows, (lds_void*)(ring + slot * SLOT + (CP * wave + i) * 1024), src[i], kb * CB);
+#pragma unroll
+        for (int nb = 0; nb < 4; ++nb)
+          b[slot][nb] = __builtin_bit_cast(
+              i32x4_t, __builtin_amdgcn_raw_buffer_load_b128(codes[EPI == MX_SWIGLU ? nb / 2 : 0],
+                                                             code_lane, (col[nb] * nkb + kb) * 1024, 0));
+      };
+      auto issue_scales = [&](int quad, auto par_c) {
+        constexpr int par = decltype(par_c)::value;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          copy_to_lds4(rscale, (lds_void*)(ring + 4 * SLOT + par * SC + (2 * wave + i) * 256), ssrc[i],
+                       quad * 16);
+#pragma unroll
+        for (int nb = 0; nb < 4; ++nb)
+          sb[par][nb] = __builtin_amdgcn_raw_buffer_load_b32(scales[EPI == MX_SWIGLU ? nb / 2 : 0],
+                                                             scale_lane, (col[nb] * nq + quad) * 256, 0);
+      };
+
+      f32x4_t acc[NRB][4];
+#pragma unroll
+      for (int rb = 0; rb < NRB; ++rb)
+#pragma unroll
+        for (int nb = 0; nb < 4; ++nb) acc[rb][nb] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      // where this lane's row of a block lies in a slot: chunk lq (and 4 + lq)
+      const int pos0 = A4 ? lq ^ (l16 >> 2) : lq ^ (l16 >> 1);
+      const int frag_lane = l16 * CB + 16 * pos0;
+      const int scale_at = 4 * SLOT + l16 * 16 + (A4 ? lq : 2 * (lq & 1) + (lq >> 1));
+
+      auto compute = [&](auto slot_c, auto par_c) {
+        constexpr int slot = decltype(slot_c)::value, par = decltype(par_c)::value;
+        auto frag = [&](int rb, i32x8_t& a, int& sa) {
+          a.lo = *reinterpret_cast<const i32x4_t*>(ring + slot * SLOT + rb * 16 * CB + frag_lane);
+          if constexpr (!A4)
+            a.hi = *reinterpret_cast<const i32x4_t*>(ring + slot * SLOT + rb * 16 * CB + (frag_lane ^ 64));
+          sa = ring[par * SC + rb * 256 + slot * 4 + scale_at];
+        };
+        i32x8_t a[3] = {};
+        int sa[3];
+        frag(0, a[0], sa[0]);
+        if (NRB > 1) frag(1, a[1], sa[1]);
+#pragma unroll
+        for (int rb = 0; rb < NRB; ++rb) {
+          if (rb + 2 < NRB) frag(rb + 2, a[(rb + 2) % 3], sa[(rb + 2) % 3]);
+#pragma unroll
+          for (int nb = 0; nb < 4; ++nb) {
+            i32x8_t w = {};
+            w.lo = b[slot][nb];
+            acc[rb][nb] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                a[rb % 3], w, acc[rb][nb], A4 ? 4 : 0, 4, 0, sa[rb % 3], slot, sb[par][nb]);
+          }
+        }
+      };
+
+      using C0 = std::integral_constant<int, 0>;
+      using C1 = std::integral_constant<int, 1>;
+      using C2 = std::integral_constant<int, 2>;
+      using C3 = std::integral_constant<int, 3>;
+      const int last = nkb - 1;
+      // one slab: wait for it, meet, issue the slab three ahead (and with the first
+      // of four the next four's scales), multiply.  No branch: past the end the last
+      // slab is loaded again, so that the number of loads in flight is known.
+      auto quad = [&](int q4, auto par_c) {
+        constexpr int par = decltype(par_c)::value;
+        const int kb = 4 * q4;
+        __builtin_amdgcn_s_waitcnt(vmcnt_imm(2 * V));
+        lds_barrier();
+        issue(min(kb + 3, last), C3{});
+        issue_scales(min(q4 + 1, nq - 1), std::integral_constant<int, 1 - par>{});
+        __builtin_amdgcn_sched_barrier(0);
+        compute(C0{}, par_c);
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_waitcnt(vmcnt_imm(2 * V + VS));
+        lds_barrier();
+        issue(min(kb + 4, last), C0{});
+        __builtin_amdgcn_sched_barrier(0);
+        compute(C1{}, par_c);
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_waitcnt(vmcnt_imm(2 * V + VS));
+        lds_barrier();
+        issue(min(kb + 5, last), C1{});
+        __builtin_amdgcn_sched_barrier(0);
+        compute(C2{}, par_c);
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_waitcnt(vmcnt_imm(2 * V));
+        lds_barrier();
+        issue(min(kb + 6, last), C2{});
+        __builtin_amdgcn_sched_barrier(0);
+        compute(C3{}, par_c);
+        __builtin_amdgcn_sched_barrier(0);
+      };
+
+      lds_barrier();  // the ring is free: the previous tile's reads are done
+      issue_scales(0, C0{});
+      issue(0, C0{});
+      __builtin_amdgcn_sched_barrier(0);
+      issue(1, C1{});
+      __builtin_amdgcn_sched_barrier(0);
+      issue(2, C2{});
+      __builtin_amdgcn_sched_barrier(0);
+      int q4 = 0;
+      for (; q4 + 2 <= nq; q4 += 2) {
+        quad(q4, C0{});
+        quad(q4 + 1, C1{});
+      }
+      if (q4 < nq) quad(q4, C0{});
+      __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));  // no copy of this tile lands in the next one's ring
+
+#pragma unroll
+      for (int rb = 0; rb < NRB; ++rb)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const int r = 16 * rb + 4 * lq + v;
+          if (r >= mcount) continue;  // (the 16 lanes of a row alike)
+          const int64_t row = static_cast<int64_t>(m0) + r;
+          if constexpr (EPI == MX_SWIGLU) {
+            store_h<A4>(p, row, nt * 4 + wave, l16, silu_f(acc[rb][0][v]) * acc[rb][2][v],
+                        silu_f(acc[rb][1][v]) * acc[rb][3][v]);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+              *reinterpret_cast<uint32_t*>(p.yb + row * p.ncols + nt * OUT + 64 * wave + 32 * j + 2 * l16) =
+                  static_cast<uint32_t>(f2bf(acc[rb][2 * j][v])) |
+                  static_cast<uint32_t>(f2bf(acc[rb][2 * j + 1][v])) << 16;
+          }
+        }
+    };
+    switch ((bhi - blo + 1) >> 1) {
+      case 1: run(std::integral_constant<int, 2>{}); break;
+      case 2: run(std::integral_constant<int, 4>{}); break;
+      case 3: run(std::integral_constant<int, 6>{}); break;
+      default: run(std::integral_constant<int, 8>{}); break;
+    }
+  }
+}
+
+template <int EPI>
+hipError_t launch_mx4_wide(bool a4, Mx4Params p, int64_t rows, hipStream_t s) {
+  const int OUT = EPI == MX_SWIGLU ? 128 : 256;
+  deal_tiles(max_row_tiles(rows, p.N, kMx4WideRows) * (p.ncols / OUT), &p.per_xcd, &p.log_run);
+  const dim3 grid(grid_of(p.per_xcd * 8)), block(kThreads);
+  if (a4)
+    hipLaunchKernelGGL((mx4_wide_kernel<EPI, true>), grid, block, 0, s, p);
+  else
+    hipLaunchKernelGGL((mx4_wide_kernel<EPI, false>), grid, block, 0, s, p);
+  return hipGetLastError();
+}
+
 // Natural codes (two a byte, the even step in the low half) and scales -> the layout
 // above.  One thread per 16 bytes of codes, then one per scale.
 __global__ __launch_bounds__(256) void mx4_pack_kernel(const u32x4_t* __restrict__ codes,
@@ -369,9 +616,16 @@ __global__ __launch_bounds__(256) void mx4_rows_kernel(const T* src, int64_t pie
 
 }  // namespace
 
-int mx4_rows_per_tile(int64_t avg_rows) { return avg_rows <= 13 ? 16 : avg_rows <= 20 ? 32 : 64; }
+int mx4_rows_per_tile(int64_t avg_rows, int64_t Tn, int64_t rows, int64_t d, int64_t I) {
+  if (avg_rows <= 13) return 16;
+  if (avg_rows <= 20) return 32;
+  // (the 128-row kernel takes whole groups of 512 steps, and byte offsets of 31 bits
+  // into x, h and a matrix)
+  const int64_t limit = int64_t(1) << 31;
+  return d % 512 || I % 512 || Tn * d >= limit || rows * I >= limit || d * I >= limit ? 64 : kMx4WideRows;
+}
 
-hipError_t launch_mx4_gateup(bool a4, const uint8_t* xq, const uint8_t* xs, const uint8_t* wg,
+hipError_t launch_mx4_gateup(bool a4, const uint8_t* xq, const uint8_t* xs, int64_t Tn, const uint8_t* wg,
                              const uint8_t* wu, const void* tiles, const int32_t* perm, int tm,
                              int64_t rows, int N, int I, int d, int K, uint8_t* hq, uint8_t* hs,
                              hipStream_t s) {
@@ -381,19 +635,31 @@ hipError_t launch_mx4_gateup(bool a4, const uint8_t* xq, const uint8_t* xs, cons
   p.tiles = static_cast<const RowTile*>(tiles) + 1;
   p.A = xq; p.As = xs; p.perm = perm; p.kdiv = K;
   p.B = wg; p.B2 = wu; p.hq = hq; p.hs = hs;
+  if (tm == kMx4WideRows) {
+    p.a_bytes = static_cast<uint32_t>(a4 ? Tn * d / 2 : Tn * d);
+    p.as_bytes = static_cast<uint32_t>(Tn * (d / 32));
+    return launch_mx4_wide<MX_SWIGLU>(a4, p, rows, s);
+  }
   if (tm == 16) return launch_mx4<MX_SWIGLU, 1, 4>(a4, p, rows, s);
   if (tm == 32) return launch_mx4<MX_SWIGLU, 2, 4>(a4, p, rows, s);
   return launch_mx4<MX_SWIGLU, 4, 4>(a4, p, rows, s);
 }
 
 hipError_t launch_mx4_down(bool a4, const uint8_t* hq, const uint8_t* hs, const uint8_t* wd,
-                           const void* tiles, int tm, int64_t rows, int N, int I, int d, float* y,
+                           const void* tiles, int tm, int64_t rows, int N, int I, int d, void* y,
                            hipStream_t s) {
   Mx4Params p{};
   p.N = N; p.ncols = d; p.K = I;
   p.total = static_cast<const int32_t*>(tiles);
   p.tiles = static_cast<const RowTile*>(tiles) + 1;
-  p.A = hq; p.As = hs; p.kdiv = 1; p.B = wd; p.y = y;
+  p.A = hq; p.As = hs; p.kdiv = 1; p.B = wd;
+  if (tm == kMx4WideRows) {
+    p.yb = static_cast<bf16_t*>(y);
+    p.a_bytes = static_cast<uint32_t>(a4 ? rows * I / 2 : rows * I);
+    p.as_bytes = static_cast<uint32_t>(rows * (I / 32));
+    return launch_mx4_wide<MX_STORE>(a4, p, rows, s);
+  }
+  p.y = static_cast<float*>(y);
   if (tm == 16) return launch_mx4<MX_STORE, 1, 4>(a4, p, rows, s);
   if (tm == 32) return launch_mx4<MX_STORE, 2, 4>(a4, p, rows, s);
   return launch_mx4<MX_STORE, 4, 4>(a4, p, rows, s);

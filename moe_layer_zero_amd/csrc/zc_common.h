@@ -387,14 +387,15 @@ hipError_t launch_int4_quantize(const bf16_t* src, uint8_t* codes, bf16_t* scale
 // 32 reduction steps; rows of x and h in MXFP8 (a4 = false: codes and slab-ordered
 // scales, as launch_mxq_rows leaves them) or MXFP4 (a4 = true: natural order, as
 // launch_mx4_rows leaves them).  d and I multiples of 128.  tiles: row tiles of tm
-// = mx4_rows_per_tile(...) rows.
-int mx4_rows_per_tile(int64_t avg_rows);
-hipError_t launch_mx4_gateup(bool a4, const uint8_t* xq, const uint8_t* xs, const uint8_t* wg,
+// = mx4_rows_per_tile(...) rows.  y is fp32 [P][d], bf16 where tm is kMx4WideRows.
+constexpr int kMx4WideRows = 128;
+int mx4_rows_per_tile(int64_t avg_rows, int64_t Tn, int64_t rows, int64_t d, int64_t I);
+hipError_t launch_mx4_gateup(bool a4, const uint8_t* xq, const uint8_t* xs, int64_t Tn, const uint8_t* wg,
                              const uint8_t* wu, const void* tiles, const int32_t* perm, int tm,
                              int64_t rows, int N, int I, int d, int K, uint8_t* hq, uint8_t* hs,
                              hipStream_t s);
 hipError_t launch_mx4_down(bool a4, const uint8_t* hq, const uint8_t* hs, const uint8_t* wd,
-                           const void* tiles, int tm, int64_t rows, int N, int I, int d, float* y,
+                           const void* tiles, int tm, int64_t rows, int N, int I, int d, void* y,
                            hipStream_t s);
 // Bytes of nmat [R][C] matrices in the kernels' order, and the packer from natural
 // codes [R][C/2] and scales [R][C/32].

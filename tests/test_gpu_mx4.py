@@ -208,7 +208,7 @@ def reference(desc, x, w, route, a):
         lo, hi = quantized_range(h, eh, a)
         off = np.maximum(hi - hq, hq - lo)
         y, ey = product(hq, Wd)
-        ey = ey + (1 + (Wd.shape[1] + 8) * U) * off @ np.abs(Wd).T + Y_ROUND * np.abs(y)
+        ey = ey + (1 + (Wd.shape[1] + 8) * U) * off @ np.abs(Wd).T + y_round(desc) * (np.abs(y) + off @ np.abs(Wd).T)
         g = gate[t, r][:, None]
         out[t] += g * y
         tol[t] += g * ey
@@ -217,7 +217,10 @@ def reference(desc, x, w, route, a):
     return out * desc.out_scale, sc * (tol + (K + 3) * U * (terms + tol))
 
 
-Y_ROUND = 0.0  # y is kept in fp32
+def y_round(desc):
+    """y is kept in fp32, but in bf16 by the kernel of many rows."""
+    many = desc.T * desc.K // desc.E > 20 and desc.d % 512 == 0 and desc.I % 512 == 0
+    return HB if many else 0.0
 
 
 def check(desc, x, w, route, packed, a):
@@ -228,7 +231,7 @@ def check(desc, x, w, route, packed, a):
     err = np.abs(out.cpu().double().numpy() - ref)
     bound = tol * (1 + HB) + HB * np.abs(ref) + 2.0 ** -133
     assert (err <= bound).all(), (err / bound).max()
-    # in the norm out's own rounding is most of it
+    # in the norm the roundings of y and out are most of it
     assert np.linalg.norm(err) <= 2 * HB * np.linalg.norm(ref)
     return out
 
