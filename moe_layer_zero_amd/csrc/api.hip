@@ -1557,7 +1557,7 @@ zc_status zc_moe_mxfp4_pack(const zc_moe_desc* desc, int which, const uint8_t* c
   const int C = static_cast<int>(which == ZC_PACK_GATE_UP ? desc->d : desc->I);
   hipStream_t s = static_cast<hipStream_t>(stream);
   ZC_LAUNCH(ZC_PH_QUANTIZE,
-            zc::launch_mx4_pack(codes, scales, static_cast<uint8_t*>(dst), desc->N, R, C, s),
+            zc::launch_mx4_pack(which == ZC_PACK_DOWN, codes, scales, static_cast<uint8_t*>(dst), desc->N, R, C, s),
             "MXFP4 packing launch");
   return ZC_OK;
 }

@@ -16,12 +16,13 @@
 // bytes 16..31 steps 64 + 16 g ..; in both the lane's scale is that of block g (steps
 // 32 g ..) of its row.
 //
-// Weights of one set (N matrices [R][C]): codes [N][R/16][C/128][lane][16 bytes]:
-// 1 KB holds 16 output columns and 128 reduction steps, a wave's operand as it lies;
-// then scales [N][R/16][ceil(C/512)][lane][4 blocks of 128 steps], E8M0: a lane's
-// four scales of 512 steps in one word.  Of 32 output columns the even ones are the
-// first 16, the odd ones the next: a lane then ends with two neighbours, which make a
-// byte of two 4-bit codes.
+// Weights of one set (N matrices [R][C]), columns in groups of G = 2 (gate, up) or 4
+// (down) blocks of 16: codes [N][R/16/G][C/128][G][lane][16 bytes]: 1 KB holds 16
+// output columns and 128 reduction steps, a wave's operand as it lies, and a group's
+// pieces of a step lie side by side; then scales [N][R/16/G][ceil(C/512)][G][lane][4
+// code blocks], E8M0: a lane's four scales of 512 steps in one word.  A group's columns
+// are dealt to its blocks in turn, so that a lane ends with G neighbours: two 4-bit
+// codes of h, a byte; 8 or 16 bytes of y.
 #include "zc_common.h"
 
 namespace zc {
@@ -32,9 +33,13 @@ constexpr int kThreads = 64 * kWaves;
 constexpr int kStep = 128;  // reduction steps of a code block
 
 enum { MX_SWIGLU = 0, MX_STORE = 1 };
+// Blocks of 16 columns that lie side by side.
+template <int EPI>
+constexpr int kGroup = EPI == MX_SWIGLU ? 2 : 4;
 
 typedef int32_t i32x4_t __attribute__((ext_vector_type(4)));
 typedef int32_t i32x8_t __attribute__((ext_vector_type(8)));
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 
 struct Mx4Params {
   int N, ncols, K;          // experts, output columns (I or d), reduction length (d or I)
@@ -96,27 +101,18 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v) {
   return max(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, v, 0x121, 0xf, 0xf, true)));
 }
 
-// A lane's two neighbouring columns 2 l16, 2 l16 + 1 of a 32-column block of h in
-// row `row`: codes and the block's scale.  The 16 lanes of the row hold the block.
+// Codes of a lane's two neighbouring columns of a 32-column block of h, a row's 16
+// lanes holding the block, and the block's scale S.
 template <bool A4>
-__device__ __forceinline__ void store_h(const Mx4Params& p, int64_t row, int block, int l16,
-                                        float h0, float h1) {
-  const int64_t at = row * p.ncols + 32 * block + 2 * l16;
+__device__ __forceinline__ uint32_t codes_h(float h0, float h1, int& S) {
   if constexpr (A4) {
-    const uint32_t amax = row_max(max(__float_as_uint(h0) & 0x7fffffffu, __float_as_uint(h1) & 0x7fffffffu));
-    const int S = mx4_scale(amax);
-    const uint32_t c = S == 255 ? 0u : mx4_codes<0>(0u, h0, h1, e8m0_f32(S));
-    p.hq[at >> 1] = static_cast<uint8_t>(c);
-    if (l16 == 0) p.hs[row * (p.ncols / 32) + block] = static_cast<uint8_t>(S);
+    S = mx4_scale(row_max(max(__float_as_uint(h0) & 0x7fffffffu, __float_as_uint(h1) & 0x7fffffffu)));
+    return S == 255 ? 0u : mx4_codes<0>(0u, h0, h1, e8m0_f32(S));
   } else {
     // (a NaN does not count in the maximum)
     const float m0 = h0 != h0 ? 0.f : fabsf(h0), m1 = h1 != h1 ? 0.f : fabsf(h1);
-    const int S = mx_scale(__uint_as_float(row_max(__float_as_uint(fmaxf(m0, m1)))));
-    const uint32_t c = mx_code(h0, S) | mx_code(h1, S) << 8;
-    *reinterpret_cast<uint16_t*>(p.hq + at) = static_cast<uint16_t>(c);
-    if (l16 == 0)
-      p.hs[row * (p.ncols / 32) + (block & ~3) + 2 * (block & 1) + ((block >> 1) & 1)] =
-          static_cast<uint8_t>(S);
+    S = mx_scale(__uint_as_float(row_max(__float_as_uint(fmaxf(m0, m1)))));
+    return mx_code(h0, S) | mx_code(h1, S) << 8;
   }
 }
 
@@ -129,6 +125,7 @@ __global__ __launch_bounds__(kThreads, 2) void mx4_kernel(Mx4Params p) {
   constexpr int OUT = (EPI == MX_SWIGLU ? NB / 2 : NB) * 16;  // output columns a workgroup
   constexpr int TM = 16 * RB;
   constexpr int ABYTES = A4 ? kStep / 2 : kStep;  // of a row in a code block
+  constexpr int G = kGroup<EPI>;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 
   const int NT = p.ncols / OUT;
@@ -163,8 +160,8 @@ __global__ __launch_bounds__(kThreads, 2) void mx4_kernel(Mx4Params p) {
       const bool up = EPI == MX_SWIGLU && nb >= NB / 2;
       const uint8_t* base = up ? p.B2 : p.B;
       const int cb = nt * (OUT / 16) + (up ? nb - NB / 2 : nb);
-      code[nb] = base + e * cmat + static_cast<int64_t>(cb) * nkb * 1024;
-      scale[nb] = base + p.N * cmat + e * smat + static_cast<int64_t>(cb) * nq * 256;
+      code[nb] = base + e * cmat + (static_cast<int64_t>(cb / G) * nkb * G + cb % G) * 1024;
+      scale[nb] = base + p.N * cmat + e * smat + (static_cast<int64_t>(cb / G) * nq * G + cb % G) * 256;
     }
     const uint32_t code_lane = lane * 16, scale_lane = lane * 4;
 
@@ -180,10 +177,10 @@ __global__ __launch_bounds__(kThreads, 2) void mx4_kernel(Mx4Params p) {
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
         f.b[nb] = __builtin_nontemporal_load(
-            reinterpret_cast<const i32x4_t*>(code[nb] + kb * 1024 + code_lane));
+            reinterpret_cast<const i32x4_t*>(code[nb] + kb * (1024 * G) + code_lane));
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
-        f.sb[nb] = scale[nb][(kb >> 2) * 256 + (kb & 3) + scale_lane];
+        f.sb[nb] = scale[nb][(kb >> 2) * (256 * G) + (kb & 3) + scale_lane];
     };
     auto load_rows = [&](int kb, Buf& f) {
 #pragma unroll
@@ -246,8 +243,8 @@ __global__ __launch_bounds__(kThreads, 2) void mx4_kernel(Mx4Params p) {
     }
 
     // the wavefronts' sums, added in order; wavefront w finishes its share of the
-    // tile: register v = w of every block, row 16 rb + 4 (lane / 16) + w, columns 2
-    // (lane % 16) (even blocks) and the next (odd ones)
+    // tile: register v = w of every block, row 16 rb + 4 (lane / 16) + w, and of 2 or 4
+    // blocks as many neighbouring columns
     __syncthreads();  // the previous tile's sums have been read
 #pragma unroll
     for (int rb = 0; rb < RB; ++rb)
@@ -270,13 +267,22 @@ __global__ __launch_bounds__(kThreads, 2) void mx4_kernel(Mx4Params p) {
         for (int j = 0; j < NB / 4; ++j) {
           const float h0 = silu_f(sum(rb, 2 * j)) * sum(rb, 2 * j + NB / 2);
           const float h1 = silu_f(sum(rb, 2 * j + 1)) * sum(rb, 2 * j + 1 + NB / 2);
-          store_h<A4>(p, row, nt * (OUT / 32) + j, l16, h0, h1);
+          const int block = nt * (OUT / 32) + j;
+          int S;
+          const uint32_t c = codes_h<A4>(h0, h1, S);
+          if constexpr (A4)
+            p.hq[(row * p.ncols + 32 * block) / 2 + l16] = static_cast<uint8_t>(c);
+          else
+            *reinterpret_cast<uint16_t*>(p.hq + row * p.ncols + 32 * block + 2 * l16) = static_cast<uint16_t>(c);
+          if (l16 == 0)
+            p.hs[row * (p.ncols / 32) +
+                 (A4 ? block : (block & ~3) + 2 * (block & 1) + ((block >> 1) & 1))] = static_cast<uint8_t>(S);
         }
       } else {
 #pragma unroll
-        for (int j = 0; j < NB / 2; ++j)
-          *reinterpret_cast<float2*>(p.y + row * p.ncols + nt * OUT + 32 * j + 2 * l16) =
-              make_float2(sum(rb, 2 * j), sum(rb, 2 * j + 1));
+        for (int j = 0; j < NB / 4; ++j)
+          *reinterpret_cast<f32x4_t*>(p.y + row * p.ncols + nt * OUT + 64 * j + 4 * l16) =
+              f32x4_t{sum(rb, 4 * j), sum(rb, 4 * j + 1), sum(rb, 4 * j + 2), sum(rb, 4 * j + 3)};
       }
     }
   }
@@ -326,7 +332,15 @@ __global__ __launch_bounds__(kThreads, 2) void mx4_wide_kernel(Mx4Params p) {
   constexpr int RPC = 1024 / CB;               // rows of a copy
   constexpr int SC = TM * 16;                  // bytes of the rows' scales of 512 steps
   constexpr int OUT = EPI == MX_SWIGLU ? 128 : 256;
-  constexpr int V = CP + 4, VS = 2 + 4;        // loads of a slab; of 512 steps' scales
+  constexpr int NBUF = A4 ? 4 : 2;             // slabs of weights in registers
+  constexpr int G = kGroup<EPI>;
+  // Loads that may be in flight when slab `slot` of four is needed.  NBUF 4: rows and
+  // weights of the two slabs after it, and the next scales if they went out since.  NBUF
+  // 2: the rows of the slab after next and the weights of the next (issued at the end
+  // of the slab before this one), the scales with the slab before this one.
+  constexpr auto wait_of = [](int slot) constexpr {
+    return NBUF == 4 ? 2 * (CP + 4) + (slot == 1 || slot == 2 ? 6 : 0) : CP + 4 + (slot == 1 ? 6 : 0);
+  };
   __shared__ __align__(16) uint8_t ring[4 * SLOT + 2 * SC];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int nkb = p.K / kStep, nq = nkb / 4;
@@ -351,6 +365,7 @@ __global__ __launch_bounds__(kThreads, 2) void mx4_wide_kernel(Mx4Params p) {
     const int m0 = tile.seg0 + 16 * blo;
     const int mcount = min(tile.seg0 + 16 * bhi, tile.seg1) - m0;
 
+    // rows past the tile's end are copied from past the buffer's: no data moves
     uint32_t src[CP], ssrc[2];
 #pragma unroll
     for (int i = 0; i < CP; ++i) {
@@ -358,14 +373,16 @@ __global__ __launch_bounds__(kThreads, 2) void mx4_wide_kernel(Mx4Params p) {
       const int row = m0 + min(r, mcount - 1);
       const int tok = EPI == MX_SWIGLU ? p.perm[row] / p.kdiv : row;
       const int chunk = A4 ? (lane & 3) ^ ((r >> 2) & 3) : (lane & 7) ^ ((r >> 1) & 7);
-      src[i] = static_cast<uint32_t>(tok) * static_cast<uint32_t>(A4 ? p.K / 2 : p.K) + 16 * chunk;
+      src[i] = r < mcount ? static_cast<uint32_t>(tok) * static_cast<uint32_t>(A4 ? p.K / 2 : p.K) + 16 * chunk
+                          : p.a_bytes;
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int r = (2 * wave + i) * 16 + (lane >> 2);
       const int row = m0 + min(r, mcount - 1);
       const int tok = EPI == MX_SWIGLU ? p.perm[row] / p.kdiv : row;
-      ssrc[i] = static_cast<uint32_t>(tok) * static_cast<uint32_t>(p.K / 32) + 4 * (lane & 3);
+      ssrc[i] = r < mcount ? static_cast<uint32_t>(tok) * static_cast<uint32_t>(p.K / 32) + 4 * (lane & 3)
+                           : p.as_bytes;
     }
 
     const int64_t cmat = static_cast<int64_t>(p.ncols) * p.K / 2, smat = cmat / 16;
@@ -378,37 +395,30 @@ __global__ __launch_bounds__(kThreads, 2) void mx4_wide_kernel(Mx4Params p) {
       scales[m] = __builtin_amdgcn_make_buffer_rsrc(base + p.N * cmat + e * smat, (short)0,
                                                     static_cast<uint32_t>(smat), 0x00020000);
     }
-    int col[4];  // the wavefront's column blocks
-#pragma unroll
-    for (int nb = 0; nb < 4; ++nb)
-      col[nb] = EPI == MX_SWIGLU ? nt * 8 + 2 * wave + (nb & 1) : nt * 16 + 4 * wave + nb;
+    const int grp = nt * 4 + wave;  // the wavefront's group of column blocks
     const uint32_t code_lane = lane * 16, scale_lane = lane * 4;
 
     auto run = [&](auto nrb_c) {
       constexpr int NRB = decltype(nrb_c)::value;
-      i32x4_t b[4][4];  // [slab % 4][column block]
-      int sb[2][4];     // [quad % 2][column block]
-      auto issue = [&](int kb, auto slot_c) {
-        constexpr int slot = decltype(slot_c)::value;
-#pragma unroll
-        for (int i = 0; i < CP; ++i)
-          copy_to_lds16(rows, (lds_void*)(ring + slot * SLOT + (CP * wave + i) * 1024), src[i], kb * CB);
-#pragma unroll
-        for (int nb = 0; nb < 4; ++nb)
-          b[slot][nb] = __builtin_bit_cast(
-              i32x4_t, __builtin_amdgcn_raw_buffer_load_b128(codes[EPI == MX_SWIGLU ? nb / 2 : 0],
-                                                             code_lane, (col[nb] * nkb + kb) * 1024, 0));
+      i32x4_t b[NBUF][4];  // [slab % NBUF][column block]
+      int sb[4], sbn[4];   // scales of these four slabs, and of the next four
+      // one load each: the i-th copy of slab kb's rows, its weights' column block nb;
+      // the i-th of four slabs' scales (two copies of the rows', then the columns')
+      auto issue_row = [&](int kb, int slot, int i) {
+        copy_to_lds16(rows, (lds_void*)(ring + slot * SLOT + (CP * wave + i) * 1024), src[i], kb * CB);
       };
-      auto issue_scales = [&](int quad, auto par_c) {
-        constexpr int par = decltype(par_c)::value;
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
+      auto issue_weight = [&](int kb, int slot, int nb) {
+        b[slot % NBUF][nb] = __builtin_bit_cast(
+            i32x4_t, __builtin_amdgcn_raw_buffer_load_b128(codes[EPI == MX_SWIGLU ? nb / 2 : 0],
+                                                           code_lane, ((grp * nkb + kb) * G + nb % G) * 1024, 0));
+      };
+      auto issue_scale = [&](int quad, int par, int* sc, int i) {
+        if (i < 2)
           copy_to_lds4(rscale, (lds_void*)(ring + 4 * SLOT + par * SC + (2 * wave + i) * 256), ssrc[i],
                        quad * 16);
-#pragma unroll
-        for (int nb = 0; nb < 4; ++nb)
-          sb[par][nb] = __builtin_amdgcn_raw_buffer_load_b32(scales[EPI == MX_SWIGLU ? nb / 2 : 0],
-                                                             scale_lane, (col[nb] * nq + quad) * 256, 0);
+        else
+          sc[i - 2] = __builtin_amdgcn_raw_buffer_load_b32(scales[EPI == MX_SWIGLU ? (i - 2) / 2 : 0],
+                                                           scale_lane, ((grp * nq + quad) * G + (i - 2) % G) * 256, 0);
       };
 
       f32x4_t acc[NRB][4];
@@ -419,30 +429,59 @@ __global__ __launch_bounds__(kThreads, 2) void mx4_wide_kernel(Mx4Params p) {
       // where this lane's row of a block lies in a slot: chunk lq (and 4 + lq)
       const int pos0 = A4 ? lq ^ (l16 >> 2) : lq ^ (l16 >> 1);
       const int frag_lane = l16 * CB + 16 * pos0;
-      const int scale_at = 4 * SLOT + l16 * 16 + (A4 ? lq : 2 * (lq & 1) + (lq >> 1));
+      // and its scale of a slab
+      int scale_at = l16 * 16 + (A4 ? lq : 2 * (lq & 1) + (lq >> 1));
 
-      auto compute = [&](auto slot_c, auto par_c) {
-        constexpr int slot = decltype(slot_c)::value, par = decltype(par_c)::value;
-        auto frag = [&](int rb, i32x8_t& a, int& sa) {
-          a.lo = *reinterpret_cast<const i32x4_t*>(ring + slot * SLOT + rb * 16 * CB + frag_lane);
+      // Fragments are read AHEAD of their multiplications (of 64 or 128 cycles).
+      constexpr int AHEAD = A4 ? (3 < NRB ? 3 : NRB) : 1;
+      const int last = nkb - 1;
+      // One slab: wait for it, meet, multiply, and between the multiplications issue,
+      // one by one, the loads of the rows three slabs ahead, of weights and (with the
+      // first of four slabs) of the next four's scales: issued at once they would
+      // hold the wavefront up until the address unit has taken them all.  No branch: past the end the
+      // last slab is loaded again, so that the number of loads in flight is known.
+      auto slab = [&](int kb, int q4, auto slot_c) {
+        constexpr int slot = decltype(slot_c)::value;
+        constexpr int NL = CP + (NBUF == 4 ? 4 : 0) + (slot == 0 ? 6 : 0);
+        __builtin_amdgcn_s_waitcnt(vmcnt_imm(wait_of(slot)));
+        lds_barrier();
+        i32x8_t a[AHEAD + 1] = {};
+        int sa[AHEAD + 1];
+        auto frag = [&](int rb) {
+          i32x8_t& f = a[rb % (AHEAD + 1)];
+          f.lo = *reinterpret_cast<const i32x4_t*>(ring + slot * SLOT + rb * 16 * CB + frag_lane);
           if constexpr (!A4)
-            a.hi = *reinterpret_cast<const i32x4_t*>(ring + slot * SLOT + rb * 16 * CB + (frag_lane ^ 64));
-          sa = ring[par * SC + rb * 256 + slot * 4 + scale_at];
+            f.hi = *reinterpret_cast<const i32x4_t*>(ring + slot * SLOT + rb * 16 * CB + (frag_lane ^ 64));
+          sa[rb % (AHEAD + 1)] = ring[4 * SLOT + rb * 256 + slot * 4 + scale_at];
         };
-        i32x8_t a[3] = {};
-        int sa[3];
-        frag(0, a[0], sa[0]);
-        if (NRB > 1) frag(1, a[1], sa[1]);
+#pragma unroll
+        for (int rb = 0; rb < AHEAD; ++rb) frag(rb);
 #pragma unroll
         for (int rb = 0; rb < NRB; ++rb) {
-          if (rb + 2 < NRB) frag(rb + 2, a[(rb + 2) % 3], sa[(rb + 2) % 3]);
+          if (rb + AHEAD < NRB) frag(rb + AHEAD);
+#pragma unroll
+          for (int i = NL * rb / NRB; i < NL * (rb + 1) / NRB; ++i) {
+            if (i < CP)
+              issue_row(min(kb + 3, last), (slot + 3) & 3, i);
+            else if (NBUF == 4 && i < CP + 4)
+              issue_weight(min(kb + 3, last), (slot + 3) & 3, i - CP);
+            else
+              issue_scale(min(q4 + 1, nq - 1), (q4 + 1) & 1, sbn, i - CP - (NBUF == 4 ? 4 : 0));
+          }
 #pragma unroll
           for (int nb = 0; nb < 4; ++nb) {
             i32x8_t w = {};
-            w.lo = b[slot][nb];
+            w.lo = b[slot % NBUF][nb];
             acc[rb][nb] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                a[rb % 3], w, acc[rb][nb], A4 ? 4 : 0, 4, 0, sa[rb % 3], slot, sb[par][nb]);
+                a[rb % (AHEAD + 1)], w, acc[rb][nb], A4 ? 4 : 0, 4, 0, sa[rb % (AHEAD + 1)], slot,
+                sb[nb]);
           }
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        if constexpr (NBUF == 2) {
+#pragma unroll
+          for (int nb = 0; nb < 4; ++nb) issue_weight(min(kb + 2, last), slot, nb);
+          __builtin_amdgcn_sched_barrier(0);
         }
       };
 
@@ -450,74 +489,69 @@ __global__ __launch_bounds__(kThreads, 2) void mx4_wide_kernel(Mx4Params p) {
       using C1 = std::integral_constant<int, 1>;
       using C2 = std::integral_constant<int, 2>;
       using C3 = std::integral_constant<int, 3>;
-      const int last = nkb - 1;
-      // one slab: wait for it, meet, issue the slab three ahead (and with the first
-      // of four the next four's scales), multiply.  No branch: past the end the last
-      // slab is loaded again, so that the number of loads in flight is known.
-      auto quad = [&](int q4, auto par_c) {
-        constexpr int par = decltype(par_c)::value;
-        const int kb = 4 * q4;
-        __builtin_amdgcn_s_waitcnt(vmcnt_imm(2 * V));
-        lds_barrier();
-        issue(min(kb + 3, last), C3{});
-        issue_scales(min(q4 + 1, nq - 1), std::integral_constant<int, 1 - par>{});
-        __builtin_amdgcn_sched_barrier(0);
-        compute(C0{}, par_c);
-        __builtin_amdgcn_sched_barrier(0);
-        __builtin_amdgcn_s_waitcnt(vmcnt_imm(2 * V + VS));
-        lds_barrier();
-        issue(min(kb + 4, last), C0{});
-        __builtin_amdgcn_sched_barrier(0);
-        compute(C1{}, par_c);
-        __builtin_amdgcn_sched_barrier(0);
-        __builtin_amdgcn_s_waitcnt(vmcnt_imm(2 * V + VS));
-        lds_barrier();
-        issue(min(kb + 5, last), C1{});
-        __builtin_amdgcn_sched_barrier(0);
-        compute(C2{}, par_c);
-        __builtin_amdgcn_sched_barrier(0);
-        __builtin_amdgcn_s_waitcnt(vmcnt_imm(2 * V));
-        lds_barrier();
-        issue(min(kb + 6, last), C2{});
-        __builtin_amdgcn_sched_barrier(0);
-        compute(C3{}, par_c);
-        __builtin_amdgcn_sched_barrier(0);
-      };
-
       lds_barrier();  // the ring is free: the previous tile's reads are done
-      issue_scales(0, C0{});
-      issue(0, C0{});
-      __builtin_amdgcn_sched_barrier(0);
-      issue(1, C1{});
-      __builtin_amdgcn_sched_barrier(0);
-      issue(2, C2{});
-      __builtin_amdgcn_sched_barrier(0);
-      int q4 = 0;
-      for (; q4 + 2 <= nq; q4 += 2) {
-        quad(q4, C0{});
-        quad(q4 + 1, C1{});
+#pragma unroll
+      for (int i = 0; i < 6; ++i) issue_scale(0, 0, sb, i);
+#pragma unroll
+      for (int kb = 0; kb < 3; ++kb) {
+#pragma unroll
+        for (int i = 0; i < CP; ++i) issue_row(kb, kb, i);
+#pragma unroll
+        for (int nb = 0; nb < 4; ++nb)
+          if (NBUF == 4 || kb < 2) issue_weight(kb, kb, nb);
+        __builtin_amdgcn_sched_barrier(0);
       }
-      if (q4 < nq) quad(q4, C0{});
+      for (int q4 = 0; q4 < nq; ++q4) {
+        slab(4 * q4, q4, C0{});
+        slab(4 * q4 + 1, q4, C1{});
+        slab(4 * q4 + 2, q4, C2{});
+        slab(4 * q4 + 3, q4, C3{});
+        scale_at ^= SC;
+#pragma unroll
+        for (int nb = 0; nb < 4; ++nb) sb[nb] = sbn[nb];
+      }
       __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));  // no copy of this tile lands in the next one's ring
 
+      // Results go out through resources that end with the tile's rows: no branch.
+      if constexpr (EPI == MX_SWIGLU) {
+        const int pitch = A4 ? p.ncols / 2 : p.ncols, sp = p.ncols / 32, block = nt * 4 + wave;
+        const __amdgpu_buffer_rsrc_t hq = __builtin_amdgcn_make_buffer_rsrc(
+            p.hq + static_cast<int64_t>(m0) * pitch, (short)0, mcount * pitch, 0x00020000);
+        const __amdgpu_buffer_rsrc_t hs = __builtin_amdgcn_make_buffer_rsrc(
+            p.hs + static_cast<int64_t>(m0) * sp, (short)0, mcount * sp, 0x00020000);
+        const int at = 4 * lq * pitch + (A4 ? 16 * block + l16 : 32 * block + 2 * l16);
+        // the first lane of a row writes its scale
+        const int sat = l16 ? 0x70000000
+                            : 4 * lq * sp + (A4 ? block : (block & ~3) + 2 * (block & 1) + ((block >> 1) & 1));
 #pragma unroll
-      for (int rb = 0; rb < NRB; ++rb)
+        for (int rb = 0; rb < NRB; ++rb)
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          const int r = 16 * rb + 4 * lq + v;
-          if (r >= mcount) continue;  // (the 16 lanes of a row alike)
-          const int64_t row = static_cast<int64_t>(m0) + r;
-          if constexpr (EPI == MX_SWIGLU) {
-            store_h<A4>(p, row, nt * 4 + wave, l16, silu_f(acc[rb][0][v]) * acc[rb][2][v],
-                        silu_f(acc[rb][1][v]) * acc[rb][3][v]);
-          } else {
+          for (int v = 0; v < 4; ++v) {
+            int S;
+            const uint32_t c = codes_h<A4>(silu_f(acc[rb][0][v]) * acc[rb][2][v],
+                                           silu_f(acc[rb][1][v]) * acc[rb][3][v], S);
+            if constexpr (A4)
+              __builtin_amdgcn_raw_buffer_store_b8(static_cast<uint8_t>(c), hq, at + (16 * rb + v) * pitch, 0, 0);
+            else
+              __builtin_amdgcn_raw_buffer_store_b16(static_cast<uint16_t>(c), hq, at + (16 * rb + v) * pitch, 0, 0);
+            __builtin_amdgcn_raw_buffer_store_b8(static_cast<uint8_t>(S), hs, sat + (16 * rb + v) * sp, 0, 0);
+          }
+      } else {
+        const __amdgpu_buffer_rsrc_t y = __builtin_amdgcn_make_buffer_rsrc(
+            p.yb + static_cast<int64_t>(m0) * p.ncols, (short)0, mcount * p.ncols * 2, 0x00020000);
+        const int at = (4 * lq * p.ncols + nt * OUT + 64 * wave + 4 * l16) * 2;
+#pragma unroll
+        for (int rb = 0; rb < NRB; ++rb)
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            u32x2_t w;
 #pragma unroll
             for (int j = 0; j < 2; ++j)
-              *reinterpret_cast<uint32_t*>(p.yb + row * p.ncols + nt * OUT + 64 * wave + 32 * j + 2 * l16) =
-                  static_cast<uint32_t>(f2bf(acc[rb][2 * j][v])) |
-                  static_cast<uint32_t>(f2bf(acc[rb][2 * j + 1][v])) << 16;
+              w[j] = static_cast<uint32_t>(f2bf(acc[rb][2 * j][v])) |
+                     static_cast<uint32_t>(f2bf(acc[rb][2 * j + 1][v])) << 16;
+            __builtin_amdgcn_raw_buffer_store_b64(w, y, at + (16 * rb + v) * p.ncols * 2, 0, 0);
           }
-        }
+      }
     };
     switch ((bhi - blo + 1) >> 1) {
       case 1: run(std::integral_constant<int, 2>{}); break;
@@ -545,28 +579,29 @@ hipError_t launch_mx4_wide(bool a4, Mx4Params p, int64_t rows, hipStream_t s) {
 __global__ __launch_bounds__(256) void mx4_pack_kernel(const u32x4_t* __restrict__ codes,
                                                        const uint8_t* __restrict__ scales,
                                                        uint8_t* __restrict__ dst, int64_t nmat,
-                                                       int R, int C) {
+                                                       int R, int C, int log_group) {
   const int nkb = C / kStep, nq = (nkb + 3) / 4;
   const int64_t pieces = nmat * R * (C / 32);
   const int64_t i0 = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   const int64_t step = static_cast<int64_t>(gridDim.x) * 256;
   // column of lane l16 of a 16-column block of the matrices' R rows
-  auto column = [](int64_t blk, int l16) { return (blk >> 1) * 32 + 2 * l16 + (blk & 1); };
+  const int G = 1 << log_group;
+  auto column = [=](int64_t group, int j, int l16) { return ((group * 16 + l16) << log_group) + j; };
   for (int64_t i = i0; i < pieces; i += step) {
-    // i = ((mat R/16 + cb) nkb + kb) 64 + lane
-    const int lane = i & 63;
-    const int64_t blk = i >> 6;
+    // i = (((mat R/16/G + group) nkb + kb) G + block) 64 + lane
+    const int lane = i & 63, j = (i >> 6) & (G - 1);
+    const int64_t blk = i >> (6 + log_group);
     const int kb = static_cast<int>(blk % nkb);
-    const int64_t row = column(blk / nkb, lane & 15);
+    const int64_t row = column(blk / nkb, j, lane & 15);
     reinterpret_cast<u32x4_t*>(dst)[i] = codes[row * (C / 32) + kb * 4 + (lane >> 4)];
   }
   const int64_t ns = nmat * (R / 16) * nq * 256;
   for (int64_t i = i0; i < ns; i += step) {
-    // i = (((mat R/16 + cb) nq + quad) 64 + lane) 4 + block of 128 steps
-    const int lane = (i >> 2) & 63;
-    const int64_t blk = i >> 8;
+    // i = ((((mat R/16/G + group) nq + quad) G + block) 64 + lane) 4 + code block
+    const int lane = (i >> 2) & 63, j = (i >> 8) & (G - 1);
+    const int64_t blk = i >> (8 + log_group);
     const int kb = static_cast<int>(blk % nq) * 4 + static_cast<int>(i & 3);
-    const int64_t row = column(blk / nq, lane & 15);
+    const int64_t row = column(blk / nq, j, lane & 15);
     dst[pieces * 16 + i] = kb < nkb ? scales[row * (C / 32) + kb * 4 + (lane >> 4)] : 0;
   }
 }
@@ -669,11 +704,11 @@ int64_t mx4_weight_bytes(int64_t nmat, int64_t R, int64_t C) {
   return nmat * R * (C / 2) + nmat * (R / 16) * ((C / kStep + 3) / 4) * 256;
 }
 
-hipError_t launch_mx4_pack(const uint8_t* codes, const uint8_t* scales, uint8_t* dst, int64_t nmat,
-                           int R, int C, hipStream_t s) {
+hipError_t launch_mx4_pack(bool down, const uint8_t* codes, const uint8_t* scales, uint8_t* dst,
+                           int64_t nmat, int R, int C, hipStream_t s) {
   const int64_t n = mx4_weight_bytes(nmat, R, C) / 16;
   hipLaunchKernelGGL(mx4_pack_kernel, dim3(grid_of((n + 255) / 256)), dim3(256), 0, s,
-                     reinterpret_cast<const u32x4_t*>(codes), scales, dst, nmat, R, C);
+                     reinterpret_cast<const u32x4_t*>(codes), scales, dst, nmat, R, C, down ? 2 : 1);
   return hipGetLastError();
 }
 

@@ -398,10 +398,10 @@ hipError_t launch_mx4_down(bool a4, const uint8_t* hq, const uint8_t* hs, const 
                            const void* tiles, int tm, int64_t rows, int N, int I, int d, void* y,
                            hipStream_t s);
 // Bytes of nmat [R][C] matrices in the kernels' order, and the packer from natural
-// codes [R][C/2] and scales [R][C/32].
+// codes [R][C/2] and scales [R][C/32] of w_down (down) or of w_gate and w_up.
 int64_t mx4_weight_bytes(int64_t nmat, int64_t R, int64_t C);
-hipError_t launch_mx4_pack(const uint8_t* codes, const uint8_t* scales, uint8_t* dst, int64_t nmat,
-                           int R, int C, hipStream_t s);
+hipError_t launch_mx4_pack(bool down, const uint8_t* codes, const uint8_t* scales, uint8_t* dst,
+                           int64_t nmat, int R, int C, hipStream_t s);
 // R rows of C values (a multiple of 32) -> natural codes and scales, and the values
 // they stand for (nullable).
 template <typename T>
