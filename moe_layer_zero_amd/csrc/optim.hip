@@ -144,52 +144,52 @@ __device__ __forceinline__ float row_max(float v) {
   return fmaxf(v, turn(v, std::integral_constant<int, 0x121>{}));
 }
 
-// E4M3 code of |q| <= 448 rounded down after r of a code's distance is added,
-// 0 <= r < 1.
-__device__ __forceinline__ uint32_t e4m3_down(float q, float r) {
-  const uint32_t a = __float_as_uint(q) & 0x7fffffffu;
-  const uint32_t eb = max(a >> 23, 121u);  // below 2^-6 the distance stays 2^-9
-  const float n = __uint_as_float(a) * __uint_as_float((257u - eb) << 23) + r;
-  uint32_t c = min(8u * (eb - 121u) + static_cast<uint32_t>(n), 0x7eu);
-  if (a > 0x7f800000u) c = 0x7fu;
-  return c | (__float_as_uint(q) >> 24 & 0x80u);
+// The smaller, larger of two numbers; NaN where one is.
+__device__ __forceinline__ float min_nan(float a, float b) { return __builtin_elementwise_minimum(a, b); }
+__device__ __forceinline__ float max_nan(float a, float b) { return __builtin_elementwise_maximum(a, b); }
+
+// a / b with the hardware's reciprocal r of b (1 ulp) and the remainder of the
+// quotient: correctly rounded for normal r.
+__device__ __forceinline__ float quotient(float a, float b, float r) {
+  const float t = a * r;
+  return fmaf(fmaf(-t, b, a), r, t);
 }
 
-// Eight values of a block as codes and the block's scale.
+// Eight values of a block as codes and the block's scale.  Rounded stochastically
+// a value goes down after 16 random bits' part of its distance is added: what the
+// hardware's conversion does with them as the upper bits of its operand (measured:
+// the same for every exponent, subnormal codes too).  ROOT: none is negative, and
+// no positive one becomes 0.
 template <bool SR, bool ROOT>
 __device__ __forceinline__ uint2 encode(const float* f, const uint32_t* noise, float& scale) {
   float amax = 0.f;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(f[e]));
+  for (int e = 0; e < 8; ++e) amax = fmaxf(amax, ROOT ? f[e] : fabsf(f[e]));
   scale = fmaxf(row_max(amax) * (1.f / 448.f), 0x1p-120f);
-  // f / scale, correctly rounded, with one division for the eight: the quotient by
-  // the reciprocal, then its remainder
   const float inv = 1.f / scale;
   float q[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    const float t = f[e] * inv;
-    q[e] = fmaf(fmaf(-t, scale, f[e]), inv, t);
+    q[e] = quotient(f[e], scale, inv);
+    if constexpr (ROOT) q[e] = f[e] > 0.f ? max_nan(q[e], 0x1p-9f) : f[e];
+    // (the quotient of the largest may be a rounding above 448)
+    q[e] = min_nan(q[e], 448.f);
+    if constexpr (!ROOT) q[e] = max_nan(q[e], -448.f);
   }
-  uint32_t w[2] = {0u, 0u};
-  if constexpr (SR) {
+  int w[2] = {0, 0};
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const uint32_t bits = ROOT ? noise[e] >> 16 : noise[e] & 0xffffu;
-      uint32_t c = e4m3_down(q[e], static_cast<float>(bits) * 0x1p-16f);
-      if (ROOT && c == 0u && f[e] > 0.f) c = 1u;
-      w[e / 4] |= c << (8 * (e % 4));
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; e += 4) {
-      int c = __builtin_amdgcn_cvt_pk_fp8_f32(q[e], q[e + 1], 0, false);
-      w[e / 4] = __builtin_amdgcn_cvt_pk_fp8_f32(q[e + 2], q[e + 3], c, true);
-    }
-    if constexpr (ROOT) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if ((w[e / 4] >> (8 * (e % 4)) & 0xffu) == 0u && f[e] > 0.f) w[e / 4] |= 1u << (8 * (e % 4));
+  for (int i = 0; i < 2; ++i) {
+    const float* v = q + 4 * i;
+    if constexpr (SR) {
+      const uint32_t* z = noise + 4 * i;
+      auto bits = [](uint32_t n) { return static_cast<int>(ROOT ? n & 0xffff0000u : n << 16); };
+      w[i] = __builtin_amdgcn_cvt_sr_fp8_f32(v[0], bits(z[0]), w[i], 0);
+      w[i] = __builtin_amdgcn_cvt_sr_fp8_f32(v[1], bits(z[1]), w[i], 1);
+      w[i] = __builtin_amdgcn_cvt_sr_fp8_f32(v[2], bits(z[2]), w[i], 2);
+      w[i] = __builtin_amdgcn_cvt_sr_fp8_f32(v[3], bits(z[3]), w[i], 3);
+    } else {
+      w[i] = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], 0, false);
+      w[i] = __builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], w[i], true);
     }
   }
   return make_uint2(w[0], w[1]);
@@ -231,10 +231,13 @@ __device__ __forceinline__ void load(const T* p, int left, float* f) {
 template <typename T, int W>
 __device__ __forceinline__ void store(T* p, int left, const float* f) {
   if (left >= W) {
-    if constexpr (sizeof(T) == 2 && W == 4) {
-      *reinterpret_cast<uint2*>(p) =
-          make_uint2(f2bf(f[0]) | static_cast<uint32_t>(f2bf(f[1])) << 16,
-                     f2bf(f[2]) | static_cast<uint32_t>(f2bf(f[3])) << 16);
+    if constexpr (sizeof(T) == 2) {
+      // (the vector type: the hardware converts two at a time)
+      typedef __bf16 bf16w_t __attribute__((ext_vector_type(W)));
+      bf16w_t v;
+#pragma unroll
+      for (int e = 0; e < W; ++e) v[e] = static_cast<__bf16>(f[e]);
+      *reinterpret_cast<bf16w_t*>(p) = v;
     } else {
 #pragma unroll
       for (int i = 0; i < W / V16<T>::n; ++i) V16<T>::store(p + i * V16<T>::n, f + i * V16<T>::n);
@@ -243,6 +246,24 @@ __device__ __forceinline__ void store(T* p, int left, const float* f) {
 #pragma unroll
     for (int e = 0; e < W; ++e)
       if (e < left) Elem<T>::st(p + e, f[e]);
+  }
+}
+// bf16 weights rounded down after 16 random bits' part of their distance is added:
+// the upper half of the sum (an infinity and a NaN stay what they are).
+template <int W>
+__device__ __forceinline__ void store_bits(bf16_t* p, int left, const float* f, const uint32_t* add) {
+  uint32_t u[W];
+#pragma unroll
+  for (int e = 0; e < W; ++e) u[e] = __float_as_uint(f[e]) + add[e];
+  if (left >= W) {
+    uint32_t w[W / 2];
+#pragma unroll
+    for (int e = 0; e < W / 2; ++e) w[e] = __builtin_amdgcn_perm(u[2 * e + 1], u[2 * e], 0x07060302u);
+    __builtin_memcpy(__builtin_assume_aligned(p, 2 * W), w, 2 * W);
+  } else {
+#pragma unroll
+    for (int e = 0; e < W; ++e)
+      if (e < left) p[e] = static_cast<bf16_t>(u[e] >> 16);
   }
 }
 __device__ __forceinline__ uint2 load_codes(const uint8_t* p, int left) {
@@ -327,7 +348,9 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamArgs a) {
       m[e] = b1 * m[e] + c1 * g[e];
       v[e] = b2 * v[e] + c2 * (g[e] * g[e]);
       const float r = sqrtf(v[e]);
-      p[e] = p[e] * keep - rate * (m[e] / (r * root + eps));
+      // (at most 2^125, so that its reciprocal is a normal number)
+      const float den = fminf(r * root + eps, 0x1p125f);
+      p[e] = p[e] * keep - rate * quotient(m[e], den, __builtin_amdgcn_rcpf(den));
       if constexpr (B8) v[e] = r;
     }
     uint32_t noise[W];
@@ -338,14 +361,13 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamArgs a) {
     }
     if constexpr (MASTER) store<float, W>(x.master + j, left, p);
     if constexpr (SR && sizeof(P) == 2 && !MASTER) {
+      uint32_t add[W];
 #pragma unroll
-      for (int e = 0; e < W; ++e) {
-        const uint32_t bits = __float_as_uint(p[e]);
-        if ((bits & 0x7f800000u) != 0x7f800000u)
-          p[e] = __uint_as_float(bits + ((noise[e] * 0xC2B2AE3Du) >> 16) & 0xffff0000u);
-      }
+      for (int e = 0; e < W; ++e) add[e] = (noise[e] * 0xC2B2AE3Du) >> 16;
+      store_bits<W>(static_cast<bf16_t*>(x.p) + j, left, p, add);
+    } else {
+      store<P, W>(static_cast<P*>(x.p) + j, left, p);
     }
-    store<P, W>(static_cast<P*>(x.p) + j, left, p);
     if constexpr (B8) {
       const int64_t blk = j >> 7;
       float sm, sv;
