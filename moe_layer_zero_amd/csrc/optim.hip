@@ -144,10 +144,6 @@ __device__ __forceinline__ float row_max(float v) {
   return fmaxf(v, turn(v, std::integral_constant<int, 0x121>{}));
 }
 
-// The smaller, larger of two numbers; NaN where one is.
-__device__ __forceinline__ float min_nan(float a, float b) { return __builtin_elementwise_minimum(a, b); }
-__device__ __forceinline__ float max_nan(float a, float b) { return __builtin_elementwise_maximum(a, b); }
-
 // a / b with the hardware's reciprocal r of b (1 ulp) and the remainder of the
 // quotient: correctly rounded for normal r.
 __device__ __forceinline__ float quotient(float a, float b, float r) {
@@ -182,8 +178,10 @@ __device__ __forceinline__ void roots(const float* x, float* r) {
 // Eight values of a block as codes and the block's scale.  Rounded stochastically
 // a value goes down after 16 random bits' part of its distance is added: what the
 // hardware's conversion does with them as the upper bits of its operand (measured:
-// the same for every exponent, subnormal codes too).  ROOT: none is negative, and
-// no positive one becomes 0.
+// the same for every exponent, subnormal codes too).  The quotient of the largest
+// may be a rounding above 448, 2^-20 of the distance to the next code: less than
+// what the random bits lack of 1, and nothing to a rounding to nearest.  ROOT: none
+// is negative, and no positive one becomes 0.
 template <bool SR, bool ROOT>
 __device__ __forceinline__ uint2 encode(const float* f, const uint32_t* noise, float& scale) {
   float amax = 0.f;
@@ -191,29 +189,28 @@ __device__ __forceinline__ uint2 encode(const float* f, const uint32_t* noise, f
   for (int e = 0; e < 8; ++e) amax = fmaxf(amax, ROOT ? f[e] : fabsf(f[e]));
   scale = fmaxf(row_max(amax) * (1.f / 448.f), 0x1p-120f);
   const float inv = 1.f / scale;
-  float q[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    q[e] = quotient(f[e], scale, inv);
-    if constexpr (ROOT) q[e] = f[e] > 0.f ? max_nan(q[e], 0x1p-9f) : f[e];
-    // (the quotient of the largest may be a rounding above 448)
-    q[e] = min_nan(q[e], 448.f);
-    if constexpr (!ROOT) q[e] = max_nan(q[e], -448.f);
-  }
   int w[2] = {0, 0};
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const float* v = q + 4 * i;
+    float q[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) q[e] = quotient(f[4 * i + e], scale, inv);
     if constexpr (SR) {
       const uint32_t* z = noise + 4 * i;
       auto bits = [](uint32_t n) { return static_cast<int>(ROOT ? n & 0xffff0000u : n << 16); };
-      w[i] = __builtin_amdgcn_cvt_sr_fp8_f32(v[0], bits(z[0]), w[i], 0);
-      w[i] = __builtin_amdgcn_cvt_sr_fp8_f32(v[1], bits(z[1]), w[i], 1);
-      w[i] = __builtin_amdgcn_cvt_sr_fp8_f32(v[2], bits(z[2]), w[i], 2);
-      w[i] = __builtin_amdgcn_cvt_sr_fp8_f32(v[3], bits(z[3]), w[i], 3);
+      w[i] = __builtin_amdgcn_cvt_sr_fp8_f32(q[0], bits(z[0]), w[i], 0);
+      w[i] = __builtin_amdgcn_cvt_sr_fp8_f32(q[1], bits(z[1]), w[i], 1);
+      w[i] = __builtin_amdgcn_cvt_sr_fp8_f32(q[2], bits(z[2]), w[i], 2);
+      w[i] = __builtin_amdgcn_cvt_sr_fp8_f32(q[3], bits(z[3]), w[i], 3);
     } else {
-      w[i] = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], 0, false);
-      w[i] = __builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], w[i], true);
+      w[i] = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
+      w[i] = __builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], w[i], true);
+    }
+    // (a byte of zeros somewhere: few blocks, or all zeros)
+    if (ROOT && __any(((w[i] - 0x01010101) & ~w[i] & 0x80808080) != 0)) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if ((w[i] >> (8 * e) & 0xff) == 0 && f[4 * i + e] > 0.f) w[i] |= 1 << (8 * e);
     }
   }
   return make_uint2(w[0], w[1]);
@@ -380,18 +377,18 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamArgs a) {
     }
     float r[W];
     roots<W>(v, r);
+    // (the hardware's reciprocal, 1 ulp: a rounding or two of the step, which is small
+    // beside p)
 #pragma unroll
     for (int e = 0; e < W; ++e) {
-#pragma clang fp contract(off)
-      // (at most 2^125, so that its reciprocal is a normal number)
-      const float den = fminf(r[e] * root + eps, 0x1p125f);
-      p[e] = p[e] * keep - rate * quotient(m[e], den, __builtin_amdgcn_rcpf(den));
+      const float q = m[e] * __builtin_amdgcn_rcpf(fmaf(r[e], root, eps));
+      p[e] = fmaf(-rate, q, p[e] * keep);
     }
     uint32_t noise[W];
     if constexpr (SR) {
       const uint32_t key = key0 + 0xC2B2AE3Du * static_cast<uint32_t>(j >> 32);
 #pragma unroll
-      for (int e = 0; e < W; ++e) noise[e] = mix((static_cast<uint32_t>(j) + e) ^ key);
+      for (int e = 0; e < W; ++e) noise[e] = mix((static_cast<uint32_t>(j) ^ key) ^ e);  // j + e = j ^ e
     }
     if constexpr (MASTER) store<float, W>(x.master + j, left, p);
     if constexpr (SR && sizeof(P) == 2 && !MASTER) {
