@@ -1017,7 +1017,8 @@ zc_status check_adamw(const zc_adamw_cfg* c, bool device_step) {
   if (c->rounding != ZC_ROUND_NEAREST && c->rounding != ZC_ROUND_STOCHASTIC)
     return fail(ZC_ERR_INVALID, "rounding %d is neither ZC_ROUND_NEAREST nor ZC_ROUND_STOCHASTIC",
                 c->rounding);
-  if (!std::isfinite(c->lr) || c->lr < 0.0) return fail(ZC_ERR_INVALID, "lr=%g", c->lr);
+  if (!std::isfinite(static_cast<float>(c->lr)) || c->lr < 0.0)
+    return fail(ZC_ERR_INVALID, "lr=%g", c->lr);
   if (!(c->beta1 >= 0.0 && c->beta1 < 1.0) || !(c->beta2 >= 0.0 && c->beta2 < 1.0))
     return fail(ZC_ERR_INVALID, "beta1=%g beta2=%g outside [0, 1)", c->beta1, c->beta2);
   const float eps = static_cast<float>(c->eps);
@@ -1072,8 +1073,10 @@ zc_status do_adamw(const zc_adamw_cfg* c, const zc_adamw_tensor* t, int64_t coun
   add_span(spans, lr, 4, -1, "lr", false);
   add_span(spans, step, 8, -1, "step", false);
   ZC_CHECK(check_spans(spans));
-  const zc::AdamwScalars sc{c->lr, c->beta1, c->beta2, c->step, factor, lr, step,
-                            static_cast<float>(c->eps), c->seed};
+  auto f = [](double v) { return static_cast<float>(v); };
+  const zc::AdamwScalars sc{std::log(c->beta1), std::log(c->beta2), c->step, factor, lr, step,
+                            f(c->lr), f(c->beta1), f(1.0 - c->beta1), f(c->beta2), f(1.0 - c->beta2),
+                            f(c->eps), c->seed};
   ZC_LAUNCH(ZC_PH_ADAMW,
             zc::launch_adamw(list.data(), count, c->p_dtype == ZC_BF16, c->g_dtype == ZC_BF16, master,
                              b8, c->rounding == ZC_ROUND_STOCHASTIC, sc, s),

@@ -27,35 +27,55 @@ namespace {
 constexpr int kThreads = 256;
 
 // Tensors of one launch, passed by value: nothing has to be copied to the device
-// before it, and a captured launch holds them.
-constexpr int kNormTensors = 128;
-constexpr int kAdamTensors = 46;
+// before it, and a captured launch holds them.  As many as the 4 KB of kernel
+// arguments take; short lists have a kernel whose arguments are short (the host
+// writes them and each workgroup reads them: 198 k weights in 5 tensors, ...).
+constexpr int kFew = 8;
+constexpr int kArgBytes = 4096;
 
+template <int CAP>
 struct NormArgs {
-  const void* g[kNormTensors];
-  int64_t n[kNormTensors];
-  int32_t first[kNormTensors + 1];  // first chunk of each
+  const void* g[CAP];
+  int64_t n[CAP];
+  int32_t first[CAP + 1];  // first chunk of each
   int32_t count;
-  double* part;                     // a sum for each chunk
+  int32_t chunk;           // elements of a chunk
+  double* part;            // a sum for each chunk
 };
+constexpr int kNormTensors = (kArgBytes - 32) / 20;
 
+// A tensor's pointers: p, g, m, v, with 8-bit states their scales, and the fp32 copy.
+enum { T_P = 0, T_G, T_M, T_V, T_MS, T_VS };
+template <int NP, int CAP>
 struct AdamArgs {
-  AdamwTensor t[kAdamTensors];
-  int32_t first[kAdamTensors + 1];
+  void* ptr[CAP][NP];
+  int64_t n[CAP];
+  float decay[CAP];
+  int32_t first[CAP + 1];  // first chunk of each
   int32_t count;
   int32_t passes;  // rounds of kThreads vectors in a chunk
-  int32_t base;    // number of t[0] in the whole list
+  int32_t base;    // number of the first tensor in the whole list
   AdamwScalars s;
 };
-static_assert(sizeof(NormArgs) <= 4096 && sizeof(AdamArgs) <= 4096, "kernel arguments");
+template <int NP>
+constexpr int kAdamTensors = (kArgBytes - 32 - int(sizeof(AdamwScalars))) / (8 * NP + 16);
+static_assert(sizeof(NormArgs<kNormTensors>) <= kArgBytes &&
+              sizeof(AdamArgs<4, kAdamTensors<4>>) <= kArgBytes &&
+              sizeof(AdamArgs<7, kAdamTensors<7>>) <= kArgBytes, "kernel arguments");
 
-// The tensor that chunk b belongs to.
-template <typename A>
-__device__ __forceinline__ int tensor_of(const A& a, int b) {
-  int lo = 0, hi = a.count;  // first[lo] <= b < first[hi]
+// The tensor that chunk b belongs to: the last whose first chunk is not behind b.
+template <int CAP>
+__device__ __forceinline__ int tensor_of(const int32_t (&first)[CAP], int count, int b) {
+  if constexpr (CAP <= kFew + 1) {
+    int i = 0;
+#pragma unroll
+    for (int k = 1; k < CAP - 1; ++k) i += k < count && first[k] <= b;
+    return i;
+  }
+  int lo = 0, hi = count;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (a.first[mid] <= b) lo = mid; else hi = mid;
+    if (first[mid] <= b) lo = mid; else hi = mid;
   }
   return lo;
 }
@@ -74,15 +94,15 @@ __device__ __forceinline__ double block_sum(double v, double* s_red) {
   return v;
 }
 
-template <typename T>
-__global__ __launch_bounds__(kThreads) void sqsum_kernel(NormArgs a, int chunk) {
+template <typename T, int CAP>
+__global__ __launch_bounds__(kThreads) void sqsum_kernel(NormArgs<CAP> a) {
   constexpr int V = V16<T>::n;
   __shared__ double s_red[kThreads / 64];
-  const int i = tensor_of(a, blockIdx.x);
+  const int i = tensor_of(a.first, a.count, blockIdx.x);
   const T* g = static_cast<const T*>(a.g[i]);
   const int64_t n = a.n[i];
-  const int64_t begin = static_cast<int64_t>(blockIdx.x - a.first[i]) * chunk;
-  const int64_t end = begin + chunk < n ? begin + chunk : n;
+  const int64_t begin = static_cast<int64_t>(blockIdx.x - a.first[i]) * a.chunk;
+  const int64_t end = begin + a.chunk < n ? begin + a.chunk : n;
   double sum = 0.0;
   int64_t j = begin + threadIdx.x * V;
   for (; j + 3 * kThreads * V + V <= end; j += 4 * kThreads * V) {
@@ -312,37 +332,30 @@ __device__ __forceinline__ void store_codes(uint8_t* p, int left, uint2 c) {
     if (e < left) p[e] = static_cast<uint8_t>(w[e / 4] >> (8 * (e % 4)));
 }
 
-// 1 - b^t in binary64 (relative error 2^-53 / (1 - b) at most, from the
-// subtraction).
-__device__ __forceinline__ double one_minus_power(double b, int64_t t) {
-  double r = 1.0;
-  for (; t > 0; t >>= 1) {
-    if (t & 1) r *= b;
-    b *= b;
-  }
-  return 1.0 - r;
-}
-
 // P weights, G gradients; MASTER: fp32 weights with bf16 copies; B8: 8-bit
 // states; SR: stochastic rounding of what has fewer than 32 bits.
-template <typename P, typename G, bool MASTER, bool B8, bool SR>
-__global__ __launch_bounds__(kThreads) void adamw_kernel(AdamArgs a) {
+template <typename P, typename G, bool MASTER, bool B8, bool SR, int CAP>
+__global__ __launch_bounds__(kThreads) void adamw_kernel(
+    AdamArgs<(B8 ? 6 : 4) + MASTER, CAP> a) {
   constexpr int W = B8 ? 8 : 4;  // elements of a thread and pass
+  constexpr int NP = (B8 ? 6 : 4) + MASTER;
   const AdamwScalars& s = a.s;
   const float factor = s.factor ? *s.factor : 1.f;
   if (factor == 0.f) return;
   const int64_t t = s.step_ptr ? *s.step_ptr : s.step;
-  const double lr = s.lr_ptr ? static_cast<double>(*s.lr_ptr) : s.lr;
-  const float rate = static_cast<float>(lr / one_minus_power(s.beta1, t > 1 ? t : 1));
-  const float root = static_cast<float>(1.0 / sqrt(one_minus_power(s.beta2, t > 1 ? t : 1)));
-  const float b1 = static_cast<float>(s.beta1), c1 = static_cast<float>(1.0 - s.beta1);
-  const float b2 = static_cast<float>(s.beta2), c2 = static_cast<float>(1.0 - s.beta2);
-  const float eps = s.eps;
+  const float lr = s.lr_ptr ? *s.lr_ptr : s.lr;
+  // 1 - b^t = -expm1(t log b); the argument in binary64, as t may be large
+  const double steps = static_cast<double>(t > 1 ? t : 1);
+  const float rate = lr / -expm1f(static_cast<float>(steps * s.log_beta1));
+  const float root = 1.f / sqrtf(-expm1f(static_cast<float>(steps * s.log_beta2)));
+  const float b1 = s.beta1, c1 = s.rest1, b2 = s.beta2, c2 = s.rest2, eps = s.eps;
 
-  const int i = tensor_of(a, blockIdx.x);
-  const AdamwTensor& x = a.t[i];
-  const float keep = static_cast<float>(1.0 - lr * x.weight_decay);
-  const int64_t n = x.n;
+  const int i = tensor_of(a.first, a.count, blockIdx.x);
+  void* const* ptr = a.ptr[i];
+  P* const xp = static_cast<P*>(ptr[T_P]);
+  float* const xmaster = MASTER ? static_cast<float*>(ptr[NP - 1]) : nullptr;
+  const float keep = 1.f - lr * a.decay[i];
+  const int64_t n = a.n[i];
   int64_t j = (static_cast<int64_t>(blockIdx.x - a.first[i]) * a.passes * kThreads + threadIdx.x) * W;
   const uint32_t key0 = (s.seed + 0x9E3779B9u * static_cast<uint32_t>(a.base + i)) ^
                         static_cast<uint32_t>(t) * 0x85EBCA77u;
@@ -351,20 +364,20 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamArgs a) {
     if (j >= n && (!B8 || (j & ~int64_t(127)) >= n)) break;
     const int left = j >= n ? 0 : n - j < W ? static_cast<int>(n - j) : W;
     float g[W], p[W], m[W], v[W];
-    load<G, W>(static_cast<const G*>(x.g) + j, left, g);
+    load<G, W>(static_cast<const G*>(ptr[T_G]) + j, left, g);
     if constexpr (MASTER)
-      load<float, W>(x.master + j, left, p);
+      load<float, W>(xmaster + j, left, p);
     else
-      load<P, W>(static_cast<const P*>(x.p) + j, left, p);
+      load<P, W>(xp + j, left, p);
     if constexpr (B8) {
       const int64_t blk = j >> 7;
-      decode(load_codes(static_cast<const uint8_t*>(x.m) + j, left), x.m_scale[blk], m);
-      decode(load_codes(static_cast<const uint8_t*>(x.v) + j, left), x.v_scale[blk], v);
+      decode(load_codes(static_cast<const uint8_t*>(ptr[T_M]) + j, left), static_cast<const float*>(ptr[T_MS])[blk], m);
+      decode(load_codes(static_cast<const uint8_t*>(ptr[T_V]) + j, left), static_cast<const float*>(ptr[T_VS])[blk], v);
 #pragma unroll
       for (int e = 0; e < W; ++e) v[e] *= v[e];
     } else {
-      load<float, W>(static_cast<const float*>(x.m) + j, left, m);
-      load<float, W>(static_cast<const float*>(x.v) + j, left, v);
+      load<float, W>(static_cast<const float*>(ptr[T_M]) + j, left, m);
+      load<float, W>(static_cast<const float*>(ptr[T_V]) + j, left, v);
     }
 #pragma unroll
     for (int e = 0; e < W; ++e) {
@@ -390,43 +403,30 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(AdamArgs a) {
 #pragma unroll
       for (int e = 0; e < W; ++e) noise[e] = mix((static_cast<uint32_t>(j) ^ key) ^ e);  // j + e = j ^ e
     }
-    if constexpr (MASTER) store<float, W>(x.master + j, left, p);
+    if constexpr (MASTER) store<float, W>(xmaster + j, left, p);
     if constexpr (SR && sizeof(P) == 2 && !MASTER) {
       uint32_t add[W];
 #pragma unroll
       for (int e = 0; e < W; ++e) add[e] = (noise[e] * 0xC2B2AE3Du) >> 16;
-      store_bits<W>(static_cast<bf16_t*>(x.p) + j, left, p, add);
+      store_bits<W>(xp + j, left, p, add);
     } else {
-      store<P, W>(static_cast<P*>(x.p) + j, left, p);
+      store<P, W>(xp + j, left, p);
     }
     if constexpr (B8) {
       const int64_t blk = j >> 7;
       float sm, sv;
       const uint2 cm = encode<SR, false>(m, noise, sm), cv = encode<SR, true>(r, noise, sv);
-      store_codes(static_cast<uint8_t*>(x.m) + j, left, cm);
-      store_codes(static_cast<uint8_t*>(x.v) + j, left, cv);
+      store_codes(static_cast<uint8_t*>(ptr[T_M]) + j, left, cm);
+      store_codes(static_cast<uint8_t*>(ptr[T_V]) + j, left, cv);
       if ((j & 127) == 0) {
-        x.m_scale[blk] = sm;
-        x.v_scale[blk] = sv;
+        static_cast<float*>(ptr[T_MS])[blk] = sm;
+        static_cast<float*>(ptr[T_VS])[blk] = sv;
       }
     } else {
-      store<float, W>(static_cast<float*>(x.m) + j, left, m);
-      store<float, W>(static_cast<float*>(x.v) + j, left, v);
+      store<float, W>(static_cast<float*>(ptr[T_M]) + j, left, m);
+      store<float, W>(static_cast<float*>(ptr[T_V]) + j, left, v);
     }
   }
-}
-
-template <typename P, typename G, bool MASTER>
-void adamw_pick(bool b8, bool sr, dim3 grid, hipStream_t s, const AdamArgs& a) {
-  if (b8 && sr)
-    hipLaunchKernelGGL((adamw_kernel<P, G, MASTER, true, true>), grid, dim3(kThreads), 0, s, a);
-  else if (b8)
-    hipLaunchKernelGGL((adamw_kernel<P, G, MASTER, true, false>), grid, dim3(kThreads), 0, s, a);
-  else if (sr && sizeof(P) == 2 && !MASTER)
-    hipLaunchKernelGGL((adamw_kernel<P, G, MASTER, false, sizeof(P) == 2 && !MASTER>), grid,
-                       dim3(kThreads), 0, s, a);
-  else  // nothing to round stochastically
-    hipLaunchKernelGGL((adamw_kernel<P, G, MASTER, false, false>), grid, dim3(kThreads), 0, s, a);
 }
 
 // Elements of a chunk of the norm: large ones where there are enough of them for
@@ -436,6 +436,108 @@ int norm_chunk(int64_t total, bool bf16) {
   int c = step;
   while (c < 32 * step && total / (2 * c) >= 2048) c *= 2;
   return c;
+}
+
+// Chunks of a launch at most (a launch holds fewer than 2^32 threads).
+constexpr int64_t kMaxChunks = int64_t(1) << 23;
+
+// Deals tensors 0 .. count - 1 of n(i) elements to launches: put(k, i) enters tensor
+// i as the launch's k-th, go(k) launches k of them.
+template <int CAP, typename A, typename N, typename Put, typename Go>
+hipError_t deal(A& a, int64_t count, int64_t chunk, N n, Put put, Go go) {
+  int k = 0;
+  a.first[0] = 0;
+  for (int64_t i = 0; i < count; ++i) {
+    const int64_t blocks = (n(i) + chunk - 1) / chunk;
+    if (k == CAP || (k && a.first[k] + blocks > kMaxChunks)) {
+      const hipError_t e = go(k);
+      if (e != hipSuccess) return e;
+      k = 0;
+    }
+    put(k, i);
+    a.first[k + 1] = static_cast<int32_t>(a.first[k] + blocks);
+    ++k;
+  }
+  return k ? go(k) : hipSuccess;
+}
+
+template <typename T, int CAP>
+hipError_t norm_parts(const void* const* g, const int64_t* n, int64_t count, int chunk, double* part,
+                      int64_t* parts, hipStream_t s) {
+  NormArgs<CAP> a;
+  a.chunk = chunk;
+  *parts = 0;
+  return deal<CAP>(
+      a, count, chunk, [&](int64_t i) { return n[i]; },
+      [&](int k, int64_t i) {
+        a.g[k] = g[i];
+        a.n[k] = n[i];
+      },
+      [&](int k) {
+        if (a.first[k] == 0) return hipSuccess;
+        a.count = k;
+        a.part = part + *parts;
+        *parts += a.first[k];
+        hipLaunchKernelGGL((sqsum_kernel<T, CAP>), dim3(a.first[k]), dim3(kThreads), 0, s, a);
+        return hipGetLastError();
+      });
+}
+
+template <typename P, typename G, bool MASTER, bool B8, bool SR, int CAP>
+hipError_t adamw_deal(const AdamwTensor* t, int64_t count, const AdamwScalars& scalars, hipStream_t s) {
+  constexpr int NP = (B8 ? 6 : 4) + MASTER, W = B8 ? 8 : 4;
+  AdamArgs<NP, CAP> a;
+  a.s = scalars;
+  int64_t total = 0, most = 0;
+  for (int64_t i = 0; i < count; ++i) {
+    total += t[i].n;
+    most = t[i].n > most ? t[i].n : most;
+  }
+  // two rounds a workgroup where that leaves enough of them (100.7 M weights, fp32
+  // states: 518 us; one 520, eight 543), more where a tensor has too many
+  int64_t passes = total / (2 * kThreads * W) >= 4096 ? 2 : 1;
+  while (most / (passes * kThreads * W) >= kMaxChunks) passes *= 2;
+  a.passes = static_cast<int32_t>(passes);
+  return deal<CAP>(
+      a, count, passes * kThreads * W, [&](int64_t i) { return t[i].n; },
+      [&](int k, int64_t i) {
+        if (k == 0) a.base = static_cast<int32_t>(i);
+        void** ptr = a.ptr[k];
+        ptr[T_P] = t[i].p;
+        ptr[T_G] = const_cast<void*>(t[i].g);
+        ptr[T_M] = t[i].m;
+        ptr[T_V] = t[i].v;
+        if constexpr (B8) {
+          ptr[T_MS] = t[i].m_scale;
+          ptr[T_VS] = t[i].v_scale;
+        }
+        if constexpr (MASTER) ptr[NP - 1] = t[i].master;
+        a.n[k] = t[i].n;
+        a.decay[k] = static_cast<float>(t[i].weight_decay);
+      },
+      [&](int k) {
+        if (a.first[k] == 0) return hipSuccess;
+        a.count = k;
+        hipLaunchKernelGGL((adamw_kernel<P, G, MASTER, B8, SR, CAP>), dim3(a.first[k]), dim3(kThreads),
+                           0, s, a);
+        return hipGetLastError();
+      });
+}
+template <typename P, typename G, bool MASTER, bool B8, bool SR>
+hipError_t adamw_list(const AdamwTensor* t, int64_t count, const AdamwScalars& c, hipStream_t s) {
+  if (count <= kFew) return adamw_deal<P, G, MASTER, B8, SR, kFew>(t, count, c, s);
+  return adamw_deal<P, G, MASTER, B8, SR, kAdamTensors<(B8 ? 6 : 4) + MASTER>>(t, count, c, s);
+}
+template <typename P, typename G, bool MASTER>
+hipError_t adamw_kind(bool b8, bool sr, const AdamwTensor* t, int64_t count, const AdamwScalars& c,
+                      hipStream_t s) {
+  if (b8)
+    return sr ? adamw_list<P, G, MASTER, true, true>(t, count, c, s)
+              : adamw_list<P, G, MASTER, true, false>(t, count, c, s);
+  if constexpr (sizeof(P) == 2 && !MASTER) {
+    if (sr) return adamw_list<P, G, MASTER, false, true>(t, count, c, s);
+  }  // (else there is nothing to round stochastically)
+  return adamw_list<P, G, MASTER, false, false>(t, count, c, s);
 }
 
 }  // namespace
@@ -451,88 +553,28 @@ int64_t grad_norm_parts(const int64_t* n, int64_t count, bool bf16) {
 hipError_t launch_grad_norm(const void* const* g, const int64_t* n, int64_t count, bool bf16,
                             double max_norm, double* part, float* out, int64_t* step,
                             hipStream_t s) {
-  int64_t total = 0;
+  int64_t total = 0, parts = 0;
   for (int64_t i = 0; i < count; ++i) total += n[i];
   const int chunk = norm_chunk(total, bf16);
-  NormArgs a;
-  int64_t parts = 0;
-  a.count = 0;
-  a.first[0] = 0;
-  auto flush = [&]() -> hipError_t {
-    const int blocks = a.first[a.count];
-    if (blocks) {
-      a.part = part + parts;
-      if (bf16)
-        hipLaunchKernelGGL(sqsum_kernel<bf16_t>, dim3(blocks), dim3(kThreads), 0, s, a, chunk);
-      else
-        hipLaunchKernelGGL(sqsum_kernel<float>, dim3(blocks), dim3(kThreads), 0, s, a, chunk);
-    }
-    parts += blocks;
-    a.count = 0;
-    return hipGetLastError();
-  };
-  for (int64_t i = 0; i < count; ++i) {
-    if (n[i] == 0) continue;
-    const int64_t blocks = (n[i] + chunk - 1) / chunk;
-    if (a.count == kNormTensors || (a.count && a.first[a.count] + blocks >= (int64_t(1) << 24))) {
-      const hipError_t e = flush();
-      if (e != hipSuccess) return e;
-    }
-    a.g[a.count] = g[i];
-    a.n[a.count] = n[i];
-    a.first[a.count + 1] = static_cast<int32_t>(a.first[a.count] + blocks);
-    ++a.count;
-  }
-  const hipError_t e = flush();
+  hipError_t e;
+  if (count <= kFew)
+    e = bf16 ? norm_parts<bf16_t, kFew>(g, n, count, chunk, part, &parts, s)
+             : norm_parts<float, kFew>(g, n, count, chunk, part, &parts, s);
+  else
+    e = bf16 ? norm_parts<bf16_t, kNormTensors>(g, n, count, chunk, part, &parts, s)
+             : norm_parts<float, kNormTensors>(g, n, count, chunk, part, &parts, s);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(norm_finish_kernel, dim3(1), dim3(1024), 0, s, part, parts, max_norm, out, step);
   return hipGetLastError();
 }
 
 hipError_t launch_adamw(const AdamwTensor* t, int64_t count, bool bf16, bool g_bf16, bool master,
-                        bool b8, bool sr, const AdamwScalars& scalars, hipStream_t s) {
-  const int W = b8 ? 8 : 4;
-  int64_t total = 0;
-  for (int64_t i = 0; i < count; ++i) total += t[i].n;
-  AdamArgs a;
-  a.s = scalars;
-  a.passes = 1;
-  while (a.passes < 2 && total / (int64_t(2) * a.passes * kThreads * W) >= 4096) a.passes *= 2;
-  const int64_t chunk = int64_t(a.passes) * kThreads * W;
-  a.count = 0;
-  a.first[0] = 0;
-  auto flush = [&]() -> hipError_t {
-    const dim3 grid(a.first[a.count]);
-    if (a.count) {
-      if (!bf16)
-        adamw_pick<float, float, false>(b8, sr, grid, s, a);
-      else if (g_bf16 && master)
-        adamw_pick<bf16_t, bf16_t, true>(b8, sr, grid, s, a);
-      else if (g_bf16)
-        adamw_pick<bf16_t, bf16_t, false>(b8, sr, grid, s, a);
-      else if (master)
-        adamw_pick<bf16_t, float, true>(b8, sr, grid, s, a);
-      else
-        adamw_pick<bf16_t, float, false>(b8, sr, grid, s, a);
-    }
-    a.count = 0;
-    return hipGetLastError();
-  };
-  for (int64_t i = 0; i < count; ++i) {
-    if (t[i].n == 0) continue;
-    const int64_t blocks = (t[i].n + chunk - 1) / chunk;
-    // (a launch holds consecutive tensors, so that base + index is a tensor's number)
-    if (a.count && (a.count == kAdamTensors || a.base + a.count != i ||
-                    a.first[a.count] + blocks >= (int64_t(1) << 24))) {
-      const hipError_t e = flush();
-      if (e != hipSuccess) return e;
-    }
-    if (a.count == 0) a.base = static_cast<int32_t>(i);
-    a.t[a.count] = t[i];
-    a.first[a.count + 1] = static_cast<int32_t>(a.first[a.count] + blocks);
-    ++a.count;
-  }
-  return flush();
+                        bool b8, bool sr, const AdamwScalars& c, hipStream_t s) {
+  if (!bf16) return adamw_kind<float, float, false>(b8, sr, t, count, c, s);
+  if (g_bf16 && master) return adamw_kind<bf16_t, bf16_t, true>(b8, sr, t, count, c, s);
+  if (g_bf16) return adamw_kind<bf16_t, bf16_t, false>(b8, sr, t, count, c, s);
+  if (master) return adamw_kind<bf16_t, float, true>(b8, sr, t, count, c, s);
+  return adamw_kind<bf16_t, float, false>(b8, sr, t, count, c, s);
 }
 
 }  // namespace zc

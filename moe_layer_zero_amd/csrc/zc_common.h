@@ -479,11 +479,11 @@ struct AdamwTensor {
   double weight_decay;
 };
 struct AdamwScalars {
-  double lr, beta1, beta2;
+  double log_beta1, log_beta2;
   int64_t step;
   const float *factor, *lr_ptr;  // device, nullable
   const int64_t* step_ptr;       // device, nullable
-  float eps;
+  float lr, beta1, rest1, beta2, rest2, eps;  // rest: 1 - beta
   uint32_t seed;
 };
 hipError_t launch_adamw(const AdamwTensor* t, int64_t count, bool bf16, bool g_bf16, bool master,

@@ -5,9 +5,10 @@ formula once, constants among them (b1, 1 - b1, ... are rounded to fp32):
   g' = factor g: u;  m = b1 m0 + c1 g': at most 5 u (|b1 m0| + |c1 g'|);
   v = b2 v0 + c2 g'^2, all terms positive: at most 7 u v;
   8-bit states are decoded with one rounding (m0) or three (v0): 6 u and 10 u;
-  the step s = rate m / (sqrt(v) root + eps): m's error, half of v's, and ten u:
-  sqrt, root, eps, rate and their products and sum one each (7), the hardware's
-  reciprocal (1 ulp) two, and the product with it one;
+  the step s = rate m / (sqrt(v) root + eps): m's error, half of v's, and 17 u: 1 -
+  b^t to 3 u (its argument, and 1 ulp of expm1), so rate to 5 (lr, quotient) and root to
+  3.5 (half of 3, sqrt, quotient); sqrt, eps, the two products and the sum one each (5);
+  the hardware's reciprocal (1 ulp) two, and the product with it one;
   p = p keep - s: two for the product, one for the difference.
 Weights in bf16 add half a step of theirs, 2^-8 |p| (a whole one where they are
 rounded stochastically); 8-bit codes half a step or a whole one likewise.
@@ -39,7 +40,7 @@ def norm_of(tensors, max_norm=1.0, step=None):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
-@pytest.mark.parametrize("sizes", [[1], [5], [0, 3, 0], SIZES, [8191, 8192, 8193], [3] * 300 + [40000] * 3,
+@pytest.mark.parametrize("sizes", [[1], [5], [0, 3, 0], SIZES, [8191, 8192, 8193], [3] * 500 + [40000] * 3,
                                    [3_000_001]])
 def test_norm(dtype, sizes):
     g = gen(len(sizes) + sizes[-1])
@@ -212,7 +213,7 @@ class Case:
             rate = lr / (1 - cfg.beta1 ** t)
             step = rate * m / den
             p = p0 * (1 - lr * self.decay[i]) - step
-            tp = 3 * U * np.abs(p0) + rate / den * tm + np.abs(step) * (rv / 2 + 10 * U) + U * np.abs(p)
+            tp = 3 * U * np.abs(p0) + rate / den * tm + np.abs(step) * (rv / 2 + 17 * U) + U * np.abs(p)
             if "master" in L:
                 got = self.get("master", i)
                 assert (np.abs(got - p) <= tp).all()
@@ -265,7 +266,7 @@ def test_adamw_settings(bits, t, kw):
 
 
 @pytest.mark.parametrize("bits", [32, 8])
-@pytest.mark.parametrize("count", [46, 47, 150])
+@pytest.mark.parametrize("count", [8, 9, 63, 84, 150])
 def test_adamw_many_tensors(bits, count):
     # more than one launch's list, with empty tensors in it: a tensor's place in the
     # list counts for its random bits
@@ -311,8 +312,8 @@ def test_adamw_from_zeros(bits):
     t = zcmoe.adamw_tensors(p, g, bits=bits)
     zcmoe.zc_adamw_step(zcmoe.AdamW(lr=0.5, eps=1e-16), t, 1)
     for q, h in zip(p, g):
-        # m / sqrt(v) = +-1 up to the roundings counted above: 5 + 7 / 2 + 10, and 1 for p
-        assert bool(((q + 0.5 * torch.sign(h)).abs() <= 0.5 * 20 * U).all())
+        # m / sqrt(v) = +-1 up to the roundings counted above: 5 + 7 / 2 + 17, and 1 for p
+        assert bool(((q + 0.5 * torch.sign(h)).abs() <= 0.5 * 27 * U).all())
     if bits == 8:
         assert all(bool((v.float() > 0).all()) for v in t.v)
 
