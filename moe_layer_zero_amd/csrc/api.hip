@@ -309,13 +309,11 @@ Saved carve_saved(char* p, const zc_moe_desc* d) {
 // down GEMM) and y when no saved buffer takes it.
 // MXFP8 and MXFP4 layers add x' (codes and scales); h' (codes and scales)
 // fits in the h piece.  Layers that list their own row tiles add the list.
-// Row-tile height of an MXFP4 layer (picks spread over all N + Z experts).
-int mxfp4_rows_per_tile(const zc_moe_desc* d) {
-  const int64_t rows = d->T * d->K;
-  return zc::mx4_rows_per_tile(rows / (d->N + d->Z), d->T, rows, d->d, d->I);
+zc::Mx4Plan mxfp4_plan(const zc_moe_desc* d) {
+  return zc::mx4_plan(d->T, d->T * d->K, d->N + d->Z, d->d, d->I);
 }
 bool fp32_y(const zc_moe_desc* d) {
-  return int4_group(d) || (mxfp4(d) && mxfp4_rows_per_tile(d) != zc::kMx4WideRows);
+  return int4_group(d) || (mxfp4(d) && !mxfp4_plan(d).wide);
 }
 int64_t xq_bytes(const zc_moe_desc* d) { return a256(mxfp4_a4(d) ? d->T * d->d / 2 : d->T * d->d); }
 int64_t fwd_ws_bytes(const zc_moe_desc* d) {
@@ -591,23 +589,23 @@ zc_status do_experts(const zc_moe_desc* d, const T* x, const T* wg, const T* wu,
       uint8_t* xq = xs - xq_bytes(d);
       uint8_t* hq = reinterpret_cast<uint8_t*>(h);
       uint8_t* hs = hq + a256(a4 ? rows * d->I / 2 : rows * d->I);
-      const int tm = mxfp4_rows_per_tile(d);
-      ZC_LAUNCH(ZC_PH_TILE_OFFSETS, zc::launch_row_tiles(r->offsets, N, tm, tiles, s),
-                "tile list launch");
-      if (!mxq)
+      const zc::Mx4Plan plan = mxfp4_plan(d);
+      if (mxq)
+        ZC_LAUNCH(ZC_PH_TILE_OFFSETS, zc::launch_row_tiles(r->offsets, N, plan.tm, tiles, s),
+                  "tile list launch");
+      else
         ZC_LAUNCH(ZC_PH_QUANTIZE,
-                  a4 ? zc::launch_mx4_rows<bf16_t>(reinterpret_cast<const bf16_t*>(x), d->T, dd, xq,
-                                                   xs, nullptr, s)
-                     : zc::launch_mxq_rows(reinterpret_cast<const bf16_t*>(x), d->T, dd, xq, xs, s),
-                  "activation quantization launch");
+                  zc::launch_mx4_start(a4, r->offsets, N, plan.tm, tiles,
+                                       reinterpret_cast<const bf16_t*>(x), d->T, dd, xq, xs, s),
+                  "tile list and activation quantization launch");
       ZC_LAUNCH(ZC_PH_GATE_UP,
                 zc::launch_mx4_gateup(a4, mxq ? mxq : xq, mxq ? mxs : xs, d->T,
                                       reinterpret_cast<const uint8_t*>(wg),
-                                      reinterpret_cast<const uint8_t*>(wu), tiles, r->perm, tm, rows,
+                                      reinterpret_cast<const uint8_t*>(wu), tiles, r->perm, plan, rows,
                                       N, I, dd, K, hq, hs, s),
                 "gate/up GEMM launch");
       ZC_LAUNCH(ZC_PH_DOWN,
-                zc::launch_mx4_down(a4, hq, hs, reinterpret_cast<const uint8_t*>(wd), tiles, tm, rows,
+                zc::launch_mx4_down(a4, hq, hs, reinterpret_cast<const uint8_t*>(wd), tiles, plan, rows,
                                     N, I, dd, y, s),
                 "down GEMM launch");
     } else if (d->weight_layout == ZC_WEIGHTS_PACKED) {

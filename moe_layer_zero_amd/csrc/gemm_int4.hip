@@ -619,29 +619,10 @@ __global__ __launch_bounds__(256) void int4_quantize_kernel(const bf16_t* __rest
   }
 }
 
-// The records of the row tiles of height tm, in expert order, and their number.
-// One workgroup: inclusive scan of the experts' tile counts by wavefront, then
-// over the 16 wavefronts' sums.
 __global__ __launch_bounds__(kMaxExperts) void row_tiles_kernel(
     const int32_t* __restrict__ offsets, int N, int tm, int32_t* __restrict__ total,
     RowTile* __restrict__ tiles) {
-  __shared__ int32_t s_sum[kMaxExperts / 64];
-  const int e = threadIdx.x, lane = e & 63, wave = e >> 6;
-  const int lo = e < N ? offsets[e] : 0, hi = e < N ? offsets[e + 1] : 0;
-  const int n = (hi - lo + tm - 1) / tm;
-  int scan = n;
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const int v = __shfl_up(scan, o);
-    if (lane >= o) scan += v;
-  }
-  if (lane == 63) s_sum[wave] = scan;
-  __syncthreads();
-  int first = scan - n;
-  for (int w = 0; w < wave; ++w) first += s_sum[w];
-  if (e == kMaxExperts - 1) *total = first + n;
-  RowTile t{e, first, n, lo, hi, {0, 0, 0}};
-  for (int i = 0; i < n; ++i) tiles[first + i] = t;
+  list_row_tiles(offsets, N, tm, total, tiles);
 }
 
 // At most this many column tiles of OUT columns by row tiles of height tm; the

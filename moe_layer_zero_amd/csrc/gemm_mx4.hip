@@ -325,7 +325,7 @@ __device__ __forceinline__ void lds_barrier() {
 
 template <int EPI, bool A4>
 __global__ __launch_bounds__(kThreads, 2) void mx4_wide_kernel(Mx4Params p) {
-  constexpr int TM = kMx4WideRows;
+  constexpr int TM = 128;                      // rows of a tile at most
   constexpr int CB = A4 ? kStep / 2 : kStep;   // bytes of a row's slab of 128 steps
   constexpr int SLOT = TM * CB;                // bytes of a ring slot
   constexpr int CP = SLOT / 1024 / kWaves;     // copies a wavefront and slab
@@ -563,9 +563,9 @@ __global__ __launch_bounds__(kThreads, 2) void mx4_wide_kernel(Mx4Params p) {
 }
 
 template <int EPI>
-hipError_t launch_mx4_wide(bool a4, Mx4Params p, int64_t rows, hipStream_t s) {
+hipError_t launch_mx4_wide(bool a4, Mx4Params p, int64_t rows, int tm, hipStream_t s) {
   const int OUT = EPI == MX_SWIGLU ? 128 : 256;
-  deal_tiles(max_row_tiles(rows, p.N, kMx4WideRows) * (p.ncols / OUT), &p.per_xcd, &p.log_run);
+  deal_tiles(max_row_tiles(rows, p.N, tm) * (p.ncols / OUT), &p.per_xcd, &p.log_run);
   const dim3 grid(grid_of(p.per_xcd * 8)), block(kThreads);
   if (a4)
     hipLaunchKernelGGL((mx4_wide_kernel<EPI, true>), grid, block, 0, s, p);
@@ -606,8 +606,25 @@ __global__ __launch_bounds__(256) void mx4_pack_kernel(const u32x4_t* __restrict
   }
 }
 
+// MXFP4 of one thread's 8 values of a block of 32 held by 4 consecutive lanes: the
+// codes, and the block's scale S.
+__device__ __forceinline__ uint32_t mx4_quad(const float* f, int& S) {
+  uint32_t amax = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) amax = max(amax, __float_as_uint(f[e]) & 0x7fffffffu);
+  amax = max(amax, static_cast<uint32_t>(__shfl_xor(static_cast<int>(amax), 1)));
+  amax = max(amax, static_cast<uint32_t>(__shfl_xor(static_cast<int>(amax), 2)));
+  S = mx4_scale(amax);
+  const float scale = e8m0_f32(S);
+  uint32_t w = mx4_codes<0>(0u, f[0], f[1], scale);
+  w = mx4_codes<1>(w, f[2], f[3], scale);
+  w = mx4_codes<2>(w, f[4], f[5], scale);
+  w = mx4_codes<3>(w, f[6], f[7], scale);
+  return S == 255 ? 0u : w;
+}
+
 // Rows -> natural codes and scales, and the values they stand for.  Eight values a
-// thread, four lanes a block.
+// thread.
 template <typename T>
 __global__ __launch_bounds__(256) void mx4_rows_kernel(const T* src, int64_t pieces,
                                                        uint32_t* __restrict__ codes,
@@ -619,22 +636,12 @@ __global__ __launch_bounds__(256) void mx4_rows_kernel(const T* src, int64_t pie
 #pragma unroll
     for (int j = 0; j < 8 / V16<T>::n; ++j)
       V16<T>::load(src + i * 8 + j * V16<T>::n, f + j * V16<T>::n);
-    uint32_t amax = 0;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) amax = max(amax, __float_as_uint(f[e]) & 0x7fffffffu);
-    amax = max(amax, static_cast<uint32_t>(__shfl_xor(static_cast<int>(amax), 1)));
-    amax = max(amax, static_cast<uint32_t>(__shfl_xor(static_cast<int>(amax), 2)));
-    const int S = mx4_scale(amax);
-    const float scale = e8m0_f32(S);
-    uint32_t w = mx4_codes<0>(0u, f[0], f[1], scale);
-    w = mx4_codes<1>(w, f[2], f[3], scale);
-    w = mx4_codes<2>(w, f[4], f[5], scale);
-    w = mx4_codes<3>(w, f[6], f[7], scale);
-    if (S == 255) w = 0u;
+    int S;
+    const uint32_t w = mx4_quad(f, S);
     codes[i] = w;
     if ((i & 3) == 0) scales[i >> 2] = static_cast<uint8_t>(S);
     if (values) {
-      const float sv = S == 255 ? __uint_as_float(0x7fc00000u) : scale;
+      const float sv = S == 255 ? __uint_as_float(0x7fc00000u) : e8m0_f32(S);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         // E2M1 as a multiple of 1/2: 0 1 2 3 4 6 8 12, a nibble each
@@ -649,19 +656,65 @@ __global__ __launch_bounds__(256) void mx4_rows_kernel(const T* src, int64_t pie
   }
 }
 
+// The first workgroup lists the row tiles, the others quantize x: both have to be
+// there before the products, and neither needs the other (one launch less: 2 us of
+// a call on one token).
+template <bool A4>
+__global__ __launch_bounds__(kMaxExperts) void mx4_start_kernel(
+    const int32_t* __restrict__ offsets, int N, int tm, int32_t* __restrict__ total,
+    RowTile* __restrict__ tiles, const bf16_t* __restrict__ x, int64_t pieces,
+    uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
+  if (blockIdx.x == 0) {
+    list_row_tiles(offsets, N, tm, total, tiles);
+    return;
+  }
+  for (int64_t i = static_cast<int64_t>(blockIdx.x - 1) * kMaxExperts + threadIdx.x; i < pieces;
+       i += static_cast<int64_t>(gridDim.x - 1) * kMaxExperts) {
+    float f[8];
+    V16<bf16_t>::load(x + i * 8, f);
+    int S;
+    if constexpr (A4) {
+      reinterpret_cast<uint32_t*>(codes)[i] = mx4_quad(f, S);
+      if ((i & 3) == 0) scales[i >> 2] = static_cast<uint8_t>(S);
+    } else {
+      reinterpret_cast<uint64_t*>(codes)[i] = mx_quad(f, S);
+      const int64_t b = i >> 2;  // (rows are whole slabs of 4 blocks: the order 0, 2, 1, 3)
+      if ((i & 3) == 0) scales[(b & ~int64_t(3)) + 2 * (b & 1) + ((b >> 1) & 1)] = static_cast<uint8_t>(S);
+    }
+  }
+}
+
 }  // namespace
 
-int mx4_rows_per_tile(int64_t avg_rows, int64_t Tn, int64_t rows, int64_t d, int64_t I) {
-  if (avg_rows <= 13) return 16;
-  if (avg_rows <= 20) return 32;
-  // (the 128-row kernel takes whole groups of 512 steps, and byte offsets of 31 bits
-  // into x, h and a matrix)
+Mx4Plan mx4_plan(int64_t Tn, int64_t rows, int64_t E, int64_t d, int64_t I) {
+  const int64_t avg = rows / E;
+  if (avg <= 13) return {16, false};
+  if (avg <= 20) return {32, false};
+  // (the kernel of many rows takes whole groups of 512 steps, and byte offsets of 31
+  // bits into x, h and a matrix)
   const int64_t limit = int64_t(1) << 31;
-  return d % 512 || I % 512 || Tn * d >= limit || rows * I >= limit || d * I >= limit ? 64 : kMx4WideRows;
+  if (d % 512 || I % 512 || Tn * d >= limit || rows * I >= limit || d * I >= limit) return {64, false};
+  return {128, true};
+}
+
+hipError_t launch_mx4_start(bool a4, const int32_t* offsets, int N, int tm, void* tiles,
+                            const bf16_t* x, int64_t Tn, int d, uint8_t* xq, uint8_t* xs,
+                            hipStream_t s) {
+  const int64_t pieces = Tn * (d / 8);
+  const dim3 grid(1 + grid_of((pieces + kMaxExperts - 1) / kMaxExperts)), block(kMaxExperts);
+  int32_t* total = static_cast<int32_t*>(tiles);
+  RowTile* list = static_cast<RowTile*>(tiles) + 1;
+  if (a4)
+    hipLaunchKernelGGL(mx4_start_kernel<true>, grid, block, 0, s, offsets, N, tm, total, list, x,
+                       pieces, xq, xs);
+  else
+    hipLaunchKernelGGL(mx4_start_kernel<false>, grid, block, 0, s, offsets, N, tm, total, list, x,
+                       pieces, xq, xs);
+  return hipGetLastError();
 }
 
 hipError_t launch_mx4_gateup(bool a4, const uint8_t* xq, const uint8_t* xs, int64_t Tn, const uint8_t* wg,
-                             const uint8_t* wu, const void* tiles, const int32_t* perm, int tm,
+                             const uint8_t* wu, const void* tiles, const int32_t* perm, Mx4Plan plan,
                              int64_t rows, int N, int I, int d, int K, uint8_t* hq, uint8_t* hs,
                              hipStream_t s) {
   Mx4Params p{};
@@ -670,33 +723,33 @@ hipError_t launch_mx4_gateup(bool a4, const uint8_t* xq, const uint8_t* xs, int6
   p.tiles = static_cast<const RowTile*>(tiles) + 1;
   p.A = xq; p.As = xs; p.perm = perm; p.kdiv = K;
   p.B = wg; p.B2 = wu; p.hq = hq; p.hs = hs;
-  if (tm == kMx4WideRows) {
+  if (plan.wide) {
     p.a_bytes = static_cast<uint32_t>(a4 ? Tn * d / 2 : Tn * d);
     p.as_bytes = static_cast<uint32_t>(Tn * (d / 32));
-    return launch_mx4_wide<MX_SWIGLU>(a4, p, rows, s);
+    return launch_mx4_wide<MX_SWIGLU>(a4, p, rows, plan.tm, s);
   }
-  if (tm == 16) return launch_mx4<MX_SWIGLU, 1, 4>(a4, p, rows, s);
-  if (tm == 32) return launch_mx4<MX_SWIGLU, 2, 4>(a4, p, rows, s);
+  if (plan.tm == 16) return launch_mx4<MX_SWIGLU, 1, 4>(a4, p, rows, s);
+  if (plan.tm == 32) return launch_mx4<MX_SWIGLU, 2, 4>(a4, p, rows, s);
   return launch_mx4<MX_SWIGLU, 4, 4>(a4, p, rows, s);
 }
 
 hipError_t launch_mx4_down(bool a4, const uint8_t* hq, const uint8_t* hs, const uint8_t* wd,
-                           const void* tiles, int tm, int64_t rows, int N, int I, int d, void* y,
+                           const void* tiles, Mx4Plan plan, int64_t rows, int N, int I, int d, void* y,
                            hipStream_t s) {
   Mx4Params p{};
   p.N = N; p.ncols = d; p.K = I;
   p.total = static_cast<const int32_t*>(tiles);
   p.tiles = static_cast<const RowTile*>(tiles) + 1;
   p.A = hq; p.As = hs; p.kdiv = 1; p.B = wd;
-  if (tm == kMx4WideRows) {
+  if (plan.wide) {
     p.yb = static_cast<bf16_t*>(y);
     p.a_bytes = static_cast<uint32_t>(a4 ? rows * I / 2 : rows * I);
     p.as_bytes = static_cast<uint32_t>(rows * (I / 32));
-    return launch_mx4_wide<MX_STORE>(a4, p, rows, s);
+    return launch_mx4_wide<MX_STORE>(a4, p, rows, plan.tm, s);
   }
   p.y = static_cast<float*>(y);
-  if (tm == 16) return launch_mx4<MX_STORE, 1, 4>(a4, p, rows, s);
-  if (tm == 32) return launch_mx4<MX_STORE, 2, 4>(a4, p, rows, s);
+  if (plan.tm == 16) return launch_mx4<MX_STORE, 1, 4>(a4, p, rows, s);
+  if (plan.tm == 32) return launch_mx4<MX_STORE, 2, 4>(a4, p, rows, s);
   return launch_mx4<MX_STORE, 4, 4>(a4, p, rows, s);
 }
 

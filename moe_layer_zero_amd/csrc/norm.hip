@@ -55,23 +55,6 @@ __device__ __forceinline__ double rsqrt_f64(double m) {
   return y * (1.5 - 0.5 * m * y * y);
 }
 
-// MXFP8 of one thread's 8 values of a block of 32 held by 4 consecutive
-// lanes.
-__device__ __forceinline__ uint64_t mx_quad(const float* f, int& S) {
-  float amax = 0.f;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(f[e]));
-  amax = fmaxf(amax, __shfl_xor(amax, 1));
-  amax = fmaxf(amax, __shfl_xor(amax, 2));
-  S = mx_scale(amax);
-  uint64_t q = 0;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    q |= static_cast<uint64_t>(mx_code(f[e], S)) << (8 * e);
-  }
-  return q;
-}
-
 template <typename T, int NV, int TPR, bool MX>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_fwd_kernel(
     const T* x, const T* res, const T* __restrict__ gamma, T* r, T* y, float* __restrict__ rstd,

@@ -114,6 +114,23 @@ __device__ __forceinline__ uint32_t mx_code(float v, int S) {
   return v != v ? 0x7fu : c;
 }
 
+// MXFP8 of one thread's 8 values of a block of 32 held by 4 consecutive
+// lanes.
+__device__ __forceinline__ uint64_t mx_quad(const float* f, int& S) {
+  float amax = 0.f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(f[e]));
+  amax = fmaxf(amax, __shfl_xor(amax, 1));
+  amax = fmaxf(amax, __shfl_xor(amax, 2));
+  S = mx_scale(amax);
+  uint64_t q = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    q |= static_cast<uint64_t>(mx_code(f[e], S)) << (8 * e);
+  }
+  return q;
+}
+
 // Row-tile height of the grouped GEMMs; the dispatch step publishes the
 // per-expert prefix of ceil(rows / kGemmBM) tiles for them.
 constexpr int kGemmBM = 128;
@@ -134,6 +151,31 @@ __device__ __forceinline__ RowTile ld_tile(const RowTile* t) {
   typedef int32_t i32x8_t __attribute__((ext_vector_type(8)));
   const i32x8_t v = *(const __attribute__((address_space(4))) i32x8_t*)t;
   return RowTile{v[0], v[1], v[2], v[3], v[4], {0, 0, 0}};
+}
+
+// The records of the row tiles of height tm, in expert order, and their number, by
+// one workgroup of kMaxExperts threads: inclusive scan of the experts' tile counts by
+// wavefront, then over the 16 wavefronts' sums.
+__device__ __forceinline__ void list_row_tiles(const int32_t* __restrict__ offsets, int N, int tm,
+                                               int32_t* __restrict__ total,
+                                               RowTile* __restrict__ tiles) {
+  __shared__ int32_t s_sum[kMaxExperts / 64];
+  const int e = threadIdx.x, lane = e & 63, wave = e >> 6;
+  const int lo = e < N ? offsets[e] : 0, hi = e < N ? offsets[e + 1] : 0;
+  const int n = (hi - lo + tm - 1) / tm;
+  int scan = n;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int v = __shfl_up(scan, o);
+    if (lane >= o) scan += v;
+  }
+  if (lane == 63) s_sum[wave] = scan;
+  __syncthreads();
+  int first = scan - n;
+  for (int w = 0; w < wave; ++w) first += s_sum[w];
+  if (e == kMaxExperts - 1) *total = first + n;
+  const RowTile t{e, first, n, lo, hi, {0, 0, 0}};
+  for (int i = 0; i < n; ++i) tiles[first + i] = t;
 }
 
 // Tile number of the in-th tile of XCD x: runs of 2^log_run consecutive tiles
@@ -386,16 +428,23 @@ hipError_t launch_int4_quantize(const bf16_t* src, uint8_t* codes, bf16_t* scale
 // Expert GEMMs on MXFP4 weights (gemm_mx4.hip): E2M1 codes with one E8M0 scale per
 // 32 reduction steps; rows of x and h in MXFP8 (a4 = false: codes and slab-ordered
 // scales, as launch_mxq_rows leaves them) or MXFP4 (a4 = true: natural order, as
-// launch_mx4_rows leaves them).  d and I multiples of 128.  tiles: row tiles of tm
-// = mx4_rows_per_tile(...) rows.  y is fp32 [P][d], bf16 where tm is kMx4WideRows.
-constexpr int kMx4WideRows = 128;
-int mx4_rows_per_tile(int64_t avg_rows, int64_t Tn, int64_t rows, int64_t d, int64_t I);
+// launch_mx4_rows leaves them).  d and I multiples of 128.  tiles: row tiles of
+// plan.tm rows.  y is fp32 [P][d], bf16 where plan.wide (many rows).
+struct Mx4Plan {
+  int tm;     // rows of a tile
+  bool wide;  // the kernel of many rows
+};
+Mx4Plan mx4_plan(int64_t Tn, int64_t rows, int64_t E, int64_t d, int64_t I);
+// The row tiles, and x [T][d] as MXFP4 or MXFP8 rows, in one launch.
+hipError_t launch_mx4_start(bool a4, const int32_t* offsets, int N, int tm, void* tiles,
+                            const bf16_t* x, int64_t Tn, int d, uint8_t* xq, uint8_t* xs,
+                            hipStream_t s);
 hipError_t launch_mx4_gateup(bool a4, const uint8_t* xq, const uint8_t* xs, int64_t Tn, const uint8_t* wg,
-                             const uint8_t* wu, const void* tiles, const int32_t* perm, int tm,
+                             const uint8_t* wu, const void* tiles, const int32_t* perm, Mx4Plan plan,
                              int64_t rows, int N, int I, int d, int K, uint8_t* hq, uint8_t* hs,
                              hipStream_t s);
 hipError_t launch_mx4_down(bool a4, const uint8_t* hq, const uint8_t* hs, const uint8_t* wd,
-                           const void* tiles, int tm, int64_t rows, int N, int I, int d, void* y,
+                           const void* tiles, Mx4Plan plan, int64_t rows, int N, int I, int d, void* y,
                            hipStream_t s);
 // Bytes of nmat [R][C] matrices in the kernels' order, and the packer from natural
 // codes [R][C/2] and scales [R][C/32] of w_down (down) or of w_gate and w_up.
