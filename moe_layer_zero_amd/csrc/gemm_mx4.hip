@@ -93,27 +93,54 @@ __device__ __forceinline__ uint32_t mx4_codes(uint32_t old, float a, float b, fl
   return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(old, a, b, scale, BYTE);
 }
 
-// Largest of the 16 lanes of a row, in every lane.
-__device__ __forceinline__ uint32_t row_max(uint32_t v) {
-  v = max(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, v, 0x128, 0xf, 0xf, true)));
-  v = max(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, v, 0x124, 0xf, 0xf, true)));
-  v = max(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, v, 0x122, 0xf, 0xf, true)));
-  return max(v, static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, v, 0x121, 0xf, 0xf, true)));
+// Largest of the 16 lanes of a row, in every lane, of R values.
+template <int R>
+__device__ __forceinline__ void row_max(uint32_t (&v)[R]) {
+#define ZC_ROR_MAX(N)                                                                   \
+  _Pragma("unroll") for (int r = 0; r < R; ++r) v[r] = max(                             \
+      v[r], static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(v[r], 0x120 + N, 0xf, 0xf, true)))
+  ZC_ROR_MAX(8);
+  ZC_ROR_MAX(4);
+  ZC_ROR_MAX(2);
+  ZC_ROR_MAX(1);
+#undef ZC_ROR_MAX
 }
 
 // Codes of a lane's two neighbouring columns of a 32-column block of h, a row's 16
-// lanes holding the block, and the block's scale S.
-template <bool A4>
-__device__ __forceinline__ uint32_t codes_h(float h0, float h1, int& S) {
-  if constexpr (A4) {
-    S = mx4_scale(row_max(max(__float_as_uint(h0) & 0x7fffffffu, __float_as_uint(h1) & 0x7fffffffu)));
-    return S == 255 ? 0u : mx4_codes<0>(0u, h0, h1, e8m0_f32(S));
-  } else {
-    // (a NaN does not count in the maximum)
-    const float m0 = h0 != h0 ? 0.f : fabsf(h0), m1 = h1 != h1 ? 0.f : fabsf(h1);
-    S = mx_scale(__uint_as_float(row_max(__float_as_uint(fmaxf(m0, m1)))));
-    return mx_code(h0, S) | mx_code(h1, S) << 8;
+// lanes holding the block, and the block's scale S, for R rows at once: what waits for
+// another lane's value finds the other rows' work to do.  A NaN makes its block's scale
+// one, with 8-bit codes too: all of the row's y are NaN either way.
+template <bool A4, int R>
+__device__ __forceinline__ void codes_h(const float (&h)[R][2], uint32_t (&c)[R], int (&S)[R]) {
+  uint32_t top[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+    top[r] = max(__float_as_uint(h[r][0]) & 0x7fffffffu, __float_as_uint(h[r][1]) & 0x7fffffffu);
+  row_max(top);
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    // the scale's bits as a float: 2^(floor(log2 top) - 2 or 8), 0 for 2^-127
+    constexpr uint32_t kDown = (A4 ? 2u : 8u) << 23;
+    const uint32_t bits = max(top[r] & 0x7f800000u, kDown) - kDown;
+    const int s = static_cast<int>(bits >> 23);
+    S[r] = top[r] > 0x7f800000u ? 255 : s;
+    if constexpr (A4) {
+      c[r] = mx4_codes<0>(0u, h[r][0], h[r][1], __uint_as_float(max(bits, 0x00400000u)));
+    } else {
+      float q[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        q[i] = fminf(fmaxf(__builtin_ldexpf(h[r][i], 127 - s), -448.f), 448.f);
+      c[r] = static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false)) & 0xffffu;
+    }
   }
+}
+
+// bf16 of a (low half) and b, nearest, ties to even, in one instruction.
+__device__ __forceinline__ uint32_t pk_bf16(float a, float b) {
+  typedef float f32x2_t __attribute__((ext_vector_type(2)));
+  typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2_t{a, b}), bf16x2_t));
 }
 
 // RB blocks of 16 rows and NB blocks of 16 weight columns a workgroup (gate/up: the
@@ -268,15 +295,17 @@ __global__ __launch_bounds__(kThreads, 2) void mx4_kernel(Mx4Params p) {
           const float h0 = silu_f(sum(rb, 2 * j)) * sum(rb, 2 * j + NB / 2);
           const float h1 = silu_f(sum(rb, 2 * j + 1)) * sum(rb, 2 * j + 1 + NB / 2);
           const int block = nt * (OUT / 32) + j;
-          int S;
-          const uint32_t c = codes_h<A4>(h0, h1, S);
+          const float h[1][2] = {{h0, h1}};
+          int S[1];
+          uint32_t c[1];
+          codes_h<A4>(h, c, S);
           if constexpr (A4)
-            p.hq[(row * p.ncols + 32 * block) / 2 + l16] = static_cast<uint8_t>(c);
+            p.hq[(row * p.ncols + 32 * block) / 2 + l16] = static_cast<uint8_t>(c[0]);
           else
-            *reinterpret_cast<uint16_t*>(p.hq + row * p.ncols + 32 * block + 2 * l16) = static_cast<uint16_t>(c);
+            *reinterpret_cast<uint16_t*>(p.hq + row * p.ncols + 32 * block + 2 * l16) = static_cast<uint16_t>(c[0]);
           if (l16 == 0)
             p.hs[row * (p.ncols / 32) +
-                 (A4 ? block : (block & ~3) + 2 * (block & 1) + ((block >> 1) & 1))] = static_cast<uint8_t>(S);
+                 (A4 ? block : (block & ~3) + 2 * (block & 1) + ((block >> 1) & 1))] = static_cast<uint8_t>(S[0]);
         }
       } else {
 #pragma unroll
@@ -524,18 +553,24 @@ __global__ __launch_bounds__(kThreads, 2) void mx4_wide_kernel(Mx4Params p) {
         const int sat = l16 ? 0x70000000
                             : 4 * lq * sp + (A4 ? block : (block & ~3) + 2 * (block & 1) + ((block >> 1) & 1));
 #pragma unroll
-        for (int rb = 0; rb < NRB; ++rb)
+        for (int rb = 0; rb < NRB; ++rb) {
+          float h[4][2];
+          uint32_t c[4];
+          int S[4];
+#pragma unroll
+          for (int v = 0; v < 4; ++v)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) h[v][i] = silu_f(acc[rb][i][v]) * acc[rb][2 + i][v];
+          codes_h<A4>(h, c, S);
 #pragma unroll
           for (int v = 0; v < 4; ++v) {
-            int S;
-            const uint32_t c = codes_h<A4>(silu_f(acc[rb][0][v]) * acc[rb][2][v],
-                                           silu_f(acc[rb][1][v]) * acc[rb][3][v], S);
             if constexpr (A4)
-              __builtin_amdgcn_raw_buffer_store_b8(static_cast<uint8_t>(c), hq, at + (16 * rb + v) * pitch, 0, 0);
+              __builtin_amdgcn_raw_buffer_store_b8(static_cast<uint8_t>(c[v]), hq, at + (16 * rb + v) * pitch, 0, 0);
             else
-              __builtin_amdgcn_raw_buffer_store_b16(static_cast<uint16_t>(c), hq, at + (16 * rb + v) * pitch, 0, 0);
-            __builtin_amdgcn_raw_buffer_store_b8(static_cast<uint8_t>(S), hs, sat + (16 * rb + v) * sp, 0, 0);
+              __builtin_amdgcn_raw_buffer_store_b16(static_cast<uint16_t>(c[v]), hq, at + (16 * rb + v) * pitch, 0, 0);
+            __builtin_amdgcn_raw_buffer_store_b8(static_cast<uint8_t>(S[v]), hs, sat + (16 * rb + v) * sp, 0, 0);
           }
+        }
       } else {
         const __amdgpu_buffer_rsrc_t y = __builtin_amdgcn_make_buffer_rsrc(
             p.yb + static_cast<int64_t>(m0) * p.ncols, (short)0, mcount * p.ncols * 2, 0x00020000);
@@ -547,8 +582,7 @@ __global__ __launch_bounds__(kThreads, 2) void mx4_wide_kernel(Mx4Params p) {
             u32x2_t w;
 #pragma unroll
             for (int j = 0; j < 2; ++j)
-              w[j] = static_cast<uint32_t>(f2bf(acc[rb][2 * j][v])) |
-                     static_cast<uint32_t>(f2bf(acc[rb][2 * j + 1][v])) << 16;
+              w[j] = pk_bf16(acc[rb][2 * j][v], acc[rb][2 * j + 1][v]);
             __builtin_amdgcn_raw_buffer_store_b64(w, y, at + (16 * rb + v) * p.ncols * 2, 0, 0);
           }
       }
