@@ -29,7 +29,7 @@ constexpr int kThreads = 256;
 // Tensors of one launch, passed by value: nothing has to be copied to the device
 // before it, and a captured launch holds them.  As many as the 4 KB of kernel
 // arguments take; short lists have a kernel whose arguments are short (the host
-// writes them and each workgroup reads them: 198 k weights in 5 tensors, ...).
+// writes all of them: a step of 5 tensors keeps it 6.2 us, with long arguments 7.2).
 constexpr int kFew = 8;
 constexpr int kArgBytes = 4096;
 
@@ -72,12 +72,15 @@ __device__ __forceinline__ int tensor_of(const int32_t (&first)[CAP], int count,
     for (int k = 1; k < CAP - 1; ++k) i += k < count && first[k] <= b;
     return i;
   }
-  int lo = 0, hi = count;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (first[mid] <= b) lo = mid; else hi = mid;
+  // (all of them at once: a search would wait for one load after the other, 0.6 us of
+  // the 19 us of 4.8 M weights in 61 tensors)
+  int i = -1;
+#pragma unroll
+  for (int k0 = 0; k0 < CAP - 1; k0 += 64) {
+    const int k = k0 + (threadIdx.x & 63);
+    i += __popcll(__ballot(k < count && first[k < CAP - 1 ? k : 0] <= b));
   }
-  return lo;
+  return i;
 }
 
 // ------------------------------------------------------------------ norm
@@ -174,7 +177,7 @@ __device__ __forceinline__ float quotient(float a, float b, float r) {
 // Square roots of N values, rounded to nearest: from the hardware's estimate of the
 // reciprocal root and the root's remainder, sqrt(x) = s + (x - s^2) / (2 s), where
 // all x are far from the ends of the exponents (8 operations each, where the general
-// routine takes some 19: 277 us -> 236 us of 100.7 M weights with 8-bit states).
+// routine takes some 19: 227 us -> 205 us of 100.7 M weights with 8-bit states).
 template <int N>
 __device__ __forceinline__ void roots(const float* x, float* r) {
   float lo = x[0], hi = x[0];
@@ -269,8 +272,8 @@ __device__ __forceinline__ void load(const T* p, int left, float* f) {
     for (int e = 0; e < W; ++e) f[e] = e < left ? Elem<T>::ld(p + e) : 0.f;
   }
 }
-// (Nothing that a step writes is read again soon: non-temporal stores, 518 us -> 485 us
-// of 100.7 M weights with fp32 copies and states.)
+// (Nothing that a step writes is read again soon: non-temporal stores, 514 us -> 459 us
+// of 100.7 M weights with fp32 copies and states, 213 us -> 205 us with 8-bit ones.)
 template <typename T, int W>
 __device__ __forceinline__ void store(T* p, int left, const float* f) {
   if (left >= W) {
@@ -493,9 +496,12 @@ hipError_t adamw_deal(const AdamwTensor* t, int64_t count, const AdamwScalars& s
     total += t[i].n;
     most = t[i].n > most ? t[i].n : most;
   }
-  // two rounds a workgroup where that leaves enough of them (100.7 M weights, fp32
-  // states: 518 us; one 520, eight 543), more where a tensor has too many
-  int64_t passes = total / (2 * kThreads * W) >= 4096 ? 2 : 1;
+  // Rounds a workgroup.  32-bit states: one, the loads of many short workgroups overlap
+  // best (100.7 M weights with fp32 copies: 458 us; two rounds 496, four 511).  8-bit
+  // ones, where the scalars of the step cost as much as a round's loads: up to four while
+  // that leaves enough workgroups (205 us; two 214, one 234).  More where a tensor has too many.
+  int64_t passes = 1;
+  while (B8 && passes < 4 && total / (2 * passes * kThreads * W) >= 4096) passes *= 2;
   while (most / (passes * kThreads * W) >= kMaxChunks) passes *= 2;
   a.passes = static_cast<int32_t>(passes);
   return deal<CAP>(
