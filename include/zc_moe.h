@@ -433,7 +433,7 @@ zc_status zc_mxfp4_quantize(int64_t R, int64_t C, int dtype, const void* src, ui
  * multiply them by rows x and h in MXFP8 (A8; the rules of zc_moe_quantize_weights)
  * or in MXFP4 too (A4, at up to twice the rate, h and x in 4 bits), sums in fp32.  x
  * is quantized once for each token, h from its fp32 values; the experts' outputs y
- * are kept in fp32, in bf16 where T*K/(N+Z) is above 20 and d and I are multiples of
+ * are kept in fp32, in bf16 where T*K/(N+Z) is above 10 and d and I are multiples of
  * 512 (many rows: y's bytes count there); the router, gates, the
  * combine and the zero-computation experts (which return the unquantized x) stay in
  * bf16/fp32.  Grids are not persistent: cu_limit does not size them.

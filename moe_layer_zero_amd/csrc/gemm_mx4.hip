@@ -147,6 +147,8 @@ __device__ __forceinline__ uint32_t pk_bf16(float a, float b) {
 // first half of them gate, the second the matching up columns).  The four wavefronts
 // split the reduction and add their sums through LDS in order, so few rows still
 // give many workgroups with many loads in flight, and there is no barrier in the loop.
+// Bound by HBM: 256 tokens (d 6144, I 2048, 512 experts, MXFP8 rows) read 10.1 GB in 1.58
+// ms, 6.4 TB/s; one token 105 MB of gate and up in 19.5 us, 5.4 TB/s.  y is fp32.
 template <int EPI, int RB, int NB, bool A4>
 __global__ __launch_bounds__(kThreads, 2) void mx4_kernel(Mx4Params p) {
   constexpr int OUT = (EPI == MX_SWIGLU ? NB / 2 : NB) * 16;  // output columns a workgroup
@@ -352,6 +354,28 @@ __device__ __forceinline__ void lds_barrier() {
   asm volatile("" ::: "memory");
 }
 
+// 128 rows by 256 weight columns a workgroup (gate/up: 128 gate and the matching up
+// columns), 64 columns a wavefront: each weight goes from memory to the registers of
+// the one wavefront that multiplies with it, the rows through LDS to all four.  Two
+// workgroups a CU; of each 24 KB (MXFP8 rows 32) a slab of 128 steps, and what is in
+// flight while a slab is multiplied is three slabs of rows, copied straight into a ring
+// of four LDS slots, and two or three slabs of weights in registers.
+//
+// What bounds it (16384 tokens, d 6144, I 2048, 512 experts, MXFP4 rows; gate/up 2.25
+// ms, 4.5 PFLOP/s and 3.6 TB/s of HBM reads): getting 24 GB from the L2s to the CUs at
+// this depth.  Measured in copies with parts left out: without the products 2.25 ms,
+// without the rows' copies 1.78, without the weights' loads 1.20, without both 1.08;
+// products alone would take 0.9 ms at the 7.2 PFLOP/s that the instruction reaches, HBM
+// 1.1 ms.  Tried and slower: 256 rows by eight wavefronts (2.52 ms), 256 rows by four
+// with 512 registers and seven slabs ahead (4.18 ms: the sums alone fill the
+// accumulation registers), weights read non-temporally (2.70 ms: the other row tiles of
+// an expert find them in the L2).  With one row tile an expert (4096 tokens) it
+// reads its weights at 5.5 TB/s, in 1.25 ms.  MXFP8 rows are held by the 4.4 PFLOP/s
+// of 8-bit by 4-bit products.
+//
+// An expert's rows are spread evenly over its tiles in blocks of 16, and a tile's sums
+// are those of 2, 4, 6 or 8 blocks.  y goes out in bf16: it would be twice the bytes
+// in fp32 (1.6 of 10.7 GB here), and costs 2^-9 of each of K terms.
 template <int EPI, bool A4>
 __global__ __launch_bounds__(kThreads, 2) void mx4_wide_kernel(Mx4Params p) {
   constexpr int TM = 128;                      // rows of a tile at most
@@ -658,7 +682,8 @@ __device__ __forceinline__ uint32_t mx4_quad(const float* f, int& S) {
 }
 
 // Rows -> natural codes and scales, and the values they stand for.  Eight values a
-// thread.
+// thread.  Bound by HBM: 16384 x 6144 values in bf16 with their values back, 456 MB, in
+// 86 us, 5.3 TB/s, a copy's rate (non-temporal loads or stores: the same).
 template <typename T>
 __global__ __launch_bounds__(256) void mx4_rows_kernel(const T* src, int64_t pieces,
                                                        uint32_t* __restrict__ codes,
@@ -720,15 +745,21 @@ __global__ __launch_bounds__(kMaxExperts) void mx4_start_kernel(
 
 }  // namespace
 
+// Row tiles by the rows an expert has on average.  Few rows: each weight is read once
+// and done with, by tiles of 16; from some 10 rows on by the kernel of many rows
+// (gate/up, down and combine with MXFP8 rows, us, tiles of 16 / of 32 / many rows):
+//   d 6144, I 2048, 512 experts:  8 rows 1782 / 1881 / 1801, 12 rows 2088 / 1996 / 1828,
+//     20 rows 3413 / 2287 / 1878
+//   d 1024, I 512, 64 experts:    8 rows 26.2 / 29.8 / 28.6, 12 rows 28.5 / 31.4 / 28.7,
+//     20 rows 34.7 / 36.1 / 29.7, 64 rows 58.4 / 60.1 / 33.6
+// That kernel takes whole groups of 512 steps, and byte offsets of 31 bits into x, h and
+// a matrix: other layers have tiles of 16, 32 or 64.
 Mx4Plan mx4_plan(int64_t Tn, int64_t rows, int64_t E, int64_t d, int64_t I) {
-  const int64_t avg = rows / E;
-  if (avg <= 13) return {16, false};
-  if (avg <= 20) return {32, false};
-  // (the kernel of many rows takes whole groups of 512 steps, and byte offsets of 31
-  // bits into x, h and a matrix)
-  const int64_t limit = int64_t(1) << 31;
-  if (d % 512 || I % 512 || Tn * d >= limit || rows * I >= limit || d * I >= limit) return {64, false};
-  return {128, true};
+  const int64_t avg = rows / E, limit = int64_t(1) << 31;
+  if (avg <= 10) return {16, false};
+  if (d % 512 == 0 && I % 512 == 0 && Tn * d < limit && rows * I < limit && d * I < limit)
+    return {128, true};
+  return {avg <= 13 ? 16 : avg <= 20 ? 32 : 64, false};
 }
 
 hipError_t launch_mx4_start(bool a4, const int32_t* offsets, int N, int tm, void* tiles,

@@ -219,7 +219,7 @@ def reference(desc, x, w, route, a):
 
 def y_round(desc):
     """y is kept in fp32, but in bf16 by the kernel of many rows."""
-    many = desc.T * desc.K // desc.E > 20 and desc.d % 512 == 0 and desc.I % 512 == 0
+    many = desc.T * desc.K // desc.E > 10 and desc.d % 512 == 0 and desc.I % 512 == 0
     return HB if many else 0.0
 
 
