@@ -379,9 +379,11 @@ __device__ __forceinline__ void lds_barrier() {
 template <int EPI, bool A4>
 __global__ __launch_bounds__(kThreads, 2) void mx4_wide_kernel(Mx4Params p) {
   constexpr int TM = 128;                      // rows of a tile at most
-  constexpr int CB = A4 ? kStep / 2 : kStep;   // bytes of a row's slab of 128 steps
-  constexpr int SLOT = TM * CB;                // bytes of a ring slot
-  constexpr int CP = SLOT / 1024 / kWaves;     // copies a wavefront and slab
+  constexpr int CB = 128;                      // bytes of a row in a ring slot: a cache line
+  constexpr int SPS = A4 ? 2 : 1;              // slabs of 128 steps in a slot
+  constexpr int SLOT = TM * CB;                // bytes of a slot
+  constexpr int CP = SLOT / 1024 / kWaves;     // copies a wavefront and slot
+  constexpr int CS = CP / SPS;                 // and slab
   constexpr int RPC = 1024 / CB;               // rows of a copy
   constexpr int SC = TM * 16;                  // bytes of the rows' scales of 512 steps
   constexpr int OUT = EPI == MX_SWIGLU ? 128 : 256;
@@ -392,7 +394,7 @@ __global__ __launch_bounds__(kThreads, 2) void mx4_wide_kernel(Mx4Params p) {
   // 2: the rows of the slab after next and the weights of the next (issued at the end
   // of the slab before this one), the scales with the slab before this one.
   constexpr auto wait_of = [](int slot) constexpr {
-    return NBUF == 4 ? 2 * (CP + 4) + (slot == 1 || slot == 2 ? 6 : 0) : CP + 4 + (slot == 1 ? 6 : 0);
+    return NBUF == 4 ? 2 * (CS + 4) + (slot == 1 || slot == 2 ? 6 : 0) : CS + 4 + (slot == 1 ? 6 : 0);
   };
   __shared__ __align__(16) uint8_t ring[4 * SLOT + 2 * SC];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -425,7 +427,7 @@ __global__ __launch_bounds__(kThreads, 2) void mx4_wide_kernel(Mx4Params p) {
       const int r = (CP * wave + i) * RPC + lane / (CB / 16);
       const int row = m0 + min(r, mcount - 1);
       const int tok = EPI == MX_SWIGLU ? p.perm[row] / p.kdiv : row;
-      const int chunk = A4 ? (lane & 3) ^ ((r >> 2) & 3) : (lane & 7) ^ ((r >> 1) & 7);
+      const int chunk = (lane & 7) ^ ((r >> 1) & 7);
       src[i] = r < mcount ? static_cast<uint32_t>(tok) * static_cast<uint32_t>(A4 ? p.K / 2 : p.K) + 16 * chunk
                           : p.a_bytes;
     }
@@ -455,10 +457,11 @@ __global__ __launch_bounds__(kThreads, 2) void mx4_wide_kernel(Mx4Params p) {
       constexpr int NRB = decltype(nrb_c)::value;
       i32x4_t b[NBUF][4];  // [slab % NBUF][column block]
       int sb[4], sbn[4];   // scales of these four slabs, and of the next four
-      // one load each: the i-th copy of slab kb's rows, its weights' column block nb;
-      // the i-th of four slabs' scales (two copies of the rows', then the columns')
-      auto issue_row = [&](int kb, int slot, int i) {
-        copy_to_lds16(rows, (lds_void*)(ring + slot * SLOT + (CP * wave + i) * 1024), src[i], kb * CB);
+      // one load each: the i-th copy of a slot's rows, `at` slots' worth into the row;
+      // the weights' column block nb of slab kb; the i-th of four slabs' scales (two
+      // copies of the rows', then the columns')
+      auto issue_row = [&](int at, int slot, int i) {
+        copy_to_lds16(rows, (lds_void*)(ring + slot * SLOT + (CP * wave + i) * 1024), src[i], at * CB);
       };
       auto issue_weight = [&](int kb, int slot, int nb) {
         b[slot % NBUF][nb] = __builtin_bit_cast(
@@ -479,9 +482,9 @@ __global__ __launch_bounds__(kThreads, 2) void mx4_wide_kernel(Mx4Params p) {
       for (int rb = 0; rb < NRB; ++rb)
 #pragma unroll
         for (int nb = 0; nb < 4; ++nb) acc[rb][nb] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-      // where this lane's row of a block lies in a slot: chunk lq (and 4 + lq)
-      const int pos0 = A4 ? lq ^ (l16 >> 2) : lq ^ (l16 >> 1);
-      const int frag_lane = l16 * CB + 16 * pos0;
+      // where this lane's row of a block lies in a slot: chunk lq, and 4 + lq (MXFP8: of
+      // the same slab, MXFP4: of the slot's second one)
+      int frag_at = l16 * CB + 16 * (lq ^ (l16 >> 1));
       // and its scale of a slab
       int scale_at = l16 * 16 + (A4 ? lq : 2 * (lq & 1) + (lq >> 1));
 
@@ -489,22 +492,22 @@ __global__ __launch_bounds__(kThreads, 2) void mx4_wide_kernel(Mx4Params p) {
       constexpr int AHEAD = A4 ? (3 < NRB ? 3 : NRB) : 1;
       const int last = nkb - 1;
       // One slab: wait for it, meet, multiply, and between the multiplications issue,
-      // one by one, the loads of the rows three slabs ahead, of weights and (with the
+      // one by one, the loads of rows three slabs ahead or more, of weights and (with the
       // first of four slabs) of the next four's scales: issued at once they would
       // hold the wavefront up until the address unit has taken them all.  No branch: past the end the
       // last slab is loaded again, so that the number of loads in flight is known.
       auto slab = [&](int kb, int q4, auto slot_c) {
         constexpr int slot = decltype(slot_c)::value;
-        constexpr int NL = CP + (NBUF == 4 ? 4 : 0) + (slot == 0 ? 6 : 0);
+        constexpr int NL = CS + (NBUF == 4 ? 4 : 0) + (slot == 0 ? 6 : 0);
         __builtin_amdgcn_s_waitcnt(vmcnt_imm(wait_of(slot)));
         lds_barrier();
         i32x8_t a[AHEAD + 1] = {};
         int sa[AHEAD + 1];
         auto frag = [&](int rb) {
           i32x8_t& f = a[rb % (AHEAD + 1)];
-          f.lo = *reinterpret_cast<const i32x4_t*>(ring + slot * SLOT + rb * 16 * CB + frag_lane);
-          if constexpr (!A4)
-            f.hi = *reinterpret_cast<const i32x4_t*>(ring + slot * SLOT + rb * 16 * CB + (frag_lane ^ 64));
+          const uint8_t* block = ring + slot / SPS * SLOT + rb * 16 * CB;
+          f.lo = *reinterpret_cast<const i32x4_t*>(block + (frag_at ^ (slot % SPS * 64)));
+          if constexpr (!A4) f.hi = *reinterpret_cast<const i32x4_t*>(block + (frag_at ^ 64));
           sa[rb % (AHEAD + 1)] = ring[4 * SLOT + rb * 256 + slot * 4 + scale_at];
         };
 #pragma unroll
@@ -514,12 +517,14 @@ __global__ __launch_bounds__(kThreads, 2) void mx4_wide_kernel(Mx4Params p) {
           if (rb + AHEAD < NRB) frag(rb + AHEAD);
 #pragma unroll
           for (int i = NL * rb / NRB; i < NL * (rb + 1) / NRB; ++i) {
-            if (i < CP)
+            if (i < CS && A4)
+              issue_row(min(kb / 2 + 2, last / 2), slot / 2 + 2 * ((q4 + 1) & 1), slot % 2 * CS + i);
+            else if (i < CS)
               issue_row(min(kb + 3, last), (slot + 3) & 3, i);
-            else if (NBUF == 4 && i < CP + 4)
-              issue_weight(min(kb + 3, last), (slot + 3) & 3, i - CP);
+            else if (NBUF == 4 && i < CS + 4)
+              issue_weight(min(kb + 3, last), (slot + 3) & 3, i - CS);
             else
-              issue_scale(min(q4 + 1, nq - 1), (q4 + 1) & 1, sbn, i - CP - (NBUF == 4 ? 4 : 0));
+              issue_scale(min(q4 + 1, nq - 1), (q4 + 1) & 1, sbn, i - CS - (NBUF == 4 ? 4 : 0));
           }
 #pragma unroll
           for (int nb = 0; nb < 4; ++nb) {
@@ -547,11 +552,17 @@ __global__ __launch_bounds__(kThreads, 2) void mx4_wide_kernel(Mx4Params p) {
       for (int i = 0; i < 6; ++i) issue_scale(0, 0, sb, i);
 #pragma unroll
       for (int kb = 0; kb < 3; ++kb) {
+        // (MXFP4: the first slot before the first slab's weights, the second one's halves
+        // after those of the next two, as the waits count)
+        if (!A4 || kb == 0)
 #pragma unroll
-        for (int i = 0; i < CP; ++i) issue_row(kb, kb, i);
+          for (int i = 0; i < CP; ++i) issue_row(kb, kb, i);
 #pragma unroll
         for (int nb = 0; nb < 4; ++nb)
           if (NBUF == 4 || kb < 2) issue_weight(kb, kb, nb);
+        if (A4 && kb > 0)
+#pragma unroll
+          for (int i = 0; i < CS; ++i) issue_row(1, 1, (kb - 1) * CS + i);
         __builtin_amdgcn_sched_barrier(0);
       }
       for (int q4 = 0; q4 < nq; ++q4) {
@@ -560,6 +571,7 @@ __global__ __launch_bounds__(kThreads, 2) void mx4_wide_kernel(Mx4Params p) {
         slab(4 * q4 + 2, q4, C2{});
         slab(4 * q4 + 3, q4, C3{});
         scale_at ^= SC;
+        if (A4) frag_at ^= 2 * SLOT;
 #pragma unroll
         for (int nb = 0; nb < 4; ++nb) sb[nb] = sbn[nb];
       }
