@@ -19,8 +19,8 @@
 // Weights of one set (N matrices [R][C]), columns in groups of G = 2 (gate, up) or 4
 // (down) blocks of 16: codes [N][R/16/G][C/128][G][lane][16 bytes]: 1 KB holds 16
 // output columns and 128 reduction steps, a wave's operand as it lies, and a group's
-// pieces of a step lie side by side; then scales [N][R/16/G][ceil(C/512)][G][lane][4
-// code blocks], E8M0: a lane's four scales of 512 steps in one word.  A group's columns
+// pieces of a step lie side by side; then scales [N][R/16/G][ceil(C/512)][lane][G][4
+// code blocks], E8M0: a lane's scales of 512 steps and a group in one load.  A group's columns
 // are dealt to its blocks in turn, so that a lane ends with G neighbours: two 4-bit
 // codes of h, a byte; 8 or 16 bytes of y.
 #include "zc_common.h"
@@ -190,9 +190,9 @@ __global__ __launch_bounds__(kThreads, 2) void mx4_kernel(Mx4Params p) {
       const uint8_t* base = up ? p.B2 : p.B;
       const int cb = nt * (OUT / 16) + (up ? nb - NB / 2 : nb);
       code[nb] = base + e * cmat + (static_cast<int64_t>(cb / G) * nkb * G + cb % G) * 1024;
-      scale[nb] = base + p.N * cmat + e * smat + (static_cast<int64_t>(cb / G) * nq * G + cb % G) * 256;
+      scale[nb] = base + p.N * cmat + e * smat + static_cast<int64_t>(cb / G) * nq * G * 256 + cb % G * 4;
     }
-    const uint32_t code_lane = lane * 16, scale_lane = lane * 4;
+    const uint32_t code_lane = lane * 16, scale_lane = lane * 4 * G;
 
     struct Buf {
       i32x4_t b[NB];
@@ -385,16 +385,18 @@ __global__ __launch_bounds__(kThreads, 2) void mx4_wide_kernel(Mx4Params p) {
   constexpr int CP = SLOT / 1024 / kWaves;     // copies a wavefront and slot
   constexpr int CS = CP / SPS;                 // and slab
   constexpr int RPC = 1024 / CB;               // rows of a copy
-  constexpr int SC = TM * 16;                  // bytes of the rows' scales of 512 steps
+  constexpr int SC = TM * 64;                  // bytes of the rows' scales of 2048 steps
   constexpr int OUT = EPI == MX_SWIGLU ? 128 : 256;
   constexpr int NBUF = A4 ? 4 : 2;             // slabs of weights in registers
   constexpr int G = kGroup<EPI>;
+  constexpr int CSC = 4 / G;                   // loads of the columns' scales of 512 steps
+  constexpr int NSC = CSC + 1;                 // and with them of the rows'
   // Loads that may be in flight when slab `slot` of four is needed.  NBUF 4: rows and
   // weights of the two slabs after it, and the next scales if they went out since.  NBUF
   // 2: the rows of the slab after next and the weights of the next (issued at the end
   // of the slab before this one), the scales with the slab before this one.
   constexpr auto wait_of = [](int slot) constexpr {
-    return NBUF == 4 ? 2 * (CS + 4) + (slot == 1 || slot == 2 ? 6 : 0) : CS + 4 + (slot == 1 ? 6 : 0);
+    return NBUF == 4 ? 2 * (CS + 4) + (slot == 1 || slot == 2 ? NSC : 0) : CS + 4 + (slot == 1 ? NSC : 0);
   };
   __shared__ __align__(16) uint8_t ring[4 * SLOT + 2 * SC];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -431,14 +433,21 @@ __global__ __launch_bounds__(kThreads, 2) void mx4_wide_kernel(Mx4Params p) {
       src[i] = r < mcount ? static_cast<uint32_t>(tok) * static_cast<uint32_t>(A4 ? p.K / 2 : p.K) + 16 * chunk
                           : p.a_bytes;
     }
+    // Rows' scales, 64 bytes (four times 512 steps) at a time; which of the four this
+    // lane copies depends on the row (the same ones of all rows would lie in the same
+    // LDS banks).
+    const int schunk = (lane & 3) ^ (lane >> 4);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int r = (2 * wave + i) * 16 + (lane >> 2);
       const int row = m0 + min(r, mcount - 1);
       const int tok = EPI == MX_SWIGLU ? p.perm[row] / p.kdiv : row;
-      ssrc[i] = r < mcount ? static_cast<uint32_t>(tok) * static_cast<uint32_t>(p.K / 32) + 4 * (lane & 3)
-                           : p.as_bytes;
+      ssrc[i] = r < mcount && schunk < nq
+                    ? static_cast<uint32_t>(tok) * static_cast<uint32_t>(p.K / 32) + 16 * schunk
+                    : p.as_bytes;
     }
+    // first of the at-th four (a row's last four end with it)
+    auto sfirst = [&](int at) { return max(min(4 * at, nq - 4), 0); };
 
     const int64_t cmat = static_cast<int64_t>(p.ncols) * p.K / 2, smat = cmat / 16;
     __amdgpu_buffer_rsrc_t codes[2], scales[2];  // gate (or down) and up
@@ -451,15 +460,15 @@ __global__ __launch_bounds__(kThreads, 2) void mx4_wide_kernel(Mx4Params p) {
                                                     static_cast<uint32_t>(smat), 0x00020000);
     }
     const int grp = nt * 4 + wave;  // the wavefront's group of column blocks
-    const uint32_t code_lane = lane * 16, scale_lane = lane * 4;
+    const uint32_t code_lane = lane * 16, scale_lane = lane * 4 * G;
 
     auto run = [&](auto nrb_c) {
       constexpr int NRB = decltype(nrb_c)::value;
       i32x4_t b[NBUF][4];  // [slab % NBUF][column block]
       int sb[4], sbn[4];   // scales of these four slabs, and of the next four
       // one load each: the i-th copy of a slot's rows, `at` slots' worth into the row;
-      // the weights' column block nb of slab kb; the i-th of four slabs' scales (two
-      // copies of the rows', then the columns')
+      // the weights' column block nb of slab kb; of the rows' scales of 2048 steps, and
+      // the columns' of 512
       auto issue_row = [&](int at, int slot, int i) {
         copy_to_lds16(rows, (lds_void*)(ring + slot * SLOT + (CP * wave + i) * 1024), src[i], at * CB);
       };
@@ -468,13 +477,21 @@ __global__ __launch_bounds__(kThreads, 2) void mx4_wide_kernel(Mx4Params p) {
             i32x4_t, __builtin_amdgcn_raw_buffer_load_b128(codes[EPI == MX_SWIGLU ? nb / 2 : 0],
                                                            code_lane, ((grp * nkb + kb) * G + nb % G) * 1024, 0));
       };
-      auto issue_scale = [&](int quad, int par, int* sc, int i) {
-        if (i < 2)
-          copy_to_lds4(rscale, (lds_void*)(ring + 4 * SLOT + par * SC + (2 * wave + i) * 256), ssrc[i],
-                       quad * 16);
-        else
-          sc[i - 2] = __builtin_amdgcn_raw_buffer_load_b32(scales[EPI == MX_SWIGLU ? (i - 2) / 2 : 0],
-                                                           scale_lane, ((grp * nq + quad) * G + (i - 2) % G) * 256, 0);
+      auto issue_row_scale = [&](int at, int i) {
+        copy_to_lds16(rscale, (lds_void*)(ring + 4 * SLOT + (at & 1) * SC + (2 * wave + i) * 1024), ssrc[i],
+                      sfirst(at) * 16);
+      };
+      auto issue_scale = [&](int quad, int* sc, int i) {
+        const int at = (grp * nq + quad) * G * 256;
+        if constexpr (G == 4) {
+          const auto w = __builtin_amdgcn_raw_buffer_load_b128(scales[0], scale_lane, at, 0);
+#pragma unroll
+          for (int nb = 0; nb < 4; ++nb) sc[nb] = w[nb];
+        } else {
+          const auto w = __builtin_amdgcn_raw_buffer_load_b64(scales[i], scale_lane, at, 0);
+          sc[2 * i] = w[0];
+          sc[2 * i + 1] = w[1];
+        }
       };
 
       f32x4_t acc[NRB][4];
@@ -486,7 +503,7 @@ __global__ __launch_bounds__(kThreads, 2) void mx4_wide_kernel(Mx4Params p) {
       // the same slab, MXFP4: of the slot's second one)
       int frag_at = l16 * CB + 16 * (lq ^ (l16 >> 1));
       // and its scale of a slab
-      int scale_at = l16 * 16 + (A4 ? lq : 2 * (lq & 1) + (lq >> 1));
+      int scale_at = 4 * SLOT + l16 * 64 + 16 * (l16 >> 2) + (A4 ? lq : 2 * (lq & 1) + (lq >> 1));
 
       // Fragments are read AHEAD of their multiplications (of 64 or 128 cycles).
       constexpr int AHEAD = A4 ? (3 < NRB ? 3 : NRB) : 1;
@@ -498,7 +515,7 @@ __global__ __launch_bounds__(kThreads, 2) void mx4_wide_kernel(Mx4Params p) {
       // last slab is loaded again, so that the number of loads in flight is known.
       auto slab = [&](int kb, int q4, auto slot_c) {
         constexpr int slot = decltype(slot_c)::value;
-        constexpr int NL = CS + (NBUF == 4 ? 4 : 0) + (slot == 0 ? 6 : 0);
+        constexpr int NL = CS + (NBUF == 4 ? 4 : 0) + (slot == 0 ? NSC : 0);
         __builtin_amdgcn_s_waitcnt(vmcnt_imm(wait_of(slot)));
         lds_barrier();
         i32x8_t a[AHEAD + 1] = {};
@@ -508,7 +525,7 @@ __global__ __launch_bounds__(kThreads, 2) void mx4_wide_kernel(Mx4Params p) {
           const uint8_t* block = ring + slot / SPS * SLOT + rb * 16 * CB;
           f.lo = *reinterpret_cast<const i32x4_t*>(block + (frag_at ^ (slot % SPS * 64)));
           if constexpr (!A4) f.hi = *reinterpret_cast<const i32x4_t*>(block + (frag_at ^ 64));
-          sa[rb % (AHEAD + 1)] = ring[4 * SLOT + rb * 256 + slot * 4 + scale_at];
+          sa[rb % (AHEAD + 1)] = ring[rb * 1024 + slot * 4 + scale_at];
         };
 #pragma unroll
         for (int rb = 0; rb < AHEAD; ++rb) frag(rb);
@@ -523,8 +540,10 @@ __global__ __launch_bounds__(kThreads, 2) void mx4_wide_kernel(Mx4Params p) {
               issue_row(min(kb + 3, last), (slot + 3) & 3, i);
             else if (NBUF == 4 && i < CS + 4)
               issue_weight(min(kb + 3, last), (slot + 3) & 3, i - CS);
-            else
-              issue_scale(min(q4 + 1, nq - 1), (q4 + 1) & 1, sbn, i - CS - (NBUF == 4 ? 4 : 0));
+            else if (i < NL - 1)
+              issue_scale(min(q4 + 1, nq - 1), sbn, i - CS - (NBUF == 4 ? 4 : 0));
+            else  // (each twice in the four quarters: so the number of loads is known)
+              issue_row_scale(q4 / 4 + 1, q4 & 1);
           }
 #pragma unroll
           for (int nb = 0; nb < 4; ++nb) {
@@ -549,7 +568,9 @@ __global__ __launch_bounds__(kThreads, 2) void mx4_wide_kernel(Mx4Params p) {
       using C3 = std::integral_constant<int, 3>;
       lds_barrier();  // the ring is free: the previous tile's reads are done
 #pragma unroll
-      for (int i = 0; i < 6; ++i) issue_scale(0, 0, sb, i);
+      for (int i = 0; i < 2; ++i) issue_row_scale(0, i);
+#pragma unroll
+      for (int i = 0; i < CSC; ++i) issue_scale(0, sb, i);
 #pragma unroll
       for (int kb = 0; kb < 3; ++kb) {
         // (MXFP4: the first slot before the first slab's weights, the second one's halves
@@ -570,7 +591,7 @@ __global__ __launch_bounds__(kThreads, 2) void mx4_wide_kernel(Mx4Params p) {
         slab(4 * q4 + 1, q4, C1{});
         slab(4 * q4 + 2, q4, C2{});
         slab(4 * q4 + 3, q4, C3{});
-        scale_at ^= SC;
+        scale_at ^= 16 * ((q4 - sfirst(q4 / 4)) ^ (q4 + 1 - sfirst((q4 + 1) / 4))) ^ ((q4 & 3) == 3 ? SC : 0);
         if (A4) frag_at ^= 2 * SLOT;
 #pragma unroll
         for (int nb = 0; nb < 4; ++nb) sb[nb] = sbn[nb];
@@ -667,8 +688,8 @@ __global__ __launch_bounds__(256) void mx4_pack_kernel(const u32x4_t* __restrict
   }
   const int64_t ns = nmat * (R / 16) * nq * 256;
   for (int64_t i = i0; i < ns; i += step) {
-    // i = ((((mat R/16/G + group) nq + quad) G + block) 64 + lane) 4 + code block
-    const int lane = (i >> 2) & 63, j = (i >> 8) & (G - 1);
+    // i = ((((mat R/16/G + group) nq + quad) 64 + lane) G + block) 4 + code block
+    const int lane = (i >> (2 + log_group)) & 63, j = (i >> 2) & (G - 1);
     const int64_t blk = i >> (8 + log_group);
     const int kb = static_cast<int>(blk % nq) * 4 + static_cast<int>(i & 3);
     const int64_t row = column(blk / nq, j, lane & 15);

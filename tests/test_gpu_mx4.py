@@ -250,6 +250,9 @@ CASES = [
     (333, 512, 3, 1, 1024, 2),    # hundreds of rows an expert, whole groups of 512 steps
     (520, 1024, 2, 1, 512, 2),
     (1100, 512, 2, 0, 512, 1),
+    (150, 2560, 2, 1, 512, 2),    # rows' scales in parts of 2048 steps, the last one short
+    (90, 512, 1, 1, 4608, 1),
+    (130, 2048, 2, 0, 3584, 1),
 ]
 
 
