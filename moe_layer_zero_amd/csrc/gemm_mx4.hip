@@ -49,6 +49,7 @@ struct Mx4Params {
   const uint8_t* As;        // their scales, [rows][K/32]
   const int32_t* perm;      // gate/up only
   int kdiv;                 // K of the layer (slot -> token)
+  uint32_t kdiv_inv;        // 2^31 / K, rounded up: divides slots below 2^27 (K <= 16)
   const uint8_t* B;         // W_g or W_d
   const uint8_t* B2;        // W_u (gate/up)
   uint8_t* hq;              // gate/up output: codes [P][I] or [P][I/2] ...
@@ -422,29 +423,14 @@ __global__ __launch_bounds__(kThreads, 2) void mx4_wide_kernel(Mx4Params p) {
     const int m0 = tile.seg0 + 16 * blo;
     const int mcount = min(tile.seg0 + 16 * bhi, tile.seg1) - m0;
 
-    // rows past the tile's end are copied from past the buffer's: no data moves
-    uint32_t src[CP], ssrc[2];
+    // Rows that this lane copies, and those whose scales: first the slots, which are
+    // under way while the first weights are asked for.
+    int slot_of[CP + 2];
 #pragma unroll
-    for (int i = 0; i < CP; ++i) {
-      const int r = (CP * wave + i) * RPC + lane / (CB / 16);
-      const int row = m0 + min(r, mcount - 1);
-      const int tok = EPI == MX_SWIGLU ? p.perm[row] / p.kdiv : row;
-      const int chunk = (lane & 7) ^ ((r >> 1) & 7);
-      src[i] = r < mcount ? static_cast<uint32_t>(tok) * static_cast<uint32_t>(A4 ? p.K / 2 : p.K) + 16 * chunk
-                          : p.a_bytes;
-    }
-    // Rows' scales, 64 bytes (four times 512 steps) at a time; which of the four this
-    // lane copies depends on the row (the same ones of all rows would lie in the same
-    // LDS banks).
-    const int schunk = (lane & 3) ^ (lane >> 4);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = (2 * wave + i) * 16 + (lane >> 2);
-      const int row = m0 + min(r, mcount - 1);
-      const int tok = EPI == MX_SWIGLU ? p.perm[row] / p.kdiv : row;
-      ssrc[i] = r < mcount && schunk < nq
-                    ? static_cast<uint32_t>(tok) * static_cast<uint32_t>(p.K / 32) + 16 * schunk
-                    : p.as_bytes;
+    for (int i = 0; i < CP + 2; ++i) {
+      const int r = i < CP ? (CP * wave + i) * RPC + lane / (CB / 16) : (2 * wave + i - CP) * 16 + (lane >> 2);
+      slot_of[i] = m0 + min(r, mcount - 1);
+      if (EPI == MX_SWIGLU) slot_of[i] = p.perm[slot_of[i]];
     }
     // first of the at-th four (a row's last four end with it)
     auto sfirst = [&](int at) { return max(min(4 * at, nq - 4), 0); };
@@ -464,6 +450,10 @@ __global__ __launch_bounds__(kThreads, 2) void mx4_wide_kernel(Mx4Params p) {
 
     auto run = [&](auto nrb_c) {
       constexpr int NRB = decltype(nrb_c)::value;
+      // (what the variants have in common would otherwise move in front of the switch,
+      // and the loops' registers with it)
+      asm volatile("; %0 blocks of rows" ::"n"(NRB));
+      uint32_t src[CP], ssrc[2];
       i32x4_t b[NBUF][4];  // [slab % NBUF][column block]
       int sb[4], sbn[4];   // scales of these four slabs, and of the next four
       // one load each: the i-th copy of a slot's rows, `at` slots' worth into the row;
@@ -566,26 +556,43 @@ __global__ __launch_bounds__(kThreads, 2) void mx4_wide_kernel(Mx4Params p) {
       using C1 = std::integral_constant<int, 1>;
       using C2 = std::integral_constant<int, 2>;
       using C3 = std::integral_constant<int, 3>;
+#pragma unroll
+      for (int i = 0; i < CSC; ++i) issue_scale(0, sb, i);
+#pragma unroll
+      for (int kb = 0; kb < (NBUF == 4 ? 3 : 2); ++kb)
+#pragma unroll
+        for (int nb = 0; nb < 4; ++nb) issue_weight(kb, kb, nb);
+      __builtin_amdgcn_sched_barrier(0);
+      // rows past the tile's end are copied from past the buffer's: no data moves
+#pragma unroll
+      for (int i = 0; i < CP; ++i) {
+        const int r = (CP * wave + i) * RPC + lane / (CB / 16);
+        const uint32_t tok = EPI == MX_SWIGLU ? __umulhi(2 * slot_of[i], p.kdiv_inv) : slot_of[i];
+        src[i] = tok * static_cast<uint32_t>(A4 ? p.K / 2 : p.K) + 16 * ((lane & 7) ^ ((r >> 1) & 7));
+        src[i] = r < mcount ? src[i] : p.a_bytes;
+      }
+      // Rows' scales, 64 bytes (four times 512 steps) at a time; which of the four this
+      // lane copies depends on the row (the same ones of all rows would lie in the same
+      // LDS banks).
+      const int schunk = (lane & 3) ^ (lane >> 4);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = (2 * wave + i) * 16 + (lane >> 2);
+        const uint32_t tok = EPI == MX_SWIGLU ? __umulhi(2 * slot_of[CP + i], p.kdiv_inv) : slot_of[CP + i];
+        ssrc[i] = tok * static_cast<uint32_t>(p.K / 32) + 16 * schunk;
+        ssrc[i] = (r < mcount) & (schunk < nq) ? ssrc[i] : p.as_bytes;
+      }
       lds_barrier();  // the ring is free: the previous tile's reads are done
 #pragma unroll
       for (int i = 0; i < 2; ++i) issue_row_scale(0, i);
 #pragma unroll
-      for (int i = 0; i < CSC; ++i) issue_scale(0, sb, i);
+      for (int at = 0; at < (A4 ? 2 : 3); ++at) {
 #pragma unroll
-      for (int kb = 0; kb < 3; ++kb) {
-        // (MXFP4: the first slot before the first slab's weights, the second one's halves
-        // after those of the next two, as the waits count)
-        if (!A4 || kb == 0)
-#pragma unroll
-          for (int i = 0; i < CP; ++i) issue_row(kb, kb, i);
-#pragma unroll
-        for (int nb = 0; nb < 4; ++nb)
-          if (NBUF == 4 || kb < 2) issue_weight(kb, kb, nb);
-        if (A4 && kb > 0)
-#pragma unroll
-          for (int i = 0; i < CS; ++i) issue_row(1, 1, (kb - 1) * CS + i);
+        for (int i = 0; i < CP; ++i) issue_row(at, at, i);
         __builtin_amdgcn_sched_barrier(0);
       }
+      // (the waits in the loop count on rows and weights in turn: here the first rows)
+      __builtin_amdgcn_s_waitcnt(vmcnt_imm((A4 ? 1 : 2) * CP));
       for (int q4 = 0; q4 < nq; ++q4) {
         slab(4 * q4, q4, C0{});
         slab(4 * q4 + 1, q4, C1{});
@@ -824,6 +831,7 @@ hipError_t launch_mx4_gateup(bool a4, const uint8_t* xq, const uint8_t* xs, int6
   if (plan.wide) {
     p.a_bytes = static_cast<uint32_t>(a4 ? Tn * d / 2 : Tn * d);
     p.as_bytes = static_cast<uint32_t>(Tn * (d / 32));
+    p.kdiv_inv = static_cast<uint32_t>(((int64_t(1) << 31) + K - 1) / K);
     return launch_mx4_wide<MX_SWIGLU>(a4, p, rows, plan.tm, s);
   }
   if (plan.tm == 16) return launch_mx4<MX_SWIGLU, 1, 4>(a4, p, rows, s);
