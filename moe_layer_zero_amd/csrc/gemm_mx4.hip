@@ -341,10 +341,6 @@ __device__ __forceinline__ void copy_to_lds16(__amdgpu_buffer_rsrc_t r, lds_void
                                               uint32_t voff, int soff) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, dst, 16, voff, soff, 0, 0);
 }
-__device__ __forceinline__ void copy_to_lds4(__amdgpu_buffer_rsrc_t r, lds_void* dst, uint32_t voff,
-                                             int soff) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, dst, 4, voff, soff, 0, 0);
-}
 // s_waitcnt immediate for "vmcnt <= n" (expcnt and lgkmcnt not waited)
 constexpr int vmcnt_imm(int n) { return 0x0f70 | (n & 15) | ((n >> 4) << 14); }
 // Barrier for LDS alone: loads stay in flight.
@@ -358,21 +354,25 @@ __device__ __forceinline__ void lds_barrier() {
 // 128 rows by 256 weight columns a workgroup (gate/up: 128 gate and the matching up
 // columns), 64 columns a wavefront: each weight goes from memory to the registers of
 // the one wavefront that multiplies with it, the rows through LDS to all four.  Two
-// workgroups a CU; of each 24 KB (MXFP8 rows 32) a slab of 128 steps, and what is in
-// flight while a slab is multiplied is three slabs of rows, copied straight into a ring
-// of four LDS slots, and two or three slabs of weights in registers.
+// workgroups a CU.  While a slab of 128 steps is multiplied, three slabs of rows are
+// under way, copied straight into a ring of four LDS slots, and two or three of weights
+// in registers.  A slot holds 128 bytes of a row, a cache line: of MXFP4 rows two slabs
+// (one a slot, half lines: gate/up 2.25 ms, two 2.07), and rows' scales come 64 bytes at
+// a time (16 bytes: 2.05 ms, 64: 2.00).
 //
-// What bounds it (16384 tokens, d 6144, I 2048, 512 experts, MXFP4 rows; gate/up 2.25
-// ms, 4.5 PFLOP/s and 3.6 TB/s of HBM reads): getting 24 GB from the L2s to the CUs at
-// this depth.  Measured in copies with parts left out: without the products 2.25 ms,
-// without the rows' copies 1.78, without the weights' loads 1.20, without both 1.08;
-// products alone would take 0.9 ms at the 7.2 PFLOP/s that the instruction reaches, HBM
-// 1.1 ms.  Tried and slower: 256 rows by eight wavefronts (2.52 ms), 256 rows by four
+// What bounds it (16384 tokens, d 6144, I 2048, 512 experts, MXFP4 rows; gate/up 1.98
+// ms, 5.0 PFLOP/s; down 1.23 ms): getting the weights to the CUs at this depth, each of
+// them for 2.5 row tiles an expert.  Measured in copies with parts left out: gate/up
+// without the weights' loads 1.39 ms, without the rows' copies 1.78, without the
+// products 1.86, without the results 1.84; products alone would take 0.92 ms at the 7.2
+// PFLOP/s that the instruction reaches, HBM 1.1 ms.  Tried and slower, before the step
+// to whole lines (2.25 ms then): 256 rows by eight wavefronts (2.52 ms), 256 rows by four
 // with 512 registers and seven slabs ahead (4.18 ms: the sums alone fill the
 // accumulation registers), weights read non-temporally (2.70 ms: the other row tiles of
-// an expert find them in the L2).  With one row tile an expert (4096 tokens) it
-// reads its weights at 5.5 TB/s, in 1.25 ms.  MXFP8 rows are held by the 4.4 PFLOP/s
-// of 8-bit by 4-bit products.
+// an expert find them in the L2).  With one row tile an expert (2048 tokens) it reads
+// its weights at 6 TB/s, in 1.14 ms.  MXFP8 rows, with products of 4.4 PFLOP/s, in
+// many small tiles (4093 tokens, d 1024, I 512, 64 experts: gate/up 30 us, down 18) are
+// bound by a tile's start and end: 8 and 4 slabs between them, 640 tiles on 512 places.
 //
 // An expert's rows are spread evenly over its tiles in blocks of 16, and a tile's sums
 // are those of 2, 4, 6 or 8 blocks.  y goes out in bf16: it would be twice the bytes
@@ -647,7 +647,8 @@ __global__ __launch_bounds__(kThreads, 2) void mx4_wide_kernel(Mx4Params p) {
 #pragma unroll
             for (int j = 0; j < 2; ++j)
               w[j] = pk_bf16(acc[rb][2 * j][v], acc[rb][2 * j + 1][v]);
-            __builtin_amdgcn_raw_buffer_store_b64(w, y, at + (16 * rb + v) * p.ncols * 2, 0, 0);
+            // (non-temporal: down of 4093 tokens of the small layer 20.5 -> 18.3 us)
+            __builtin_amdgcn_raw_buffer_store_b64(w, y, at + (16 * rb + v) * p.ncols * 2, 0, 2);
           }
       }
     };
