@@ -47,7 +47,7 @@ enum { I4_SWIGLU = 0, I4_STORE = 1 };
 struct I4Params {
   int N, ncols, K;          // experts, output columns (I or d), reduction length (d or I)
   const int32_t* total;     // number of row tiles
-  const RowTile* tiles;        // one of each (as many as the grid has row tiles)
+  const RowTile* tiles;     // one of each (as many as the grid has row tiles)
   const bf16_t* A;          // x [T][d] gathered through perm, or h [P][I]
   uint32_t a_bytes;         // its size where 31 bits hold it
   const int32_t* perm;      // gate/up only
