@@ -1030,7 +1030,9 @@ zc_status check_adamw(const zc_adamw_cfg* c, bool device_step) {
 zc_status do_adamw(const zc_adamw_cfg* c, const zc_adamw_tensor* t, int64_t count,
                    const float* factor, const float* lr, const int64_t* step, hipStream_t s) {
   const bool b8 = c->state == ZC_STATE_8BIT;
-  const bool master = count > 0 && t[0].master != nullptr;
+  // (a tensor without elements may have no pointers)
+  const zc_adamw_tensor* some = std::find_if(t, t + count, [](const zc_adamw_tensor& x) { return x.n > 0; });
+  const bool master = some != t + count && some->master != nullptr;
   if (master && c->p_dtype != ZC_BF16)
     return fail(ZC_ERR_INVALID, "master weights go with bf16 weights");
   std::vector<zc::AdamwTensor> list(static_cast<size_t>(count));

@@ -143,7 +143,8 @@ __global__ __launch_bounds__(1024) void norm_finish_kernel(const double* __restr
   const double norm = sqrt(sum);
   const bool fine = norm <= 1.7976931348623157e308;
   out[0] = static_cast<float>(norm);
-  out[1] = !fine ? 0.f : norm > max_norm ? static_cast<float>(max_norm / norm) : 1.f;
+  // (0 stands for a norm that is not finite, not for a small quotient)
+  out[1] = !fine ? 0.f : norm > max_norm ? fmaxf(static_cast<float>(max_norm / norm), 0x1p-149f) : 1.f;
   if (step && fine) *step += 1;
 }
 

@@ -824,8 +824,8 @@ def zc_rmsnorm_backward(desc: NormDesc, dy, r, gamma, rstd, dr, dgamma, dres=Non
 
 # ------------------------------------------------------- the weights' step
 def _list_of(tensors, name, dtypes, like=None):
-    """tensors as a list of contiguous GPU tensors of one dtype (among dtypes) on
-    one GPU; like: another list, whose sizes they have."""
+    """tensors as a list of contiguous GPU tensors of one dtype (among dtypes);
+    like: the sizes they have."""
     out = list(tensors)
     if like is not None and len(out) != len(like):
         raise ValueError(f"{name}: {len(out)} tensors, expected {len(like)}")
@@ -840,7 +840,8 @@ def _list_of(tensors, name, dtypes, like=None):
             raise ValueError("tensors passed to the HIP library must be contiguous")
         if like is not None and t.numel() != like[i]:
             raise ValueError(f"{name}[{i}]: {t.numel()} elements, expected {like[i]}")
-    return out
+    # (of their own: a tensor that is given other memory later would take this from us)
+    return [t.detach() for t in out]
 
 
 def _one_gpu(where, tensors):
@@ -854,7 +855,8 @@ def _one_gpu(where, tensors):
 
 class TensorList:
     """The gradients that zc_grad_norm takes: contiguous GPU tensors of one dtype
-    (bf16 or fp32).  Holds the tensors; their contents may change between calls."""
+    (bf16 or fp32).  Holds the tensors' memory, whose contents may change between calls;
+    a tensor that is given other memory (t.data = ...) needs a new list."""
 
     def __init__(self, tensors):
         self.tensors = _list_of(tensors, "tensors", (torch.float32, torch.bfloat16))
@@ -907,7 +909,8 @@ class AdamWTensors:
     master, and a weight decay for all or for each.  States: fp32, or
     torch.float8_e4m3fn with m_scale and v_scale, fp32 [ceil(n / 128)] (v's codes
     are of its square root); see adamw_tensors for a set that starts at zero.
-    Holds the tensors; gradients may be written anew between steps."""
+    Holds the tensors' memory; gradients may be written anew between steps, and a
+    tensor that is given other memory (t.data = ...) needs a new set."""
 
     def __init__(self, params, grads, m, v, master=None, m_scale=None, v_scale=None,
                  weight_decay=0.0):

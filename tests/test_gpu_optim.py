@@ -82,6 +82,18 @@ def test_norm_of_nothing():
     assert int(step) == 2
 
 
+def test_norm_beyond_fp32():
+    # factor 0 is for norms that are not finite: this one is, in 64 bits
+    step = torch.tensor([0], device="cuda")
+    out = norm_of([torch.full((4,), 3e38, device="cuda")], 1e-9, step)
+    assert out[0] == float("inf") and 0 < float(out[1]) <= 2.0 ** -148 and int(step) == 1
+
+
+def test_norm_of_an_empty_list():
+    step = torch.tensor([0], device="cuda")
+    assert norm_of([], 1.0, step).tolist() == [0.0, 1.0] and int(step) == 1
+
+
 def test_norm_is_the_same_each_time():
     ts = [torch.randn(n, device="cuda") for n in (100, 5_000_011, 77)]
     first = norm_of(ts, 1.0)
@@ -302,6 +314,29 @@ def test_factor_zero_leaves_everything(dtype, gdtype, master, bits):
     zcmoe.zc_adamw_step(zcmoe.AdamW(rounding=1), c.t, 2, factor=torch.zeros(1, device="cuda"))
     after = c.bytes()
     assert all(torch.equal(before[k], after[k]) for k in before)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_adamw_first_tensor_empty(bits):
+    c = Case([0, 300, 0, 7], BF, BF, True, bits, seed=6)
+    cfg = zcmoe.AdamW(lr=1e-3)
+    zcmoe.zc_adamw_step(cfg, c.t, 2)
+    torch.cuda.synchronize()
+    c.check(cfg, 2)
+
+
+def test_lists_keep_their_memory():
+    # a tensor that is given other memory leaves the list with what it was made of
+    g, p = torch.full((1000,), 2.0, device="cuda"), torch.ones(1000, device="cuda")
+    grads, opt = zcmoe.TensorList([g]), zcmoe.adamw_tensors([p], [g])
+    before = p.detach()
+    g.data, p.data = torch.zeros(1000, device="cuda"), torch.zeros(1000, device="cuda")
+    torch.full((1000,), 7.0, device="cuda")  # takes no block that the lists still use
+    out = torch.zeros(2, device="cuda")
+    zcmoe.zc_grad_norm(grads, 1.0, out)
+    zcmoe.zc_adamw_step(zcmoe.AdamW(lr=0.5, eps=1e-12), opt, 1)
+    assert abs(float(out[0]) - 4000 ** 0.5) < 1e-4 and not bool(p.any())
+    assert bool((before - 0.5).abs().max() < 1e-5)
 
 
 @pytest.mark.parametrize("bits", [32, 8])

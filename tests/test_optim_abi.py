@@ -120,6 +120,9 @@ def test_adamw_refusals():
     t = tensors(2)
     t[1].master = ptr(60)
     assert adamw(t) == BAD
+    t = tensors(3, master=True)
+    t[0].n, t[0].master, t[2].master = 0, None, None  # (the first counts for neither)
+    assert adamw(t) == BAD
 
 
 def test_adamw_overlaps():
