@@ -361,18 +361,21 @@ __device__ __forceinline__ void lds_barrier() {
 // a time (16 bytes: 2.05 ms, 64: 2.00).
 //
 // What bounds it (16384 tokens, d 6144, I 2048, 512 experts, MXFP4 rows; gate/up 1.98
-// ms, 5.0 PFLOP/s; down 1.23 ms): getting the weights to the CUs at this depth, each of
-// them for 2.5 row tiles an expert.  Measured in copies with parts left out: gate/up
-// without the weights' loads 1.39 ms, without the rows' copies 1.78, without the
-// products 1.86, without the results 1.84; products alone would take 0.92 ms at the 7.2
-// PFLOP/s that the instruction reaches, HBM 1.1 ms.  Tried and slower, before the step
-// to whole lines (2.25 ms then): 256 rows by eight wavefronts (2.52 ms), 256 rows by four
-// with 512 registers and seven slabs ahead (4.18 ms: the sums alone fill the
-// accumulation registers), weights read non-temporally (2.70 ms: the other row tiles of
-// an expert find them in the L2).  With one row tile an expert (2048 tokens) it reads
-// its weights at 6 TB/s, in 1.14 ms.  MXFP8 rows, with products of 4.4 PFLOP/s, in
-// many small tiles (4093 tokens, d 1024, I 512, 64 experts: gate/up 30 us, down 18) are
-// bound by a tile's start and end: 8 and 4 slabs between them, 640 tiles on 512 places.
+// ms, 5.0 PFLOP/s; down 1.22 ms).  Products alone would take 0.92 ms at the 7.2 PFLOP/s
+// that the instruction reaches, HBM 1.1 ms.  In copies whose weights all came from the
+// first-level cache gate/up took 1.50 ms: products, the loads' way through the address
+// unit (busy 83% of the time) and the tiles' ends; from the L2s 1.65; the rest is HBM, each
+// weight for 2.5 row tiles an expert.  With parts left out: without the weights' loads
+// 1.39 ms, the rows' copies 1.78, the products 1.86, the results 1.84.  The same time:
+// weights two slabs ahead in place of three, a barrier once in four slabs.  Slower: row
+// tiles of an expert some slabs apart (2.03 to 2.4 ms), and, before the step to whole
+// lines (2.25 ms then), 256 rows by eight wavefronts (2.52 ms), 256 rows by four with
+// 512 registers and seven slabs ahead (4.18 ms: the sums alone fill the accumulation
+// registers), weights read non-temporally (2.70 ms: the other row tiles of an expert
+// find them in the L2).  With one row tile an expert (2048 tokens) it reads its weights
+// at 6 TB/s, in 1.14 ms.  MXFP8 rows, with products of 4.4 PFLOP/s, in many small tiles
+// (4093 tokens, d 1024, I 512, 64 experts: gate/up 30 us, down 18) are bound by a
+// tile's start and end: 8 and 4 slabs between them, 640 tiles on 512 places.
 //
 // An expert's rows are spread evenly over its tiles in blocks of 16, and a tile's sums
 // are those of 2, 4, 6 or 8 blocks.  y goes out in bf16: it would be twice the bytes
