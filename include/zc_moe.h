@@ -434,7 +434,8 @@ zc_status zc_mxfp4_quantize(int64_t R, int64_t C, int dtype, const void* src, ui
  * or in MXFP4 too (A4, at up to twice the rate, h and x in 4 bits), sums in fp32.  x
  * is quantized once for each token, h from its fp32 values; the experts' outputs y
  * are kept in fp32, in bf16 where T*K/(N+Z) is above 10 and d and I are multiples of
- * 512 (many rows: y's bytes count there); the router, gates, the
+ * 512 (many rows: y's bytes count there; x, h and a matrix of fewer than 2^31
+ * values each); the router, gates, the
  * combine and the zero-computation experts (which return the unquantized x) stay in
  * bf16/fp32.  Grids are not persistent: cu_limit does not size them.
  *  zc_moe_mxfp4_pack: natural codes [N][R][C/2] and scales [N][R][C/32]

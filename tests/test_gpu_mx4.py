@@ -270,6 +270,30 @@ def test_experts_ragged_tiles(rows, a):
 
 
 @pytest.mark.parametrize("a", [8, 4])
+def test_experts_past_31_bits(a):
+    # h of more than 2^31 bytes in 8 bits: the last tokens' rows lie behind that
+    T, n = 70000, 24
+    desc, x, w, route, packed = make(T, 512, 2, 0, 32768, 1, a)
+    assert T * 32768 > 1 << 31
+    out = torch.full((T, 512), float("nan"), dtype=BF, device="cuda")
+    zcmoe.zc_moe_experts(desc, x.cuda(), route, *packed, out)
+    torch.cuda.synchronize()
+    assert not bool(torch.isnan(out).any())
+    tail = dataclasses.replace(desc, T=n)
+    for part in (slice(0, n), slice(T - n, T)):
+        r = zcmoe.RouteBuffers(tail, "cpu")
+        r.topk_idx, r.topk_gate = route.topk_idx[part], route.topk_gate[part]
+        ref, tol = reference(tail, x[part], w, r, a)
+        err = np.abs(out[part].cpu().double().numpy() - ref)
+        assert (err <= tol * (1 + HB) + HB * np.abs(ref) + 2.0 ** -133).all()
+
+
+def test_no_rows_to_quantize():
+    codes, scales = zcmoe.zc_mxfp4_quantize(torch.empty((0, 64), dtype=BF, device="cuda"))
+    assert codes.shape == (0, 32) and scales.shape == (0, 2)
+
+
+@pytest.mark.parametrize("a", [8, 4])
 def test_experts_left_without_rows(a):
     T, N = 600, 24
     desc, x, w, route, packed = make(T, 512, N, 4, 512, 3, a)
