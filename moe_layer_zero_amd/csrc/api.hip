@@ -310,7 +310,7 @@ Saved carve_saved(char* p, const zc_moe_desc* d) {
 // MXFP8 and MXFP4 layers add x' (codes and scales); h' (codes and scales)
 // fits in the h piece.  Layers that list their own row tiles add the list.
 zc::Mx4Plan mxfp4_plan(const zc_moe_desc* d) {
-  return zc::mx4_plan(d->T, d->T * d->K, d->N + d->Z, d->d, d->I);
+  return zc::mx4_plan(mxfp4_a4(d), d->T, d->T * d->K, d->N + d->Z, d->d, d->I);
 }
 bool fp32_y(const zc_moe_desc* d) {
   return int4_group(d) || (mxfp4(d) && !mxfp4_plan(d).wide);

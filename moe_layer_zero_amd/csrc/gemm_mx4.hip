@@ -351,18 +351,20 @@ __device__ __forceinline__ void lds_barrier() {
   asm volatile("" ::: "memory");
 }
 
-// 128 rows by 256 weight columns a workgroup (gate/up: 128 gate and the matching up
+// TM rows by 256 weight columns a workgroup (gate/up: 128 gate and the matching up
 // columns), 64 columns a wavefront: each weight goes from memory to the registers of
 // the one wavefront that multiplies with it, the rows through LDS to all four.  Two
-// workgroups a CU.  While a slab of 128 steps is multiplied, three slabs of rows are
-// under way, copied straight into a ring of four LDS slots, and two or three of weights
-// in registers.  A slot holds 128 bytes of a row, a cache line: of MXFP4 rows two slabs
-// (one a slot, half lines: gate/up 2.25 ms, two 2.07), and rows' scales come 64 bytes at
-// a time (16 bytes: 2.05 ms, 64: 2.00).
+// workgroups a CU.  While a slab of 128 steps is multiplied, two or three slabs of rows
+// are under way, copied straight into a ring of three or four LDS slots, and one to three
+// of weights in registers.  A slot holds 128 bytes of a row, a cache line: of MXFP4
+// rows two slabs (one a slot, half lines: gate/up 2.25 ms, two 2.07), and rows' scales
+// come 64 bytes at a time (16 bytes: 2.05 ms, 64: 2.00).  Tiles of 160 rows leave room for
+// two slabs of weights in place of four, 2% of the time, and read them for fewer row
+// tiles.
 //
-// What bounds it (16384 tokens, d 6144, I 2048, 512 experts, MXFP4 rows; gate/up 1.98
-// ms, 5.0 PFLOP/s; down 1.22 ms).  Products alone would take 0.92 ms at the 7.2 PFLOP/s
-// that the instruction reaches, HBM 1.1 ms.  In copies whose weights all came from the
+// What bounds it (16384 tokens, d 6144, I 2048, 512 experts, MXFP4 rows; gate/up 1.89
+// ms, 5.2 PFLOP/s; down 1.18 ms).  Products alone would take 0.92 ms at the 7.2 PFLOP/s
+// that the instruction reaches, HBM 1.1 ms.  With tiles of 128 rows (1.98 ms), in copies whose weights all came from the
 // first-level cache gate/up took 1.50 ms: products, the loads' way through the address
 // unit (busy 83% of the time) and the tiles' ends; from the L2s 1.65; the rest is HBM, each
 // weight for 2.5 row tiles an expert.  With parts left out: without the weights' loads
@@ -378,31 +380,34 @@ __device__ __forceinline__ void lds_barrier() {
 // tile's start and end: 8 and 4 slabs between them, 640 tiles on 512 places.
 //
 // An expert's rows are spread evenly over its tiles in blocks of 16, and a tile's sums
-// are those of 2, 4, 6 or 8 blocks.  y goes out in bf16: it would be twice the bytes
+// are those of 2, 4, 6, 8 or 10 blocks.  y goes out in bf16: it would be twice the bytes
 // in fp32 (1.6 of 10.7 GB here), and costs 2^-9 of each of K terms.
-template <int EPI, bool A4>
+template <int EPI, bool A4, int TM>
 __global__ __launch_bounds__(kThreads, 2) void mx4_wide_kernel(Mx4Params p) {
-  constexpr int TM = 128;                      // rows of a tile at most
   constexpr int CB = 128;                      // bytes of a row in a ring slot: a cache line
   constexpr int SPS = A4 ? 2 : 1;              // slabs of 128 steps in a slot
+  constexpr int SLOTS = TM > 128 ? 3 : 4;
   constexpr int SLOT = TM * CB;                // bytes of a slot
   constexpr int CP = SLOT / 1024 / kWaves;     // copies a wavefront and slot
-  constexpr int CS = CP / SPS;                 // and slab
   constexpr int RPC = 1024 / CB;               // rows of a copy
   constexpr int SC = TM * 64;                  // bytes of the rows' scales of 2048 steps
+  constexpr int SCP = (SC / 1024 + kWaves - 1) / kWaves;  // copies a wavefront of them
   constexpr int OUT = EPI == MX_SWIGLU ? 128 : 256;
-  constexpr int NBUF = A4 ? 4 : 2;             // slabs of weights in registers
   constexpr int G = kGroup<EPI>;
   constexpr int CSC = 4 / G;                   // loads of the columns' scales of 512 steps
   constexpr int NSC = CSC + 1;                 // and with them of the rows'
-  // Loads that may be in flight when slab `slot` of four is needed.  NBUF 4: rows and
-  // weights of the two slabs after it, and the next scales if they went out since.  NBUF
-  // 2: the rows of the slab after next and the weights of the next (issued at the end
-  // of the slab before this one), the scales with the slab before this one.
+  // Copies of rows that go out in a slab (MXFP4: a slot's in two slabs).
+  constexpr int CEVEN = (CP + SPS - 1) / SPS, CODD = A4 ? CP / 2 : CP;
+  // Slabs of weights in registers: four where the sums and rows leave room for them, their
+  // loads between the multiplications; else two, loaded at a slab's end.
+  constexpr int NBUF = A4 && TM == 128 ? 4 : 2;
+  // Loads that may be in flight when slab `slot` of four is needed: those of the two
+  // slabs before it, or of the one before it (rows are older).
   constexpr auto wait_of = [](int slot) constexpr {
-    return NBUF == 4 ? 2 * (CS + 4) + (slot == 1 || slot == 2 ? NSC : 0) : CS + 4 + (slot == 1 ? NSC : 0);
+    return NBUF == 4 ? CEVEN + CODD + 8 + (slot == 1 || slot == 2 ? NSC : 0)
+                     : (slot % 2 ? CEVEN : CODD) + 4 + (slot == 1 ? NSC : 0);
   };
-  __shared__ __align__(16) uint8_t ring[4 * SLOT + 2 * SC];
+  __shared__ __align__(16) uint8_t ring[SLOTS * SLOT + 2 * SC];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int nkb = p.K / kStep, nq = nkb / 4;
   const int NT = p.ncols / OUT;
@@ -426,12 +431,15 @@ __global__ __launch_bounds__(kThreads, 2) void mx4_wide_kernel(Mx4Params p) {
     const int m0 = tile.seg0 + 16 * blo;
     const int mcount = min(tile.seg0 + 16 * bhi, tile.seg1) - m0;
 
+    // the i-th block of 16 rows whose scales this wavefront copies (where there are too
+    // few blocks for all wavefronts, the last ones again)
+    auto scale_rows = [&](int i) { return wave + kWaves * i < TM / 16 ? wave + kWaves * i : wave + kWaves * (i - 1); };
     // Rows that this lane copies, and those whose scales: first the slots, which are
     // under way while the first weights are asked for.
-    int slot_of[CP + 2];
+    int slot_of[CP + SCP];
 #pragma unroll
-    for (int i = 0; i < CP + 2; ++i) {
-      const int r = i < CP ? (CP * wave + i) * RPC + lane / (CB / 16) : (2 * wave + i - CP) * 16 + (lane >> 2);
+    for (int i = 0; i < CP + SCP; ++i) {
+      const int r = i < CP ? (CP * wave + i) * RPC + lane / (CB / 16) : 16 * scale_rows(i - CP) + (lane >> 2);
       slot_of[i] = m0 + min(r, mcount - 1);
       if (EPI == MX_SWIGLU) slot_of[i] = p.perm[slot_of[i]];
     }
@@ -456,7 +464,7 @@ __global__ __launch_bounds__(kThreads, 2) void mx4_wide_kernel(Mx4Params p) {
       // (what the variants have in common would otherwise move in front of the switch,
       // and the loops' registers with it)
       asm volatile("; %0 blocks of rows" ::"n"(NRB));
-      uint32_t src[CP], ssrc[2];
+      uint32_t src[CP], ssrc[SCP];
       i32x4_t b[NBUF][4];  // [slab % NBUF][column block]
       int sb[4], sbn[4];   // scales of these four slabs, and of the next four
       // one load each: the i-th copy of a slot's rows, `at` slots' worth into the row;
@@ -471,8 +479,8 @@ __global__ __launch_bounds__(kThreads, 2) void mx4_wide_kernel(Mx4Params p) {
                                                            code_lane, ((grp * nkb + kb) * G + nb % G) * 1024, 0));
       };
       auto issue_row_scale = [&](int at, int i) {
-        copy_to_lds16(rscale, (lds_void*)(ring + 4 * SLOT + (at & 1) * SC + (2 * wave + i) * 1024), ssrc[i],
-                      sfirst(at) * 16);
+        copy_to_lds16(rscale, (lds_void*)(ring + SLOTS * SLOT + (at & 1) * SC + scale_rows(i) * 1024),
+                      i == 0 ? ssrc[0] : i == 1 ? ssrc[1] : ssrc[SCP - 1], sfirst(at) * 16);
       };
       auto issue_scale = [&](int quad, int* sc, int i) {
         const int at = (grp * nq + quad) * G * 256;
@@ -494,12 +502,15 @@ __global__ __launch_bounds__(kThreads, 2) void mx4_wide_kernel(Mx4Params p) {
         for (int nb = 0; nb < 4; ++nb) acc[rb][nb] = f32x4_t{0.f, 0.f, 0.f, 0.f};
       // where this lane's row of a block lies in a slot: chunk lq, and 4 + lq (MXFP8: of
       // the same slab, MXFP4: of the slot's second one)
-      int frag_at = l16 * CB + 16 * (lq ^ (l16 >> 1));
+      const int frag_at = l16 * CB + 16 * (lq ^ (l16 >> 1));
+      // MXFP4: the slot of these four slabs' first half
+      int first = 0;
+      auto after = [](int s, int n) { return s + n < SLOTS ? s + n : s + n - SLOTS; };
       // and its scale of a slab
-      int scale_at = 4 * SLOT + l16 * 64 + 16 * (l16 >> 2) + (A4 ? lq : 2 * (lq & 1) + (lq >> 1));
+      int scale_at = SLOTS * SLOT + l16 * 64 + 16 * (l16 >> 2) + (A4 ? lq : 2 * (lq & 1) + (lq >> 1));
 
       // Fragments are read AHEAD of their multiplications (of 64 or 128 cycles).
-      constexpr int AHEAD = A4 ? (3 < NRB ? 3 : NRB) : 1;
+      constexpr int AHEAD = !A4 ? 1 : NRB > 8 ? 2 : 3 < NRB ? 3 : NRB;
       const int last = nkb - 1;
       // One slab: wait for it, meet, multiply, and between the multiplications issue,
       // one by one, the loads of rows three slabs ahead or more, of weights and (with the
@@ -508,16 +519,17 @@ __global__ __launch_bounds__(kThreads, 2) void mx4_wide_kernel(Mx4Params p) {
       // last slab is loaded again, so that the number of loads in flight is known.
       auto slab = [&](int kb, int q4, auto slot_c) {
         constexpr int slot = decltype(slot_c)::value;
-        constexpr int NL = CS + (NBUF == 4 ? 4 : 0) + (slot == 0 ? NSC : 0);
+        constexpr int NR = slot % 2 ? CODD : CEVEN, NW = NR + (NBUF == 4 ? 4 : 0);  // rows, weights
+        constexpr int NL = NW + (slot == 0 ? NSC : 0);
+        const uint8_t* at = ring + (A4 ? after(first, slot / 2) * SLOT : slot * SLOT);
         __builtin_amdgcn_s_waitcnt(vmcnt_imm(wait_of(slot)));
         lds_barrier();
         i32x8_t a[AHEAD + 1] = {};
         int sa[AHEAD + 1];
         auto frag = [&](int rb) {
           i32x8_t& f = a[rb % (AHEAD + 1)];
-          const uint8_t* block = ring + slot / SPS * SLOT + rb * 16 * CB;
-          f.lo = *reinterpret_cast<const i32x4_t*>(block + (frag_at ^ (slot % SPS * 64)));
-          if constexpr (!A4) f.hi = *reinterpret_cast<const i32x4_t*>(block + (frag_at ^ 64));
+          f.lo = *reinterpret_cast<const i32x4_t*>(at + (frag_at ^ (slot % SPS * 64)) + rb * 16 * CB);
+          if constexpr (!A4) f.hi = *reinterpret_cast<const i32x4_t*>(at + (frag_at ^ 64) + rb * 16 * CB);
           sa[rb % (AHEAD + 1)] = ring[rb * 1024 + slot * 4 + scale_at];
         };
 #pragma unroll
@@ -527,16 +539,17 @@ __global__ __launch_bounds__(kThreads, 2) void mx4_wide_kernel(Mx4Params p) {
           if (rb + AHEAD < NRB) frag(rb + AHEAD);
 #pragma unroll
           for (int i = NL * rb / NRB; i < NL * (rb + 1) / NRB; ++i) {
-            if (i < CS && A4)
-              issue_row(min(kb / 2 + 2, last / 2), slot / 2 + 2 * ((q4 + 1) & 1), slot % 2 * CS + i);
-            else if (i < CS)
+            if (i < NR && A4)
+              issue_row(min(2 * q4 + slot / 2 + 2, last / 2), after(first, 2 + slot / 2),
+                        slot % 2 * CEVEN + i);
+            else if (i < NR)
               issue_row(min(kb + 3, last), (slot + 3) & 3, i);
-            else if (NBUF == 4 && i < CS + 4)
-              issue_weight(min(kb + 3, last), (slot + 3) & 3, i - CS);
+            else if (i < NW)
+              issue_weight(min(kb + 3, last), (slot + 3) & 3, i - NR);
             else if (i < NL - 1)
-              issue_scale(min(q4 + 1, nq - 1), sbn, i - CS - (NBUF == 4 ? 4 : 0));
-            else  // (each twice in the four quarters: so the number of loads is known)
-              issue_row_scale(q4 / 4 + 1, q4 & 1);
+              issue_scale(min(q4 + 1, nq - 1), sbn, i - NW);
+            else  // (some of them twice in the four quarters: so the number of loads is known)
+              issue_row_scale(q4 / 4 + 1, min(q4 & 3, SCP - 1));
           }
 #pragma unroll
           for (int nb = 0; nb < 4; ++nb) {
@@ -579,15 +592,15 @@ __global__ __launch_bounds__(kThreads, 2) void mx4_wide_kernel(Mx4Params p) {
       // LDS banks).
       const int schunk = (lane & 3) ^ (lane >> 4);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int r = (2 * wave + i) * 16 + (lane >> 2);
+      for (int i = 0; i < SCP; ++i) {
+        const int r = 16 * scale_rows(i) + (lane >> 2);
         const uint32_t tok = EPI == MX_SWIGLU ? __umulhi(2 * slot_of[CP + i], p.kdiv_inv) : slot_of[CP + i];
         ssrc[i] = tok * static_cast<uint32_t>(p.K / 32) + 16 * schunk;
-        ssrc[i] = (r < mcount) & (schunk < nq) ? ssrc[i] : p.as_bytes;
+        ssrc[i] = r < mcount && schunk < nq ? ssrc[i] : p.as_bytes;
       }
       lds_barrier();  // the ring is free: the previous tile's reads are done
 #pragma unroll
-      for (int i = 0; i < 2; ++i) issue_row_scale(0, i);
+      for (int i = 0; i < SCP; ++i) issue_row_scale(0, i);
 #pragma unroll
       for (int at = 0; at < (A4 ? 2 : 3); ++at) {
 #pragma unroll
@@ -601,8 +614,9 @@ __global__ __launch_bounds__(kThreads, 2) void mx4_wide_kernel(Mx4Params p) {
         slab(4 * q4 + 1, q4, C1{});
         slab(4 * q4 + 2, q4, C2{});
         slab(4 * q4 + 3, q4, C3{});
-        scale_at ^= 16 * ((q4 - sfirst(q4 / 4)) ^ (q4 + 1 - sfirst((q4 + 1) / 4))) ^ ((q4 & 3) == 3 ? SC : 0);
-        if (A4) frag_at ^= 2 * SLOT;
+        scale_at ^= 16 * ((q4 - sfirst(q4 / 4)) ^ (q4 + 1 - sfirst((q4 + 1) / 4)));
+        scale_at += (q4 & 3) < 3 ? 0 : q4 & 4 ? -SC : SC;
+        first = after(first, 2);
 #pragma unroll
         for (int nb = 0; nb < 4; ++nb) sb[nb] = sbn[nb];
       }
@@ -659,7 +673,12 @@ __global__ __launch_bounds__(kThreads, 2) void mx4_wide_kernel(Mx4Params p) {
       case 1: run(std::integral_constant<int, 2>{}); break;
       case 2: run(std::integral_constant<int, 4>{}); break;
       case 3: run(std::integral_constant<int, 6>{}); break;
-      default: run(std::integral_constant<int, 8>{}); break;
+      case 4:
+        if constexpr (TM > 128) {
+          run(std::integral_constant<int, 8>{});
+          break;
+        }
+      default: run(std::integral_constant<int, TM / 16>{}); break;
     }
   }
 }
@@ -669,10 +688,12 @@ hipError_t launch_mx4_wide(bool a4, Mx4Params p, int64_t rows, int tm, hipStream
   const int OUT = EPI == MX_SWIGLU ? 128 : 256;
   deal_tiles(max_row_tiles(rows, p.N, tm) * (p.ncols / OUT), &p.per_xcd, &p.log_run);
   const dim3 grid(grid_of(p.per_xcd * 8)), block(kThreads);
-  if (a4)
-    hipLaunchKernelGGL((mx4_wide_kernel<EPI, true>), grid, block, 0, s, p);
+  if (!a4)
+    hipLaunchKernelGGL((mx4_wide_kernel<EPI, false, 128>), grid, block, 0, s, p);
+  else if (tm == 128)
+    hipLaunchKernelGGL((mx4_wide_kernel<EPI, true, 128>), grid, block, 0, s, p);
   else
-    hipLaunchKernelGGL((mx4_wide_kernel<EPI, false>), grid, block, 0, s, p);
+    hipLaunchKernelGGL((mx4_wide_kernel<EPI, true, 160>), grid, block, 0, s, p);
   return hipGetLastError();
 }
 
@@ -796,13 +817,17 @@ __global__ __launch_bounds__(kMaxExperts) void mx4_start_kernel(
 //     20 rows 3413 / 2287 / 1878
 //   d 1024, I 512, 64 experts:    8 rows 26.2 / 29.8 / 28.6, 12 rows 28.5 / 31.4 / 28.7,
 //     20 rows 34.7 / 36.1 / 29.7, 64 rows 58.4 / 60.1 / 33.6
+// With MXFP4 rows its tiles have up to 160 rows from 110 rows an expert on, where that
+// saves tiles (the large layer's gate/up, tiles of 128 / of 160): 101 rows 1258 / 1274, 128
+// rows 1452 / 1334, 187 rows (two tiles either way) 1685 / 1760, 256 rows 2007 / 1906, 375
+// rows 2587 / 2605; the small one's at 128 rows 18.6 / 15.8, 255 rows 24.5 / 22.2.
 // That kernel takes whole groups of 512 steps, and byte offsets of 31 bits into x, h and
 // a matrix: other layers have tiles of 16, 32 or 64.
-Mx4Plan mx4_plan(int64_t Tn, int64_t rows, int64_t E, int64_t d, int64_t I) {
+Mx4Plan mx4_plan(bool a4, int64_t Tn, int64_t rows, int64_t E, int64_t d, int64_t I) {
   const int64_t avg = rows / E, limit = int64_t(1) << 31;
   if (avg <= 10) return {16, false};
   if (d % 512 == 0 && I % 512 == 0 && Tn * d < limit && rows * I < limit && d * I < limit)
-    return {128, true};
+    return {a4 && avg >= 110 ? 160 : 128, true};
   return {avg <= 13 ? 16 : avg <= 20 ? 32 : 64, false};
 }
 

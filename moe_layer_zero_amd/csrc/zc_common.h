@@ -434,7 +434,7 @@ struct Mx4Plan {
   int tm;     // rows of a tile
   bool wide;  // the kernel of many rows
 };
-Mx4Plan mx4_plan(int64_t Tn, int64_t rows, int64_t E, int64_t d, int64_t I);
+Mx4Plan mx4_plan(bool a4, int64_t Tn, int64_t rows, int64_t E, int64_t d, int64_t I);
 // The row tiles, and x [T][d] as MXFP4 or MXFP8 rows, in one launch.
 hipError_t launch_mx4_start(bool a4, const int32_t* offsets, int N, int tm, void* tiles,
                             const bf16_t* x, int64_t Tn, int d, uint8_t* xq, uint8_t* xs,

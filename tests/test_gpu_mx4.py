@@ -253,6 +253,8 @@ CASES = [
     (150, 2560, 2, 1, 512, 2),    # rows' scales in parts of 2048 steps, the last one short
     (90, 512, 1, 1, 4608, 1),
     (130, 2048, 2, 0, 3584, 1),
+    (340, 2560, 2, 1, 512, 2),    # tiles of 160 MXFP4 rows
+    (230, 512, 1, 1, 4608, 1),
 ]
 
 
@@ -267,6 +269,12 @@ def test_experts(case, a):
 def test_experts_ragged_tiles(rows, a):
     # one expert takes everything: tiles that end inside a block of rows
     check(*make(rows, 512, 3, 1, 512, 1, a, seed=rows, skew=1), a)
+
+
+@pytest.mark.parametrize("a", [8, 4])
+@pytest.mark.parametrize("rows", [109, 110, 127, 129, 144, 145, 159, 160, 161, 177, 319, 320, 321, 500])
+def test_experts_ragged_tiles_of_many_rows(rows, a):
+    check(*make(rows, 512, 1, 0, 1024, 1, a, seed=rows), a)
 
 
 @pytest.mark.parametrize("a", [8, 4])
