@@ -149,7 +149,8 @@ __device__ __forceinline__ uint32_t pk_bf16(float a, float b) {
 // split the reduction and add their sums through LDS in order, so few rows still
 // give many workgroups with many loads in flight, and there is no barrier in the loop.
 // Bound by HBM: 256 tokens (d 6144, I 2048, 512 experts, MXFP8 rows) read 10.1 GB in 1.58
-// ms, 6.4 TB/s; one token 105 MB of gate and up in 19.5 us, 5.4 TB/s.  y is fp32.
+// ms, 6.4 TB/s; one token 105 MB of gate and up in 19.5 us, 5.4 TB/s (three or four slabs
+// in registers in place of two: the same, both).  y is fp32.
 template <int EPI, int RB, int NB, bool A4>
 __global__ __launch_bounds__(kThreads, 2) void mx4_kernel(Mx4Params p) {
   constexpr int OUT = (EPI == MX_SWIGLU ? NB / 2 : NB) * 16;  // output columns a workgroup
