@@ -306,22 +306,31 @@ Saved carve_saved(char* p, const zc_moe_desc* d) {
 }
 
 // Forward scratch: routing scratch, h in the layer dtype (operand of the
-// down GEMM) and y when no saved buffer takes it.
-// MXFP8 and MXFP4 layers add x' (codes and scales); h' (codes and scales)
-// fits in the h piece.  Layers that list their own row tiles add the list.
+// down GEMM) or its codes and scales, and y when no saved buffer takes it.
+// MXFP8 and MXFP4 layers add x' (codes and scales).  Layers that list their own
+// row tiles add the list.
 zc::Mx4Plan mxfp4_plan(const zc_moe_desc* d) {
   return zc::mx4_plan(mxfp4_a4(d), d->T, d->T * d->K, d->N + d->Z, d->d, d->I);
 }
 bool fp32_y(const zc_moe_desc* d) {
   return int4_group(d) || (mxfp4(d) && !mxfp4_plan(d).wide);
 }
-int64_t xq_bytes(const zc_moe_desc* d) { return a256(mxfp4_a4(d) ? d->T * d->d / 2 : d->T * d->d); }
+bool mx_rows(const zc_moe_desc* d) { return d->weight_layout == ZC_WEIGHTS_MXFP8 || mxfp4(d); }
+// n values of x or h as codes; their scales, n / 32 bytes, lie behind them.
+int64_t mx_code_bytes(const zc_moe_desc* d, int64_t n) { return a256(mxfp4_a4(d) ? n / 2 : n); }
+int64_t mx_bytes(const zc_moe_desc* d, int64_t n) { return mx_code_bytes(d, n) + a256(n / 32); }
+// (codes and scales take no more than h in bf16, but for the 128 values of one row of
+// I = 128: 256 bytes each)
+int64_t h_bytes(const zc_moe_desc* d) {
+  const int64_t n = d->T * d->K * d->I, b = a256(n * esize(d));
+  return mx_rows(d) ? std::max(b, mx_bytes(d, n)) : b;
+}
 int64_t fwd_ws_bytes(const zc_moe_desc* d) {
-  const int64_t rows = d->T * d->K, es = esize(d);
+  const int64_t rows = d->T * d->K;
   // y is fp32 with 4-bit weights (but for many rows of MXFP4 ones)
-  const int64_t ys = fp32_y(d) ? 4 : es;
-  int64_t b = route_ws_bytes(d) + a256(rows * d->I * es) + a256(rows * d->d * ys);
-  if (d->weight_layout == ZC_WEIGHTS_MXFP8 || mxfp4(d)) b += xq_bytes(d) + a256(d->T * d->d / 32);
+  const int64_t ys = fp32_y(d) ? 4 : esize(d);
+  int64_t b = route_ws_bytes(d) + h_bytes(d) + a256(rows * d->d * ys);
+  if (mx_rows(d)) b += mx_bytes(d, d->T * d->d);
   if (own_tiles(d)) b += a256(zc::row_tiles_bytes(rows, d->N));
   return b;
 }
@@ -527,7 +536,7 @@ zc_status do_experts(const zc_moe_desc* d, const T* x, const T* wg, const T* wu,
   const int64_t rows = d->T * d->K;
   char* p = ws + route_ws_bytes(d);
   T* h = reinterpret_cast<T*>(p);
-  T* y = reinterpret_cast<T*>(p + a256(rows * d->I * esize(d)));
+  T* y = reinterpret_cast<T*>(p + h_bytes(d));
   float *sa = nullptr, *su = nullptr, *sh = nullptr;
   if (saved) {
     Saved sv = carve_saved(static_cast<char*>(saved), d);
@@ -541,11 +550,10 @@ zc_status do_experts(const zc_moe_desc* d, const T* x, const T* wg, const T* wu,
     if (d->weight_layout == ZC_WEIGHTS_MXFP8) {
       // MXFP8 inference: x quantized once, h quantized in the gate/up
       // epilogue (validated: bf16, no saved buffer)
-      uint8_t* xq = reinterpret_cast<uint8_t*>(ws + fwd_ws_bytes(d) - a256(d->T * d->d) -
-                                               a256(d->T * d->d / 32));
-      uint8_t* xs = xq + a256(d->T * d->d);
+      uint8_t* xq = reinterpret_cast<uint8_t*>(ws + fwd_ws_bytes(d) - mx_bytes(d, d->T * d->d));
+      uint8_t* xs = xq + mx_code_bytes(d, d->T * d->d);
       uint8_t* hq = reinterpret_cast<uint8_t*>(h);
-      uint8_t* hs = hq + a256(rows * d->I);
+      uint8_t* hs = hq + mx_code_bytes(d, rows * d->I);
       if (!mxq)
         ZC_LAUNCH(ZC_PH_QUANTIZE,
                   zc::launch_mxq_rows(reinterpret_cast<const bf16_t*>(x), d->T, dd, xq, xs, s),
@@ -585,10 +593,10 @@ zc_status do_experts(const zc_moe_desc* d, const T* x, const T* wg, const T* wu,
       // MXFP4 weights (validated: bf16, no saved buffer)
       const bool a4 = mxfp4_a4(d);
       char* tiles = ws + fwd_ws_bytes(d) - a256(zc::row_tiles_bytes(rows, N));
-      uint8_t* xs = reinterpret_cast<uint8_t*>(tiles - a256(d->T * d->d / 32));
-      uint8_t* xq = xs - xq_bytes(d);
+      uint8_t* xq = reinterpret_cast<uint8_t*>(tiles - mx_bytes(d, d->T * d->d));
+      uint8_t* xs = xq + mx_code_bytes(d, d->T * d->d);
       uint8_t* hq = reinterpret_cast<uint8_t*>(h);
-      uint8_t* hs = hq + a256(a4 ? rows * d->I / 2 : rows * d->I);
+      uint8_t* hs = hq + mx_code_bytes(d, rows * d->I);
       const zc::Mx4Plan plan = mxfp4_plan(d);
       if (mxq)
         ZC_LAUNCH(ZC_PH_TILE_OFFSETS, zc::launch_row_tiles(r->offsets, N, plan.tm, tiles, s),
