@@ -23,6 +23,7 @@
 // code blocks], E8M0: a lane's scales of 512 steps and a group in one load.  A group's columns
 // are dealt to its blocks in turn, so that a lane ends with G neighbours: two 4-bit
 // codes of h, a byte; 8 or 16 bytes of y.
+#include "row_split.h"
 #include "zc_common.h"
 
 namespace zc {
@@ -428,7 +429,7 @@ __global__ __launch_bounds__(kThreads, 2) void mx4_wide_kernel(Mx4Params p) {
     const int nt = q / tile.mte, mt = q % tile.mte;
     // the expert's blocks of 16 rows spread evenly over its row tiles
     const int nbe = (tile.seg1 - tile.seg0 + 15) >> 4;
-    const int blo = nbe * mt / tile.mte, bhi = nbe * (mt + 1) / tile.mte;
+    const int blo = first_block(nbe, mt, tile.mte), bhi = first_block(nbe, mt + 1, tile.mte);
     const int m0 = tile.seg0 + 16 * blo;
     const int mcount = min(tile.seg0 + 16 * bhi, tile.seg1) - m0;
 
