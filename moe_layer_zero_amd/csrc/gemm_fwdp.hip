@@ -40,6 +40,7 @@
 // the same L2, and an XCD's workgroups claim its tiles from a counter.
 #include <type_traits>
 
+#include "row_split.h"
 #include "zc_common.h"
 
 namespace zc {
@@ -209,7 +210,7 @@ __global__ __launch_bounds__(NTHR, 1) void fwdp_kernel(PParams p) {
     // same work, stream the panel at the same pace and find it in L2
     const int seg0 = ld_scalar(p.offsets + e), seg1 = ld_scalar(p.offsets + e + 1);
     const int nbe = (seg1 - seg0 + 31) >> 5;
-    const int blo = nbe * mt / mte, bhi = nbe * (mt + 1) / mte;
+    const int blo = first_block32(nbe, mt, mte), bhi = first_block32(nbe, mt + 1, mte);
     const int m0 = seg0 + 32 * blo;
     const int mcount = min(seg0 + 32 * bhi, seg1) - m0;
     const int n0 = nt * OUTN;
@@ -526,7 +527,7 @@ __global__ __launch_bounds__(NTHR8, 1) void down8_kernel(PParams p) {
     const int nt = rr / gsz;
     const int seg0 = ld_scalar(p.offsets + e), seg1 = ld_scalar(p.offsets + e + 1);
     const int nbe = (seg1 - seg0 + 31) >> 5;
-    const int blo = nbe * mt / mte, bhi = nbe * (mt + 1) / mte;
+    const int blo = first_block32(nbe, mt, mte), bhi = first_block32(nbe, mt + 1, mte);
     t.m0 = seg0 + 32 * blo;
     t.mcount = min(seg0 + 32 * bhi, seg1) - t.m0;
     t.n0 = nt * OUTN;

@@ -39,6 +39,7 @@
 //    weight set is the N experts' codes followed by their scales.
 #include <type_traits>
 
+#include "row_split.h"
 #include "zc_common.h"
 
 namespace zc {
@@ -183,7 +184,7 @@ __global__ __launch_bounds__(NTHR, 1) void fwdq_kernel(QParams p) {
     // same work, stream the panel at the same pace and find it in L2
     const int seg0 = ld_scalar(p.offsets + e), seg1 = ld_scalar(p.offsets + e + 1);
     const int nbe = (seg1 - seg0 + 31) >> 5;
-    const int blo = nbe * mt / mte, bhi = nbe * (mt + 1) / mte;
+    const int blo = first_block32(nbe, mt, mte), bhi = first_block32(nbe, mt + 1, mte);
     const int m0 = seg0 + 32 * blo;
     const int mcount = min(seg0 + 32 * bhi, seg1) - m0;
     const int n0 = nt * OUTN;
@@ -577,7 +578,7 @@ __global__ __launch_bounds__(NTHR, 1) void downq_kernel(QParams p) {
     // the expert's 32-row blocks spread evenly over its row tiles
     const int seg0 = ld_scalar(p.offsets + e), seg1 = ld_scalar(p.offsets + e + 1);
     const int nbe = (seg1 - seg0 + 31) >> 5;
-    const int blo = nbe * mt / mte, bhi = nbe * (mt + 1) / mte;
+    const int blo = first_block32(nbe, mt, mte), bhi = first_block32(nbe, mt + 1, mte);
     t.m0 = seg0 + 32 * blo;
     t.mcount = min(seg0 + 32 * bhi, seg1) - t.m0;
     t.n0 = nt * OUTN;

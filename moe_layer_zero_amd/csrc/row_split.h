@@ -14,4 +14,11 @@ constexpr int first_block(int blocks, int mt, int tiles) {
   return each * mt + (blocks - each * tiles) * mt / tiles;
 }
 
+// The same in one step, for products of at most 2^31 (fewer than 2^22 rows in blocks
+// of 32 and tiles of 256: 2^17 * 2^14, 31 bits passed by one).
+constexpr int first_block32(int blocks, int mt, int tiles) {
+  return static_cast<int>(static_cast<unsigned>(blocks) * static_cast<unsigned>(mt) /
+                          static_cast<unsigned>(tiles));
+}
+
 }  // namespace zc

@@ -13,6 +13,7 @@ ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 SRC = """
 #include "row_split.h"
 extern "C" int first(int blocks, int mt, int tiles) { return zc::first_block(blocks, mt, tiles); }
+extern "C" int first32(int blocks, int mt, int tiles) { return zc::first_block32(blocks, mt, tiles); }
 // the first tile whose start is not the quotient in 64 bits, -1 if there is none
 extern "C" int differs(int blocks, int tiles) {
   for (int mt = 0; mt <= tiles; ++mt)
@@ -53,3 +54,11 @@ def test_small_layers(split):
     for tiles in range(1, 40):
         for blocks in range(tiles, 10 * tiles + 1, 3):
             assert split.differs(blocks, tiles) == -1
+
+
+@pytest.mark.parametrize("rows", [1, 257, 70000, (1 << 22) - 257, (1 << 22) - 32, (1 << 22) - 31, (1 << 22) - 1])
+def test_spread_of_32_row_blocks(split, rows):
+    # blocks of 32 rows, tiles of 256: the product reaches 2^31 itself
+    blocks, tiles = -(-rows // 32), -(-rows // 256)
+    got = [split.first32(blocks, mt, tiles) for mt in range(tiles + 1)]
+    assert got == [blocks * mt // tiles for mt in range(tiles + 1)]
