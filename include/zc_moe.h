@@ -530,8 +530,8 @@ zc_status zc_grad_norm(const zc_grad_tensor* tensors, int64_t count, int g_dtype
  * the step runs, so that nothing has to come to the host between zc_grad_norm
  * and the step, and a captured step goes on when it is replayed; lr >= 0.  Where factor
  * is 0 nothing is written.  A gradient that is not finite makes what it touches NaN
- * or infinite (with 8-bit states all its 128 values).  No buffer may overlap
- * another, and none be in the list twice.  The scales, factor, lr and step are
+ * or infinite (an infinite one, with 8-bit states, the states of all its 128
+ * values).  No buffer may overlap another, and none be in the list twice.  The scales, factor, lr and step are
  * aligned like their elements, the other buffers to 16 bytes.  tensors: host array,
  * as above; n < 2^36, count <= 2^20. */
 enum { ZC_STATE_F32 = 0, ZC_STATE_8BIT = 1 };

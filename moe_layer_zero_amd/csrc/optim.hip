@@ -298,12 +298,13 @@ __device__ __forceinline__ void store(T* p, int left, const float* f) {
   }
 }
 // bf16 weights rounded down after 16 random bits' part of their distance is added:
-// the upper half of the sum (an infinity and a NaN stay what they are).
+// the upper half of the sum.  An infinity stays one; a NaN, whose lower bits may be
+// set too and carry out of the sum, becomes the one without them.
 template <int W>
 __device__ __forceinline__ void store_bits(bf16_t* p, int left, const float* f, const uint32_t* add) {
   uint32_t u[W];
 #pragma unroll
-  for (int e = 0; e < W; ++e) u[e] = __float_as_uint(f[e]) + add[e];
+  for (int e = 0; e < W; ++e) u[e] = f[e] != f[e] ? 0x7fc00000u : __float_as_uint(f[e]) + add[e];
   if (left >= W) {
     typedef uint32_t words_t __attribute__((ext_vector_type(W / 2)));
     words_t w;
