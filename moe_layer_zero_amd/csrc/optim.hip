@@ -304,7 +304,15 @@ template <int W>
 __device__ __forceinline__ void store_bits(bf16_t* p, int left, const float* f, const uint32_t* add) {
   uint32_t u[W];
 #pragma unroll
-  for (int e = 0; e < W; ++e) u[e] = f[e] != f[e] ? 0x7fc00000u : __float_as_uint(f[e]) + add[e];
+  for (int e = 0; e < W; ++e) u[e] = __float_as_uint(f[e]) + add[e];
+  bool nan = false;
+#pragma unroll
+  for (int e = 0; e < W; e += 2) nan |= __builtin_isunordered(f[e], f[e + 1]);
+  if (__any(nan)) {  // (a branch of the wavefront's)
+#pragma unroll
+    for (int e = 0; e < W; ++e)
+      if (f[e] != f[e]) u[e] = 0x7fc00000u;
+  }
   if (left >= W) {
     typedef uint32_t words_t __attribute__((ext_vector_type(W / 2)));
     words_t w;
