@@ -433,7 +433,7 @@ zc_status zc_mxfp4_quantize(int64_t R, int64_t C, int dtype, const void* src, ui
  * multiply them by rows x and h in MXFP8 (A8; the rules of zc_moe_quantize_weights)
  * or in MXFP4 too (A4, at up to twice the rate, h and x in 4 bits), sums in fp32.  x
  * is quantized once for each token, h from its fp32 values; the experts' outputs y
- * are kept in fp32, in bf16 where T*K/(N+Z) is above 10 and d and I are multiples of
+ * are kept in fp32, in bf16 where T*K/(N+Z) is 11 or more and d and I are multiples of
  * 512 (many rows: y's bytes count there; x, h and a matrix of fewer than 2^31
  * values each); the router, gates, the
  * combine and the zero-computation experts (which return the unquantized x) stay in
@@ -494,8 +494,9 @@ zc_status zc_rmsnorm_backward(const zc_norm_desc* desc, const void* dy, const vo
  *   norm   = sqrt(sum of g^2), squares and sums in binary64, in a fixed order;
  *   factor = max_norm / norm where norm > max_norm, else 1; 0 where norm is not
  *            finite: zc_adamw_step then leaves everything as it is.
- * out (device, fp32 [2]): norm, factor.  step (device, int64, nullable): one more
- * where norm is finite.  max_norm > 0, infinity for no clipping.  tensors is a
+ * out (device, fp32 [2]): norm (infinity where it is beyond fp32; factor is still that
+ * of the norm in binary64), factor.  step (device, int64, nullable): one more where
+ * norm is finite in binary64.  max_norm > 0, infinity for no clipping.  tensors is a
  * host array, read during the call; its pointers are device pointers (NULL where
  * n is 0).  n < 2^36, count <= 2^20.  ws: zc_grad_norm_workspace_size bytes (0
  * for invalid arguments).  No output may overlap an input or another output. */
@@ -518,7 +519,7 @@ zc_status zc_grad_norm(const zc_grad_tensor* tensors, int64_t count, int g_dtype
  *   ZC_STATE_F32:  m, v fp32 [n].
  *   ZC_STATE_8BIT: m, v E4M3 codes [n] and m_scale, v_scale fp32 [ceil(n / 128)],
  *     one for each 128 values: m = code * scale; v = (code * scale)^2, so that the
- *     codes span its range; scale = max / 448 over the new values, at least
+ *     codes span its range; scale = max * (1 / 448) over the new values in fp32, at least
  *     2^-120; no positive v becomes 0 but the smallest code.
  * rounding: how what has fewer than 32 bits is rounded.  ZC_ROUND_NEAREST: ties to
  * even.  ZC_ROUND_STOCHASTIC: 8-bit codes, and bf16 weights without master, go to
@@ -531,9 +532,9 @@ zc_status zc_grad_norm(const zc_grad_tensor* tensors, int64_t count, int g_dtype
  * and the step, and a captured step goes on when it is replayed; lr >= 0.  Where factor
  * is 0 nothing is written.  A gradient that is not finite makes what it touches NaN
  * or infinite (an infinite one, with 8-bit states, the states of all its 128
- * values).  No buffer may overlap another, and none be in the list twice.  The scales, factor, lr and step are
- * aligned like their elements, the other buffers to 16 bytes.  tensors: host array,
- * as above; n < 2^36, count <= 2^20. */
+ * values).  No buffer may overlap another, and none be in the list twice.  The
+ * scales, factor, lr and step are aligned like their elements, the other buffers to
+ * 16 bytes.  tensors: host array, as above; n < 2^36, count <= 2^20. */
 enum { ZC_STATE_F32 = 0, ZC_STATE_8BIT = 1 };
 enum { ZC_ROUND_NEAREST = 0, ZC_ROUND_STOCHASTIC = 1 };
 typedef struct {
@@ -552,7 +553,7 @@ typedef struct {
   int32_t state;            /* ZC_STATE_F32 or ZC_STATE_8BIT */
   int32_t rounding;
   double lr, beta1, beta2;  /* lr >= 0; 0 <= beta < 1 */
-  double eps;               /* > 0 in fp32 */
+  double eps;               /* at least 2^-126, finite in fp32 */
   int64_t step;             /* >= 1 where it counts */
   uint32_t seed;
 } zc_adamw_cfg;

@@ -50,7 +50,8 @@ struct Mx4Params {
   const uint8_t* As;        // their scales, [rows][K/32]
   const int32_t* perm;      // gate/up only
   int kdiv;                 // K of the layer (slot -> token)
-  uint32_t kdiv_inv;        // 2^31 / K, rounded up: divides slots below 2^27 (K <= 16)
+  uint32_t kdiv_inv;        // many rows: 2^31 / K, rounded up: divides slots below 2^31 / K
+                            // (K <= 32, and fewer than 2^22 slots there)
   const uint8_t* B;         // W_g or W_d
   const uint8_t* B2;        // W_u (gate/up)
   uint8_t* hq;              // gate/up output: codes [P][I] or [P][I/2] ...
@@ -383,7 +384,9 @@ __device__ __forceinline__ void lds_barrier() {
 //
 // An expert's rows are spread evenly over its tiles in blocks of 16, and a tile's sums
 // are those of 2, 4, 6, 8 or 10 blocks.  y goes out in bf16: it would be twice the bytes
-// in fp32 (1.6 of 10.7 GB here), and costs 2^-9 of each of K terms.
+// in fp32 (1.6 of 10.7 GB here), and costs up to 2^-8 of each of K terms: the result's
+// error to 64 bits is 1.9e-3 of its norm, with y in fp32 (256 tokens) 1.7e-3, most of it
+// out's own rounding.
 template <int EPI, bool A4, int TM>
 __global__ __launch_bounds__(kThreads, 2) void mx4_wide_kernel(Mx4Params p) {
   constexpr int CB = 128;                      // bytes of a row in a ring slot: a cache line
@@ -750,7 +753,7 @@ __device__ __forceinline__ uint32_t mx4_quad(const float* f, int& S) {
 
 // Rows -> natural codes and scales, and the values they stand for.  Eight values a
 // thread.  Bound by HBM: 16384 x 6144 values in bf16 with their values back, 456 MB, in
-// 86 us, 5.3 TB/s, a copy's rate (non-temporal loads or stores: the same).
+// 81 us, 5.6 TB/s, a copy's rate (non-temporal loads or stores: the same).
 template <typename T>
 __global__ __launch_bounds__(256) void mx4_rows_kernel(const T* src, int64_t pieces,
                                                        uint32_t* __restrict__ codes,
@@ -819,10 +822,11 @@ __global__ __launch_bounds__(kMaxExperts) void mx4_start_kernel(
 //     20 rows 3413 / 2287 / 1878
 //   d 1024, I 512, 64 experts:    8 rows 26.2 / 29.8 / 28.6, 12 rows 28.5 / 31.4 / 28.7,
 //     20 rows 34.7 / 36.1 / 29.7, 64 rows 58.4 / 60.1 / 33.6
-// With MXFP4 rows its tiles have up to 160 rows from 110 rows an expert on, where that
-// saves tiles (the large layer's gate/up, tiles of 128 / of 160): 101 rows 1258 / 1274, 128
-// rows 1452 / 1334, 187 rows (two tiles either way) 1685 / 1760, 256 rows 2007 / 1906, 375
-// rows 2587 / 2605; the small one's at 128 rows 18.6 / 15.8, 255 rows 24.5 / 22.2.
+// With MXFP4 rows its tiles have up to 160 rows from 110 rows an expert on: that gains
+// where it saves tiles, and loses up to 4.5% where it does not (the large layer's
+// gate/up, tiles of 128 / of 160): 101 rows 1258 / 1274, 128 rows 1452 / 1334, 187 rows (two
+// tiles either way) 1685 / 1760, 256 rows 2007 / 1906, 375 rows 2587 / 2605; the small
+// one's at 128 rows 18.6 / 15.8, 255 rows 24.5 / 22.2.
 // That kernel takes whole groups of 512 steps, and byte offsets of 31 bits into x, h and
 // a matrix: other layers have tiles of 16, 32 or 64.
 Mx4Plan mx4_plan(bool a4, int64_t Tn, int64_t rows, int64_t E, int64_t d, int64_t I) {
